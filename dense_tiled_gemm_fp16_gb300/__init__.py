@@ -13,6 +13,9 @@ gate/up product) for each.  The torch-tensor forms read pointers, strides and
 the current stream from the tensors: ``matmul``, ``bmm``, ``grouped_mm``,
 ``fused_mm`` (2-D or batched) and ``grouped_fused_mm``; ``plan_for`` and
 ``fused_plan_for`` report the execution plan.
+
+``mxf4.py`` binds the MXFP4 matrices of ``include/gemm_mxf4.h`` (``mxf4_quantize``,
+``mxf4_dequantize``, ``mxf4_mm``).
 """
 from __future__ import annotations
 
@@ -21,6 +24,9 @@ import os
 import threading
 
 from . import ledger  # noqa: F401  (pure-Python cost ledger)
+from . import mxf4
+from .mxf4 import (Mxf4Matrix, gemm_mxf4, mxf4_dequantize, mxf4_dequantize_ptr, mxf4_mm, mxf4_quantize,  # noqa: F401
+                   mxf4_quantize_ptr, mxf4_sizes)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgemm_f16.so")
@@ -145,6 +151,7 @@ def lib():
                 L.gemm_f16_fused_get_plan.argtypes = [P, I64, I64, P, I64, I64, P, P, P, I, P, I64, I64, I64, I64,
                                                       ctypes.POINTER(Plan)]
                 L.gemm_f16_fused_get_plan.restype = ctypes.c_int
+                mxf4.declare(L)
                 _lib = L
     return _lib
 

@@ -13,6 +13,7 @@
 
 #include "gemm_f16.h"
 #include "gemm_kernel.cuh"
+#include "host.h"
 #include "repack.cuh"
 static_assert(GEMM_F16_MAX_GROUPS == gemm_f16_dev::kMaxGroups, "the header and the kernel agree on the group limit");
 
@@ -1341,6 +1342,45 @@ bool total_rows(const int64_t* group_rows, int64_t groups, int64_t* total)
 }
 
 }  // namespace
+
+// What host.h hands to the library's other translation units.
+namespace gemm_f16_host {
+
+gemm_f16_status current_device(Device* out)
+{
+    DevInfo* d = nullptr;
+    const gemm_f16_status st = device_info(&d);
+    if (st != GEMM_F16_OK) return st;
+    load_entry_points();
+    out->sms = d->sms;
+    out->status = d->status_ptr;
+    return GEMM_F16_OK;
+}
+
+bool device_range_ok(const void* p, int64_t bytes) { return ::device_range_ok(p, bytes); }
+
+bool view_extent(int64_t rows, int64_t cols, int64_t s_r, int64_t s_c, int64_t* elems)
+{
+    return ::view_extent(rows, cols, s_r, s_c, elems);
+}
+
+bool batch_extent(int64_t e, int64_t n, int64_t stride, int64_t* total) { return ::batch_extent(e, n, stride, total); }
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
+{
+    load_entry_points();
+    return g_encode;
+}
+
+int64_t option(int o) { return opt(o); }
+
+uint64_t timeout_ns()
+{
+    const int64_t ms = opt(GEMM_F16_OPT_TIMEOUT_MS);
+    return static_cast<uint64_t>(ms > 0 ? ms : 1000) * 1000000ull;
+}
+
+}  // namespace gemm_f16_host
 
 extern "C" {
 

@@ -1,0 +1,217 @@
+// Host side of the MXFP4 entry points (gemm_mxf4.h): argument checks, the
+// choice of form, tensor maps and launches.
+#include <algorithm>
+#include <cstdint>
+#include <mutex>
+
+#include "gemm_mxf4.h"
+#include "host.h"
+#include "mxf4_convert.cuh"
+#include "mxf4_gemm.cuh"
+
+using namespace gemm_f16_host;
+
+namespace {
+
+constexpr int kMaxSmem = 232448;
+
+struct Sizes {
+    int64_t blocks, pitch, kt, row_tiles, code_bytes, scale_bytes;   // bytes of the whole batch
+};
+
+bool sizes_of(int64_t rows, int64_t k, int64_t batch, Sizes* s)
+{
+    if (rows < 1 || k < 1 || batch < 1 || rows > GEMM_F16_MAX_DIM || k > GEMM_F16_MAX_DIM) return false;
+    s->blocks = cdiv(k, 32);
+    s->pitch = s->blocks * 16;
+    s->kt = cdiv(s->blocks, 4);
+    s->row_tiles = cdiv(rows, 128);
+    if (__builtin_mul_overflow(rows * s->pitch, batch, &s->code_bytes)) return false;
+    return !__builtin_mul_overflow(s->row_tiles * s->kt * mxf4_dev::kScaleTile, batch, &s->scale_bytes);
+}
+
+bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+int64_t elem_bytes(int dtype) { return dtype == MXF4_F32 ? 4 : 2; }
+
+// Batches are the third grid dimension.
+constexpr int64_t kMaxBatch = 65535;
+
+bool encode_codes(CUtensorMap* tm, const void* codes, int64_t rows, int64_t pitch, uint32_t box_rows)
+{
+    const auto encode = tensor_map_encoder();
+    if (!encode) return false;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(pitch), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
+    cuuint32_t box[2] = {128, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return encode(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T>
+gemm_f16_status launch_quantize(const mxf4_dev::QuantParams& p, int64_t batch, cudaStream_t stream)
+{
+    const int64_t tiles = p.row_tiles * p.col_tiles;
+    if (tiles > INT32_MAX) return GEMM_F16_ERR_INVALID_VALUE;
+    const dim3 grid(static_cast<unsigned>(tiles), 1, static_cast<unsigned>(batch));
+    return launch_kernel(p.sk == 1 ? mxf4_dev::quantize_rows<T> : mxf4_dev::quantize_strided<T>, grid,
+                         mxf4_dev::kConvThreads, 0, 1, stream, p);
+}
+
+template <typename T>
+gemm_f16_status launch_dequantize(const mxf4_dev::DequantParams& p, int64_t batch, cudaStream_t stream)
+{
+    const int64_t blocks = cdiv(p.rows * p.k, 8 * mxf4_dev::kConvThreads);
+    if (blocks > INT32_MAX) return GEMM_F16_ERR_INVALID_VALUE;
+    const dim3 grid(static_cast<unsigned>(blocks), 1, static_cast<unsigned>(batch));
+    return launch_kernel(p.k % 8 == 0 ? mxf4_dev::dequantize<T, true> : mxf4_dev::dequantize<T, false>, grid,
+                         mxf4_dev::kConvThreads, 0, 1, stream, p);
+}
+
+// Dynamic shared memory above 48 KB is allowed once per device.
+bool allow_smem(int device)
+{
+    static std::mutex mutex;
+    static bool done[64] = {};
+    std::lock_guard<std::mutex> lk(mutex);
+    if (device < 0 || device >= 64) return false;
+    if (!done[device]) {
+        if (cudaFuncSetAttribute(mxf4_dev::gemm_mxf4_tile, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem / 2) !=
+            cudaSuccess) {
+            cudaGetLastError();
+            return false;
+        }
+        done[device] = true;
+    }
+    return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_f16_status mxf4_sizes(int64_t rows, int64_t k, int64_t batch, int64_t* code_bytes, int64_t* scale_bytes)
+{
+    Sizes s;
+    if (!code_bytes || !scale_bytes || !sizes_of(rows, k, batch, &s)) return GEMM_F16_ERR_INVALID_VALUE;
+    *code_bytes = s.code_bytes;
+    *scale_bytes = s.scale_bytes;
+    return GEMM_F16_OK;
+}
+
+gemm_f16_status mxf4_quantize(const void* x, int dtype, int64_t stride_b, int64_t stride_r, int64_t stride_k,
+                              void* codes, void* scales, int64_t rows, int64_t k, int64_t batch, cudaStream_t stream)
+{
+    Sizes s;
+    if (!x || !codes || !scales || dtype < MXF4_F16 || dtype > MXF4_F32 || !sizes_of(rows, k, batch, &s))
+        return GEMM_F16_ERR_INVALID_VALUE;
+    if (stride_r <= 0 || stride_k <= 0 || stride_b < 0 || batch > kMaxBatch) return GEMM_F16_ERR_INVALID_VALUE;
+    const int64_t eb = elem_bytes(dtype);
+    if (!aligned(x, eb) || !aligned(codes, 16) || !aligned(scales, 16)) return GEMM_F16_ERR_INVALID_VALUE;
+    int64_t ex, bytes;
+    if (!view_extent(rows, k, stride_r, stride_k, &ex) || !batch_extent(ex, batch, stride_b, &ex) ||
+        __builtin_mul_overflow(ex, eb, &bytes))
+        return GEMM_F16_ERR_INVALID_VALUE;
+    if (overlaps(codes, s.code_bytes, x, bytes) || overlaps(scales, s.scale_bytes, x, bytes) ||
+        overlaps(codes, s.code_bytes, scales, s.scale_bytes))
+        return GEMM_F16_ERR_ALIAS;
+    Device dev;
+    const gemm_f16_status st = current_device(&dev);
+    if (st != GEMM_F16_OK) return st;
+    if (!device_range_ok(x, bytes) || !device_range_ok(codes, s.code_bytes) || !device_range_ok(scales, s.scale_bytes))
+        return GEMM_F16_ERR_INVALID_VALUE;
+    const mxf4_dev::QuantParams p{x, stride_b, stride_r, stride_k, static_cast<uint8_t*>(codes),
+                                  static_cast<uint8_t*>(scales), rows, k, s.pitch, s.kt, s.row_tiles,
+                                  cdiv(k, mxf4_dev::kTileVals)};
+    return dtype == MXF4_F16    ? launch_quantize<__half>(p, batch, stream)
+           : dtype == MXF4_BF16 ? launch_quantize<__nv_bfloat16>(p, batch, stream)
+                                : launch_quantize<float>(p, batch, stream);
+}
+
+gemm_f16_status mxf4_dequantize(const void* codes, const void* scales, void* y, int dtype, int64_t rows, int64_t k,
+                                int64_t batch, cudaStream_t stream)
+{
+    Sizes s;
+    int64_t bytes;
+    if (!codes || !scales || !y || dtype < MXF4_F16 || dtype > MXF4_F32 || !sizes_of(rows, k, batch, &s) ||
+        batch > kMaxBatch || __builtin_mul_overflow(rows * k, batch, &bytes) ||
+        __builtin_mul_overflow(bytes, elem_bytes(dtype), &bytes))
+        return GEMM_F16_ERR_INVALID_VALUE;
+    if (!aligned(y, elem_bytes(dtype)) || !aligned(codes, 16) || !aligned(scales, 16)) return GEMM_F16_ERR_INVALID_VALUE;
+    if (overlaps(y, bytes, codes, s.code_bytes) || overlaps(y, bytes, scales, s.scale_bytes)) return GEMM_F16_ERR_ALIAS;
+    Device dev;
+    const gemm_f16_status st = current_device(&dev);
+    if (st != GEMM_F16_OK) return st;
+    if (!device_range_ok(y, bytes) || !device_range_ok(codes, s.code_bytes) || !device_range_ok(scales, s.scale_bytes))
+        return GEMM_F16_ERR_INVALID_VALUE;
+    const mxf4_dev::DequantParams p{static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), y, rows, k,
+                                    s.pitch, s.kt, s.row_tiles};
+    return dtype == MXF4_F16    ? launch_dequantize<__half>(p, batch, stream)
+           : dtype == MXF4_BF16 ? launch_dequantize<__nv_bfloat16>(p, batch, stream)
+                                : launch_dequantize<float>(p, batch, stream);
+}
+
+gemm_f16_status gemm_mxf4(const void* A_codes, const void* A_scales, const void* B_codes, const void* B_scales,
+                          const void* bias, int act, void* C, int64_t ldc, int64_t M, int64_t N, int64_t K,
+                          cudaStream_t stream)
+{
+    Sizes sa, sb;
+    int64_t ec;
+    if (!A_codes || !A_scales || !B_codes || !B_scales || !C || !sizes_of(M, K, 1, &sa) || !sizes_of(N, K, 1, &sb))
+        return GEMM_F16_ERR_INVALID_VALUE;
+    if (act < GEMM_F16_ACT_NONE || act > GEMM_F16_ACT_GELU || ldc < N || !view_extent(M, N, ldc, 1, &ec))
+        return GEMM_F16_ERR_INVALID_VALUE;
+    if (!aligned(A_codes, 16) || !aligned(A_scales, 16) || !aligned(B_codes, 16) || !aligned(B_scales, 16) ||
+        !aligned(C, 2) || !aligned(bias, 2))
+        return GEMM_F16_ERR_INVALID_VALUE;
+    if (overlaps(C, 2 * ec, A_codes, sa.code_bytes) || overlaps(C, 2 * ec, A_scales, sa.scale_bytes) ||
+        overlaps(C, 2 * ec, B_codes, sb.code_bytes) || overlaps(C, 2 * ec, B_scales, sb.scale_bytes) ||
+        (bias && overlaps(C, 2 * ec, bias, 2 * N)))
+        return GEMM_F16_ERR_ALIAS;
+    Device dev;
+    const gemm_f16_status st = current_device(&dev);
+    if (st != GEMM_F16_OK) return st;
+    if (!device_range_ok(A_codes, sa.code_bytes) || !device_range_ok(A_scales, sa.scale_bytes) ||
+        !device_range_ok(B_codes, sb.code_bytes) || !device_range_ok(B_scales, sb.scale_bytes) ||
+        !device_range_ok(C, 2 * ec) || (bias && !device_range_ok(bias, 2 * N)))
+        return GEMM_F16_ERR_INVALID_VALUE;
+
+    mxf4_dev::GemmParams p = {};
+    // Few rows of A: B's rows take the 128 lanes and A's rows the narrow side.
+    p.swapped = M <= 64 && M < N;
+    p.bn = !p.swapped ? 128 : M <= 16 ? 16 : M <= 32 ? 32 : 64;
+    p.M = p.swapped ? N : M;
+    p.N = p.swapped ? M : N;
+    p.sfa = static_cast<const uint8_t*>(p.swapped ? B_scales : A_scales);
+    p.sfb = static_cast<const uint8_t*>(p.swapped ? A_scales : B_scales);
+    p.kt = sa.kt;
+    p.bias = static_cast<const __half*>(bias);
+    p.C = static_cast<__half*>(C);
+    p.ldc = ldc;
+    p.k64 = static_cast<int32_t>(cdiv(K, 64));
+    p.steps = static_cast<int32_t>(cdiv(K, 256));
+    p.act = act;
+    p.timeout_ns = timeout_ns();
+    p.status = dev.status;
+    p.test_stall = option(GEMM_F16_OPT_TEST_STALL) == 1;
+    const uint32_t sbytes = mxf4_dev::gemm_stage_bytes(p.bn);
+    // two CTAs an SM, so that one's loads run under the other's last part
+    p.stages = static_cast<int32_t>(std::min<int64_t>(16, (kMaxSmem / 2 - 2048) / sbytes));
+    p.tmem_cols = p.bn == 128 ? 256 : p.bn == 64 ? 128 : p.bn == 32 ? 64 : 32;
+    const int64_t tiles = cdiv(p.M, 128) * cdiv(p.N, p.bn);
+    int cluster = 1;
+    while (cluster < 8 && tiles * cluster * 2 <= 2 * dev.sms && cluster * 2 <= p.steps) cluster *= 2;
+    if (tiles * cluster > INT32_MAX) return GEMM_F16_ERR_INVALID_VALUE;
+    if (!encode_codes(&p.tmA, p.swapped ? B_codes : A_codes, p.M, sa.pitch, 128) ||
+        !encode_codes(&p.tmB, p.swapped ? A_codes : B_codes, p.N, sa.pitch, static_cast<uint32_t>(p.bn)))
+        return GEMM_F16_ERR_LAUNCH;
+    int d = 0;
+    cudaGetDevice(&d);
+    if (!allow_smem(d)) return GEMM_F16_ERR_LAUNCH;
+    return launch_kernel(mxf4_dev::gemm_mxf4_tile, dim3(static_cast<unsigned>(tiles * cluster)), mxf4_dev::kGemmThreads,
+                         p.stages * sbytes + 1024, cluster, stream, p);
+}
+
+}  // extern "C"

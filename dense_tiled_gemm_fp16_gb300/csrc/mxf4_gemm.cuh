@@ -1,0 +1,310 @@
+// C[m, n] = act(sum_k A[m, k] B[n, k] + bias[n]) for two MXFP4 matrices.
+//
+// The tensor cores take e2m1 codes from shared memory and the blocks' scales
+// from tensor memory (tcgen05.mma kind::mxf4, block_scale, 64 values of K an
+// instruction): every product is exact, sums are fp32 in tensor memory, and
+// nothing is dequantised on the way.  A row of a pipeline slot is 128 bytes =
+// 256 values; its scales are two 512-byte tiles for each 128 rows, which
+// tcgen05.cp copies to 4 columns of tensor memory each, repeated for the four
+// lane quarters as the instruction wants them.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "gemm_f16.h"
+#include "mxf4_convert.cuh"
+#include "ptx.cuh"
+
+namespace mxf4_dev {
+
+// ------------------------------------------------------------------ PTX
+// D[tmem] (+)= A * B with block scales; the two scales of each row's 64 values
+// are the bytes 2 * half, 2 * half + 1 of the scale columns' words, `half` set
+// in the instruction descriptor.
+__device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t sfa, uint32_t sfb, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// A 512-byte scale tile (32 rows of 16 bytes) to 4 tensor-memory columns, the
+// same in each quarter of the lanes.
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t desc)
+{
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// Unswizzled descriptor of a scale tile: 8-row groups 128 bytes apart.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr)
+{
+    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(1) << 16) |
+           (static_cast<uint64_t>(8) << 32) | (static_cast<uint64_t>(1) << 46);
+}
+
+// Instruction descriptor: e2m1 A and B (bits 7-9, 10-12), E8M0 scales (23),
+// N / 8 (17-22), M / 128 (27-28), the scales' byte pair of B (4-5) and A (29-30).
+__host__ __device__ constexpr uint32_t idesc_mxf4(uint32_t m, uint32_t n, uint32_t half)
+{
+    return (1u << 7) | (1u << 10) | (1u << 23) | ((n >> 3) << 17) | ((m >> 7) << 27) | ((2 * half) << 4) |
+           ((2 * half) << 29);
+}
+
+struct GemmParams {
+    CUtensorMap tmA, tmB;        // codes: {16 * blocks bytes, rows}, box {128, 128 or bn}
+    const uint8_t* sfa;          // scale tiles of the kernel's A and B
+    const uint8_t* sfb;
+    int64_t kt;                  // scale tiles along k
+    const __half* bias;
+    __half* C;
+    int64_t ldc;
+    int64_t M, N;                // of the kernel's A and B rows
+    int32_t k64;                 // 64-value MMA steps in all: ceil(k / 64)
+    int32_t steps;               // 256-value slots in all
+    int32_t stages, act;
+    int32_t swapped;             // the kernel's A is the caller's B: C[n][m], bias along m
+    int32_t bn;                  // rows of the kernel's B a tile takes
+    uint32_t tmem_cols;
+    int32_t test_stall;          // failure test: the MMA thread first waits on a barrier nothing arrives on
+    uint64_t timeout_ns;
+    int* status;
+};
+
+constexpr int kGemmThreads = 192;   // warps 0-3 epilogue, 4 loads, 5 MMA
+constexpr uint64_t kDrainNs = 1000000000ull;
+constexpr uint32_t kABytes = 128 * 128, kSfBytes = 2 * kScaleTile;
+
+__host__ __device__ inline uint32_t gemm_stage_bytes(int bn) { return kABytes + bn * 128 + 2 * kSfBytes; }
+
+__device__ __forceinline__ float act_f32(int act, float x)
+{
+    switch (act) {
+    case 1: return x < 0.f ? 0.f : x;
+    case 2: return x / (1.f + expf(-x));
+    case 3: return x * (0.5f * erfcf(-x * 0.70710678118654752f));
+    default: return x;
+    }
+}
+
+// Sum over the cluster's parts of one output's K range, by distributed shared
+// memory: `at` is the same offset in every CTA.
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// 16 finished sums of row m, columns n .. n + 15, to C.
+__device__ __forceinline__ void store16(const GemmParams& p, int64_t m, int64_t n, float* v)
+{
+    if (m >= p.M) return;
+    if (p.swapped) {   // lanes hold neighbouring columns of C
+        const float b = p.bias ? __half2float(p.bias[m]) : 0.f;
+        __half* c = p.C + m;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (n + i < p.N) c[(n + i) * p.ldc] = __float2half_rn(act_f32(p.act, v[i] + b));
+        return;
+    }
+    if (p.bias) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (n + i < p.N) v[i] += __half2float(p.bias[n + i]);
+    }
+    if (p.act) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = act_f32(p.act, v[i]);
+    }
+    __half* c = p.C + m * p.ldc + n;
+    if (n + 16 <= p.N && reinterpret_cast<uintptr_t>(c) % 16 == 0) {
+        uint4 o[2];
+        o[0] = make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]), pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
+        o[1] = make_uint4(pack_half2(v[8], v[9]), pack_half2(v[10], v[11]), pack_half2(v[12], v[13]),
+                          pack_half2(v[14], v[15]));
+        reinterpret_cast<uint4*>(c)[0] = o[0];
+        reinterpret_cast<uint4*>(c)[1] = o[1];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (n + i < p.N) c[i] = __float2half_rn(v[i]);
+    }
+}
+
+// One 128 x bn tile a cluster, its K slots dealt to the cluster's CTAs in
+// contiguous parts; with more than one CTA the parts are summed by rank over
+// distributed shared memory (a fixed order, no workspace and no atomics).
+__global__ void __launch_bounds__(kGemmThreads) gemm_mxf4_tile(const __grid_constant__ GemmParams p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    __shared__ __align__(8) uint64_t bars[2 * 16 + 2];
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int abort_flag;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t bn = p.bn, sbytes = gemm_stage_bytes(p.bn);
+    const uint32_t bar0 = smem_u32(bars);
+    auto full = [&](int s) { return bar0 + 16u * s; };
+    auto empty = [&](int s) { return bar0 + 16u * s + 8u; };
+    const uint32_t done = bar0 + 16u * 16u, never = done + 8u;
+
+    uint32_t crank = 0, csize = 1;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(crank));
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(csize));
+    const int64_t tile = blockIdx.x / csize;
+    const int64_t tiles_m = (p.M + 127) >> 7;
+    const int64_t m0 = (tile % tiles_m) * 128, n0 = (tile / tiles_m) * bn;
+    const int s_lo = static_cast<int>(static_cast<int64_t>(p.steps) * crank / csize);
+    const int s_hi = static_cast<int>(static_cast<int64_t>(p.steps) * (crank + 1) / csize);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        mbar_init(done, 1);
+        mbar_init(never, 1);
+        abort_flag = 0;
+        fence_mbarrier_init();
+        tma_prefetch_desc(&p.tmA);
+        tma_prefetch_desc(&p.tmB);
+    }
+    if (warp == 5) {
+        tmem_alloc(smem_u32(&tmem_slot), p.tmem_cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    griddep_wait();
+    griddep_launch_dependents();
+
+    const volatile int* abort = &abort_flag;
+    auto fail = [&]() {
+        abort_flag = 1;
+        atomicExch(p.status, GEMM_F16_ERR_TIMEOUT);
+    };
+    if (warp == 4) {
+        if (lane == 0) {
+            int st = 0;
+            uint32_t ph = 0;
+            const uint8_t* sa = p.sfa + (m0 >> 7) * p.kt * kScaleTile;
+            const uint8_t* sb = p.sfb + (n0 >> 7) * p.kt * kScaleTile;
+            bool ok = true;
+            int issued = 0;
+            for (int s = s_lo; s < s_hi; ++s, ++issued) {
+                ok = mbar_wait(empty(st), ph ^ 1u, abort, p.timeout_ns);
+                if (!ok) break;
+                const uint32_t a = base + st * sbytes, b = a + kABytes, fa = b + bn * 128, fb = fa + kSfBytes;
+                // (an odd last scale tile: the second one is not this row tile's)
+                const uint32_t sf = min(static_cast<int64_t>(2), p.kt - 2 * s) * kScaleTile;
+                mbar_arrive_expect_tx(full(st), kABytes + bn * 128 + 2 * sf);
+                tma_load_2d(a, &p.tmA, s * 128, static_cast<int32_t>(m0), full(st));
+                tma_load_2d(b, &p.tmB, s * 128, static_cast<int32_t>(n0), full(st));
+                bulk_load(fa, sa + static_cast<int64_t>(s) * kSfBytes, sf, full(st));
+                bulk_load(fb, sb + static_cast<int64_t>(s) * kSfBytes, sf, full(st));
+                if (++st == p.stages) st = 0, ph ^= 1u;
+            }
+            if (!ok) {   // copies in flight land before the CTA leaves
+                fail();
+                for (int q = 0; q < p.stages && q < issued; ++q)
+                    mbar_wait(full(q), ((issued - q + p.stages - 1) / p.stages - 1) & 1u, nullptr, kDrainNs);
+            }
+        }
+    } else if (warp == 5) {
+        if (lane == 0) {
+            int st = 0;
+            uint32_t ph = 0;
+            const uint32_t tsa = tmem + bn, tsb = tsa + 8;
+            const uint32_t id0 = idesc_mxf4(128, bn, 0), id1 = idesc_mxf4(128, bn, 1);
+            bool ok = !p.test_stall || mbar_wait(never, 0, abort, p.timeout_ns);
+            for (int s = s_lo; s < s_hi && ok; ++s) {
+                ok = mbar_wait(full(st), ph, abort, p.timeout_ns);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t a = base + st * sbytes, b = a + kABytes, fa = b + bn * 128, fb = fa + kSfBytes;
+                const uint64_t da = umma_desc_sw128(a, 16, 1024), db = umma_desc_sw128(b, 16, 1024);
+                const int n64 = min(4, p.k64 - 4 * s);
+                for (int h = 0; h < (n64 + 1) / 2; ++h) {
+                    tmem_copy_scales(tsa + 4 * h, scale_desc(fa + h * kScaleTile));
+                    tmem_copy_scales(tsb + 4 * h, scale_desc(fb + h * kScaleTile));
+                }
+                for (int q = 0; q < n64; ++q)
+                    umma_mxf4(tmem, da + 2 * q, db + 2 * q, q & 1 ? id1 : id0, tsa + 4 * (q >> 1), tsb + 4 * (q >> 1),
+                              s > s_lo || q > 0);
+                umma_commit(empty(st));
+                if (++st == p.stages) st = 0, ph ^= 1u;
+            }
+            umma_commit(done);
+            if (!ok) {
+                fail();
+                mbar_wait(done, 0, nullptr, kDrainNs);
+            }
+        }
+    } else {
+        const bool ok = mbar_wait(done, 0, abort, p.timeout_ns);
+        if (!ok) fail();
+        tc_fence_after();
+        const int64_t m = m0 + warp * 32 + lane;
+        const uint32_t trow = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        if (csize == 1) {
+            for (uint32_t c = 0; ok && c < bn; c += 16) {
+                uint32_t r[16];
+                tmem_ld_x16(trow + c, r);
+                tmem_wait_ld();
+                float v[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+                store16(p, m, n0 + c, v);
+            }
+        } else if (ok) {
+            // this CTA's part, column by column (lanes hold rows: consecutive words),
+            // where the drained pipeline slots were
+            for (uint32_t c = 0; c < bn; c += 16) {
+                uint32_t r[16];
+                tmem_ld_x16(trow + c, r);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + ((c + i) * 128 + warp * 32 + lane) * 4), "r"(r[i])
+                                 : "memory");
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (csize > 1) {
+        __syncwarp();
+        cluster_sync_all();
+        // each CTA finishes a share of the tile's 16-column groups
+        const bool bad = abort_flag != 0;
+        if (warp < 4 && !bad) {
+            for (uint32_t c = 16 * crank; c < bn; c += 16 * csize) {
+                float v[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const uint32_t at = base + ((c + i) * 128 + warp * 32 + lane) * 4;
+                    v[i] = 0.f;
+                    for (uint32_t q = 0; q < csize; ++q) v[i] += ld_cluster_f32(mapa_shared(at, q));
+                }
+                store16(p, m0 + warp * 32 + lane, n0 + c, v);
+            }
+        }
+        __syncwarp();
+        cluster_sync_all();   // no CTA leaves while its part is being read
+    }
+    tc_fence_after();
+    if (warp == 5) tmem_dealloc(tmem, p.tmem_cols);
+}
+
+}  // namespace mxf4_dev
