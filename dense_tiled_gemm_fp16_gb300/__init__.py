@@ -15,7 +15,8 @@ the current stream from the tensors: ``matmul``, ``bmm``, ``grouped_mm``,
 ``fused_plan_for`` report the execution plan.
 
 ``mxf4.py`` binds the MXFP4 matrices of ``include/gemm_mxf4.h`` (``mxf4_quantize``,
-``mxf4_dequantize``, ``mxf4_mm``).
+``mxf4_dequantize``, ``mxf4_mm``); ``moe.py`` the mixture-of-experts layer for a
+few tokens of ``include/moe_f16.h`` (``moe_few``).
 """
 from __future__ import annotations
 
@@ -24,7 +25,8 @@ import os
 import threading
 
 from . import ledger  # noqa: F401  (pure-Python cost ledger)
-from . import mxf4
+from . import moe, mxf4
+from .moe import MoeWeight, moe_f16, moe_f16_workspace_size, moe_few  # noqa: F401
 from .mxf4 import (Mxf4Matrix, gemm_mxf4, mxf4_dequantize, mxf4_dequantize_ptr, mxf4_mm, mxf4_quantize,  # noqa: F401
                    mxf4_quantize_ptr, mxf4_sizes)
 
@@ -152,6 +154,7 @@ def lib():
                                                       ctypes.POINTER(Plan)]
                 L.gemm_f16_fused_get_plan.restype = ctypes.c_int
                 mxf4.declare(L)
+                moe.declare(L)
                 _lib = L
     return _lib
 

@@ -14,7 +14,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libgemm_f16.so")
-SOURCES = [os.path.join(HERE, "csrc", n) for n in ("gemm_f16.cu", "gemm_mxf4.cu")]
+SOURCES = [os.path.join(HERE, "csrc", n) for n in ("gemm_f16.cu", "gemm_mxf4.cu", "moe_f16.cu")]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = [

@@ -1,0 +1,231 @@
+// Host side of the mixture-of-experts layer (moe_f16.h): argument checks, the
+// workspace and the two launches.
+#include <algorithm>
+#include <cstdint>
+#include <mutex>
+
+#include "gemm_mxf4.h"
+#include "host.h"
+#include "moe_f16.h"
+#include "moe_kernel.cuh"
+
+using namespace gemm_f16_host;
+
+static_assert(MOE_F16_MAX_TOKENS == moe_dev::kMaxTokens && MOE_F16_MAX_EXPERTS == moe_dev::kMaxExperts &&
+                  MOE_F16_MAX_TOP_K == moe_dev::kMaxTop,
+              "the header and the kernels agree on the limits");
+
+namespace {
+
+int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+// Places in the workspace.
+struct Layout {
+    int64_t dp, fp, xp, hp, bytes;
+};
+
+bool layout_of(int64_t T, int64_t D, int64_t F, int64_t E, int64_t top, Layout* l)
+{
+    if (T < 1 || T > MOE_F16_MAX_TOKENS || E < 1 || E > MOE_F16_MAX_EXPERTS || top < 1 || top > MOE_F16_MAX_TOP_K ||
+        top > E || D < 1 || D > MOE_F16_MAX_DIM || F < 1 || F > MOE_F16_MAX_DIM)
+        return false;
+    l->dp = round_up(D, 64);
+    l->fp = round_up(F, 64);
+    l->xp = 256;
+    l->hp = l->xp + round_up(T * l->dp * 2, 256);
+    l->bytes = l->hp + round_up(T * top * 2 * l->fp * 2, 256);
+    return true;
+}
+
+// Bytes that one projection spans; false where the description is not valid.
+bool weight_span(const moe_f16_weight& w, int64_t E, int64_t in, int64_t out, int64_t* data, int64_t* scales)
+{
+    if (!w.data) return false;
+    if (w.format == MOE_F16_WEIGHT_MXF4)
+        return w.scales && aligned(w.data, 16) && aligned(w.scales, 16) &&
+               mxf4_sizes(out, in, E, data, scales) == GEMM_F16_OK;
+    if (w.format != MOE_F16_WEIGHT_F16 || w.scales || !aligned(w.data, 2)) return false;
+    if (w.stride_e < 0 || w.stride_i <= 0 || w.stride_o <= 0) return false;
+    int64_t e;
+    if (!view_extent(in, out, w.stride_i, w.stride_o, &e) || !batch_extent(e, E, w.stride_e, &e)) return false;
+    *scales = 0;
+    return !__builtin_mul_overflow(e, 2, data);
+}
+
+// 16-byte words along the contracted axis: every row of 8 values starts aligned.
+bool rows_aligned(const moe_f16_weight& w)
+{
+    return w.stride_i == 1 && w.stride_o % 8 == 0 && w.stride_e % 8 == 0 && aligned(w.data, 16);
+}
+
+moe_dev::Weight weight_of(const moe_f16_weight& w, int64_t E, int64_t in, int64_t out)
+{
+    moe_dev::Weight r = {};
+    r.data = static_cast<const uint8_t*>(w.data);
+    r.scales = static_cast<const uint8_t*>(w.scales);
+    if (w.format == MOE_F16_WEIGHT_MXF4) {
+        int64_t code, scale;
+        mxf4_sizes(out, in, 1, &code, &scale);
+        r.so = code / out;
+        r.se = code;
+        r.scale_se = scale;
+        r.kt = static_cast<int32_t>(cdiv(in, 128));
+    } else {
+        r.se = w.stride_e, r.si = w.stride_i, r.so = w.stride_o;
+    }
+    return r;
+}
+
+constexpr int kMaxDevices = 64;
+
+// More dynamic shared memory than the default, once a device and kernel.
+bool allow_smem(const void* kernel, int slot, int bytes)
+{
+    static std::mutex mutex;
+    static int have[kMaxDevices][16] = {};
+    int d = 0;
+    if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= kMaxDevices) {
+        cudaGetLastError();
+        return false;
+    }
+    std::lock_guard<std::mutex> lk(mutex);
+    if (have[d][slot] >= bytes) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    have[d][slot] = bytes;
+    return true;
+}
+
+template <int kLayout>
+gemm_f16_status launch_route(const moe_dev::Params& p, cudaStream_t stream)
+{
+    const int chunks = p.dp >> 5, tiles = (p.E + 31) >> 5;
+    const int smem = ((chunks / moe_dev::kRouteCluster + 1) * 32 + 8) * 8 * 2 + moe_dev::kWarps * 32 * 8 * 4 + 8 * tiles * 32 * 4;
+    if (!allow_smem(reinterpret_cast<const void*>(moe_dev::moe_route<kLayout>), kLayout, smem)) return GEMM_F16_ERR_LAUNCH;
+    const unsigned groups = static_cast<unsigned>((p.T + 7) / 8);
+    return launch_kernel(moe_dev::moe_route<kLayout>, dim3(groups * moe_dev::kRouteCluster), moe_dev::kThreads, smem,
+                         moe_dev::kRouteCluster, stream, p);
+}
+
+template <int kFmt, int kGroups>
+gemm_f16_status launch_experts(const moe_dev::Params& p, int sms, cudaStream_t stream)
+{
+    using St = moe_dev::Stage<kFmt>;
+    const int ring = moe_dev::kWarps * St::kRing * St::kBytes;
+    const int smem = ring + std::max(2 * moe_dev::kWarps * kGroups * 32 * 16, moe_dev::kWarps * p.T * 16 * 4);
+    const void* fn = reinterpret_cast<const void*>(moe_dev::moe_experts<kFmt, kGroups>);
+    if (!allow_smem(fn, 3 + 2 * kFmt + (kGroups > 1), smem)) return GEMM_F16_ERR_LAUNCH;
+    return launch_kernel(moe_dev::moe_experts<kFmt, kGroups>, dim3(static_cast<unsigned>(sms)), moe_dev::kThreads, smem, 1,
+                         stream, p);
+}
+
+template <int kFmt>
+gemm_f16_status launch_experts(const moe_dev::Params& p, int sms, cudaStream_t stream)
+{
+    return p.T <= 8 ? launch_experts<kFmt, 1>(p, sms, stream) : launch_experts<kFmt, 2>(p, sms, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_f16_status moe_f16_workspace_size(int64_t T, int64_t D, int64_t F, int64_t E, int64_t top_k, size_t* bytes)
+{
+    Layout l;
+    if (!bytes || !layout_of(T, D, F, E, top_k, &l)) return GEMM_F16_ERR_INVALID_VALUE;
+    *bytes = static_cast<size_t>(l.bytes);
+    return GEMM_F16_OK;
+}
+
+gemm_f16_status moe_f16(const void* x, int64_t stride_xt, int64_t stride_xi, const void* router, int64_t stride_ri,
+                        int64_t stride_re, const moe_f16_weight* gate, const moe_f16_weight* up,
+                        const moe_f16_weight* down, int64_t T, int64_t D, int64_t F, int64_t E, int64_t top_k,
+                        int renormalize, int act, void* y, int64_t ldy, float* weights, int32_t* ids, void* workspace,
+                        size_t workspace_bytes, cudaStream_t stream)
+{
+    Layout l;
+    if (!x || !router || !gate || !up || !down || !y || !weights || !ids || !workspace || !layout_of(T, D, F, E, top_k, &l))
+        return GEMM_F16_ERR_INVALID_VALUE;
+    if (stride_xt <= 0 || stride_xi <= 0 || stride_ri <= 0 || stride_re <= 0 || ldy < D || act < GEMM_F16_ACT_NONE ||
+        act > GEMM_F16_ACT_GELU || gate->format != up->format || gate->format != down->format)
+        return GEMM_F16_ERR_INVALID_VALUE;
+    if (!aligned(x, 2) || !aligned(router, 2) || !aligned(y, 2) || !aligned(weights, 4) || !aligned(ids, 4) ||
+        !aligned(workspace, 256))
+        return GEMM_F16_ERR_INVALID_VALUE;
+    struct Span {
+        const void* p;
+        int64_t bytes;
+    };
+    Span in[8], out[4];
+    int nin = 0, nout = 0;
+    int64_t e;
+    if (!view_extent(T, D, stride_xt, stride_xi, &e) || __builtin_mul_overflow(e, 2, &e)) return GEMM_F16_ERR_INVALID_VALUE;
+    in[nin++] = Span{x, e};
+    if (!view_extent(D, E, stride_ri, stride_re, &e) || __builtin_mul_overflow(e, 2, &e)) return GEMM_F16_ERR_INVALID_VALUE;
+    in[nin++] = Span{router, e};
+    const moe_f16_weight* ws[3] = {gate, up, down};
+    for (int i = 0; i < 3; ++i) {
+        int64_t data, scales;
+        if (!weight_span(*ws[i], E, i < 2 ? D : F, i < 2 ? F : D, &data, &scales)) return GEMM_F16_ERR_INVALID_VALUE;
+        in[nin++] = Span{ws[i]->data, data};
+        if (scales) in[nin++] = Span{ws[i]->scales, scales};
+    }
+    if (!view_extent(T, D, ldy, 1, &e) || __builtin_mul_overflow(e, 2, &e)) return GEMM_F16_ERR_INVALID_VALUE;
+    out[nout++] = Span{y, e};
+    out[nout++] = Span{weights, T * top_k * 4};
+    out[nout++] = Span{ids, T * top_k * 4};
+    out[nout++] = Span{workspace, l.bytes};
+    for (int i = 0; i < nout; ++i) {
+        for (int j = 0; j < nin; ++j)
+            if (overlaps(out[i].p, out[i].bytes, in[j].p, in[j].bytes)) return GEMM_F16_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlaps(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return GEMM_F16_ERR_ALIAS;
+    }
+    if (workspace_bytes < static_cast<size_t>(l.bytes)) return GEMM_F16_ERR_OUT_OF_MEMORY;
+    Device dev;
+    gemm_f16_status st = current_device(&dev);
+    if (st != GEMM_F16_OK) return st;
+    for (int i = 0; i < nin; ++i)
+        if (!device_range_ok(in[i].p, in[i].bytes)) return GEMM_F16_ERR_INVALID_VALUE;
+    for (int i = 0; i < nout; ++i)
+        if (!device_range_ok(out[i].p, out[i].bytes)) return GEMM_F16_ERR_INVALID_VALUE;
+
+    moe_dev::Params p = {};
+    p.x = static_cast<const __half*>(x);
+    p.sxt = stride_xt, p.sxi = stride_xi;
+    p.router = static_cast<const __half*>(router);
+    p.sri = stride_ri, p.sre = stride_re;
+    p.gate = weight_of(*gate, E, D, F);
+    p.up = weight_of(*up, E, D, F);
+    p.down = weight_of(*down, E, F, D);
+    p.T = static_cast<int32_t>(T), p.D = static_cast<int32_t>(D), p.F = static_cast<int32_t>(F);
+    p.E = static_cast<int32_t>(E), p.top = static_cast<int32_t>(top_k);
+    p.renorm = renormalize != 0, p.act = act;
+    p.dp = static_cast<int32_t>(l.dp), p.fp = static_cast<int32_t>(l.fp);
+    p.y = static_cast<__half*>(y);
+    p.ldy = ldy;
+    p.weights = weights;
+    p.ids = ids;
+    uint8_t* base = static_cast<uint8_t*>(workspace);
+    p.ctl = reinterpret_cast<moe_dev::Control*>(base);
+    p.xp = reinterpret_cast<__half*>(base + l.xp);
+    p.hp = reinterpret_cast<__half*>(base + l.hp);
+    p.test_stall = option(GEMM_F16_OPT_TEST_STALL) == 1;
+    p.timeout_ns = timeout_ns();
+    p.status = dev.status;
+
+    const bool aligned16 = aligned(router, 16);
+    st = aligned16 && stride_ri == 1 && stride_re % 8 == 0   ? launch_route<moe_dev::kInContiguous>(p, stream)
+         : aligned16 && stride_re == 1 && stride_ri % 8 == 0 ? launch_route<moe_dev::kOutContiguous>(p, stream)
+                                                              : launch_route<moe_dev::kAnyStrides>(p, stream);
+    if (st != GEMM_F16_OK) return st;
+    if (gate->format == MOE_F16_WEIGHT_MXF4) return launch_experts<moe_dev::kMxf4>(p, dev.sms, stream);
+    return rows_aligned(*gate) && rows_aligned(*up) && rows_aligned(*down)
+               ? launch_experts<moe_dev::kF16Rows>(p, dev.sms, stream)
+               : launch_experts<moe_dev::kF16Strided>(p, dev.sms, stream);
+}
+
+}  // extern "C"
