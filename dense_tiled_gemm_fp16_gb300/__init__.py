@@ -27,7 +27,7 @@ import threading
 from . import ledger  # noqa: F401  (pure-Python cost ledger)
 from . import moe, mxf4
 from .moe import MoeWeight, moe_f16, moe_f16_workspace_size, moe_few  # noqa: F401
-from .mxf4 import (Mxf4Matrix, gemm_mxf4, mxf4_dequantize, mxf4_dequantize_ptr, mxf4_mm, mxf4_quantize,  # noqa: F401
+from .mxf4 import (Mxf4Matrix, gemm_mxf4, gemm_mxf4_a16, mxf4_dequantize, mxf4_dequantize_ptr, mxf4_mm, mxf4_quantize,  # noqa: F401
                    mxf4_quantize_ptr, mxf4_sizes)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))

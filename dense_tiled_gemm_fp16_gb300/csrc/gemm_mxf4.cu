@@ -88,96 +88,48 @@ bool allow_smem(int device)
     return true;
 }
 
-}  // namespace
-
-extern "C" {
-
-gemm_f16_status mxf4_sizes(int64_t rows, int64_t k, int64_t batch, int64_t* code_bytes, int64_t* scale_bytes)
+// Checks of a product's operands but A; `work`: bytes of A's buffers that C and
+// the inputs must keep out of.
+gemm_f16_status check_product(const void* B_codes, const void* B_scales, const void* bias, int act, const void* C,
+                              int64_t ldc, int64_t M, int64_t N, int64_t K, Sizes* sa, Sizes* sb, int64_t* c_bytes)
 {
-    Sizes s;
-    if (!code_bytes || !scale_bytes || !sizes_of(rows, k, batch, &s)) return GEMM_F16_ERR_INVALID_VALUE;
-    *code_bytes = s.code_bytes;
-    *scale_bytes = s.scale_bytes;
+    int64_t ec;
+    if (!B_codes || !B_scales || !C || !sizes_of(M, K, 1, sa) || !sizes_of(N, K, 1, sb)) return GEMM_F16_ERR_INVALID_VALUE;
+    if (act < GEMM_F16_ACT_NONE || act > GEMM_F16_ACT_GELU || ldc < N || !view_extent(M, N, ldc, 1, &ec) ||
+        __builtin_mul_overflow(ec, 2, c_bytes))
+        return GEMM_F16_ERR_INVALID_VALUE;
+    if (!aligned(B_codes, 16) || !aligned(B_scales, 16) || !aligned(C, 2) || !aligned(bias, 2))
+        return GEMM_F16_ERR_INVALID_VALUE;
+    if (overlaps(C, *c_bytes, B_codes, sb->code_bytes) || overlaps(C, *c_bytes, B_scales, sb->scale_bytes) ||
+        (bias && overlaps(C, *c_bytes, bias, 2 * N)))
+        return GEMM_F16_ERR_ALIAS;
     return GEMM_F16_OK;
 }
 
-gemm_f16_status mxf4_quantize(const void* x, int dtype, int64_t stride_b, int64_t stride_r, int64_t stride_k,
-                              void* codes, void* scales, int64_t rows, int64_t k, int64_t batch, cudaStream_t stream)
+bool product_memory_ok(const void* B_codes, const void* B_scales, const void* bias, const void* C, int64_t N,
+                       const Sizes& sb, int64_t c_bytes)
 {
-    Sizes s;
-    if (!x || !codes || !scales || dtype < MXF4_F16 || dtype > MXF4_F32 || !sizes_of(rows, k, batch, &s))
-        return GEMM_F16_ERR_INVALID_VALUE;
-    if (stride_r <= 0 || stride_k <= 0 || stride_b < 0 || batch > kMaxBatch) return GEMM_F16_ERR_INVALID_VALUE;
-    const int64_t eb = elem_bytes(dtype);
-    if (!aligned(x, eb) || !aligned(codes, 16) || !aligned(scales, 16)) return GEMM_F16_ERR_INVALID_VALUE;
-    int64_t ex, bytes;
-    if (!view_extent(rows, k, stride_r, stride_k, &ex) || !batch_extent(ex, batch, stride_b, &ex) ||
-        __builtin_mul_overflow(ex, eb, &bytes))
-        return GEMM_F16_ERR_INVALID_VALUE;
-    if (overlaps(codes, s.code_bytes, x, bytes) || overlaps(scales, s.scale_bytes, x, bytes) ||
-        overlaps(codes, s.code_bytes, scales, s.scale_bytes))
-        return GEMM_F16_ERR_ALIAS;
-    Device dev;
-    const gemm_f16_status st = current_device(&dev);
-    if (st != GEMM_F16_OK) return st;
-    if (!device_range_ok(x, bytes) || !device_range_ok(codes, s.code_bytes) || !device_range_ok(scales, s.scale_bytes))
-        return GEMM_F16_ERR_INVALID_VALUE;
-    const mxf4_dev::QuantParams p{x, stride_b, stride_r, stride_k, static_cast<uint8_t*>(codes),
-                                  static_cast<uint8_t*>(scales), rows, k, s.pitch, s.kt, s.row_tiles,
-                                  cdiv(k, mxf4_dev::kTileVals)};
+    return device_range_ok(B_codes, sb.code_bytes) && device_range_ok(B_scales, sb.scale_bytes) &&
+           device_range_ok(C, c_bytes) && (!bias || device_range_ok(bias, 2 * N));
+}
+
+gemm_f16_status run_quantize(const void* x, int dtype, int64_t sb, int64_t sr, int64_t sk, void* codes, void* scales,
+                             int64_t rows, int64_t k, int64_t batch, const Sizes& s, cudaStream_t stream)
+{
+    const mxf4_dev::QuantParams p{x, sb, sr, sk, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales), rows, k,
+                                  s.pitch, s.kt, s.row_tiles, cdiv(k, mxf4_dev::kTileVals)};
     return dtype == MXF4_F16    ? launch_quantize<__half>(p, batch, stream)
            : dtype == MXF4_BF16 ? launch_quantize<__nv_bfloat16>(p, batch, stream)
                                 : launch_quantize<float>(p, batch, stream);
 }
 
-gemm_f16_status mxf4_dequantize(const void* codes, const void* scales, void* y, int dtype, int64_t rows, int64_t k,
-                                int64_t batch, cudaStream_t stream)
+// The product of checked operands.
+gemm_f16_status product(const Device& dev, const void* A_codes, const void* A_scales, const void* B_codes,
+                        const void* B_scales, const void* bias, int act, void* C, int64_t ldc, int64_t M, int64_t N,
+                        int64_t K, cudaStream_t stream)
 {
-    Sizes s;
-    int64_t bytes;
-    if (!codes || !scales || !y || dtype < MXF4_F16 || dtype > MXF4_F32 || !sizes_of(rows, k, batch, &s) ||
-        batch > kMaxBatch || __builtin_mul_overflow(rows * k, batch, &bytes) ||
-        __builtin_mul_overflow(bytes, elem_bytes(dtype), &bytes))
-        return GEMM_F16_ERR_INVALID_VALUE;
-    if (!aligned(y, elem_bytes(dtype)) || !aligned(codes, 16) || !aligned(scales, 16)) return GEMM_F16_ERR_INVALID_VALUE;
-    if (overlaps(y, bytes, codes, s.code_bytes) || overlaps(y, bytes, scales, s.scale_bytes)) return GEMM_F16_ERR_ALIAS;
-    Device dev;
-    const gemm_f16_status st = current_device(&dev);
-    if (st != GEMM_F16_OK) return st;
-    if (!device_range_ok(y, bytes) || !device_range_ok(codes, s.code_bytes) || !device_range_ok(scales, s.scale_bytes))
-        return GEMM_F16_ERR_INVALID_VALUE;
-    const mxf4_dev::DequantParams p{static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), y, rows, k,
-                                    s.pitch, s.kt, s.row_tiles};
-    return dtype == MXF4_F16    ? launch_dequantize<__half>(p, batch, stream)
-           : dtype == MXF4_BF16 ? launch_dequantize<__nv_bfloat16>(p, batch, stream)
-                                : launch_dequantize<float>(p, batch, stream);
-}
-
-gemm_f16_status gemm_mxf4(const void* A_codes, const void* A_scales, const void* B_codes, const void* B_scales,
-                          const void* bias, int act, void* C, int64_t ldc, int64_t M, int64_t N, int64_t K,
-                          cudaStream_t stream)
-{
-    Sizes sa, sb;
-    int64_t ec;
-    if (!A_codes || !A_scales || !B_codes || !B_scales || !C || !sizes_of(M, K, 1, &sa) || !sizes_of(N, K, 1, &sb))
-        return GEMM_F16_ERR_INVALID_VALUE;
-    if (act < GEMM_F16_ACT_NONE || act > GEMM_F16_ACT_GELU || ldc < N || !view_extent(M, N, ldc, 1, &ec))
-        return GEMM_F16_ERR_INVALID_VALUE;
-    if (!aligned(A_codes, 16) || !aligned(A_scales, 16) || !aligned(B_codes, 16) || !aligned(B_scales, 16) ||
-        !aligned(C, 2) || !aligned(bias, 2))
-        return GEMM_F16_ERR_INVALID_VALUE;
-    if (overlaps(C, 2 * ec, A_codes, sa.code_bytes) || overlaps(C, 2 * ec, A_scales, sa.scale_bytes) ||
-        overlaps(C, 2 * ec, B_codes, sb.code_bytes) || overlaps(C, 2 * ec, B_scales, sb.scale_bytes) ||
-        (bias && overlaps(C, 2 * ec, bias, 2 * N)))
-        return GEMM_F16_ERR_ALIAS;
-    Device dev;
-    const gemm_f16_status st = current_device(&dev);
-    if (st != GEMM_F16_OK) return st;
-    if (!device_range_ok(A_codes, sa.code_bytes) || !device_range_ok(A_scales, sa.scale_bytes) ||
-        !device_range_ok(B_codes, sb.code_bytes) || !device_range_ok(B_scales, sb.scale_bytes) ||
-        !device_range_ok(C, 2 * ec) || (bias && !device_range_ok(bias, 2 * N)))
-        return GEMM_F16_ERR_INVALID_VALUE;
-
+    Sizes sa;
+    sizes_of(M, K, 1, &sa);
     mxf4_dev::GemmParams p = {};
     // Few rows of A: B's rows take the 128 lanes and A's rows the narrow side.
     p.swapped = M <= 64 && M < N;
@@ -212,6 +164,115 @@ gemm_f16_status gemm_mxf4(const void* A_codes, const void* A_scales, const void*
     if (!allow_smem(d)) return GEMM_F16_ERR_LAUNCH;
     return launch_kernel(mxf4_dev::gemm_mxf4_tile, dim3(static_cast<unsigned>(tiles * cluster)), mxf4_dev::kGemmThreads,
                          p.stages * sbytes + 1024, cluster, stream, p);
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_f16_status mxf4_sizes(int64_t rows, int64_t k, int64_t batch, int64_t* code_bytes, int64_t* scale_bytes)
+{
+    Sizes s;
+    if (!code_bytes || !scale_bytes || !sizes_of(rows, k, batch, &s)) return GEMM_F16_ERR_INVALID_VALUE;
+    *code_bytes = s.code_bytes;
+    *scale_bytes = s.scale_bytes;
+    return GEMM_F16_OK;
+}
+
+gemm_f16_status mxf4_quantize(const void* x, int dtype, int64_t stride_b, int64_t stride_r, int64_t stride_k,
+                              void* codes, void* scales, int64_t rows, int64_t k, int64_t batch, cudaStream_t stream)
+{
+    Sizes s;
+    if (!x || !codes || !scales || dtype < MXF4_F16 || dtype > MXF4_F32 || !sizes_of(rows, k, batch, &s))
+        return GEMM_F16_ERR_INVALID_VALUE;
+    if (stride_r <= 0 || stride_k <= 0 || stride_b < 0 || batch > kMaxBatch) return GEMM_F16_ERR_INVALID_VALUE;
+    const int64_t eb = elem_bytes(dtype);
+    if (!aligned(x, eb) || !aligned(codes, 16) || !aligned(scales, 16)) return GEMM_F16_ERR_INVALID_VALUE;
+    int64_t ex, bytes;
+    if (!view_extent(rows, k, stride_r, stride_k, &ex) || !batch_extent(ex, batch, stride_b, &ex) ||
+        __builtin_mul_overflow(ex, eb, &bytes))
+        return GEMM_F16_ERR_INVALID_VALUE;
+    if (overlaps(codes, s.code_bytes, x, bytes) || overlaps(scales, s.scale_bytes, x, bytes) ||
+        overlaps(codes, s.code_bytes, scales, s.scale_bytes))
+        return GEMM_F16_ERR_ALIAS;
+    Device dev;
+    const gemm_f16_status st = current_device(&dev);
+    if (st != GEMM_F16_OK) return st;
+    if (!device_range_ok(x, bytes) || !device_range_ok(codes, s.code_bytes) || !device_range_ok(scales, s.scale_bytes))
+        return GEMM_F16_ERR_INVALID_VALUE;
+    return run_quantize(x, dtype, stride_b, stride_r, stride_k, codes, scales, rows, k, batch, s, stream);
+}
+
+gemm_f16_status mxf4_dequantize(const void* codes, const void* scales, void* y, int dtype, int64_t rows, int64_t k,
+                                int64_t batch, cudaStream_t stream)
+{
+    Sizes s;
+    int64_t bytes;
+    if (!codes || !scales || !y || dtype < MXF4_F16 || dtype > MXF4_F32 || !sizes_of(rows, k, batch, &s) ||
+        batch > kMaxBatch || __builtin_mul_overflow(rows * k, batch, &bytes) ||
+        __builtin_mul_overflow(bytes, elem_bytes(dtype), &bytes))
+        return GEMM_F16_ERR_INVALID_VALUE;
+    if (!aligned(y, elem_bytes(dtype)) || !aligned(codes, 16) || !aligned(scales, 16)) return GEMM_F16_ERR_INVALID_VALUE;
+    if (overlaps(y, bytes, codes, s.code_bytes) || overlaps(y, bytes, scales, s.scale_bytes)) return GEMM_F16_ERR_ALIAS;
+    Device dev;
+    const gemm_f16_status st = current_device(&dev);
+    if (st != GEMM_F16_OK) return st;
+    if (!device_range_ok(y, bytes) || !device_range_ok(codes, s.code_bytes) || !device_range_ok(scales, s.scale_bytes))
+        return GEMM_F16_ERR_INVALID_VALUE;
+    const mxf4_dev::DequantParams p{static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), y, rows, k,
+                                    s.pitch, s.kt, s.row_tiles};
+    return dtype == MXF4_F16    ? launch_dequantize<__half>(p, batch, stream)
+           : dtype == MXF4_BF16 ? launch_dequantize<__nv_bfloat16>(p, batch, stream)
+                                : launch_dequantize<float>(p, batch, stream);
+}
+
+gemm_f16_status gemm_mxf4(const void* A_codes, const void* A_scales, const void* B_codes, const void* B_scales,
+                          const void* bias, int act, void* C, int64_t ldc, int64_t M, int64_t N, int64_t K,
+                          cudaStream_t stream)
+{
+    Sizes sa, sb;
+    int64_t bytes;
+    if (!A_codes || !A_scales || !aligned(A_codes, 16) || !aligned(A_scales, 16)) return GEMM_F16_ERR_INVALID_VALUE;
+    gemm_f16_status st = check_product(B_codes, B_scales, bias, act, C, ldc, M, N, K, &sa, &sb, &bytes);
+    if (st != GEMM_F16_OK) return st;
+    if (overlaps(C, bytes, A_codes, sa.code_bytes) || overlaps(C, bytes, A_scales, sa.scale_bytes))
+        return GEMM_F16_ERR_ALIAS;
+    Device dev;
+    st = current_device(&dev);
+    if (st != GEMM_F16_OK) return st;
+    if (!device_range_ok(A_codes, sa.code_bytes) || !device_range_ok(A_scales, sa.scale_bytes) ||
+        !product_memory_ok(B_codes, B_scales, bias, C, N, sb, bytes))
+        return GEMM_F16_ERR_INVALID_VALUE;
+    return product(dev, A_codes, A_scales, B_codes, B_scales, bias, act, C, ldc, M, N, K, stream);
+}
+
+gemm_f16_status gemm_mxf4_a16(const void* A, int64_t stride_am, int64_t stride_ak, void* work, const void* B_codes,
+                              const void* B_scales, const void* bias, int act, void* C, int64_t ldc, int64_t M,
+                              int64_t N, int64_t K, cudaStream_t stream)
+{
+    Sizes sa, sb;
+    int64_t bytes, ea;
+    if (!A || !work || !aligned(A, 2) || !aligned(work, 16) || stride_am <= 0 || stride_ak <= 0)
+        return GEMM_F16_ERR_INVALID_VALUE;
+    gemm_f16_status st = check_product(B_codes, B_scales, bias, act, C, ldc, M, N, K, &sa, &sb, &bytes);
+    if (st != GEMM_F16_OK) return st;
+    if (!view_extent(M, K, stride_am, stride_ak, &ea) || __builtin_mul_overflow(ea, 2, &ea))
+        return GEMM_F16_ERR_INVALID_VALUE;
+    const int64_t wb = sa.code_bytes + sa.scale_bytes;
+    if (overlaps(C, bytes, A, ea) || overlaps(C, bytes, work, wb) || overlaps(work, wb, A, ea) ||
+        overlaps(work, wb, B_codes, sb.code_bytes) || overlaps(work, wb, B_scales, sb.scale_bytes) ||
+        (bias && overlaps(work, wb, bias, 2 * N)))
+        return GEMM_F16_ERR_ALIAS;
+    Device dev;
+    st = current_device(&dev);
+    if (st != GEMM_F16_OK) return st;
+    if (!device_range_ok(A, ea) || !device_range_ok(work, wb) || !product_memory_ok(B_codes, B_scales, bias, C, N, sb, bytes))
+        return GEMM_F16_ERR_INVALID_VALUE;
+    uint8_t* scales = static_cast<uint8_t*>(work);
+    uint8_t* codes = scales + sa.scale_bytes;
+    st = run_quantize(A, MXF4_F16, 0, stride_am, stride_ak, codes, scales, M, K, 1, sa, stream);
+    if (st != GEMM_F16_OK) return st;
+    return product(dev, codes, scales, B_codes, B_scales, bias, act, C, ldc, M, N, K, stream);
 }
 
 }  // extern "C"

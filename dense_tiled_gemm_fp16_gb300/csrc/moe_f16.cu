@@ -22,8 +22,12 @@ bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p)
 
 // Places in the workspace.
 struct Layout {
-    int64_t dp, fp, xp, hp, bytes;
+    int64_t dp, fp, counts, xp, hp, parts, bytes;
 };
+
+// Most shares of the experts' K: with many tokens the shares' sums cost more
+// than idle CTAs in the last turn.
+int max_splits(int64_t T) { return T <= 16 ? moe_dev::kMaxSplits : 4; }
 
 bool layout_of(int64_t T, int64_t D, int64_t F, int64_t E, int64_t top, Layout* l)
 {
@@ -32,9 +36,11 @@ bool layout_of(int64_t T, int64_t D, int64_t F, int64_t E, int64_t top, Layout* 
         return false;
     l->dp = round_up(D, 64);
     l->fp = round_up(F, 64);
-    l->xp = 256;
+    l->counts = 256;
+    l->xp = l->counts + moe_dev::kMaxRanges * 4;
     l->hp = l->xp + round_up(T * l->dp * 2, 256);
-    l->bytes = l->hp + round_up(T * top * 2 * l->fp * 2, 256);
+    l->parts = l->hp + round_up(T * top * 2 * l->fp * 2, 256);
+    l->bytes = l->parts + max_splits(T) * T * l->dp * 4;
     return true;
 }
 
@@ -53,10 +59,16 @@ bool weight_span(const moe_f16_weight& w, int64_t E, int64_t in, int64_t out, in
     return !__builtin_mul_overflow(e, 2, data);
 }
 
-// 16-byte words along the contracted axis: every row of 8 values starts aligned.
+// 16-byte words along the contracted axis, or along the other one: every row of
+// 8 values starts aligned.
 bool rows_aligned(const moe_f16_weight& w)
 {
     return w.stride_i == 1 && w.stride_o % 8 == 0 && w.stride_e % 8 == 0 && aligned(w.data, 16);
+}
+
+bool cols_aligned(const moe_f16_weight& w)
+{
+    return w.stride_o == 1 && w.stride_i % 8 == 0 && w.stride_e % 8 == 0 && aligned(w.data, 16);
 }
 
 moe_dev::Weight weight_of(const moe_f16_weight& w, int64_t E, int64_t in, int64_t out)
@@ -83,7 +95,7 @@ constexpr int kMaxDevices = 64;
 bool allow_smem(const void* kernel, int slot, int bytes)
 {
     static std::mutex mutex;
-    static int have[kMaxDevices][16] = {};
+    static int have[kMaxDevices][24] = {};
     int d = 0;
     if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= kMaxDevices) {
         cudaGetLastError();
@@ -110,22 +122,36 @@ gemm_f16_status launch_route(const moe_dev::Params& p, cudaStream_t stream)
                          moe_dev::kRouteCluster, stream, p);
 }
 
-template <int kFmt, int kGroups>
-gemm_f16_status launch_experts(const moe_dev::Params& p, int sms, cudaStream_t stream)
+template <int kFmt, int kGroups, int kRing>
+gemm_f16_status launch_experts(moe_dev::Params& p, int sms, cudaStream_t stream)
 {
-    using St = moe_dev::Stage<kFmt>;
-    const int ring = moe_dev::kWarps * St::kRing * St::kBytes;
-    const int smem = ring + std::max(2 * moe_dev::kWarps * kGroups * 32 * 16, moe_dev::kWarps * p.T * 16 * 4);
-    const void* fn = reinterpret_cast<const void*>(moe_dev::moe_experts<kFmt, kGroups>);
-    if (!allow_smem(fn, 3 + 2 * kFmt + (kGroups > 1), smem)) return GEMM_F16_ERR_LAUNCH;
-    return launch_kernel(moe_dev::moe_experts<kFmt, kGroups>, dim3(static_cast<unsigned>(sms)), moe_dev::kThreads, smem, 1,
-                         stream, p);
+    constexpr int kOut = moe_dev::Step<kFmt, false>::kOut;
+    // The count that leaves the fewest idle parts in the last turn of the CTAs.
+    const int64_t ranges = cdiv(p.D, kOut);
+    p.splits = 1;
+    double best = 0;
+    for (int s = 1; s <= max_splits(p.T); ++s) {
+        const double fill = static_cast<double>(ranges * s) / (cdiv(ranges * s, sms) * sms);
+        if (fill > best + 0.04) best = fill, p.splits = s;
+    }
+    const int ring = moe_dev::kWarps * kRing * moe_dev::Stage<kFmt>::kBytes;
+    const int smem = ring + std::max(2 * moe_dev::kWarps * kGroups * 32 * 16, moe_dev::kWarps * p.T * kOut * 4);
+    const auto kernel = moe_dev::moe_experts<kFmt, kGroups, kRing>;
+    if (!allow_smem(reinterpret_cast<const void*>(kernel), 3 + 4 * kFmt + (kGroups > 1) + 2 * (kRing == 2), smem))
+        return GEMM_F16_ERR_LAUNCH;
+    return launch_kernel(kernel, dim3(static_cast<unsigned>(sms)), moe_dev::kThreads, smem, 1, stream, p);
 }
 
-template <int kFmt>
-gemm_f16_status launch_experts(const moe_dev::Params& p, int sms, cudaStream_t stream)
+// Pieces of 8 tokens an expert, or of 16 when there are more than 8 in all.
+template <int kFmt, int kRing>
+gemm_f16_status launch_experts(moe_dev::Params& p, int sms, cudaStream_t stream)
 {
-    return p.T <= 8 ? launch_experts<kFmt, 1>(p, sms, stream) : launch_experts<kFmt, 2>(p, sms, stream);
+    if (p.T <= 8) return launch_experts<kFmt, 1, kRing>(p, sms, stream);
+    // (32-column ranges of more than 32 tokens: the sums take the ring's room)
+    if constexpr (kFmt == moe_dev::kF16Cols) {
+        if (p.T > 32) return launch_experts<kFmt, 2, 2>(p, sms, stream);
+    }
+    return launch_experts<kFmt, 2, kRing>(p, sms, stream);
 }
 
 }  // namespace
@@ -211,6 +237,8 @@ gemm_f16_status moe_f16(const void* x, int64_t stride_xt, int64_t stride_xi, con
     p.ids = ids;
     uint8_t* base = static_cast<uint8_t*>(workspace);
     p.ctl = reinterpret_cast<moe_dev::Control*>(base);
+    p.counts = reinterpret_cast<int32_t*>(base + l.counts);
+    p.parts = reinterpret_cast<float*>(base + l.parts);
     p.xp = reinterpret_cast<__half*>(base + l.xp);
     p.hp = reinterpret_cast<__half*>(base + l.hp);
     p.test_stall = option(GEMM_F16_OPT_TEST_STALL) == 1;
@@ -222,10 +250,12 @@ gemm_f16_status moe_f16(const void* x, int64_t stride_xt, int64_t stride_xi, con
          : aligned16 && stride_re == 1 && stride_ri % 8 == 0 ? launch_route<moe_dev::kOutContiguous>(p, stream)
                                                               : launch_route<moe_dev::kAnyStrides>(p, stream);
     if (st != GEMM_F16_OK) return st;
-    if (gate->format == MOE_F16_WEIGHT_MXF4) return launch_experts<moe_dev::kMxf4>(p, dev.sms, stream);
-    return rows_aligned(*gate) && rows_aligned(*up) && rows_aligned(*down)
-               ? launch_experts<moe_dev::kF16Rows>(p, dev.sms, stream)
-               : launch_experts<moe_dev::kF16Strided>(p, dev.sms, stream);
+    if (gate->format == MOE_F16_WEIGHT_MXF4) return launch_experts<moe_dev::kMxf4, 8>(p, dev.sms, stream);
+    if (rows_aligned(*gate) && rows_aligned(*up) && rows_aligned(*down))
+        return launch_experts<moe_dev::kF16Rows, 4>(p, dev.sms, stream);
+    if (cols_aligned(*gate) && cols_aligned(*up) && cols_aligned(*down))
+        return launch_experts<moe_dev::kF16Cols, 4>(p, dev.sms, stream);
+    return launch_experts<moe_dev::kF16Strided, 4>(p, dev.sms, stream);
 }
 
 }  // extern "C"

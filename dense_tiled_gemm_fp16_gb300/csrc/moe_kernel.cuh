@@ -29,6 +29,7 @@ using namespace gemm_f16_dev;
 
 constexpr int kMaxTokens = 64, kMaxExperts = 512, kMaxTop = 8, kMaxSlots = kMaxTokens * kMaxTop;
 constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kMaxSplits = 8, kMaxRanges = 2048;   // ranges of 16 columns at least, 32768 in all
 constexpr int kRouteCluster = 8;   // CTAs that share a router product, and tokens of a group
 
 __device__ __forceinline__ float act_f32(int act, float x)
@@ -111,6 +112,9 @@ struct Params {
     float* weights;
     int32_t* ids;
     Control* ctl;
+    int32_t splits;        // shares of the experts' K a range of y's columns is cut into
+    int32_t* counts;       // [column ranges]: finished shares, zeroed by the routing kernel
+    float* parts;          // [splits][T][dp]: their sums
     __half* xp;            // [T][dp]: the tokens, packed, zeros past D
     __half* hp;            // [T * top][2][fp]: the hidden values as high and low halves, by expert
     int32_t test_stall;
@@ -174,7 +178,10 @@ __global__ void __launch_bounds__(kThreads) moe_route(const __grid_constant__ Pa
 
     griddep_wait();
     griddep_launch_dependents();
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.ctl = Control{0, 0, 0};
+    if (blockIdx.x == 0) {
+        if (threadIdx.x == 0) *p.ctl = Control{0, 0, 0};
+        for (int i = threadIdx.x; i < kMaxRanges; i += kThreads) p.counts[i] = 0;
+    }
 
     for (int i = threadIdx.x; i < 8 * width; i += kThreads) {
         const int t = i / width, k = i - t * width;
@@ -347,23 +354,36 @@ __global__ void __launch_bounds__(kThreads) moe_route(const __grid_constant__ Pa
 }
 
 // ---------------------------------------------------------------- experts
-// Weight formats of the experts' kernel.
-enum { kF16Rows = 0, kF16Strided = 1, kMxf4 = 2 };
+// Weight formats of the experts' kernel: fp16 with the contracted axis
+// contiguous, with the other one contiguous, at any strides, and MXFP4.
+enum { kF16Rows = 0, kF16Cols = 1, kF16Strided = 2, kMxf4 = 3 };
 
+// What a warp does at once.  A step is kVals of K for kTiles 16-row tiles: 2 KB
+// of fp16 in either orientation (64-byte pieces of global rows at least, which
+// is what the copies need to run at the memory's rate), 1 KB of codes.
+template <int kFmt, bool kUp>
+struct Step {
+    static constexpr int kTiles = kFmt == kF16Cols ? (kUp ? 4 : 2) : 1;
+    static constexpr int kVals = kFmt == kF16Cols ? (kUp ? 16 : 32) : kFmt == kMxf4 ? 128 : 64;
+    static constexpr int kOut = (kUp ? 8 : 16) * kTiles;   // hidden values, or columns of y, of a unit
+    static constexpr int kWords = kVals / 8;               // 32-bit words of a column a thread holds
+};
 template <int kFmt>
 struct Stage {
-    static constexpr int kVals = kFmt == kMxf4 ? 128 : 64;             // values of K a step
-    static constexpr int kRowBytes = kFmt == kMxf4 ? 64 : 128;
-    static constexpr int kBytes = 16 * kRowBytes + (kFmt == kMxf4 ? 64 : 0);   // 16 rows, and their scales
-    static constexpr int kRing = kFmt == kMxf4 ? 8 : 4;                        // stages of a warp's ring
+    static constexpr int kBytes = kFmt == kMxf4 ? 1024 + 64 : 2048;   // with the 16 rows' scales
 };
 
-// 16 weight rows x kVals of K into a stage: row r of the stage is row o0 + r of
-// one projection, or with `pair` rows o0 + r (r < 8) of w0 and o0 + r - 8 of w1.
-// Rows from `rows` on and values from K on are zeros.
-template <int kFmt>
-__device__ __forceinline__ void load_stage(uint32_t dst, const Weight& w0, const Weight& w1, bool pair, int e, int o0,
-                                           int rows, int k0, int K, int lane)
+// A step of one projection (down) or of two (up: w0 the gate, w1 the up rows)
+// into a stage: outputs o0 .., values k0 ..; outputs from `rows` and values
+// from K on are zeros.
+//   kF16Rows/kF16Strided: 16 rows of 64 values, word c of row r at c ^ 4 (r & 1);
+//     a pair's rows 0-7 are the gate's, 8-15 the up projection's.
+//   kF16Cols: rows of K; up: 16 of 32 gate and 32 up outputs, down: 32 of 32
+//     outputs.  Two down rows k, k + 16 share 128 bytes.
+//   kMxf4: 16 rows of 128 codes, then their 4 scales each.
+template <int kFmt, bool kUp>
+__device__ __forceinline__ void load_stage(uint32_t dst, const Weight& w0, const Weight& w1, int e, int o0, int rows,
+                                           int k0, int K, int lane)
 {
     if (kFmt == kF16Rows) {
         const int c = lane & 7, k = k0 + 8 * c;
@@ -371,8 +391,8 @@ __device__ __forceinline__ void load_stage(uint32_t dst, const Weight& w0, const
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int r = (lane >> 3) + 4 * j;
-            const Weight& w = pair && j >= 2 ? w1 : w0;
-            const int o = o0 + (pair ? r & 7 : r);
+            const Weight& w = kUp && j >= 2 ? w1 : w0;
+            const int o = o0 + (kUp ? r & 7 : r);
             const bool in = o < rows && bytes;
             const __half* src = reinterpret_cast<const __half*>(w.data) + (in ? e * w.se + o * w.so + k : 0);
             cp_async16(dst + r * 128 + ((c ^ ((r & 1) << 2)) << 4), src, in ? bytes : 0u);
@@ -382,8 +402,8 @@ __device__ __forceinline__ void load_stage(uint32_t dst, const Weight& w0, const
 #pragma unroll 1
         for (int j = 0; j < 4; ++j) {
             const int r = (lane >> 3) + 4 * j;
-            const Weight& w = pair && j >= 2 ? w1 : w0;
-            const int o = o0 + (pair ? r & 7 : r);
+            const Weight& w = kUp && j >= 2 ? w1 : w0;
+            const int o = o0 + (kUp ? r & 7 : r);
             uint32_t u[4] = {};
             if (o < rows) {
                 const __half* src = reinterpret_cast<const __half*>(w.data) + e * w.se + o * w.so;
@@ -393,20 +413,31 @@ __device__ __forceinline__ void load_stage(uint32_t dst, const Weight& w0, const
             }
             st_smem_v4(dst + r * 128 + ((c ^ ((r & 1) << 2)) << 4), make_uint4(u[0], u[1], u[2], u[3]));
         }
+    } else if (kFmt == kF16Cols) {
+        const int c = lane & 7;   // 16-byte word of the stage's 128-byte row
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = (lane >> 3) + 4 * j;   // of 16 stage rows
+            const Weight& w = kUp && c >= 4 ? w1 : w0;
+            const int k = k0 + r + (!kUp && c >= 4 ? 16 : 0), o = o0 + 8 * (c & 3);
+            const uint32_t bytes = k < K ? 2 * max(0, min(8, rows - o)) : 0;
+            const __half* src = reinterpret_cast<const __half*>(w.data) + (bytes ? e * w.se + k * w.si + o : 0);
+            cp_async16(dst + r * 128 + ((c ^ (((r >> 2) << 1) | (r & 1))) << 4), src, bytes);
+        }
     } else {
         const int c = lane & 3, k = k0 + 32 * c;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int r = (lane >> 2) + 8 * j;
-            const Weight& w = pair && j ? w1 : w0;
-            const int o = o0 + (pair ? r & 7 : r);
+            const Weight& w = kUp && j ? w1 : w0;
+            const int o = o0 + (kUp ? r & 7 : r);
             const bool in = o < rows && k < K;
             const uint8_t* src = w.data + (in ? e * w.se + o * w.so + (k >> 1) : 0);
             cp_async16(dst + r * 64 + ((c ^ ((r >> 1) & 3)) << 4), src, in ? 16u : 0u);
         }
         if (lane < 16) {
-            const Weight& w = pair && lane >= 8 ? w1 : w0;
-            const int o = o0 + (pair ? lane & 7 : lane);
+            const Weight& w = kUp && lane >= 8 ? w1 : w0;
+            const int o = o0 + (kUp ? lane & 7 : lane);
             const bool in = o < rows && k0 < K;
             const uint8_t* src = w.scales + (in ? e * w.scale_se + mxf4_dev::scale_at(o, k0 >> 5, w.kt) : 0);
             cp_async4(dst + 1024 + lane * 4, src, in ? 4u : 0u);
@@ -414,13 +445,46 @@ __device__ __forceinline__ void load_stage(uint32_t dst, const Weight& w0, const
     }
 }
 
-// acc += the stage's rows times the step's values of the columns' vectors b
-// (one 16-byte word for each 32 values and group of 8 columns).
-template <int kFmt, int kGroups>
-__device__ __forceinline__ void mma_stage(float (*acc)[4], uint32_t src, const uint4 (*b)[kGroups], int groups, int g,
-                                          int c)
+// Four 8x8 pieces, each transposed: operand registers of a 16-row tile from
+// stage rows of K.
+__device__ __forceinline__ void ldmatrix_trans(uint32_t addr, uint32_t* a)
 {
-    if (kFmt != kMxf4) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// A thread's words of one column: the values 8c .. 8c + 7 of each 32, or with
+// 16 values a step 4c .. 4c + 3.
+template <int kVals>
+__device__ __forceinline__ void load_column(const __half* col, int k0, int end, bool on, uint32_t* b)
+{
+    if constexpr (kVals == 16) {
+        uint2 v = make_uint2(0, 0);
+        if (on && k0 < end)
+            asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(col + k0));
+        b[0] = v.x, b[1] = v.y;
+    } else {
+#pragma unroll
+        for (int h = 0; h < kVals / 32; ++h) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (on && k0 + 32 * h < end)
+                asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                             : "l"(col + k0 + 32 * h));
+            b[4 * h] = v.x, b[4 * h + 1] = v.y, b[4 * h + 2] = v.z, b[4 * h + 3] = v.w;
+        }
+    }
+}
+
+// acc[tile][group] += the stage's rows times the step's values of the columns.
+template <int kFmt, bool kUp, int kGroups>
+__device__ __forceinline__ void mma_stage(float (*acc)[kGroups][4], uint32_t src, const uint32_t (*b)[Step<kFmt, kUp>::kWords],
+                                          int groups, int lane)
+{
+    const int g = lane >> 2, c = lane & 3;
+    if (kFmt == kF16Rows || kFmt == kF16Strided) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const uint32_t at = src + g * 128 + (((4 * h + c) ^ ((g & 1) << 2)) << 4);
@@ -428,9 +492,39 @@ __device__ __forceinline__ void mma_stage(float (*acc)[4], uint32_t src, const u
 #pragma unroll
             for (int q = 0; q < kGroups; ++q) {
                 if (q < groups) {
-                    mma16816(acc[q], lo.x, hi.x, lo.y, hi.y, b[h][q].x, b[h][q].y);
-                    mma16816(acc[q], lo.z, hi.z, lo.w, hi.w, b[h][q].z, b[h][q].w);
+                    mma16816(acc[0][q], lo.x, hi.x, lo.y, hi.y, b[q][4 * h], b[q][4 * h + 1]);
+                    mma16816(acc[0][q], lo.z, hi.z, lo.w, hi.w, b[q][4 * h + 2], b[q][4 * h + 3]);
                 }
+            }
+        }
+    } else if (kFmt == kF16Cols && kUp) {
+        // row 4 (j / 2) + j % 2 of K is row j of a piece, 2 rows on the same of
+        // the second half of K; pieces in operand order: gate, up, gate, up
+        const int j = lane & 7, piece = lane >> 3;
+        const int r = 4 * (j >> 1) + (j & 1) + 2 * (piece >> 1);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            uint32_t a[4];
+            ldmatrix_trans(src + r * 128 + (((t + 4 * (piece & 1)) ^ j) << 4), a);
+#pragma unroll
+            for (int q = 0; q < kGroups; ++q)
+                if (q < groups) mma16816(acc[t][q], a[0], a[1], a[2], a[3], b[q][0], b[q][1]);
+        }
+    } else if (kFmt == kF16Cols) {
+        // row 8 (j / 2) + j % 2 + 2m of 32 is row j of the m-th quarter of K; K
+        // rows from 16 on are the upper words of the stage's rows
+        const int j = lane & 7, piece = lane >> 3;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            const int k = 8 * (j >> 1) + (j & 1) + 4 * m + 2 * (piece >> 1), r = k & 15;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                uint32_t a[4];
+                const int word = 2 * t + (piece & 1) + (k >= 16 ? 4 : 0);
+                ldmatrix_trans(src + r * 128 + ((word ^ (((r >> 2) << 1) | (r & 1))) << 4), a);
+#pragma unroll
+                for (int q = 0; q < kGroups; ++q)
+                    if (q < groups) mma16816(acc[t][q], a[0], a[1], a[2], a[3], b[q][2 * m], b[q][2 * m + 1]);
             }
         }
     } else {
@@ -447,23 +541,16 @@ __device__ __forceinline__ void mma_stage(float (*acc)[4], uint32_t src, const u
                 if (q < groups) {
                     // the block's sum, exact products of fp16 values, then its scale
                     float d[4] = {};
-                    mma16816(d, lo[0], hi[0], lo[1], hi[1], b[h][q].x, b[h][q].y);
-                    mma16816(d, lo[2], hi[2], lo[3], hi[3], b[h][q].z, b[h][q].w);
-                    acc[q][0] = fmaf(d[0], s0, acc[q][0]);
-                    acc[q][1] = fmaf(d[1], s0, acc[q][1]);
-                    acc[q][2] = fmaf(d[2], s1, acc[q][2]);
-                    acc[q][3] = fmaf(d[3], s1, acc[q][3]);
+                    mma16816(d, lo[0], hi[0], lo[1], hi[1], b[q][4 * h], b[q][4 * h + 1]);
+                    mma16816(d, lo[2], hi[2], lo[3], hi[3], b[q][4 * h + 2], b[q][4 * h + 3]);
+                    acc[0][q][0] = fmaf(d[0], s0, acc[0][q][0]);
+                    acc[0][q][1] = fmaf(d[1], s0, acc[0][q][1]);
+                    acc[0][q][2] = fmaf(d[2], s1, acc[0][q][2]);
+                    acc[0][q][3] = fmaf(d[3], s1, acc[0][q][3]);
                 }
             }
         }
     }
-}
-
-__device__ __forceinline__ uint4 ld_v4(const void* p)
-{
-    uint4 v;
-    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
 }
 
 // What a piece of an expert's work is: up to 8 * kGroups tokens of one expert
@@ -478,7 +565,7 @@ struct Shared {
     Item item[kMaxSlots];
     uint16_t first_of[kMaxExperts];
     uint32_t scan[kWarps];
-    int items, ticket, ok;
+    int items, ticket, last, ok;
 };
 
 // All experts of the layer.  Two phases, gate/up and down, each cut into
@@ -487,16 +574,21 @@ struct Shared {
 // gate/up parts are taken by running CTAs only and are all gone before any CTA
 // waits, so the wait ends whichever CTAs the device holds at once.  A down
 // part's first weights are on their way before the wait.
-template <int kFmt, int kGroups>
+//
+// A down unit is a range of columns and one of `splits` shares of the experts'
+// K; with more than one share the sums go to the workspace, and the CTA that
+// finishes a column range last adds the shares in order.
+template <int kFmt, int kGroups, int kRing>
 __global__ void __launch_bounds__(kThreads, 1) moe_experts(const __grid_constant__ Params p)
 {
-    using St = Stage<kFmt>;
-    constexpr int kB = St::kVals / 32, kRing = St::kRing;
+    using Up = Step<kFmt, true>;
+    using Down = Step<kFmt, false>;
+    constexpr int kBytes = Stage<kFmt>::kBytes;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ Shared sh;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const uint32_t ring = smem_u32(smem) + warp * (kRing * St::kBytes);
-    uint8_t* tail = smem + kWarps * kRing * St::kBytes;   // sums: gate/up [2][16][kGroups][32] float4, down [16][T][16]
+    const uint32_t ring = smem_u32(smem) + warp * (kRing * kBytes);
+    uint8_t* tail = smem + kWarps * kRing * kBytes;   // sums: gate/up [2][16][groups][32] float4, down [16][T][kOut]
     const int parts = gridDim.x;
 
     griddep_wait();
@@ -556,115 +648,131 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const __grid_constant
     const int items = sh.items;
     int ticket = sh.ticket;
 
-    // ---- gate and up: a unit is one piece's 8 hidden values, K dealt to the warps
-    const int units_each = p.fp >> 3, steps = (p.D + St::kVals - 1) / St::kVals;
-    const int wsteps = (steps - warp + kWarps - 1) / kWarps;   // this warp's steps of a unit
-    while (ticket < parts) {
-        const int64_t all = static_cast<int64_t>(items) * units_each;
-        const int u_lo = static_cast<int>(all * ticket / parts), u_hi = static_cast<int>(all * (ticket + 1) / parts);
-        const int mine = (u_hi - u_lo) * wsteps;   // steps of this warp in all
-        int pu = u_lo, ps = 0;                     // the next one to load
-        auto issue = [&](int n) {
-            if (n < mine) {
-                const int it = pu / units_each, f0 = (pu - it * units_each) * 8;
-                load_stage<kFmt>(ring + (n % kRing) * St::kBytes, p.gate, p.up, true, sh.item[it].expert, f0, p.F,
-                                 (warp + ps * kWarps) * St::kVals, p.D, lane);
-                if (++ps == wsteps) ps = 0, ++pu;
-            }
-            cp_async_commit();
-        };
-        for (int n = 0; n < kRing - 1; ++n) issue(n);
-        int n = 0;
-        for (int u = u_lo; u < u_hi; ++u) {
-            const int it = u / units_each, f0 = (u - it * units_each) * 8;
-            const Item im = sh.item[it];
-            const int groups = (im.count + 7) >> 3;
-            const __half* col[kGroups];
+    // ---- gate and up: a unit is one piece's next kOut hidden values, K dealt to the warps
+    {
+        constexpr int kVals = Up::kVals, kTiles = Up::kTiles, kWords = Up::kWords;
+        const int units_each = p.fp / Up::kOut, steps = (p.D + kVals - 1) / kVals;
+        const int wsteps = (steps - warp + kWarps - 1) / kWarps;   // this warp's steps of a unit
+        uint32_t turn = 0;
+        while (ticket < parts) {
+            const int64_t all = static_cast<int64_t>(items) * units_each;
+            const int u_lo = static_cast<int>(all * ticket / parts), u_hi = static_cast<int>(all * (ticket + 1) / parts);
+            const int mine = (u_hi - u_lo) * wsteps;   // steps of this warp in all
+            int pu = u_lo, ps = 0;                     // the next one to load
+            auto issue = [&](int n) {
+                if (n < mine) {
+                    const int it = pu / units_each, f0 = (pu - it * units_each) * Up::kOut;
+                    load_stage<kFmt, true>(ring + (n % kRing) * kBytes, p.gate, p.up, sh.item[it].expert, f0, p.F,
+                                           (warp + ps * kWarps) * kVals, p.D, lane);
+                    if (++ps == wsteps) ps = 0, ++pu;
+                }
+                cp_async_commit();
+            };
+            for (int n = 0; n < kRing - 1; ++n) issue(n);
+            int n = 0;
+            for (int u = u_lo; u < u_hi; ++u) {
+                const int it = u / units_each, f0 = (u - it * units_each) * Up::kOut;
+                const Item im = sh.item[it];
+                const int groups = (im.count + 7) >> 3;
+                const __half* col[kGroups];
 #pragma unroll
-            for (int q = 0; q < kGroups; ++q)
-                col[q] = p.xp + static_cast<int64_t>(sh.slot[im.first + min(8 * q + g, im.count - 1)] / p.top) * p.dp + 8 * c;
-            float acc[kGroups][4] = {};
-            for (int s = 0; s < wsteps; ++s, ++n) {
-                uint4 b[kB][kGroups];
-                const int k0 = (warp + s * kWarps) * St::kVals;
-#pragma unroll
-                for (int h = 0; h < kB; ++h)
+                for (int q = 0; q < kGroups; ++q)
+                    col[q] = p.xp + static_cast<int64_t>(sh.slot[im.first + min(8 * q + g, im.count - 1)] / p.top) * p.dp +
+                             (kVals == 16 ? 4 : 8) * c;
+                float acc[kTiles][kGroups][4] = {};
+                for (int s = 0; s < wsteps; ++s, ++n) {
+                    uint32_t b[kGroups][kWords];
 #pragma unroll
                     for (int q = 0; q < kGroups; ++q)
-                        b[h][q] = q < groups && k0 + 32 * h < p.dp ? ld_v4(col[q] + k0 + 32 * h) : make_uint4(0, 0, 0, 0);
-                cp_async_wait<kRing - 2>();
-                __syncwarp();   // (every lane is done with the stage that is filled next)
-                issue(n + kRing - 1);
-                mma_stage<kFmt, kGroups>(acc, ring + (n % kRing) * St::kBytes, b, groups, g, c);
-            }
-            float4* sums = reinterpret_cast<float4*>(tail) + (u & 1) * (kWarps * kGroups * 32);
-#pragma unroll
-            for (int q = 0; q < kGroups; ++q)
-                if (q < groups) sums[(warp * kGroups + q) * 32 + lane] = make_float4(acc[q][0], acc[q][1], acc[q][2], acc[q][3]);
-            __syncthreads();
-            // one warp a group adds the 16 parts; the warps take turns
-            const int q = (warp + kWarps - u * kGroups % kWarps) % kWarps;
-            if (q < groups) {
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float4 a = sums[(w * kGroups + q) * 32 + lane];
-                    v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
+                        load_column<kVals>(col[q], (warp + s * kWarps) * kVals, p.dp, q < groups, b[q]);
+                    cp_async_wait<kRing - 2>();
+                    __syncwarp();   // (every lane is done with the stage that is filled next)
+                    issue(n + kRing - 1);
+                    mma_stage<kFmt, true, kGroups>(acc, ring + (n % kRing) * kBytes, b, groups, lane);
                 }
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int j = 8 * q + 2 * c + i;
-                    if (j < im.count) {
-                        // (past F: zeros, whatever the tokens hold)
-                        const float hv = f0 + g < p.F ? act_f32(p.act, i ? v.y : v.x) * (i ? v.w : v.z) : 0.f;
-                        const __half hi = __float2half_rn(hv);
-                        const float back = __half2float(hi);
-                        const __half lo = isfinite(back) ? __float2half_rn(hv - back) : __ushort_as_half(0);
-                        __half* dst = p.hp + static_cast<int64_t>(im.first + j) * 2 * p.fp + f0 + g;
-                        dst[0] = hi;
-                        dst[p.fp] = lo;
+                for (int t = 0; t < kTiles; ++t) {
+                    float4* sums = reinterpret_cast<float4*>(tail) + (turn & 1) * (kWarps * kGroups * 32);
+#pragma unroll
+                    for (int q = 0; q < kGroups; ++q)
+                        if (q < groups)
+                            sums[(warp * kGroups + q) * 32 + lane] =
+                                make_float4(acc[t][q][0], acc[t][q][1], acc[t][q][2], acc[t][q][3]);
+                    __syncthreads();
+                    // one warp a group adds the 16 parts; the warps take turns
+                    const int q = static_cast<int>((warp - turn * kGroups) % kWarps);
+                    ++turn;
+                    if (q < groups) {
+                        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                        for (int w = 0; w < kWarps; ++w) {
+                            const float4 a = sums[(w * kGroups + q) * 32 + lane];
+                            v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
+                        }
+                        const int f = f0 + 8 * t + g;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int j = 8 * q + 2 * c + i;
+                            if (j < im.count) {
+                                // (past F: zeros, whatever the tokens hold)
+                                const float hv = f < p.F ? act_f32(p.act, i ? v.y : v.x) * (i ? v.w : v.z) : 0.f;
+                                const __half hi = __float2half_rn(hv);
+                                const float back = __half2float(hi);
+                                const __half lo = isfinite(back) ? __float2half_rn(hv - back) : __ushort_as_half(0);
+                                __half* dst = p.hp + static_cast<int64_t>(im.first + j) * 2 * p.fp + f;
+                                dst[0] = hi;
+                                dst[p.fp] = lo;
+                            }
+                        }
                     }
                 }
             }
+            cp_async_wait<0>();
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                if (!p.test_stall) atom_add_acq_rel_gpu(&p.ctl->done_up, 1);
+                sh.ticket = atomicAdd(&p.ctl->ticket_up, 1);
+            }
+            __syncthreads();
+            ticket = sh.ticket;
         }
-        cp_async_wait<0>();
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            if (!p.test_stall) atom_add_acq_rel_gpu(&p.ctl->done_up, 1);
-            sh.ticket = atomicAdd(&p.ctl->ticket_up, 1);
-        }
-        __syncthreads();
-        ticket = sh.ticket;
     }
 
-    // ---- down: a part is a range of 16-column tiles; a warp takes a range of a
-    // tile's (piece, step) pairs and keeps its own weighted sums of the tokens
+    // ---- down: a warp takes a range of a unit's (piece, step) pairs and keeps
+    // its own weighted sums of the tokens
     if (threadIdx.x == 0) sh.ticket = atomicAdd(&p.ctl->ticket_down, 1);
     __syncthreads();
     ticket = sh.ticket;
+    constexpr int kVals = Down::kVals, kTiles = Down::kTiles, kWords = Down::kWords, kOut = Down::kOut;
     constexpr int kCols = 2 * kGroups;   // groups of 8 columns: a choice takes two (high and low half)
-    const int tiles = (p.D + 15) >> 4, fsteps = (p.F + St::kVals - 1) / St::kVals;
-    const int total = items * fsteps;
-    const int w_lo = total * warp / kWarps, w_hi = total * (warp + 1) / kWarps, per = w_hi - w_lo;
+    const int tiles = (p.D + kOut - 1) / kOut, fsteps = (p.F + kVals - 1) / kVals;
+    const int total = items * fsteps, units = tiles * p.splits;
     float* ysum = reinterpret_cast<float*>(tail);
-    float* mysum = ysum + warp * p.T * 16;
+    float* mysum = ysum + warp * p.T * kOut;
+    auto share = [&](int unit, int* lo, int* hi) {   // this warp's pairs
+        const int w = (unit % p.splits) * kWarps + warp, n = p.splits * kWarps;
+        *lo = static_cast<int>(static_cast<int64_t>(total) * w / n);
+        *hi = static_cast<int>(static_cast<int64_t>(total) * (w + 1) / n);
+    };
     bool waited = false;
     while (ticket < parts) {
-        const int t_lo = static_cast<int>(static_cast<int64_t>(tiles) * ticket / parts),
-                  t_hi = static_cast<int>(static_cast<int64_t>(tiles) * (ticket + 1) / parts);
-        const int mine = (t_hi - t_lo) * per;
-        int pt = t_lo, pi = w_lo;
+        const int u_lo = static_cast<int>(static_cast<int64_t>(units) * ticket / parts),
+                  u_hi = static_cast<int>(static_cast<int64_t>(units) * (ticket + 1) / parts);
+        int pu = u_lo, pi = 0, pend = 0;
+        if (u_lo < u_hi) share(u_lo, &pi, &pend);
         auto issue = [&](int n) {
-            if (n < mine) {
+            while (pu < u_hi && pi == pend)
+                if (++pu < u_hi) share(pu, &pi, &pend);
+            if (pu < u_hi) {
                 const int it = pi / fsteps;
-                load_stage<kFmt>(ring + (n % kRing) * St::kBytes, p.down, p.down, false, sh.item[it].expert, pt * 16, p.D,
-                                 (pi - it * fsteps) * St::kVals, p.F, lane);
-                if (++pi == w_hi) pi = w_lo, ++pt;
+                load_stage<kFmt, false>(ring + (n % kRing) * kBytes, p.down, p.down, sh.item[it].expert,
+                                        pu / p.splits * kOut, p.D, (pi - it * fsteps) * kVals, p.F, lane);
+                ++pi;
             }
             cp_async_commit();
         };
         for (int n = 0; n < kRing - 1; ++n) issue(n);
-        for (int i = threadIdx.x; i < kWarps * p.T * 16; i += kThreads) ysum[i] = 0.f;
+        for (int i = threadIdx.x; i < kWarps * p.T * kOut; i += kThreads) ysum[i] = 0.f;
         if (!waited) {
             if (threadIdx.x == 0) {
                 const uint64_t t0 = globaltimer_ns();
@@ -682,26 +790,31 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const __grid_constant
         __syncthreads();
         if (!sh.ok) break;
         int n = 0;
-        for (int tile = t_lo; tile < t_hi; ++tile) {
+        for (int unit = u_lo; unit < u_hi; ++unit) {
+            int lo, hi;
+            share(unit, &lo, &hi);
             int it = -1;
             Item im = {};
             int groups = 0;
             const __half* col[kCols];
-            float acc[kCols][4];
+            float acc[kTiles][kCols][4];
             auto flush = [&]() {
 #pragma unroll
                 for (int q = 0; q < kCols; ++q) {
                     const int j = 4 * q + c;   // this thread's columns are the halves of choice j
                     if (j < im.count) {
                         const float w = sh.weight[im.first + j];
-                        float* to = mysum + sh.slot[im.first + j] / p.top * 16;
-                        to[g] = fmaf(w, acc[q][0] + acc[q][1], to[g]);
-                        to[g + 8] = fmaf(w, acc[q][2] + acc[q][3], to[g + 8]);
+                        float* to = mysum + sh.slot[im.first + j] / p.top * kOut;
+#pragma unroll
+                        for (int t = 0; t < kTiles; ++t) {
+                            to[16 * t + g] = fmaf(w, acc[t][q][0] + acc[t][q][1], to[16 * t + g]);
+                            to[16 * t + g + 8] = fmaf(w, acc[t][q][2] + acc[t][q][3], to[16 * t + g + 8]);
+                        }
                     }
                 }
                 __syncwarp();
             };
-            for (int i = w_lo; i < w_hi; ++i, ++n) {
+            for (int i = lo; i < hi; ++i, ++n) {
                 if (i / fsteps != it) {
                     if (it >= 0) flush();
                     it = i / fsteps;
@@ -712,34 +825,52 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const __grid_constant
                         const int j = im.first + min(4 * q + (g >> 1), im.count - 1);
                         col[q] = p.hp + (static_cast<int64_t>(j) * 2 + (g & 1)) * p.fp + 8 * c;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[q][e] = 0.f;
+                        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) acc[t][q][e] = 0.f;
                     }
                 }
-                const int k0 = (i - it * fsteps) * St::kVals;
-                uint4 b[kB][kCols];
+                uint32_t b[kCols][kWords];
 #pragma unroll
-                for (int h = 0; h < kB; ++h)
-#pragma unroll
-                    for (int q = 0; q < kCols; ++q)
-                        b[h][q] = q < groups && k0 + 32 * h < p.fp ? ld_v4(col[q] + k0 + 32 * h) : make_uint4(0, 0, 0, 0);
+                for (int q = 0; q < kCols; ++q)
+                    load_column<kVals>(col[q], (i - it * fsteps) * kVals, p.fp, q < groups, b[q]);
                 cp_async_wait<kRing - 2>();
                 __syncwarp();   // (every lane is done with the stage that is filled next)
                 issue(n + kRing - 1);
-                mma_stage<kFmt, kCols>(acc, ring + (n % kRing) * St::kBytes, b, groups, g, c);
+                mma_stage<kFmt, false, kCols>(acc, ring + (n % kRing) * kBytes, b, groups, lane);
             }
             if (it >= 0) flush();
             __syncthreads();
-            for (int i = threadIdx.x; i < p.T * 16; i += kThreads) {
+            const int tile = unit / p.splits;
+            for (int i = threadIdx.x; i < p.T * kOut; i += kThreads) {
                 float v = 0.f;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
-                    v += ysum[w * p.T * 16 + i];
-                    ysum[w * p.T * 16 + i] = 0.f;
+                    v += ysum[w * p.T * kOut + i];
+                    ysum[w * p.T * kOut + i] = 0.f;
                 }
-                const int t = i >> 4, d = tile * 16 + (i & 15);
-                if (d < p.D) p.y[t * p.ldy + d] = __float2half_rn(v);
+                const int t = i / kOut, d = tile * kOut + i % kOut;
+                if (d < p.D) {
+                    if (p.splits == 1)
+                        p.y[t * p.ldy + d] = __float2half_rn(v);
+                    else
+                        p.parts[(static_cast<int64_t>(unit % p.splits) * p.T + t) * p.dp + d] = v;
+                }
             }
             __syncthreads();
+            if (p.splits > 1) {
+                if (threadIdx.x == 0) sh.last = atom_add_acq_rel_gpu(&p.counts[tile], 1) == p.splits - 1;
+                __syncthreads();
+                if (sh.last) {
+                    for (int i = threadIdx.x; i < p.T * kOut; i += kThreads) {
+                        const int t = i / kOut, d = tile * kOut + i % kOut;
+                        if (d >= p.D) continue;
+                        float v = 0.f;
+                        for (int s = 0; s < p.splits; ++s) v += ld_cg_f32(p.parts + (static_cast<int64_t>(s) * p.T + t) * p.dp + d);
+                        p.y[t * p.ldy + d] = __float2half_rn(v);
+                    }
+                }
+            }
         }
         cp_async_wait<0>();
         __syncthreads();

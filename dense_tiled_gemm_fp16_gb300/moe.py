@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 
-from .mxf4 import Mxf4Matrix, _empty, _pkg, _stream
+from .mxf4 import Mxf4Matrix, _empty, _on, _pkg, _stream, _torch
 
 WEIGHT_F16, WEIGHT_MXF4 = 0, 1
 MAX_TOKENS, MAX_EXPERTS, MAX_TOP_K, MAX_DIM = 64, 512, 8, 32768
@@ -55,20 +55,19 @@ def moe_f16(x: int, stride_xt: int, stride_xi: int, router: int, stride_ri: int,
 def _weight(w, rows: int, cols: int, experts: int, name: str):
     """The MoeWeight of an fp16 tensor [E, rows, cols] or the Mxf4Matrix that
     mxf4_quantize(.., axis=-2) makes of one ([E, cols, rows])."""
-    import torch
-
     if isinstance(w, Mxf4Matrix):
         if w.shape != (experts, cols, rows):
             raise ValueError(f"{name} in MXFP4 must be quantised along its contracted axis: expected "
                              f"{(experts, cols, rows)}, got {w.shape}")
-        return MoeWeight(WEIGHT_MXF4, w.codes.data_ptr(), w.scales.data_ptr(), 0, 0, 0)
-    if w.dtype != torch.float16:
+        return MoeWeight(WEIGHT_MXF4, w.codes_ptr, w.scales_ptr, 0, 0, 0)
+    if w.dtype is not _torch().float16:
         raise TypeError("moe_few takes float16 tensors and Mxf4Matrix weights")
-    if tuple(w.shape) != (experts, rows, cols):
+    if w.shape != (experts, rows, cols):
         raise ValueError(f"{name} must be [{experts}, {rows}, {cols}], got {tuple(w.shape)}")
+    se, si, so = w.stride()
     # (a dimension of one element may carry any stride)
-    return MoeWeight(WEIGHT_F16, w.data_ptr(), None, w.stride(0) if experts > 1 else 0, w.stride(1) if rows > 1 else 1,
-                     w.stride(2) if cols > 1 else max(8, rows))
+    return MoeWeight(WEIGHT_F16, w.data_ptr(), None, se if experts > 1 else 0, si if rows > 1 else 1,
+                     so if cols > 1 else (rows + 7) // 8 * 8)
 
 
 def moe_few(x, router, gate, up, down, top_k: int, act="silu", renormalize: bool = True, out=None, stream=None):
@@ -81,33 +80,36 @@ def moe_few(x, router, gate, up, down, top_k: int, act="silu", renormalize: bool
     two in order of falling router logits, equal logits in index order.  With
     `renormalize` a token's weights are the softmax over its chosen experts,
     otherwise over all."""
-    import torch
-
-    g = _pkg()
+    g, t = _pkg(), _torch()
     if x.dim() != 2 or router.dim() != 2 or x.shape[1] != router.shape[0]:
         raise ValueError("moe_few takes x [T, D] and router [D, E]")
     T, D = x.shape
     E = router.shape[1]
-    quantised = [isinstance(w, Mxf4Matrix) for w in (gate, up, down)]
-    if any(quantised) != all(quantised):
+    quantised = isinstance(gate, Mxf4Matrix)
+    if isinstance(up, Mxf4Matrix) != quantised or isinstance(down, Mxf4Matrix) != quantised:
         raise TypeError("the three projections share one format")
     if len(gate.shape) != 3:
         raise ValueError("gate must be [E, D, F]")
-    F = gate.shape[1] if quantised[0] else gate.shape[2]
+    F = gate.shape[1] if quantised else gate.shape[2]
     code = g._act(act)
-    weights = [_weight(w, r, c, E, n) for w, r, c, n in ((gate, D, F, "gate"), (up, D, F, "up"), (down, F, D, "down"))]
-    g._check_out(out, (T, D), "[T, D]")
-    g._check_tensors(x, router, out)
-    if any(w.device != x.device for w in (gate, up, down)):
+    wg, wu, wd = _weight(gate, D, F, E, "gate"), _weight(up, D, F, E, "up"), _weight(down, F, D, E, "down")
+    if out is not None:
+        g._check_out(out, (T, D), "[T, D]")
+    for v in (x, router, out):
+        if v is not None and v.dtype is not t.float16:
+            raise TypeError("gemm_f16 takes float16 tensors")
+    device = x.device
+    if device.type != "cuda" or any(v is not None and v.device != device for v in (router, gate, up, down, out)):
         raise ValueError("tensors must share one CUDA device")
     need = moe_f16_workspace_size(T, D, F, E, top_k)
-    y = _empty((T, D), torch.float16, x.device, stream) if out is None else out
-    probs = _empty((T, top_k), torch.float32, x.device, stream)
-    ids = _empty((T, top_k), torch.int32, x.device, stream)
-    space = _empty(need, torch.uint8, x.device, stream)
-    with torch.cuda.device(x.device):
-        moe_f16(x.data_ptr(), x.stride(0) if T > 1 else max(1, D), x.stride(1) if D > 1 else 1, router.data_ptr(),
-                router.stride(0) if D > 1 else 1, router.stride(1) if E > 1 else max(8, D), *weights, T, D, F, E, top_k,
-                1 if renormalize else 0, code, y.data_ptr(), y.stride(0) if T > 1 else D, probs.data_ptr(),
-                ids.data_ptr(), space.data_ptr(), need, _stream(x.device, stream))
+    y = _empty((T, D), t.float16, device, stream) if out is None else out
+    probs = _empty((T, top_k), t.float32, device, stream)
+    ids = _empty((T, top_k), t.int32, device, stream)
+    space = _empty(need, t.uint8, device, stream)
+    sxt, sxi = x.stride()
+    sri, sre = router.stride()
+    _on(device, moe_f16, x.data_ptr(), sxt if T > 1 else D, sxi if D > 1 else 1, router.data_ptr(),
+        sri if D > 1 else (E + 7) // 8 * 8, sre if E > 1 else (D + 7) // 8 * 8, wg, wu, wd, T, D, F, E, top_k,
+        1 if renormalize else 0, code, y.data_ptr(), y.stride(0) if T > 1 else D, probs.data_ptr(), ids.data_ptr(),
+        space.data_ptr(), need, _stream(device, stream))
     return y, probs, ids

@@ -1,9 +1,9 @@
 """MXFP4 matrices on CUDA torch tensors: quantisation, its inverse and the product.
 
-Mirrors ``include/gemm_mxf4.h`` (``mxf4_sizes``, ``gemm_mxf4`` and the pointer
-forms of the two conversions) and adds the tensor forms ``mxf4_quantize``,
-``mxf4_dequantize`` and ``mxf4_mm``.  Like the rest of the binding it only
-marshals arguments; PyTorch supplies memory and streams.
+Mirrors ``include/gemm_mxf4.h`` (``mxf4_sizes``, ``gemm_mxf4``, ``gemm_mxf4_a16``
+and the pointer forms of the two conversions) and adds the tensor forms
+``mxf4_quantize``, ``mxf4_dequantize`` and ``mxf4_mm``.  Like the rest of the
+binding it only marshals arguments; PyTorch supplies memory and streams.
 """
 from __future__ import annotations
 
@@ -12,7 +12,7 @@ import ctypes
 F16, BF16, F32 = range(3)
 
 # Every symbol include/gemm_mxf4.h declares.
-EXPORTED = ("mxf4_sizes", "mxf4_quantize", "mxf4_dequantize", "gemm_mxf4")
+EXPORTED = ("mxf4_sizes", "mxf4_quantize", "mxf4_dequantize", "gemm_mxf4", "gemm_mxf4_a16")
 
 
 def declare(L) -> None:
@@ -22,13 +22,31 @@ def declare(L) -> None:
     L.mxf4_quantize.argtypes = [P, I, I64, I64, I64, P, P, I64, I64, I64, P]
     L.mxf4_dequantize.argtypes = [P, P, P, I, I64, I64, I64, P]
     L.gemm_mxf4.argtypes = [P, P, P, P, P, I, P, I64, I64, I64, I64, P]
+    L.gemm_mxf4_a16.argtypes = [P, I64, I64, P, P, P, P, I, P, I64, I64, I64, I64, P]
     for name in EXPORTED:
         getattr(L, name).restype = I
 
 
+# The package and torch, looked up at the first call (the package imports this
+# module, and its C mirrors work without torch).
+_g = None
+_t = None
+
+
 def _pkg():
-    import dense_tiled_gemm_fp16_gb300 as g
-    return g
+    global _g
+    if _g is None:
+        import dense_tiled_gemm_fp16_gb300 as g
+        _g = g
+    return _g
+
+
+def _torch():
+    global _t
+    if _t is None:
+        import torch
+        _t = torch
+    return _t
 
 
 # ------------------------------------------------------------ C-ABI mirrors
@@ -63,56 +81,94 @@ def gemm_mxf4(A_codes: int, A_scales: int, B_codes: int, B_scales: int, bias: in
                                stream or None), "gemm_mxf4")
 
 
+def gemm_mxf4_a16(A: int, stride_am: int, stride_ak: int, work: int, B_codes: int, B_scales: int, bias: int, act: int,
+                  C: int, ldc: int, M: int, N: int, K: int, stream: int = 0) -> None:
+    """gemm_mxf4 with A in fp16, quantised into `work` (see include/gemm_mxf4.h)."""
+    g = _pkg()
+    g._check(g.lib().gemm_mxf4_a16(A, stride_am, stride_ak, work, B_codes, B_scales, bias or None, act, C, ldc, M, N,
+                                   K, stream or None), "gemm_mxf4_a16")
+
+
 # ------------------------------------------------------------ torch helpers
+def _bytes(rows: int, k: int, batch: int):
+    """mxf4_sizes without its checks: (codes, scales)."""
+    blocks = (k + 31) >> 5
+    return batch * rows * blocks * 16, batch * ((rows + 127) >> 7) * ((blocks + 3) >> 2) * 512
+
+
 class Mxf4Matrix:
     """A matrix [rows, k], or a batch [batch, rows, k], held in MXFP4 along k:
-    ``codes`` and ``scales`` are the byte arrays include/gemm_mxf4.h lays out."""
+    ``codes`` and ``scales`` are the byte arrays include/gemm_mxf4.h lays out,
+    ``codes_ptr`` and ``scales_ptr`` their device addresses."""
 
-    __slots__ = ("codes", "scales", "rows", "k", "batch")
+    __slots__ = ("_data", "_split", "rows", "k", "batch", "device", "codes_ptr", "scales_ptr")
 
     def __init__(self, codes, scales, rows: int, k: int, batch=None):
-        self.codes, self.scales, self.rows, self.k, self.batch = codes, scales, rows, k, batch
+        if (codes.numel(), scales.numel()) != _bytes(rows, k, batch or 1) or codes.device != scales.device:
+            raise ValueError("codes and scales do not hold a matrix of these sizes")
+        self._data, self._split = (codes, scales), None
+        self.rows, self.k, self.batch, self.device = rows, k, batch, codes.device
+        self.codes_ptr, self.scales_ptr = codes.data_ptr(), scales.data_ptr()
+
+    @classmethod
+    def _of(cls, data, split: int, rows: int, k: int, batch, device):
+        """Both arrays in one buffer, the codes from byte `split` on."""
+        q = cls.__new__(cls)
+        q._data, q._split = data, split
+        q.rows, q.k, q.batch, q.device = rows, k, batch, device
+        q.scales_ptr = p = data.data_ptr()
+        q.codes_ptr = p + split
+        return q
+
+    @property
+    def codes(self):
+        return self._data[0] if self._split is None else self._data[self._split:]
+
+    @property
+    def scales(self):
+        return self._data[1] if self._split is None else self._data[:self._split]
 
     @property
     def shape(self):
         return (self.rows, self.k) if self.batch is None else (self.batch, self.rows, self.k)
 
     @property
-    def device(self):
-        return self.codes.device
-
-    @property
     def nbytes(self) -> int:
-        return self.codes.numel() + self.scales.numel()
+        return sum(_bytes(self.rows, self.k, self.batch or 1))
 
     def __repr__(self):
         return f"Mxf4Matrix{self.shape} on {self.device}"
 
 
 def _dtype_code(dtype) -> int:
-    import torch
-
-    code = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}.get(dtype)
+    t = _torch()
+    code = F16 if dtype is t.float16 else BF16 if dtype is t.bfloat16 else F32 if dtype is t.float32 else None
     if code is None:
         raise TypeError("MXFP4 conversions take float16, bfloat16 or float32")
     return code
 
 
 def _stream(device, stream):
-    import torch
-
-    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+    return (stream if stream is not None else _torch().cuda.current_stream(device)).cuda_stream
 
 
 def _empty(shape, dtype, device, stream):
     """torch.empty for `stream`: what the allocator hands out is ordered with
     the stream that will write it, the current one unless one is given."""
-    import torch
-
+    t = _torch()
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return t.empty(shape, dtype=dtype, device=device)
+    with t.cuda.stream(stream):
+        return t.empty(shape, dtype=dtype, device=device)
+
+
+def _on(device, call, *args):
+    """call(*args) with `device` current."""
+    t = _torch()
+    if device.index == t.cuda.current_device():
+        return call(*args)
+    with t.cuda.device(device):
+        return call(*args)
 
 
 def mxf4_quantize(x, axis: int = -1, stream=None) -> Mxf4Matrix:
@@ -120,40 +176,38 @@ def mxf4_quantize(x, axis: int = -1, stream=None) -> Mxf4Matrix:
     positive strides) in MXFP4 along `axis`, the one a product will contract: a
     weight [K, N] takes axis=-2 and becomes the [N, K] matrix that mxf4_mm and
     moe_few read."""
-    import torch
-
-    if x.dim() not in (2, 3):
+    nd = x.dim()
+    if nd != 2 and nd != 3:
         raise ValueError("mxf4_quantize takes a matrix or a batch of matrices")
-    if axis not in (-1, -2, x.dim() - 1, x.dim() - 2):
+    if axis not in (-1, -2, nd - 1, nd - 2):
         raise ValueError("axis must be one of the two matrix dimensions")
     code = _dtype_code(x.dtype)
     if not x.is_cuda:
         raise ValueError("tensors must be on a CUDA device")
-    if axis % x.dim() == x.dim() - 2:
-        x = x.transpose(-1, -2)
-    rows, k = x.shape[-2:]
-    batch = x.shape[0] if x.dim() == 3 else 1
-    nc, ns = mxf4_sizes(rows, k, batch)
-    codes = _empty(nc, torch.uint8, x.device, stream)
-    scales = _empty(ns, torch.uint8, x.device, stream)
-    with torch.cuda.device(x.device):
-        # (a dimension of one element may carry any stride, a batch of stride 0 repeats)
-        mxf4_quantize_ptr(x.data_ptr(), code, x.stride(0) if x.dim() == 3 and batch > 1 else 0,
-                          x.stride(-2) if rows > 1 else max(1, k), x.stride(-1) if k > 1 else 1, codes.data_ptr(),
-                          scales.data_ptr(), rows, k, batch, _stream(x.device, stream))
-    return Mxf4Matrix(codes, scales, rows, k, batch if x.dim() == 3 else None)
+    *lead, rows, k = x.shape
+    *sb, sr, sk = x.stride()
+    if axis == -2 or axis == nd - 2:
+        rows, k, sr, sk = k, rows, sk, sr
+    batch = lead[0] if lead else 1
+    device = x.device
+    nc, ns = _bytes(rows, k, batch)
+    data = _empty(nc + ns, _t.uint8, device, stream)
+    q = Mxf4Matrix._of(data, ns, rows, k, batch if lead else None, device)
+    # (a dimension of one element may carry any stride, a batch of stride 0 repeats)
+    _on(device, mxf4_quantize_ptr, x.data_ptr(), code, sb[0] if batch > 1 else 0, sr if rows > 1 else max(1, k),
+        sk if k > 1 else 1, q.codes_ptr, q.scales_ptr, rows, k, batch, _stream(device, stream))
+    return q
 
 
 def mxf4_dequantize(q: Mxf4Matrix, dtype=None, stream=None):
     """The values of q, rounded once to `dtype` (float16 unless given)."""
-    import torch
-
-    dtype = torch.float16 if dtype is None else dtype
+    if dtype is None:
+        dtype = _torch().float16
     code = _dtype_code(dtype)
-    y = _empty(q.shape, dtype, q.device, stream)
-    with torch.cuda.device(q.device):
-        mxf4_dequantize_ptr(q.codes.data_ptr(), q.scales.data_ptr(), y.data_ptr(), code, q.rows, q.k, q.batch or 1,
-                            _stream(q.device, stream))
+    device = q.device
+    y = _empty(q.shape, dtype, device, stream)
+    _on(device, mxf4_dequantize_ptr, q.codes_ptr, q.scales_ptr, y.data_ptr(), code, q.rows, q.k, q.batch or 1,
+        _stream(device, stream))
     return y
 
 
@@ -161,32 +215,38 @@ def mxf4_mm(a, b: Mxf4Matrix, bias=None, act="none", out=None, stream=None):
     """fp16 C[m, n] = act(sum_k a[m, k] b[n, k] + bias[n]): b an Mxf4Matrix
     [N, K], a an Mxf4Matrix [M, K] or a float16 tensor [M, K] that is quantised
     on the way; returns C."""
-    import torch
-
-    g = _pkg()
+    g, t = _pkg(), _torch()
     if not isinstance(b, Mxf4Matrix) or b.batch is not None:
         raise TypeError("mxf4_mm takes b as an Mxf4Matrix of two dimensions")
-    if isinstance(a, Mxf4Matrix):
-        if a.batch is not None:
-            raise ValueError("mxf4_mm takes matrices, not batches")
-    elif a.dim() != 2:
+    held = isinstance(a, Mxf4Matrix)
+    if len(a.shape) != 2:
         raise ValueError("expected two matrices")
-    if a.shape[1] != b.k:
-        raise ValueError(f"inner dimensions differ: {a.shape[1]} vs {b.k}")
-    M, N = a.shape[0], b.rows
+    M, K = a.shape
+    N = b.rows
+    if K != b.k:
+        raise ValueError(f"inner dimensions differ: {K} vs {b.k}")
     code = g._act(act)
     if bias is not None and (bias.dim() != 1 or bias.shape[0] != N or bias.stride(0) != 1):
         raise ValueError("bias must hold N values with unit stride")
-    g._check_out(out, (M, N), "[M, N]")
-    g._check_tensors(None if isinstance(a, Mxf4Matrix) else a, out, bias)
-    if any(t is not None and t.device != b.device for t in (a, out, bias)):
+    device = b.device
+    if out is not None:
+        g._check_out(out, (M, N), "[M, N]")
+    for x in (None if held else a, out, bias):
+        if x is not None and x.dtype is not t.float16:
+            raise TypeError("gemm_f16 takes float16 tensors")
+    if device.type != "cuda" or any(x is not None and x.device != device for x in (a, out, bias)):
         raise ValueError("tensors must share one CUDA device")
     if out is None:
-        out = _empty((M, N), torch.float16, b.device, stream)
-    if not isinstance(a, Mxf4Matrix):
-        a = mxf4_quantize(a, stream=stream)
-    with torch.cuda.device(b.device):
-        gemm_mxf4(a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(), b.scales.data_ptr(),
-                  0 if bias is None else bias.data_ptr(), code, out.data_ptr(), out.stride(0), M, N, b.k,
-                  _stream(b.device, stream))
+        out = _empty((M, N), t.float16, device, stream)
+    raw = _stream(device, stream)
+    ldc = out.stride(0) if M > 1 else N
+    bp = 0 if bias is None else bias.data_ptr()
+    if held:
+        _on(device, gemm_mxf4, a.codes_ptr, a.scales_ptr, b.codes_ptr, b.scales_ptr, bp, code, out.data_ptr(), ldc, M,
+            N, K, raw)
+    else:
+        sm, sk = a.stride()
+        work = _empty(sum(_bytes(M, K, 1)), t.uint8, device, stream)
+        _on(device, gemm_mxf4_a16, a.data_ptr(), sm if M > 1 else max(1, K), sk if K > 1 else 1, work.data_ptr(),
+            b.codes_ptr, b.scales_ptr, bp, code, out.data_ptr(), ldc, M, N, K, raw)
     return out

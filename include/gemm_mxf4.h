@@ -57,6 +57,14 @@ gemm_f16_status gemm_mxf4(const void* A_codes, const void* A_scales, const void*
                           const void* bias, int act, void* C, int64_t ldc, int64_t M, int64_t N, int64_t K,
                           cudaStream_t stream);
 
+/* The same product with A in fp16 (element (m, k) at m * stride_am +
+ * k * stride_ak), quantised within the call into `work`: mxf4_sizes(M, K, 1)
+ * bytes, the scales first and then the codes, 16-byte aligned, the call's own
+ * until its kernels have run. */
+gemm_f16_status gemm_mxf4_a16(const void* A, int64_t stride_am, int64_t stride_ak, void* work, const void* B_codes,
+                              const void* B_scales, const void* bias, int act, void* C, int64_t ldc, int64_t M,
+                              int64_t N, int64_t K, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -102,7 +102,7 @@ def test_tensor_form_checks_before_any_call():
         g.moe_few(x.float(), r, gate, gate, down, 2)
     with pytest.raises(TypeError):
         g.moe_few(x, r, gate.float(), gate, down, 2)
-    q = g.Mxf4Matrix(torch.zeros(512, dtype=torch.uint8), torch.zeros(2048, dtype=torch.uint8), 8, 16, 4)
+    q = g.Mxf4Matrix(torch.zeros(4 * 8 * 16, dtype=torch.uint8), torch.zeros(2048, dtype=torch.uint8), 8, 16, 4)
     with pytest.raises(TypeError):                        # one format for the three
         g.moe_few(x, r, q, gate, down, 2)
     with pytest.raises(ValueError):                       # quantised along the wrong axis

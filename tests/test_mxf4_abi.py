@@ -93,12 +93,33 @@ def test_gemm_refuses(args):
     _refused(lambda: g.gemm_mxf4(*args))
 
 
+@pytest.mark.parametrize("args", [
+    (0, 64, 1, S, X, Y, 0, 0, 1 << 36, 8, 8, 8, 64), (C, 64, 1, 0, X, Y, 0, 0, 1 << 36, 8, 8, 8, 64),
+    (C, 64, 1, S, 0, Y, 0, 0, 1 << 36, 8, 8, 8, 64), (C, 64, 1, S, X, 0, 0, 0, 1 << 36, 8, 8, 8, 64),
+    (C, 64, 1, S, X, Y, 0, 0, 0, 8, 8, 8, 64),
+    (C + 1, 64, 1, S, X, Y, 0, 0, 1 << 36, 8, 8, 8, 64),     # misaligned A
+    (C, 64, 1, S + 8, X, Y, 0, 0, 1 << 36, 8, 8, 8, 64),     # misaligned work
+    (C, 0, 1, S, X, Y, 0, 0, 1 << 36, 8, 8, 8, 64), (C, 64, -1, S, X, Y, 0, 0, 1 << 36, 8, 8, 8, 64),
+    (C, 1 << 62, 1, S, X, Y, 0, 0, 1 << 36, 8, 8, 8, 64),    # extent overflows
+    (C, 64, 1, S, X, Y, 0, 5, 1 << 36, 8, 8, 8, 64), (C, 64, 1, S, X, Y, 0, 0, 1 << 36, 4, 8, 8, 64),
+])
+def test_gemm_a16_refuses(args):
+    _refused(lambda: g.gemm_mxf4_a16(*args))
+
+
+def test_gemm_a16_overlaps_are_refused():
+    call = lambda a=C, w=S, b=X, bs=Y, bias=0, c=1 << 36: g.gemm_mxf4_a16(a, 64, 1, w, b, bs, bias, 0, c, 8, 8, 8, 64)  # noqa: E731
+    for bad in (dict(c=C), dict(c=S + 512), dict(w=C), dict(w=X), dict(w=Y), dict(bias=S + 16), dict(c=X), dict(c=Y)):
+        _refused(lambda: call(**bad), g.ERR_ALIAS)
+
+
 def test_valid_calls_reach_the_device_check():
     if torch.cuda.is_available():
         pytest.skip("a GPU is present")
     _refused(lambda: g.mxf4_quantize_ptr(X, 0, 0, 64, 1, C, S, 4, 64, 1), g.ERR_UNSUPPORTED_DEVICE)
     _refused(lambda: g.mxf4_dequantize_ptr(C, S, Y, 0, 4, 64, 1), g.ERR_UNSUPPORTED_DEVICE)
     _refused(lambda: g.gemm_mxf4(C, S, X, Y, 0, 0, 1 << 36, 8, 8, 8, 64), g.ERR_UNSUPPORTED_DEVICE)
+    _refused(lambda: g.gemm_mxf4_a16(C, 64, 1, S, X, Y, 0, 0, 1 << 36, 8, 8, 8, 64), g.ERR_UNSUPPORTED_DEVICE)
 
 
 def test_tensor_forms_check_before_any_call():
@@ -111,10 +132,12 @@ def test_tensor_forms_check_before_any_call():
         g.mxf4_quantize(torch.zeros(64, dtype=h))
     with pytest.raises(ValueError):
         g.mxf4_quantize(torch.zeros((4, 4, 64), dtype=h), axis=0)
-    q = g.Mxf4Matrix(torch.zeros(128, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8), 4, 64)
+    q = g.Mxf4Matrix(torch.zeros(4 * 32, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8), 4, 64)
     with pytest.raises(TypeError):
         g.mxf4_dequantize(q, torch.int8)
     a = torch.zeros((3, 64), dtype=h)
+    with pytest.raises(ValueError):                      # arrays of other sizes
+        g.Mxf4Matrix(torch.zeros(128, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8), 5, 64)
     with pytest.raises(TypeError):                       # b must be quantised
         g.mxf4_mm(a, a)
     with pytest.raises(ValueError):                      # inner dimensions
