@@ -8,6 +8,7 @@
 #include "host.h"
 #include "moe_f16.h"
 #include "moe_kernel.cuh"
+#include "moe_stream.cuh"
 
 using namespace gemm_f16_host;
 
@@ -20,9 +21,14 @@ namespace {
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
+// The counters at the workspace's start.
+constexpr int64_t kControlBytes = 8448;
+static_assert(sizeof(moe_dev::StreamControl) <= kControlBytes && 256 + moe_dev::kMaxRanges * 4 <= kControlBytes, "room");
+
 // Places in the workspace.
 struct Layout {
-    int64_t dp, fp, counts, xp, hp, parts, bytes;
+    int64_t dp, fp, xp, hp, parts, bytes;              // any format
+    int64_t dq, fq, dw, fw, xq, xs, hq, hs;            // MXFP4 columns: row pitches of codes and of scales
 };
 
 // Most shares of the experts' K: with many tokens the shares' sums cost more
@@ -36,11 +42,23 @@ bool layout_of(int64_t T, int64_t D, int64_t F, int64_t E, int64_t top, Layout* 
         return false;
     l->dp = round_up(D, 64);
     l->fp = round_up(F, 64);
-    l->counts = 256;
-    l->xp = l->counts + moe_dev::kMaxRanges * 4;
-    l->hp = l->xp + round_up(T * l->dp * 2, 256);
-    l->parts = l->hp + round_up(T * top * 2 * l->fp * 2, 256);
-    l->bytes = l->parts + max_splits(T) * T * l->dp * 4;
+    l->dq = round_up(D, 256) / 2, l->fq = round_up(F, 256) / 2;
+    l->dw = round_up(D, 256) / 32, l->fw = round_up(F, 256) / 32;
+    int64_t at = kControlBytes;
+    auto take = [&](int64_t bytes) {
+        const int64_t place = at;
+        at += round_up(bytes, 256);
+        return place;
+    };
+    l->xp = take(T * l->dp * 2);
+    l->hp = take(T * top * 2 * l->fp * 2);
+    l->xq = take(T * moe_dev::kPieces * l->dq);
+    l->xs = take(T * moe_dev::kPieces * l->dw);
+    l->hq = take(T * top * moe_dev::kPieces * l->fq);
+    l->hs = take(T * top * moe_dev::kPieces * l->fw);
+    l->parts = take(std::max(max_splits(T) * T * l->dp * 4,
+                             static_cast<int64_t>(moe_dev::kMaxParts) * 2 * std::max<int64_t>(T, 16) * 128 * 4));
+    l->bytes = at;
     return true;
 }
 
@@ -59,17 +77,16 @@ bool weight_span(const moe_f16_weight& w, int64_t E, int64_t in, int64_t out, in
     return !__builtin_mul_overflow(e, 2, data);
 }
 
-// 16-byte words along the contracted axis, or along the other one: every row of
-// 8 values starts aligned.
-bool rows_aligned(const moe_f16_weight& w)
+// What a tensor map can address: unit stride along one matrix axis, the other
+// strides positive multiples of 16 bytes below 2^40, an aligned start.
+bool map_strides(const moe_f16_weight& w, int64_t pitch, int64_t E)
 {
-    return w.stride_i == 1 && w.stride_o % 8 == 0 && w.stride_e % 8 == 0 && aligned(w.data, 16);
+    return pitch % 8 == 0 && pitch < int64_t(1) << 39 && aligned(w.data, 16) &&
+           (E == 1 || (w.stride_e > 0 && w.stride_e % 8 == 0 && w.stride_e < int64_t(1) << 39));
 }
 
-bool cols_aligned(const moe_f16_weight& w)
-{
-    return w.stride_o == 1 && w.stride_i % 8 == 0 && w.stride_e % 8 == 0 && aligned(w.data, 16);
-}
+bool rows_aligned(const moe_f16_weight& w, int64_t E) { return w.stride_i == 1 && map_strides(w, w.stride_o, E); }
+bool cols_aligned(const moe_f16_weight& w, int64_t E) { return w.stride_o == 1 && map_strides(w, w.stride_i, E); }
 
 moe_dev::Weight weight_of(const moe_f16_weight& w, int64_t E, int64_t in, int64_t out)
 {
@@ -90,6 +107,8 @@ moe_dev::Weight weight_of(const moe_f16_weight& w, int64_t E, int64_t in, int64_
 }
 
 constexpr int kMaxDevices = 64;
+constexpr int kMaxSmem = 232448;     // 227 KiB a block
+constexpr int kStaticSmem = 8192;    // more than the stream kernel's own
 
 // More dynamic shared memory than the default, once a device and kernel.
 bool allow_smem(const void* kernel, int slot, int bytes)
@@ -152,6 +171,67 @@ gemm_f16_status launch_experts(moe_dev::Params& p, int sms, cudaStream_t stream)
         if (p.T > 32) return launch_experts<kFmt, 2, 2>(p, sms, stream);
     }
     return launch_experts<kFmt, 2, kRing>(p, sms, stream);
+}
+
+// A 3-D map of one projection: inner, outer, expert; boxes of 128 bytes x rows.
+bool encode_weight(CUtensorMap* tm, const void* data, bool bytes, uint64_t inner, uint64_t outer, uint64_t experts,
+                   uint64_t pitch, uint64_t expert_pitch)
+{
+    const auto encode = tensor_map_encoder();
+    if (!encode) return false;
+    cuuint64_t dims[3] = {inner, outer, experts};
+    cuuint64_t strides[2] = {pitch, experts > 1 ? expert_pitch : pitch * outer};
+    cuuint32_t box[3] = {bytes ? 128u : 64u, 64, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return encode(tm, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(data),
+                  dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kFmt>
+gemm_f16_status launch_stream(const moe_dev::Params& p, const Layout& l, uint8_t* ws, const moe_f16_weight* const* w,
+                              int sms, cudaStream_t stream)
+{
+    constexpr bool kMx = kFmt == moe_dev::kStreamMxf4;
+    moe_dev::StreamParams sp = {};
+    sp.p = p;
+    CUtensorMap* maps[3] = {&sp.gate, &sp.up, &sp.down};
+    const moe_dev::Weight* dw[3] = {&p.gate, &p.up, &p.down};
+    for (int i = 0; i < 3; ++i) {
+        const uint64_t in = i < 2 ? p.D : p.F, out = i < 2 ? p.F : p.D;
+        const bool good =
+            kMx ? encode_weight(maps[i], w[i]->data, true, dw[i]->so, out, p.E, dw[i]->so, dw[i]->se)
+            : kFmt == moe_dev::kStreamRows
+                ? encode_weight(maps[i], w[i]->data, false, in, out, p.E, 2 * dw[i]->so, 2 * dw[i]->se)
+                : encode_weight(maps[i], w[i]->data, false, out, in, p.E, 2 * dw[i]->si, 2 * dw[i]->se);
+        if (!good) return GEMM_F16_ERR_LAUNCH;
+    }
+    sp.ctl = reinterpret_cast<moe_dev::StreamControl*>(ws);
+    sp.sums = reinterpret_cast<float*>(ws + l.parts);
+    sp.x = kMx ? ws + l.xq : ws + l.xp;
+    sp.xs = ws + l.xs;
+    sp.h = kMx ? ws + l.hq : ws + l.hp;
+    sp.hs = ws + l.hs;
+    sp.xpitch = static_cast<int32_t>(kMx ? l.dq : 2 * l.dp);
+    sp.hpitch = static_cast<int32_t>(kMx ? l.fq : 2 * l.fp);
+    sp.xwords = static_cast<int32_t>(l.dw / 4);
+    sp.hwords = static_cast<int32_t>(l.fw / 4);
+    // Tokens of one reading of an expert's weights: all of them for few tokens,
+    // 16 otherwise; fewer leave the shared memory to the weights' ring.
+    sp.cap = p.T <= 4 ? 4 : p.T <= 8 ? 8 : 16;
+    sp.b_bytes = kMx ? sp.cap * moe_dev::kPieces * 128 : std::max(16, 2 * sp.cap) * 128;
+    sp.stage_bytes = static_cast<int32_t>(moe_dev::kTileBytes) + sp.b_bytes + (kMx ? 4 * mxf4_dev::kScaleTile : 0);
+    const int tail = (sp.cap + p.T) * 128 * 4;
+    sp.stages = std::min(16, (kMaxSmem - kStaticSmem - 1024 - tail) / sp.stage_bytes);
+    sp.loaders = std::min(sp.stages, moe_dev::kLoadWarps);
+    sp.acc_cols = kMx ? sp.cap * moe_dev::kPieces : 32;
+    const uint32_t need = 2 * sp.acc_cols + (kMx ? 16 : 0);
+    sp.tmem_cols = need <= 64 ? 64 : need <= 128 ? 128 : need <= 256 ? 256 : 512;
+    const int smem = sp.stages * sp.stage_bytes + tail + 1024;
+    const auto kernel = moe_dev::moe_stream<kFmt>;
+    if (!allow_smem(reinterpret_cast<const void*>(kernel), 20 + kFmt, kMaxSmem - kStaticSmem)) return GEMM_F16_ERR_LAUNCH;
+    return launch_kernel(kernel, dim3(static_cast<unsigned>(std::min(sms, moe_dev::kMaxParts))), moe_dev::kThreads, smem,
+                         kCooperative, stream, sp);
 }
 
 }  // namespace
@@ -236,8 +316,16 @@ gemm_f16_status moe_f16(const void* x, int64_t stride_xt, int64_t stride_xi, con
     p.weights = weights;
     p.ids = ids;
     uint8_t* base = static_cast<uint8_t*>(workspace);
+    p.zero = reinterpret_cast<int*>(base);
+    p.nzero = static_cast<int32_t>(kControlBytes / 4);
     p.ctl = reinterpret_cast<moe_dev::Control*>(base);
-    p.counts = reinterpret_cast<int32_t*>(base + l.counts);
+    p.counts = reinterpret_cast<int32_t*>(base + 256);
+    if (gate->format == MOE_F16_WEIGHT_MXF4) {
+        p.xq = base + l.xq;
+        p.xs = base + l.xs;
+        p.xq_pitch = static_cast<int32_t>(l.dq);
+        p.xs_pitch = static_cast<int32_t>(l.dw);
+    }
     p.parts = reinterpret_cast<float*>(base + l.parts);
     p.xp = reinterpret_cast<__half*>(base + l.xp);
     p.hp = reinterpret_cast<__half*>(base + l.hp);
@@ -250,11 +338,12 @@ gemm_f16_status moe_f16(const void* x, int64_t stride_xt, int64_t stride_xi, con
          : aligned16 && stride_re == 1 && stride_ri % 8 == 0 ? launch_route<moe_dev::kOutContiguous>(p, stream)
                                                               : launch_route<moe_dev::kAnyStrides>(p, stream);
     if (st != GEMM_F16_OK) return st;
-    if (gate->format == MOE_F16_WEIGHT_MXF4) return launch_experts<moe_dev::kMxf4, 8>(p, dev.sms, stream);
-    if (rows_aligned(*gate) && rows_aligned(*up) && rows_aligned(*down))
-        return launch_experts<moe_dev::kF16Rows, 4>(p, dev.sms, stream);
-    if (cols_aligned(*gate) && cols_aligned(*up) && cols_aligned(*down))
-        return launch_experts<moe_dev::kF16Cols, 4>(p, dev.sms, stream);
+    if (gate->format == MOE_F16_WEIGHT_MXF4)
+        return launch_stream<moe_dev::kStreamMxf4>(p, l, base, ws, dev.sms, stream);
+    if (rows_aligned(*gate, E) && rows_aligned(*up, E) && rows_aligned(*down, E))
+        return launch_stream<moe_dev::kStreamRows>(p, l, base, ws, dev.sms, stream);
+    if (cols_aligned(*gate, E) && cols_aligned(*up, E) && cols_aligned(*down, E))
+        return launch_stream<moe_dev::kStreamCols>(p, l, base, ws, dev.sms, stream);
     return launch_experts<moe_dev::kF16Strided, 4>(p, dev.sms, stream);
 }
 

@@ -20,7 +20,7 @@
 #include <cstdint>
 
 #include "gemm_f16.h"
-#include "mxf4_convert.cuh"
+#include "mxf4_format.cuh"
 #include "ptx.cuh"
 
 namespace moe_dev {
@@ -28,6 +28,7 @@ namespace moe_dev {
 using namespace gemm_f16_dev;
 
 constexpr int kMaxTokens = 64, kMaxExperts = 512, kMaxTop = 8, kMaxSlots = kMaxTokens * kMaxTop;
+constexpr int kPieces = 8;   // MXFP4 columns that a value of the narrow side is held in
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxSplits = 8, kMaxRanges = 2048;   // ranges of 16 columns at least, 32768 in all
 constexpr int kRouteCluster = 8;   // CTAs that share a router product, and tokens of a group
@@ -94,9 +95,9 @@ struct Weight {
     int32_t kt;           // MXFP4: scale tiles along the contracted axis
 };
 
-// Counters of one call, zeroed by the routing kernel.
+// Counters of one call.
 struct Control {
-    int ticket_up, done_up, ticket_down;
+    int ticket_up, done_up, ticket_down, unused;
 };
 
 struct Params {
@@ -111,9 +112,14 @@ struct Params {
     int64_t ldy;
     float* weights;
     int32_t* ids;
+    int* zero;             // the experts' kernel's counters: the routing kernel sets `nzero` words to 0
+    int32_t nzero;
+    uint8_t* xq;           // MXFP4 weights: the tokens as [T][kPieces] rows of xq_pitch bytes of codes,
+    uint8_t* xs;           // and their scales, xs_pitch bytes a row (otherwise null)
+    int32_t xq_pitch, xs_pitch;
     Control* ctl;
     int32_t splits;        // shares of the experts' K a range of y's columns is cut into
-    int32_t* counts;       // [column ranges]: finished shares, zeroed by the routing kernel
+    int32_t* counts;       // [column ranges]: finished shares
     float* parts;          // [splits][T][dp]: their sums
     __half* xp;            // [T][dp]: the tokens, packed, zeros past D
     __half* hp;            // [T * top][2][fp]: the hidden values as high and low halves, by expert
@@ -153,6 +159,34 @@ __device__ __forceinline__ int expert_row(int mt, int h, int g)
     return kLayout == kOutContiguous ? 8 * (g >> 1) + 2 * (2 * mt + h) + (g & 1) : 16 * mt + 8 * h + g;
 }
 
+// One block of 32 values, one a lane, as kPieces MXFP4 columns: the codes of
+// column q at codes + q * pitch (16 bytes), its scale at scales + q * spitch.
+__device__ __forceinline__ void split_block(float v, int lane, uint8_t* codes, int64_t pitch, uint8_t* scales,
+                                            int64_t spitch)
+{
+#pragma unroll 2
+    for (int q = 0; q < kPieces; ++q) {
+        const uint32_t top = __reduce_max_sync(~0u, __float_as_uint(v) & 0x7FFFFFFFu);
+        const uint32_t code = mxf4_dev::scale_code<float>(top);
+        uint32_t e = 0;
+        if (code != 255u) {
+            const float t = v * mxf4_dev::pow2f(127 - static_cast<int>(code));
+            uint32_t back;
+            asm("{\n\t.reg .b8 b;\n\t"
+                "cvt.rn.satfinite.e2m1x2.f32 b, %3, %2;\n\t"
+                "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+                "mov.b32 %0, {b, b, b, b};\n\t}"
+                : "=r"(e), "=r"(back)
+                : "f"(t), "f"(0.f));
+            e &= 15u;
+            v -= mxf4_dev::scale_value(code) * __half2float(__ushort_as_half(static_cast<unsigned short>(back)));
+        }
+        e |= __shfl_down_sync(~0u, e, 1) << 4;
+        if ((lane & 1) == 0) codes[q * pitch + (lane >> 1)] = static_cast<uint8_t>(e);
+        if (lane == 0) scales[q * spitch] = static_cast<uint8_t>(code);
+    }
+}
+
 // A cluster of 8 CTAs routes 8 tokens: CTA r sums the r-th part of D for all
 // experts and tokens, then takes token r: adds the 8 parts over distributed
 // shared memory and picks its experts.  Bound by latency: the router is read
@@ -178,10 +212,8 @@ __global__ void __launch_bounds__(kThreads) moe_route(const __grid_constant__ Pa
 
     griddep_wait();
     griddep_launch_dependents();
-    if (blockIdx.x == 0) {
-        if (threadIdx.x == 0) *p.ctl = Control{0, 0, 0};
-        for (int i = threadIdx.x; i < kMaxRanges; i += kThreads) p.counts[i] = 0;
-    }
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < p.nzero; i += kThreads) p.zero[i] = 0;
 
     for (int i = threadIdx.x; i < 8 * width; i += kThreads) {
         const int t = i / width, k = i - t * width;
@@ -294,6 +326,13 @@ __global__ void __launch_bounds__(kThreads) moe_route(const __grid_constant__ Pa
         }
         __syncthreads();
     }
+    if (p.xq)
+        for (int i = warp; i < nt * (width >> 5); i += kWarps) {
+            const int t = i / (width >> 5), blk = i - t * (width >> 5);
+            const int64_t row = static_cast<int64_t>(t0 + t) * kPieces, at = (k_lo >> 5) + blk;
+            split_block(__half2float(xs[t * xpitch + blk * 32 + lane]), lane, p.xq + row * p.xq_pitch + at * 16, p.xq_pitch,
+                        p.xs + row * p.xs_pitch + at, p.xs_pitch);
+        }
     cluster_sync_all();
     if (rank < nt && warp == 0) {
         float l[kMaxExperts / 32];
@@ -559,14 +598,69 @@ struct Item {
     uint16_t expert, first, count;   // first: place in the list of choices ordered by expert
 };
 
-struct Shared {
+// The choices ordered by expert, in shared memory.
+struct Choices {
     uint16_t slot[kMaxSlots];        // choices (token * top + j) ordered by expert, then by token
     float weight[kMaxSlots];         // their routing weights
     Item item[kMaxSlots];
     uint16_t first_of[kMaxExperts];
     uint32_t scan[kWarps];
-    int items, ticket, last, ok;
+    int items;
 };
+
+// Fills `ch` with pieces of `cap` tokens at most; `wcount`: room for 16 x E
+// counts.  A counting sort by all kThreads threads of a CTA: each slot's rank
+// within its warp by matching, then the warps' counts of each expert in turn,
+// so that the order is that of the slots.  Ends with a barrier.
+__device__ __forceinline__ void order_choices(const Params& p, Choices& ch, uint16_t* wcount, int cap)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int slots = p.T * p.top, nw = (slots + 31) >> 5;
+    for (int i = threadIdx.x; i < nw * p.E; i += kThreads) wcount[i] = 0;
+    __syncthreads();
+    const bool mine = static_cast<int>(threadIdx.x) < slots;
+    const int e = mine ? p.ids[threadIdx.x] : -1;
+    const uint32_t same = __match_any_sync(~0u, e);
+    const int before = __popc(same & ((1u << lane) - 1u));
+    if (mine && before == 0) wcount[warp * p.E + e] = static_cast<uint16_t>(__popc(same));
+    __syncthreads();
+    // thread e: this expert's count, its place, its pieces
+    const int ex = threadIdx.x;
+    int count = 0;
+    if (ex < p.E)
+        for (int w = 0; w < nw; ++w) {
+            const int n = wcount[w * p.E + ex];
+            wcount[w * p.E + ex] = static_cast<uint16_t>(count);
+            count += n;
+        }
+    const int pieces = (count + cap - 1) / cap;
+    uint32_t sum = static_cast<uint32_t>(count) << 16 | pieces;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+        const uint32_t o = __shfl_up_sync(~0u, sum, s);
+        if (lane >= s) sum += o;
+    }
+    if (lane == 31) ch.scan[warp] = sum;
+    __syncthreads();
+    uint32_t base = 0;
+    for (int w = 0; w < warp; ++w) base += ch.scan[w];
+    sum += base;
+    const int first = static_cast<int>(sum >> 16) - count, piece0 = static_cast<int>(sum & 0xFFFFu) - pieces;
+    if (ex < p.E) {
+        ch.first_of[ex] = static_cast<uint16_t>(first);
+        for (int i = 0; i < pieces; ++i)
+            ch.item[piece0 + i] = Item{static_cast<uint16_t>(ex), static_cast<uint16_t>(first + i * cap),
+                                       static_cast<uint16_t>(min(cap, count - i * cap))};
+    }
+    if (threadIdx.x == kThreads - 1) ch.items = static_cast<int>(sum & 0xFFFFu);
+    __syncthreads();
+    if (mine) {
+        const int at = ch.first_of[e] + wcount[warp * p.E + e] + before;
+        ch.slot[at] = static_cast<uint16_t>(threadIdx.x);
+        ch.weight[at] = p.weights[threadIdx.x];
+    }
+    __syncthreads();
+}
 
 // All experts of the layer.  Two phases, gate/up and down, each cut into
 // gridDim parts of equal bytes; a CTA takes a part by ticket and, before it
@@ -585,7 +679,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const __grid_constant
     using Down = Step<kFmt, false>;
     constexpr int kBytes = Stage<kFmt>::kBytes;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ Shared sh;
+    __shared__ Choices sh;
+    __shared__ int ticket_slot, last_flag, wait_ok;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const uint32_t ring = smem_u32(smem) + warp * (kRing * kBytes);
     uint8_t* tail = smem + kWarps * kRing * kBytes;   // sums: gate/up [2][16][groups][32] float4, down [16][T][kOut]
@@ -594,59 +689,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const __grid_constant
     griddep_wait();
     griddep_launch_dependents();
 
-    // ---- the choices ordered by expert
-    const int slots = p.T * p.top;
-    {
-        uint16_t* wcount = reinterpret_cast<uint16_t*>(smem);   // [16 warps][E], in the ring before its first use
-        const int nw = (slots + 31) >> 5;
-        for (int i = threadIdx.x; i < nw * p.E; i += kThreads) wcount[i] = 0;
-        if (threadIdx.x == 0) sh.ticket = atomicAdd(&p.ctl->ticket_up, 1);
-        __syncthreads();
-        const bool mine = static_cast<int>(threadIdx.x) < slots;
-        const int e = mine ? p.ids[threadIdx.x] : -1;
-        const uint32_t same = __match_any_sync(~0u, e);
-        const int before = __popc(same & ((1u << lane) - 1u));
-        if (mine && before == 0) wcount[warp * p.E + e] = static_cast<uint16_t>(__popc(same));
-        __syncthreads();
-        // thread e: this expert's count, its place, its pieces
-        const int ex = threadIdx.x;
-        int count = 0;
-        if (ex < p.E)
-            for (int w = 0; w < nw; ++w) {
-                const int n = wcount[w * p.E + ex];
-                wcount[w * p.E + ex] = static_cast<uint16_t>(count);
-                count += n;
-            }
-        const int pieces = (count + 8 * kGroups - 1) / (8 * kGroups);
-        uint32_t sum = static_cast<uint32_t>(count) << 16 | pieces;
-#pragma unroll
-        for (int s = 1; s < 32; s <<= 1) {
-            const uint32_t o = __shfl_up_sync(~0u, sum, s);
-            if (lane >= s) sum += o;
-        }
-        if (lane == 31) sh.scan[warp] = sum;
-        __syncthreads();
-        uint32_t base = 0;
-        for (int w = 0; w < warp; ++w) base += sh.scan[w];
-        sum += base;
-        const int first = static_cast<int>(sum >> 16) - count, piece0 = static_cast<int>(sum & 0xFFFFu) - pieces;
-        if (ex < p.E) {
-            sh.first_of[ex] = static_cast<uint16_t>(first);
-            for (int i = 0; i < pieces; ++i)
-                sh.item[piece0 + i] = Item{static_cast<uint16_t>(ex), static_cast<uint16_t>(first + i * 8 * kGroups),
-                                           static_cast<uint16_t>(min(8 * kGroups, count - i * 8 * kGroups))};
-        }
-        if (threadIdx.x == kThreads - 1) sh.items = static_cast<int>(sum & 0xFFFFu);
-        __syncthreads();
-        if (mine) {
-            const int at = sh.first_of[e] + wcount[warp * p.E + e] + before;
-            sh.slot[at] = static_cast<uint16_t>(threadIdx.x);
-            sh.weight[at] = p.weights[threadIdx.x];
-        }
-        __syncthreads();
-    }
+    if (threadIdx.x == 0) ticket_slot = atomicAdd(&p.ctl->ticket_up, 1);
+    order_choices(p, sh, reinterpret_cast<uint16_t*>(smem), 8 * kGroups);
     const int items = sh.items;
-    int ticket = sh.ticket;
+    int ticket = ticket_slot;
 
     // ---- gate and up: a unit is one piece's next kOut hidden values, K dealt to the warps
     {
@@ -731,18 +777,18 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const __grid_constant
             __syncthreads();
             if (threadIdx.x == 0) {
                 if (!p.test_stall) atom_add_acq_rel_gpu(&p.ctl->done_up, 1);
-                sh.ticket = atomicAdd(&p.ctl->ticket_up, 1);
+                ticket_slot = atomicAdd(&p.ctl->ticket_up, 1);
             }
             __syncthreads();
-            ticket = sh.ticket;
+            ticket = ticket_slot;
         }
     }
 
     // ---- down: a warp takes a range of a unit's (piece, step) pairs and keeps
     // its own weighted sums of the tokens
-    if (threadIdx.x == 0) sh.ticket = atomicAdd(&p.ctl->ticket_down, 1);
+    if (threadIdx.x == 0) ticket_slot = atomicAdd(&p.ctl->ticket_down, 1);
     __syncthreads();
-    ticket = sh.ticket;
+    ticket = ticket_slot;
     constexpr int kVals = Down::kVals, kTiles = Down::kTiles, kWords = Down::kWords, kOut = Down::kOut;
     constexpr int kCols = 2 * kGroups;   // groups of 8 columns: a choice takes two (high and low half)
     const int tiles = (p.D + kOut - 1) / kOut, fsteps = (p.F + kVals - 1) / kVals;
@@ -776,10 +822,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const __grid_constant
         if (!waited) {
             if (threadIdx.x == 0) {
                 const uint64_t t0 = globaltimer_ns();
-                sh.ok = 1;
+                wait_ok = 1;
                 while (ld_acquire_gpu(&p.ctl->done_up) < parts) {
                     if (globaltimer_ns() - t0 > p.timeout_ns) {
-                        sh.ok = 0;
+                        wait_ok = 0;
                         atomicExch(p.status, GEMM_F16_ERR_TIMEOUT);
                         break;
                     }
@@ -788,7 +834,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const __grid_constant
             waited = true;
         }
         __syncthreads();
-        if (!sh.ok) break;
+        if (!wait_ok) break;
         int n = 0;
         for (int unit = u_lo; unit < u_hi; ++unit) {
             int lo, hi;
@@ -859,9 +905,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const __grid_constant
             }
             __syncthreads();
             if (p.splits > 1) {
-                if (threadIdx.x == 0) sh.last = atom_add_acq_rel_gpu(&p.counts[tile], 1) == p.splits - 1;
+                if (threadIdx.x == 0) last_flag = atom_add_acq_rel_gpu(&p.counts[tile], 1) == p.splits - 1;
                 __syncthreads();
-                if (sh.last) {
+                if (last_flag) {
                     for (int i = threadIdx.x; i < p.T * kOut; i += kThreads) {
                         const int t = i / kOut, d = tile * kOut + i % kOut;
                         if (d >= p.D) continue;
@@ -874,9 +920,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const __grid_constant
         }
         cp_async_wait<0>();
         __syncthreads();
-        if (threadIdx.x == 0) sh.ticket = atomicAdd(&p.ctl->ticket_down, 1);
+        if (threadIdx.x == 0) ticket_slot = atomicAdd(&p.ctl->ticket_down, 1);
         __syncthreads();
-        ticket = sh.ticket;
+        ticket = ticket_slot;
     }
     cp_async_wait<0>();
 }

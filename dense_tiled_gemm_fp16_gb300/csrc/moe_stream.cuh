@@ -1,0 +1,505 @@
+// The experts' kernel of the mixture-of-experts layer for weights that TMA can
+// address: fp16 in either orientation, and MXFP4.
+//
+// The layer is bound by reading the chosen experts' weights once, so the kernel
+// is built around that stream: one thread a CTA keeps a ring of 16 KB weight
+// tiles in flight by TMA, the tensor cores take them from shared memory as the
+// 128-row side (tcgen05.mma), and a few token columns are the narrow side.  No
+// instruction is spent per weight: MXFP4 codes are multiplied as they lie,
+// their scales applied by the block-scaled MMA.
+//
+// Both operands of an MMA have one type, so the narrow side is held in the
+// weights' format.  fp16: a hidden value is two columns, its fp16 rounding and
+// the fp16 rounding of the rest.  MXFP4: a value is 8 columns, each the MXFP4
+// rounding of what the columns before it leave; a column takes at least 3/4 off
+// the largest remainder of a block of 32, so that 8 leave under 2^-16 of the
+// block's largest magnitude, less than fp16 itself.  The epilogue adds the
+// columns in fp32.
+//
+// Work is cut into gridDim parts of equal bytes in each of the two phases
+// (gate/up, down), wherever that falls: a part's first and last output tile may
+// be shared with its neighbours, whose sums go through the workspace; the part
+// that finishes such a tile last adds them in order.
+#pragma once
+
+#include <cuda.h>
+
+#include "moe_kernel.cuh"
+#include "mxf4_ptx.cuh"
+
+namespace moe_dev {
+
+constexpr int kLoadWarps = 10;  // warps from 6 on bring the narrow side, at most these
+constexpr uint32_t kTileBytes = 128 * 128;
+constexpr int kMaxParts = 160;
+
+// Counters of one call, zeroed by the routing kernel.
+struct StreamControl {
+    int done;                 // finished gate/up parts
+    int up[kMaxParts];        // by the first part of a shared tile: parts that have stored their sums
+    int down[kMaxParts];
+};
+
+struct StreamParams {
+    CUtensorMap gate, up, down;
+    Params p;
+    StreamControl* ctl;
+    const uint8_t* x;         // narrow side of gate/up: rows (token, column) of xpitch bytes
+    const uint8_t* xs;        // MXFP4: their scales, xwords 32-bit words a row
+    uint8_t* h;               // narrow side of down: rows (choice by expert, column) of hpitch bytes
+    uint8_t* hs;
+    float* sums;              // [parts][2][max(cap, T)][128]
+    int32_t xpitch, xwords, hpitch, hwords;
+    int32_t cap;              // tokens of a piece of an expert's work
+    int32_t stages, stage_bytes, b_bytes;
+    int32_t loaders;          // warps that bring the narrow side: no more than stages, so that none
+                              // waits for a stage's use after next (its parity would be the last one's)
+    uint32_t tmem_cols, acc_cols;
+};
+
+// Ranges of a phase, walked alike by every role of a CTA.
+struct Segment {
+    int tile, item, s0, s1;   // steps s0 .. s1 - 1 of `steps` for (tile, item)
+};
+
+enum { kStreamRows = 0, kStreamCols = 1, kStreamMxf4 = 2 };
+
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Whether an output tile, `steps` steps from `first` on, lies in more than one
+// part, and in which.
+struct Parts {
+    int64_t total;
+    int count;
+    __device__ int64_t start(int part) const { return total * min(part, count) / count; }
+    __device__ int of(int64_t step) const
+    {
+        int v = static_cast<int>((step * count) / total);
+        while (start(v + 1) <= step) ++v;
+        while (start(v) > step) --v;
+        return v;
+    }
+};
+
+template <int kFmt>
+__global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant__ StreamParams sp)
+{
+    constexpr bool kMx = kFmt == kStreamMxf4;
+    const Params& p = sp.p;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
+    __shared__ Choices ch;
+    __shared__ __align__(8) uint64_t bars[3 * 16 + 5];
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int abort_flag;
+    __shared__ int last_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int part = blockIdx.x, parts = gridDim.x;
+
+    const uint32_t bar0 = smem_u32(bars);
+    auto full_a = [&](int s) { return bar0 + 24u * s; };
+    auto full_b = [&](int s) { return bar0 + 24u * s + 8u; };
+    auto empty = [&](int s) { return bar0 + 24u * s + 16u; };
+    auto tfull = [&](int b) { return bar0 + 24u * 16u + 8u * b; };
+    auto tempty = [&](int b) { return bar0 + 24u * 16u + 16u + 8u * b; };
+    const uint32_t drain = bar0 + 24u * 16u + 32u;
+    float* ex = reinterpret_cast<float*>(smem + sp.stages * sp.stage_bytes);   // [cap][128]: sums of a gate/up tile
+    float* ysum = ex + sp.cap * 128;                                           // [T][128]: sums of y's rows
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < sp.stages; ++s) {
+            mbar_init(full_a(s), 1);
+            mbar_init(full_b(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(tfull(b), 1);
+            mbar_init(tempty(b), 4);
+        }
+        mbar_init(drain, 1);
+        abort_flag = 0;
+        fence_mbarrier_init();
+        tma_prefetch_desc(&sp.gate);
+        tma_prefetch_desc(&sp.up);
+        tma_prefetch_desc(&sp.down);
+    }
+    if (warp == 5) {
+        tmem_alloc(smem_u32(&tmem_slot), sp.tmem_cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    griddep_wait();
+    griddep_launch_dependents();
+    order_choices(p, ch, reinterpret_cast<uint16_t*>(smem), sp.cap);
+    fence_proxy_async_smem();   // the counts lay where the copies will write
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const int items = ch.items;
+
+    // Phase 0: (piece, 64 hidden values) tiles of d_steps steps; phase 1: 128
+    // columns of y, for each all pieces of f_steps steps.
+    constexpr int kVals = kMx ? 256 : 64;
+    const int d_steps = (p.D + kVals - 1) / kVals, f_steps = (p.F + kVals - 1) / kVals;
+    const int f_tiles = (p.F + 63) >> 6, y_tiles = (p.D + 127) >> 7;
+    const int64_t up_steps = static_cast<int64_t>(items) * f_tiles * d_steps,
+                  down_steps = static_cast<int64_t>(y_tiles) * items * f_steps;
+    // (no part is empty but those past the number of steps)
+    const Parts phase[2] = {{up_steps, static_cast<int>(min(up_steps, static_cast<int64_t>(parts)))},
+                            {down_steps, static_cast<int>(min(down_steps, static_cast<int64_t>(parts)))}};
+    auto segment = [&](int ph, int64_t at, int64_t hi) {
+        Segment g;
+        const int steps = ph ? f_steps : d_steps;
+        const int64_t q = at / steps;
+        g.s0 = static_cast<int>(at - q * steps);
+        g.s1 = static_cast<int>(min(static_cast<int64_t>(steps), g.s0 + hi - at));
+        if (ph) {
+            g.tile = static_cast<int>(q / items);
+            g.item = static_cast<int>(q - static_cast<int64_t>(g.tile) * items);
+        } else {
+            g.item = static_cast<int>(q / f_tiles);
+            g.tile = static_cast<int>(q - static_cast<int64_t>(g.item) * f_tiles);
+        }
+        return g;
+    };
+    const volatile int* abort = &abort_flag;
+    auto fail = [&]() {
+        abort_flag = 1;
+        atomicExch(p.status, GEMM_F16_ERR_TIMEOUT);
+    };
+    auto columns = [&](int ph, int count) { return kMx ? count * kPieces : ph ? 2 * count : count; };
+
+    if (warp == 4) {
+        // ---------------------------------------------------------- weights
+        if (lane == 0) {
+            int n = 0, st = 0;
+            uint32_t par = 0;
+            bool ok = true;
+            for (int ph = 0; ph < 2 && ok; ++ph) {
+                const int64_t hi = phase[ph].start(part + 1);
+                for (int64_t at = phase[ph].start(part); at < hi && ok;) {
+                    const Segment g = segment(ph, at, hi);
+                    at += g.s1 - g.s0;
+                    const int e = ch.item[g.item].expert;
+                    const CUtensorMap* m0 = ph ? &sp.down : &sp.gate;
+                    const CUtensorMap* m1 = ph ? &sp.down : &sp.up;
+                    const int o0 = ph ? g.tile * 128 : g.tile * 64, o1 = ph ? o0 + 64 : o0;
+                    for (int s = g.s0; s < g.s1; ++s, ++n) {
+                        ok = mbar_wait(empty(st), par ^ 1u, abort, p.timeout_ns);
+                        if (!ok) break;
+                        const uint32_t a = base + st * sp.stage_bytes;
+                        mbar_arrive_expect_tx(full_a(st), kTileBytes);
+                        if (kFmt == kStreamCols) {
+                            tma_load_3d(a, m0, o0, s * 64, e, full_a(st));
+                            tma_load_3d(a + kTileBytes / 2, m1, o1, s * 64, e, full_a(st));
+                        } else {
+                            tma_load_3d(a, m0, s * (kMx ? 128 : 64), o0, e, full_a(st));
+                            tma_load_3d(a + kTileBytes / 2, m1, s * (kMx ? 128 : 64), o1, e, full_a(st));
+                        }
+                        if (++st == sp.stages) st = 0, par ^= 1u;
+                    }
+                }
+            }
+            if (!ok) {   // copies in flight land before the CTA leaves
+                fail();
+                for (int q = 0; q < sp.stages && q < n; ++q)
+                    mbar_wait(full_a(q), ((n - q + sp.stages - 1) / sp.stages - 1) & 1u, nullptr, mxf4_dev::kDrainNs);
+            }
+        }
+    } else if (warp == 5) {
+        // -------------------------------------------------------------- MMA
+        if (lane == 0) {
+            int st = 0, buf = 0;
+            uint32_t par = 0, bpar = 0;
+            bool ok = true;
+            const uint32_t tsa = tmem + 2 * sp.acc_cols, tsb = tsa + 8;
+            for (int ph = 0; ph < 2 && ok; ++ph) {
+                const int64_t hi = phase[ph].start(part + 1);
+                const int k64 = ((ph ? p.F : p.D) + 63) >> 6;
+                for (int64_t at = phase[ph].start(part); at < hi && ok;) {
+                    const Segment g = segment(ph, at, hi);
+                    at += g.s1 - g.s0;
+                    const int cols = columns(ph, ch.item[g.item].count);
+                    const uint32_t d = tmem + buf * sp.acc_cols;
+                    ok = mbar_wait(tempty(buf), bpar ^ 1u, abort, p.timeout_ns);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t id0 = kMx ? mxf4_dev::idesc_mxf4(128, cols, 0)
+                                             : (1u << 4) | ((kFmt == kStreamCols ? 1u : 0u) << 15) |
+                                                   ((static_cast<uint32_t>(cols + 15) >> 4) << 18) | (8u << 24);
+                    const uint32_t id1 = kMx ? mxf4_dev::idesc_mxf4(128, cols, 1) : 0u;
+                    for (int s = g.s0; s < g.s1; ++s) {
+                        ok = mbar_wait(full_a(st), par, abort, p.timeout_ns) && mbar_wait(full_b(st), par, abort, p.timeout_ns);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t a = base + st * sp.stage_bytes, b = a + kTileBytes;
+                        const int nk = min(4, kMx ? k64 - 4 * s : 4);
+                        if (kMx) {
+                            const uint32_t fa = b + sp.b_bytes, fb = fa + 2 * mxf4_dev::kScaleTile;
+                            for (int q = 0; q < (nk + 1) / 2; ++q) {
+                                mxf4_dev::tmem_copy_scales(tsa + 4 * q, mxf4_dev::scale_desc(fa + q * mxf4_dev::kScaleTile));
+                                mxf4_dev::tmem_copy_scales(tsb + 4 * q, mxf4_dev::scale_desc(fb + q * mxf4_dev::kScaleTile));
+                            }
+                        }
+                        for (int q = 0; q < nk; ++q) {
+                            const uint64_t da = kFmt == kStreamCols ? umma_desc_sw128(a + q * 2048, 8192, 1024)
+                                                                    : umma_desc_sw128(a + q * 32, 16, 1024);
+                            const uint64_t db = umma_desc_sw128(b + q * 32, 16, 1024);
+                            const uint32_t acc = s > g.s0 || q > 0;
+                            if (kMx)
+                                mxf4_dev::umma_mxf4(d, da, db, q & 1 ? id1 : id0, tsa + 4 * (q >> 1), tsb + 4 * (q >> 1), acc);
+                            else
+                                umma_f16(d, da, db, id0, acc);
+                        }
+                        umma_commit(empty(st));
+                        if (++st == sp.stages) st = 0, par ^= 1u;
+                    }
+                    if (!ok) break;
+                    umma_commit(tfull(buf));
+                    if (++buf == 2) buf = 0, bpar ^= 1u;
+                }
+            }
+            if (!ok) {   // MMAs in flight end before the CTA's memory goes
+                fail();
+                umma_commit(drain);
+                mbar_wait(drain, 0, nullptr, mxf4_dev::kDrainNs);
+            }
+        }
+    } else if (warp >= 6 + sp.loaders) {
+        // (here for the ordering of the choices alone)
+    } else if (warp >= 6) {
+        // ------------------------------------- narrow side and MXFP4 scales
+        int n = 0, st = 0;
+        uint32_t par = 0;
+        bool ok = true;
+        for (int ph = 0; ph < 2 && ok; ++ph) {
+            const int64_t hi = phase[ph].start(part + 1);
+            const int width = kMx ? kPieces : ph ? 2 : 1;   // rows of a token
+            const uint8_t* rows = ph ? sp.h : sp.x;
+            const uint8_t* scales = ph ? sp.hs : sp.xs;
+            const int64_t pitch = ph ? sp.hpitch : sp.xpitch, words = ph ? sp.hwords : sp.xwords;
+            bool waited = ph == 0;
+            for (int64_t at = phase[ph].start(part); at < hi && ok;) {
+                const Segment g = segment(ph, at, hi);
+                at += g.s1 - g.s0;
+                const Item im = ch.item[g.item];
+                const int nrows = im.count * width;
+                for (int s = g.s0; s < g.s1; ++s, ++n) {
+                    const int at_st = st;
+                    const uint32_t at_par = par;
+                    if (++st == sp.stages) st = 0, par ^= 1u;
+                    if (n % sp.loaders != warp - 6) continue;
+                    if (!waited) {   // every hidden value is there
+                        if (lane == 0) {
+                            const uint64_t t0 = globaltimer_ns();
+                            while (ok && ld_acquire_gpu(&sp.ctl->done) < parts)
+                                ok = !*abort && globaltimer_ns() - t0 <= p.timeout_ns;
+                        }
+                        ok = __shfl_sync(~0u, ok, 0);
+                        if (!ok) break;
+                        waited = true;
+                    }
+                    ok = mbar_wait(empty(at_st), at_par ^ 1u, abort, p.timeout_ns);
+                    ok = __all_sync(~0u, ok);
+                    if (!ok) break;
+                    const uint32_t b = base + at_st * sp.stage_bytes + kTileBytes;
+                    for (int i = lane; i < nrows * 8; i += 32) {
+                        const int r = i >> 3, c = i & 7, j = r / width, q = r - j * width;
+                        const int64_t row = static_cast<int64_t>(ph ? im.first + j : ch.slot[im.first + j] / p.top) * width + q;
+                        cp_async16(b + r * 128 + ((c ^ (r & 7)) << 4), rows + row * pitch + static_cast<int64_t>(s) * 128 + c * 16, 16u);
+                    }
+                    if (kMx) {
+                        const uint32_t fa = b + sp.b_bytes, fb = fa + 2 * mxf4_dev::kScaleTile;
+                        const Weight& w0 = ph ? p.down : p.gate;
+                        const int halves = min(2, w0.kt - 2 * s);
+                        for (int q = 0; q < halves; ++q) {
+                            if (ph) {
+                                cp_async16(fa + q * mxf4_dev::kScaleTile + lane * 16,
+                                           w0.scales + im.expert * w0.scale_se +
+                                               (static_cast<int64_t>(g.tile) * w0.kt + 2 * s + q) * mxf4_dev::kScaleTile + lane * 16,
+                                           16u);
+                            } else {
+                                // 64 gate rows and 64 up rows: half a scale tile of each
+                                const int64_t off = (static_cast<int64_t>(g.tile >> 1) * w0.kt + 2 * s + q) * mxf4_dev::kScaleTile +
+                                                    lane * 16 + (g.tile & 1) * 8;
+                                cp_async8(fa + q * mxf4_dev::kScaleTile + lane * 16, p.gate.scales + im.expert * p.gate.scale_se + off);
+                                cp_async8(fa + q * mxf4_dev::kScaleTile + lane * 16 + 8, p.up.scales + im.expert * p.up.scale_se + off);
+                            }
+                            for (int r = lane; r < nrows; r += 32) {
+                                const int j = r / width, i = r - j * width;
+                                const int64_t row = static_cast<int64_t>(ph ? im.first + j : ch.slot[im.first + j] / p.top) * width + i;
+                                cp_async4(fb + q * mxf4_dev::kScaleTile + (r & 31) * 16 + (r >> 5) * 4,
+                                          scales + (row * words + 2 * s + q) * 4, 4u);
+                            }
+                        }
+                    }
+                    cp_async_commit();
+                    cp_async_wait<0>();
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full_b(at_st));
+                }
+            }
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        if (!ok && lane == 0) fail();
+    } else {
+        // --------------------------------------------------------- epilogue
+        int buf = 0;
+        uint32_t bpar = 0;
+        bool ok = true;
+        const int row = threadIdx.x;   // of the tile
+        const uint32_t trow = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        const int sum_rows = max(sp.cap, p.T);
+        // this thread's value of token j of a finished accumulator
+        auto take = [&](uint32_t d, int j, int ph) {
+            float v = 0.f;
+            if (kMx) {
+                uint32_t r[8];
+                asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                             : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                             : "r"(d + j * kPieces)
+                             : "memory");
+                tmem_wait_ld();
+#pragma unroll
+                for (int q = kPieces - 1; q >= 0; --q) v += __uint_as_float(r[q]);   // the small ones first
+            } else if (ph) {
+                uint32_t r[2];
+                asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(d + 2 * j) : "memory");
+                tmem_wait_ld();
+                v = __uint_as_float(r[1]) + __uint_as_float(r[0]);
+            } else {
+                uint32_t r;
+                asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(d + j) : "memory");
+                tmem_wait_ld();
+                v = __uint_as_float(r);
+            }
+            return v;
+        };
+        // the four warps go on or leave together
+        auto all_of = [&](bool mine) {
+            uint32_t r;
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\t"
+                "setp.ne.u32 p, %1, 0;\n\t"
+                "barrier.cta.red.and.pred q, 1, 128, p;\n\t"
+                "selp.u32 %0, 1, 0, q;\n\t}"
+                : "=r"(r)
+                : "r"(static_cast<uint32_t>(mine))
+                : "memory");
+            return r != 0;
+        };
+        // the sums of a tile shared by several parts: whether this part is the
+        // last to store its own (`first`: the tile's first part)
+        auto last_of = [&](int* counter, int sharers) {
+            named_bar_sync(1, 128);
+            if (threadIdx.x == 0) last_flag = atom_add_acq_rel_gpu(counter, 1) == sharers - 1;
+            named_bar_sync(1, 128);
+            return last_flag != 0;
+        };
+        auto slot_of = [&](const Parts& w, int v, int64_t first) {   // a part that began before the tile's end: slot 0
+            return sp.sums + (static_cast<int64_t>(v) * 2 + (w.start(v) > first ? 0 : 1)) * sum_rows * 128;
+        };
+        for (int ph = 0; ph < 2 && ok; ++ph) {
+            const Parts& w = phase[ph];
+            const int64_t lo = w.start(part), hi = w.start(part + 1);
+            bool begun = false;   // (down) ysum holds sums of the current tile
+            for (int64_t at = lo; at < hi && ok;) {
+                const Segment g = segment(ph, at, hi);
+                const Item im = ch.item[g.item];
+                ok = all_of(mbar_wait(tfull(buf), bpar, abort, p.timeout_ns));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t d = trow + buf * sp.acc_cols;
+                if (ph == 0) {
+                    const int64_t first = at - g.s0;
+                    const bool whole = g.s0 == 0 && g.s1 == d_steps;
+                    at += g.s1 - g.s0;
+                    float* to = whole ? ex : slot_of(w, part, first);
+                    for (int j = 0; j < im.count; ++j) to[j * 128 + row] = take(d, j, 0);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(tempty(buf));
+                    if (++buf == 2) buf = 0, bpar ^= 1u;
+                    if (!whole) {
+                        const int v0 = w.of(first), v1 = w.of(first + d_steps - 1);
+                        if (!last_of(&sp.ctl->up[v0], v1 - v0 + 1)) continue;
+                        for (int j = 0; j < im.count; ++j) {
+                            float v = 0.f;
+                            for (int q = v0; q <= v1; ++q) v += ld_cg_f32(slot_of(w, q, first) + j * 128 + row);
+                            ex[j * 128 + row] = v;
+                        }
+                    }
+                    named_bar_sync(1, 128);
+                    // warps 0, 2 take hidden values 0-31 of the tile, 1, 3 the rest; every other token each
+                    const int f = g.tile * 64 + (warp & 1) * 32 + lane;
+                    for (int j = warp >> 1; j < im.count; j += 2) {
+                        const float* e = ex + j * 128 + (warp & 1) * 32 + lane;
+                        // (past F: zeros, whatever the tokens hold)
+                        const float hv = f < p.F ? act_f32(p.act, e[0]) * e[64] : 0.f;
+                        const int64_t r = im.first + j;
+                        if (kMx) {
+                            split_block(hv, lane, sp.h + r * kPieces * sp.hpitch + ((f - lane) >> 1), sp.hpitch,
+                                        sp.hs + r * kPieces * sp.hwords * 4 + ((f - lane) >> 5), sp.hwords * 4);
+                        } else {
+                            const __half hh = __float2half_rn(hv);
+                            const float back = __half2float(hh);
+                            __half* dst = reinterpret_cast<__half*>(sp.h + r * 2 * sp.hpitch) + f;
+                            dst[0] = hh;
+                            dst[sp.hpitch >> 1] = isfinite(back) ? __float2half_rn(hv - back) : __ushort_as_half(0);
+                        }
+                    }
+                    named_bar_sync(1, 128);
+                } else {
+                    const int64_t per = static_cast<int64_t>(items) * f_steps, first = g.tile * per;
+                    at += g.s1 - g.s0;
+                    if (!begun)
+                        for (int t = 0; t < p.T; ++t) ysum[t * 128 + row] = 0.f;
+                    begun = true;
+                    for (int j = 0; j < im.count; ++j) {
+                        float* y = ysum + ch.slot[im.first + j] / p.top * 128 + row;
+                        *y = fmaf(ch.weight[im.first + j], take(d, j, 1), *y);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(tempty(buf));
+                    if (++buf == 2) buf = 0, bpar ^= 1u;
+                    if (at < hi && at < first + per) continue;   // more of this tile
+                    begun = false;
+                    const int col = g.tile * 128 + row;
+                    if (lo <= first && at == first + per) {
+                        if (col < p.D)
+                            for (int t = 0; t < p.T; ++t) p.y[t * p.ldy + col] = __float2half_rn(ysum[t * 128 + row]);
+                        continue;
+                    }
+                    float* to = slot_of(w, part, first);
+                    for (int t = 0; t < p.T; ++t) to[t * 128 + row] = ysum[t * 128 + row];
+                    const int v0 = w.of(first), v1 = w.of(first + per - 1);
+                    if (!last_of(&sp.ctl->down[v0], v1 - v0 + 1)) continue;
+                    if (col < p.D)
+                        for (int t = 0; t < p.T; ++t) {
+                            float v = 0.f;
+                            for (int q = v0; q <= v1; ++q) v += ld_cg_f32(slot_of(w, q, first) + t * 128 + row);
+                            p.y[t * p.ldy + col] = __float2half_rn(v);
+                        }
+                }
+            }
+            if (ph == 0 && ok) {
+                named_bar_sync(1, 128);
+                if (threadIdx.x == 0 && !p.test_stall) atom_add_acq_rel_gpu(&sp.ctl->done, 1);
+            }
+        }
+        if (!ok) abort_flag = 1;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 5) tmem_dealloc(tmem, sp.tmem_cols);
+}
+
+}  // namespace moe_dev

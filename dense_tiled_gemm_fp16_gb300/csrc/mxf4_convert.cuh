@@ -8,126 +8,11 @@
 // bytes of codes, one full line.
 #pragma once
 
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include <cstdint>
-
-#include "ptx.cuh"
+#include "mxf4_format.cuh"
 
 namespace mxf4_dev {
 
-using namespace gemm_f16_dev;
-
 constexpr int kTileRows = 128, kTileVals = 256, kConvThreads = 256;
-constexpr int kScaleTile = 512;   // bytes: 128 rows x 4 blocks
-
-// Place of (row, block) in a matrix's scales, `kt` scale tiles per 128 rows.
-__host__ __device__ inline int64_t scale_at(int64_t row, int64_t blk, int64_t kt)
-{
-    return ((row >> 7) * kt + (blk >> 2)) * kScaleTile + (row & 31) * 16 + ((row >> 5) & 3) * 4 + (blk & 3);
-}
-
-// 2^e exactly, -126 <= e <= 127.
-__device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
-// The scale's value: 2^(code - 127), 2^-127 is subnormal, 255 is NaN.
-__device__ __forceinline__ float scale_value(uint32_t code)
-{
-    return code == 255u ? __uint_as_float(0x7FFFFFFFu) : code == 0u ? __uint_as_float(1u << 22) : pow2f(int(code) - 127);
-}
-
-template <typename T>
-struct Elem;
-template <>
-struct Elem<__half> {
-    static constexpr uint32_t kAbs = 0x7FFFu, kInf = 0x7C00u;
-    static __device__ float to_f32(uint32_t b) { return __half2float(__ushort_as_half(static_cast<unsigned short>(b))); }
-    static __device__ __half from_f32(float v) { return __float2half_rn(v); }
-};
-template <>
-struct Elem<__nv_bfloat16> {
-    static constexpr uint32_t kAbs = 0x7FFFu, kInf = 0x7F80u;
-    static __device__ float to_f32(uint32_t b) { return __uint_as_float(b << 16); }
-    static __device__ __nv_bfloat16 from_f32(float v) { return __float2bfloat16_rn(v); }
-};
-template <>
-struct Elem<float> {
-    static constexpr uint32_t kAbs = 0x7FFFFFFFu, kInf = 0x7F800000u;
-    static __device__ float to_f32(uint32_t b) { return __uint_as_float(b); }
-    static __device__ float from_f32(float v) { return v; }
-};
-
-// Largest magnitude of 8 values as the bits of |x|: for IEEE types the order
-// of the bits is the order of the magnitudes, infinity and NaN above them all.
-template <typename T>
-__device__ __forceinline__ uint32_t top_bits(const uint32_t* w)
-{
-    if (sizeof(T) == 4) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, w[i] & Elem<T>::kAbs);
-        return m;
-    }
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
-    return max(m & 0xFFFFu, m >> 16);
-}
-
-template <typename T>
-__device__ __forceinline__ float value_of(const uint32_t* w, int i)
-{
-    if (sizeof(T) == 4) return Elem<T>::to_f32(w[i]);
-    return Elem<T>::to_f32(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu);
-}
-
-// Scale code of a block whose largest magnitude has the bits `top`.
-template <typename T>
-__device__ __forceinline__ uint32_t scale_code(uint32_t top)
-{
-    if (top >= Elem<T>::kInf) return 255u;
-    const float a = Elem<T>::to_f32(top);
-    // floor(log2 a) from the bits; a subnormal a (fp32, bf16) is at most 2^-127
-    // below the clamp anyway, since s = floor(log2 a) - 2 is at least -127.
-    const int e = static_cast<int>(__float_as_uint(a) >> 23) - 127;   // zero and subnormals: -127
-    return static_cast<uint32_t>(max(e - 2, -127) + 127);
-}
-
-// Eight values times 2^-s as e2m1 codes, the first in the low nibble: round to
-// nearest even, magnitudes above 6 saturate.  The products are exact but where
-// they fall below 2^-126, far under the rounding point 0.25.
-template <typename T>
-__device__ __forceinline__ uint32_t codes_of(const uint32_t* w, uint32_t code)
-{
-    if (code == 255u) return 0u;
-    const float f = pow2f(127 - static_cast<int>(code));
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = value_of<T>(w, i) * f;
-    uint32_t r;
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
-        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
-        : "=r"(r)
-        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
-    return r;
-}
-
-// Eight e2m1 codes (a 32-bit word) as four half2, exactly.
-__device__ __forceinline__ void halves_of(uint32_t codes, uint32_t* h)
-{
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-        : "r"(codes));
-}
 
 struct QuantParams {
     const void* x;

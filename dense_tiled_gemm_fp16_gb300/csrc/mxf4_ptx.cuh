@@ -1,0 +1,51 @@
+// Block-scaled MMA on MXFP4 operands: the tcgen05 forms the product and the
+// mixture-of-experts kernels share.
+#pragma once
+
+#include <cstdint>
+
+#include "mxf4_format.cuh"
+
+namespace mxf4_dev {
+
+// Limit of the waits that let work in flight end before a CTA gives up.
+constexpr uint64_t kDrainNs = 1000000000ull;
+
+// D[tmem] (+)= A * B with block scales; the two scales of each row's 64 values
+// are the bytes 2 * half, 2 * half + 1 of the scale columns' words, `half` set
+// in the instruction descriptor.
+__device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t sfa, uint32_t sfb, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// A 512-byte scale tile (32 rows of 16 bytes) to 4 tensor-memory columns, the
+// same in each quarter of the lanes.
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t desc)
+{
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// Unswizzled descriptor of a scale tile: 8-row groups 128 bytes apart.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr)
+{
+    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(1) << 16) |
+           (static_cast<uint64_t>(8) << 32) | (static_cast<uint64_t>(1) << 46);
+}
+
+// Instruction descriptor: e2m1 A and B (bits 7-9, 10-12), E8M0 scales (23),
+// N / 8 (17-22), M / 128 (27-28), the scales' byte pair of B (4-5) and A (29-30).
+__host__ __device__ constexpr uint32_t idesc_mxf4(uint32_t m, uint32_t n, uint32_t half)
+{
+    return (1u << 7) | (1u << 10) | (1u << 23) | ((n >> 3) << 17) | ((m >> 7) << 27) | ((2 * half) << 4) |
+           ((2 * half) << 29);
+}
+
+}  // namespace mxf4_dev

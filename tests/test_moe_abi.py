@@ -21,7 +21,7 @@ def _w(data=G, fmt=0, scales=None, se=4096, si=1, so=64):
 
 def _args(**k):
     a = dict(x=X, sxt=64, sxi=1, router=R, sri=4, sre=1, gate=_w(G), up=_w(U), down=_w(DN), T=2, D=64, F=64, E=4, top=2,
-             renorm=1, act=2, y=Y, ldy=64, weights=W, ids=I, ws=WS, wb=1 << 20)
+             renorm=1, act=2, y=Y, ldy=64, weights=W, ids=I, ws=WS, wb=1 << 24)
     assert set(k) <= set(a)
     return tuple({**a, **k}.values())
 
