@@ -57,7 +57,7 @@ bool layout_of(int64_t T, int64_t D, int64_t F, int64_t E, int64_t top, Layout* 
     l->hq = take(T * top * moe_dev::kPieces * l->fq);
     l->hs = take(T * top * moe_dev::kPieces * l->fw);
     l->parts = take(std::max(max_splits(T) * T * l->dp * 4,
-                             static_cast<int64_t>(moe_dev::kMaxParts) * 2 * std::max<int64_t>(T, 16) * 128 * 4));
+                             static_cast<int64_t>(moe_dev::kMaxParts) * 2 * std::max<int64_t>(T, 16) * 256 * 4));
     l->bytes = at;
     return true;
 }
@@ -174,18 +174,21 @@ gemm_f16_status launch_experts(moe_dev::Params& p, int sms, cudaStream_t stream)
 }
 
 // A 3-D map of one projection: inner, outer, expert; boxes of 128 bytes x rows.
-bool encode_weight(CUtensorMap* tm, const void* data, bool bytes, uint64_t inner, uint64_t outer, uint64_t experts,
-                   uint64_t pitch, uint64_t expert_pitch)
+// The L2 brings 256 bytes of a row where the next step reads the other half,
+// 128 where that is another unit's.
+bool encode_weight(CUtensorMap* tm, const void* data, bool bytes, uint32_t box_rows, bool along_k, uint64_t inner,
+                   uint64_t outer, uint64_t experts, uint64_t pitch, uint64_t expert_pitch)
 {
     const auto encode = tensor_map_encoder();
     if (!encode) return false;
     cuuint64_t dims[3] = {inner, outer, experts};
     cuuint64_t strides[2] = {pitch, experts > 1 ? expert_pitch : pitch * outer};
-    cuuint32_t box[3] = {bytes ? 128u : 64u, 64, 1};
+    cuuint32_t box[3] = {bytes ? 128u : 64u, box_rows, 1};
     cuuint32_t estr[3] = {1, 1, 1};
     return encode(tm, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(data),
                   dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                  along_k ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int kFmt>
@@ -200,10 +203,10 @@ gemm_f16_status launch_stream(const moe_dev::Params& p, const Layout& l, uint8_t
     for (int i = 0; i < 3; ++i) {
         const uint64_t in = i < 2 ? p.D : p.F, out = i < 2 ? p.F : p.D;
         const bool good =
-            kMx ? encode_weight(maps[i], w[i]->data, true, dw[i]->so, out, p.E, dw[i]->so, dw[i]->se)
+            kMx ? encode_weight(maps[i], w[i]->data, true, 128, true, dw[i]->so, out, p.E, dw[i]->so, dw[i]->se)
             : kFmt == moe_dev::kStreamRows
-                ? encode_weight(maps[i], w[i]->data, false, in, out, p.E, 2 * dw[i]->so, 2 * dw[i]->se)
-                : encode_weight(maps[i], w[i]->data, false, out, in, p.E, 2 * dw[i]->si, 2 * dw[i]->se);
+                ? encode_weight(maps[i], w[i]->data, false, 128, true, in, out, p.E, 2 * dw[i]->so, 2 * dw[i]->se)
+                : encode_weight(maps[i], w[i]->data, false, 64, false, out, in, p.E, 2 * dw[i]->si, 2 * dw[i]->se);
         if (!good) return GEMM_F16_ERR_LAUNCH;
     }
     sp.ctl = reinterpret_cast<moe_dev::StreamControl*>(ws);
@@ -219,13 +222,12 @@ gemm_f16_status launch_stream(const moe_dev::Params& p, const Layout& l, uint8_t
     // Tokens of one reading of an expert's weights: all of them for few tokens,
     // 16 otherwise; fewer leave the shared memory to the weights' ring.
     sp.cap = p.T <= 4 ? 4 : p.T <= 8 ? 8 : 16;
-    sp.b_bytes = kMx ? sp.cap * moe_dev::kPieces * 128 : std::max(16, 2 * sp.cap) * 128;
-    sp.stage_bytes = static_cast<int32_t>(moe_dev::kTileBytes) + sp.b_bytes + (kMx ? 4 * mxf4_dev::kScaleTile : 0);
-    const int tail = (sp.cap + p.T) * 128 * 4;
+    sp.b_bytes = static_cast<int32_t>(round_up(kMx ? sp.cap * moe_dev::kPieces : std::max(16, 2 * sp.cap), 8) * 128);
+    sp.stage_bytes = 2 * static_cast<int32_t>(moe_dev::kTileBytes) + sp.b_bytes + (kMx ? 6 * mxf4_dev::kScaleTile : 0);
+    const int tail = p.T * 256 * 4;
     sp.stages = std::min(16, (kMaxSmem - kStaticSmem - 1024 - tail) / sp.stage_bytes);
-    sp.loaders = std::min(sp.stages, moe_dev::kLoadWarps);
-    sp.acc_cols = kMx ? sp.cap * moe_dev::kPieces : 32;
-    const uint32_t need = 2 * sp.acc_cols + (kMx ? 16 : 0);
+    sp.acc_cols = kMx ? static_cast<uint32_t>(round_up(sp.cap * moe_dev::kPieces, 8)) : 32;
+    const uint32_t need = 4 * sp.acc_cols + (kMx ? 24 : 0);
     sp.tmem_cols = need <= 64 ? 64 : need <= 128 ? 128 : need <= 256 ? 256 : 512;
     const int smem = sp.stages * sp.stage_bytes + tail + 1024;
     const auto kernel = moe_dev::moe_stream<kFmt>;

@@ -28,7 +28,7 @@ namespace moe_dev {
 using namespace gemm_f16_dev;
 
 constexpr int kMaxTokens = 64, kMaxExperts = 512, kMaxTop = 8, kMaxSlots = kMaxTokens * kMaxTop;
-constexpr int kPieces = 8;   // MXFP4 columns that a value of the narrow side is held in
+constexpr int kPieces = 6;   // MXFP4 columns that a value of the narrow side is held in
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxSplits = 8, kMaxRanges = 2048;   // ranges of 16 columns at least, 32768 in all
 constexpr int kRouteCluster = 8;   // CTAs that share a router product, and tokens of a group
@@ -161,15 +161,19 @@ __device__ __forceinline__ int expert_row(int mt, int h, int g)
 
 // One block of 32 values, one a lane, as kPieces MXFP4 columns: the codes of
 // column q at codes + q * pitch (16 bytes), its scale at scales + q * spitch.
+// Unlike a quantised operand, whose largest magnitudes saturate (6 to 8 times
+// 2^s), a column's scale is a step larger there, so that no remainder is above
+// half a step of the grid, 1/5 of the largest magnitude.
 __device__ __forceinline__ void split_block(float v, int lane, uint8_t* codes, int64_t pitch, uint8_t* scales,
                                             int64_t spitch)
 {
 #pragma unroll 2
     for (int q = 0; q < kPieces; ++q) {
         const uint32_t top = __reduce_max_sync(~0u, __float_as_uint(v) & 0x7FFFFFFFu);
-        const uint32_t code = mxf4_dev::scale_code<float>(top);
+        uint32_t code = mxf4_dev::scale_code<float>(top);
         uint32_t e = 0;
         if (code != 255u) {
+            code += (top & 0x7FFFFFu) > 0x400000u && code > 0u;   // above 6 * 2^s: mantissa above 1.5
             const float t = v * mxf4_dev::pow2f(127 - static_cast<int>(code));
             uint32_t back;
             asm("{\n\t.reg .b8 b;\n\t"

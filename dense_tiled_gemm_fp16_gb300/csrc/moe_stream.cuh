@@ -2,19 +2,22 @@
 // address: fp16 in either orientation, and MXFP4.
 //
 // The layer is bound by reading the chosen experts' weights once, so the kernel
-// is built around that stream: one thread a CTA keeps a ring of 16 KB weight
-// tiles in flight by TMA, the tensor cores take them from shared memory as the
-// 128-row side (tcgen05.mma), and a few token columns are the narrow side.  No
-// instruction is spent per weight: MXFP4 codes are multiplied as they lie,
-// their scales applied by the block-scaled MMA.
+// is built around that stream: one thread a CTA keeps a ring of 32 KB pairs of
+// weight tiles in flight by TMA, the tensor cores take them from shared memory
+// as the 128-row side (tcgen05.mma), and a few token columns are the narrow
+// side.  No instruction is spent per weight: MXFP4 codes are multiplied as they
+// lie, their scales applied by the block-scaled MMA.  A pair is the gate and
+// the up rows of the same 128 hidden values, whose sums meet in one lane, or 256
+// rows of the down projection.
 //
 // Both operands of an MMA have one type, so the narrow side is held in the
 // weights' format.  fp16: a hidden value is two columns, its fp16 rounding and
-// the fp16 rounding of the rest.  MXFP4: a value is 8 columns, each the MXFP4
-// rounding of what the columns before it leave; a column takes at least 3/4 off
-// the largest remainder of a block of 32, so that 8 leave under 2^-16 of the
-// block's largest magnitude, less than fp16 itself.  The epilogue adds the
-// columns in fp32.
+// the fp16 rounding of the rest.  MXFP4: a value is 6 columns, each the e2m1
+// rounding of what the columns before it leave, under a scale that none of the
+// block's 32 values exceeds: a column takes at least 4/5 off the largest
+// remainder, so that 6 leave under 2^-13.9 of the block's largest magnitude,
+// less than a fp16 value's own last place unless it is 8 times smaller.  The
+// epilogue adds the columns in fp32.
 //
 // Work is cut into gridDim parts of equal bytes in each of the two phases
 // (gate/up, down), wherever that falls: a part's first and last output tile may
@@ -29,7 +32,7 @@
 
 namespace moe_dev {
 
-constexpr int kLoadWarps = 10;  // warps from 6 on bring the narrow side, at most these
+constexpr int kLoadWarps = 10;  // warps 6 .. 15 bring the narrow side
 constexpr uint32_t kTileBytes = 128 * 128;
 constexpr int kMaxParts = 160;
 
@@ -48,12 +51,10 @@ struct StreamParams {
     const uint8_t* xs;        // MXFP4: their scales, xwords 32-bit words a row
     uint8_t* h;               // narrow side of down: rows (choice by expert, column) of hpitch bytes
     uint8_t* hs;
-    float* sums;              // [parts][2][max(cap, T)][128]
+    float* sums;              // [parts][2][max(cap, T)][256]
     int32_t xpitch, xwords, hpitch, hwords;
     int32_t cap;              // tokens of a piece of an expert's work
-    int32_t stages, stage_bytes, b_bytes;
-    int32_t loaders;          // warps that bring the narrow side: no more than stages, so that none
-                              // waits for a stage's use after next (its parity would be the last one's)
+    int32_t stages, stage_bytes, b_bytes;   // 3 stages at least
     uint32_t tmem_cols, acc_cols;
 };
 
@@ -64,9 +65,33 @@ struct Segment {
 
 enum { kStreamRows = 0, kStreamCols = 1, kStreamMxf4 = 2 };
 
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src)
+// Four tokens' sums of this thread's row: `width` adjacent columns each, the
+// later, smaller ones added first.
+template <int kWidth>
+__device__ __forceinline__ void take4(uint32_t taddr, float* v)
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+    uint32_t r[4 * kWidth];
+    if constexpr (kWidth == 1) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(taddr)
+                     : "memory");
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4 * kWidth; i += 8)
+            asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]),
+                           "=r"(r[i + 6]), "=r"(r[i + 7])
+                         : "r"(taddr + i)
+                         : "memory");
+    }
+    tmem_wait_ld();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        v[j] = __uint_as_float(r[j * kWidth + kWidth - 1]);
+#pragma unroll
+        for (int q = kWidth - 2; q >= 0; --q) v[j] += __uint_as_float(r[j * kWidth + q]);
+    }
 }
 
 // Whether an output tile, `steps` steps from `first` on, lies in more than one
@@ -96,7 +121,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
     __shared__ __align__(8) uint64_t bars[3 * 16 + 5];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
-    __shared__ int last_flag;
+    __shared__ int last_flag, fixes;
+    __shared__ int3 fix[2];   // shared tiles of y that this part adds up: tile, first and last part
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int part = blockIdx.x, parts = gridDim.x;
 
@@ -107,13 +133,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
     auto tfull = [&](int b) { return bar0 + 24u * 16u + 8u * b; };
     auto tempty = [&](int b) { return bar0 + 24u * 16u + 16u + 8u * b; };
     const uint32_t drain = bar0 + 24u * 16u + 32u;
-    float* ex = reinterpret_cast<float*>(smem + sp.stages * sp.stage_bytes);   // [cap][128]: sums of a gate/up tile
-    float* ysum = ex + sp.cap * 128;                                           // [T][128]: sums of y's rows
+    float* ysum = reinterpret_cast<float*>(smem + sp.stages * sp.stage_bytes);   // [T][256]: sums of y's rows
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < sp.stages; ++s) {
             mbar_init(full_a(s), 1);
-            mbar_init(full_b(s), 1);
+            mbar_init(full_b(s), kLoadWarps);
             mbar_init(empty(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -122,6 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
         }
         mbar_init(drain, 1);
         abort_flag = 0;
+        fixes = 0;
         fence_mbarrier_init();
         tma_prefetch_desc(&sp.gate);
         tma_prefetch_desc(&sp.up);
@@ -141,11 +167,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
     const uint32_t tmem = tmem_slot;
     const int items = ch.items;
 
-    // Phase 0: (piece, 64 hidden values) tiles of d_steps steps; phase 1: 128
+    // Phase 0: (piece, 128 hidden values) tiles of d_steps steps; phase 1: 256
     // columns of y, for each all pieces of f_steps steps.
     constexpr int kVals = kMx ? 256 : 64;
     const int d_steps = (p.D + kVals - 1) / kVals, f_steps = (p.F + kVals - 1) / kVals;
-    const int f_tiles = (p.F + 63) >> 6, y_tiles = (p.D + 127) >> 7;
+    const int f_tiles = (p.F + 127) >> 7, y_tiles = (p.D + 255) >> 8;
     const int64_t up_steps = static_cast<int64_t>(items) * f_tiles * d_steps,
                   down_steps = static_cast<int64_t>(y_tiles) * items * f_steps;
     // (no part is empty but those past the number of steps)
@@ -187,18 +213,38 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
                     const int e = ch.item[g.item].expert;
                     const CUtensorMap* m0 = ph ? &sp.down : &sp.gate;
                     const CUtensorMap* m1 = ph ? &sp.down : &sp.up;
-                    const int o0 = ph ? g.tile * 128 : g.tile * 64, o1 = ph ? o0 + 64 : o0;
+                    const int o0 = ph ? g.tile * 256 : g.tile * 128, o1 = ph ? o0 + 128 : o0;
+                    const Weight& w0 = ph ? p.down : p.gate;
+                    const Weight& w1 = ph ? p.down : p.up;
                     for (int s = g.s0; s < g.s1; ++s, ++n) {
                         ok = mbar_wait(empty(st), par ^ 1u, abort, p.timeout_ns);
                         if (!ok) break;
                         const uint32_t a = base + st * sp.stage_bytes;
-                        mbar_arrive_expect_tx(full_a(st), kTileBytes);
+                        if (kMx) {
+                            // scales of 128 rows and, but at an odd end, two tiles of K; rows
+                            // 128 on may be past y's last scale tile (and then past its columns)
+                            const uint32_t sf = min(2, w0.kt - 2 * s) * mxf4_dev::kScaleTile;
+                            const bool both = o1 < (ph ? p.D : p.F);
+                            const uint32_t fa = a + 2 * kTileBytes + sp.b_bytes;
+                            mbar_arrive_expect_tx(full_a(st), 2 * kTileBytes + (both ? 2 : 1) * sf);
+                            bulk_load(fa, w0.scales + e * w0.scale_se + (static_cast<int64_t>(o0 >> 7) * w0.kt + 2 * s) * mxf4_dev::kScaleTile,
+                                      sf, full_a(st));
+                            if (both)
+                                bulk_load(fa + 2 * mxf4_dev::kScaleTile,
+                                          w1.scales + e * w1.scale_se + (static_cast<int64_t>(o1 >> 7) * w1.kt + 2 * s) * mxf4_dev::kScaleTile,
+                                          sf, full_a(st));
+                        } else {
+                            mbar_arrive_expect_tx(full_a(st), 2 * kTileBytes);
+                        }
                         if (kFmt == kStreamCols) {
-                            tma_load_3d(a, m0, o0, s * 64, e, full_a(st));
-                            tma_load_3d(a + kTileBytes / 2, m1, o1, s * 64, e, full_a(st));
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                tma_load_3d(a + h * (kTileBytes / 2), m0, o0 + 64 * h, s * 64, e, full_a(st));
+                                tma_load_3d(a + kTileBytes + h * (kTileBytes / 2), m1, o1 + 64 * h, s * 64, e, full_a(st));
+                            }
                         } else {
                             tma_load_3d(a, m0, s * (kMx ? 128 : 64), o0, e, full_a(st));
-                            tma_load_3d(a + kTileBytes / 2, m1, s * (kMx ? 128 : 64), o1, e, full_a(st));
+                            tma_load_3d(a + kTileBytes, m1, s * (kMx ? 128 : 64), o1, e, full_a(st));
                         }
                         if (++st == sp.stages) st = 0, par ^= 1u;
                     }
@@ -216,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
             int st = 0, buf = 0;
             uint32_t par = 0, bpar = 0;
             bool ok = true;
-            const uint32_t tsa = tmem + 2 * sp.acc_cols, tsb = tsa + 8;
+            const uint32_t tsa = tmem + 4 * sp.acc_cols, tsb = tsa + 16;
             for (int ph = 0; ph < 2 && ok; ++ph) {
                 const int64_t hi = phase[ph].start(part + 1);
                 const int k64 = ((ph ? p.F : p.D) + 63) >> 6;
@@ -224,37 +270,43 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
                     const Segment g = segment(ph, at, hi);
                     at += g.s1 - g.s0;
                     const int cols = columns(ph, ch.item[g.item].count);
-                    const uint32_t d = tmem + buf * sp.acc_cols;
+                    const uint32_t d = tmem + 2 * buf * sp.acc_cols;
                     ok = mbar_wait(tempty(buf), bpar ^ 1u, abort, p.timeout_ns);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t id0 = kMx ? mxf4_dev::idesc_mxf4(128, cols, 0)
+                    const uint32_t id0 = kMx ? mxf4_dev::idesc_mxf4(128, (cols + 7) & ~7, 0)
                                              : (1u << 4) | ((kFmt == kStreamCols ? 1u : 0u) << 15) |
                                                    ((static_cast<uint32_t>(cols + 15) >> 4) << 18) | (8u << 24);
-                    const uint32_t id1 = kMx ? mxf4_dev::idesc_mxf4(128, cols, 1) : 0u;
+                    const uint32_t id1 = kMx ? mxf4_dev::idesc_mxf4(128, (cols + 7) & ~7, 1) : 0u;
                     for (int s = g.s0; s < g.s1; ++s) {
                         ok = mbar_wait(full_a(st), par, abort, p.timeout_ns) && mbar_wait(full_b(st), par, abort, p.timeout_ns);
                         if (!ok) break;
                         tc_fence_after();
-                        const uint32_t a = base + st * sp.stage_bytes, b = a + kTileBytes;
+                        const uint32_t a = base + st * sp.stage_bytes, b = a + 2 * kTileBytes;
                         const int nk = min(4, kMx ? k64 - 4 * s : 4);
                         if (kMx) {
-                            const uint32_t fa = b + sp.b_bytes, fb = fa + 2 * mxf4_dev::kScaleTile;
+                            const uint32_t fa = b + sp.b_bytes, fb = fa + 4 * mxf4_dev::kScaleTile;
                             for (int q = 0; q < (nk + 1) / 2; ++q) {
-                                mxf4_dev::tmem_copy_scales(tsa + 4 * q, mxf4_dev::scale_desc(fa + q * mxf4_dev::kScaleTile));
-                                mxf4_dev::tmem_copy_scales(tsb + 4 * q, mxf4_dev::scale_desc(fb + q * mxf4_dev::kScaleTile));
+                                const uint32_t at = q * mxf4_dev::kScaleTile;
+                                mxf4_dev::tmem_copy_scales(tsa + 4 * q, mxf4_dev::scale_desc(fa + at));
+                                mxf4_dev::tmem_copy_scales(tsa + 8 + 4 * q, mxf4_dev::scale_desc(fa + 2 * mxf4_dev::kScaleTile + at));
+                                mxf4_dev::tmem_copy_scales(tsb + 4 * q, mxf4_dev::scale_desc(fb + at));
                             }
                         }
-                        for (int q = 0; q < nk; ++q) {
-                            const uint64_t da = kFmt == kStreamCols ? umma_desc_sw128(a + q * 2048, 8192, 1024)
-                                                                    : umma_desc_sw128(a + q * 32, 16, 1024);
-                            const uint64_t db = umma_desc_sw128(b + q * 32, 16, 1024);
-                            const uint32_t acc = s > g.s0 || q > 0;
-                            if (kMx)
-                                mxf4_dev::umma_mxf4(d, da, db, q & 1 ? id1 : id0, tsa + 4 * (q >> 1), tsb + 4 * (q >> 1), acc);
-                            else
-                                umma_f16(d, da, db, id0, acc);
-                        }
+#pragma unroll
+                        for (int t = 0; t < 2; ++t)
+                            for (int q = 0; q < nk; ++q) {
+                                const uint32_t at = a + t * kTileBytes;
+                                const uint64_t da = kFmt == kStreamCols ? umma_desc_sw128(at + q * 2048, 8192, 1024)
+                                                                        : umma_desc_sw128(at + q * 32, 16, 1024);
+                                const uint64_t db = umma_desc_sw128(b + q * 32, 16, 1024);
+                                const uint32_t acc = s > g.s0 || q > 0;
+                                if (kMx)
+                                    mxf4_dev::umma_mxf4(d + t * sp.acc_cols, da, db, q & 1 ? id1 : id0, tsa + 8 * t + 4 * (q >> 1),
+                                                        tsb + 4 * (q >> 1), acc);
+                                else
+                                    umma_f16(d + t * sp.acc_cols, da, db, id0, acc);
+                            }
                         umma_commit(empty(st));
                         if (++st == sp.stages) st = 0, par ^= 1u;
                     }
@@ -269,84 +321,85 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
                 mbar_wait(drain, 0, nullptr, mxf4_dev::kDrainNs);
             }
         }
-    } else if (warp >= 6 + sp.loaders) {
-        // (here for the ordering of the choices alone)
     } else if (warp >= 6) {
-        // ------------------------------------- narrow side and MXFP4 scales
-        int n = 0, st = 0;
+        // ---------------------------------------------------- narrow side
+        // Every warp brings some rows of every step and is up to two steps ahead
+        // of the one whose copies it has waited for: a stage's next use needs only
+        // steps that this warp has handed over (3 stages at least).
+        int st = 0, pend = 0, pst = 0;   // steps under way, the stage of the oldest
         uint32_t par = 0;
         bool ok = true;
+        const int w = warp - 6, c = lane & 7;
+        auto hand_over = [&]() {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full_b(pst));
+            if (++pst == sp.stages) pst = 0;
+            --pend;
+        };
+        auto flush = [&]() {
+            cp_async_wait<0>();
+            while (pend) hand_over();
+        };
         for (int ph = 0; ph < 2 && ok; ++ph) {
-            const int64_t hi = phase[ph].start(part + 1);
+            const int64_t lo = phase[ph].start(part), hi = phase[ph].start(part + 1);
             const int width = kMx ? kPieces : ph ? 2 : 1;   // rows of a token
             const uint8_t* rows = ph ? sp.h : sp.x;
             const uint8_t* scales = ph ? sp.hs : sp.xs;
             const int64_t pitch = ph ? sp.hpitch : sp.xpitch, words = ph ? sp.hwords : sp.xwords;
-            bool waited = ph == 0;
-            for (int64_t at = phase[ph].start(part); at < hi && ok;) {
+            const int kt = (ph ? p.down : p.gate).kt;
+            if (ph == 1 && lo < hi) {   // every hidden value is there
+                flush();
+                if (lane == 0) {
+                    const uint64_t t0 = globaltimer_ns();
+                    while (ok && ld_acquire_gpu(&sp.ctl->done) < parts)
+                        ok = !*abort && globaltimer_ns() - t0 <= p.timeout_ns;
+                }
+                ok = __shfl_sync(~0u, ok, 0);
+                if (!ok) break;
+            }
+            for (int64_t at = lo; at < hi && ok;) {
                 const Segment g = segment(ph, at, hi);
                 at += g.s1 - g.s0;
                 const Item im = ch.item[g.item];
                 const int nrows = im.count * width;
-                for (int s = g.s0; s < g.s1; ++s, ++n) {
-                    const int at_st = st;
-                    const uint32_t at_par = par;
-                    if (++st == sp.stages) st = 0, par ^= 1u;
-                    if (n % sp.loaders != warp - 6) continue;
-                    if (!waited) {   // every hidden value is there
-                        if (lane == 0) {
-                            const uint64_t t0 = globaltimer_ns();
-                            while (ok && ld_acquire_gpu(&sp.ctl->done) < parts)
-                                ok = !*abort && globaltimer_ns() - t0 <= p.timeout_ns;
-                        }
-                        ok = __shfl_sync(~0u, ok, 0);
-                        if (!ok) break;
-                        waited = true;
-                    }
-                    ok = mbar_wait(empty(at_st), at_par ^ 1u, abort, p.timeout_ns);
-                    ok = __all_sync(~0u, ok);
+                auto row_of = [&](int r) {
+                    const int j = r / width;
+                    return static_cast<int64_t>(ph ? im.first + j : ch.slot[im.first + j] / p.top) * width + r - j * width;
+                };
+                constexpr int kRows = (16 * (kMx ? kPieces : 2) + 4 * kLoadWarps - 1) / (4 * kLoadWarps);   // a lane's rows
+                const uint8_t* src[kRows];
+                uint32_t dst[kRows];
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) {
+                    const int r = (i * kLoadWarps + w) * 4 + (lane >> 3);
+                    src[i] = r < nrows ? rows + row_of(r) * pitch + c * 16 : nullptr;
+                    dst[i] = r * 128 + ((c ^ (r & 7)) << 4);
+                }
+                const int sr = w * 32 + lane;   // the row whose scales this lane brings
+                const uint8_t* ssrc = kMx && sr < nrows ? scales + row_of(sr) * words * 4 : nullptr;
+                for (int s = g.s0; s < g.s1; ++s) {
+                    ok = __all_sync(~0u, mbar_wait(empty(st), par ^ 1u, abort, p.timeout_ns));
                     if (!ok) break;
-                    const uint32_t b = base + at_st * sp.stage_bytes + kTileBytes;
-                    for (int i = lane; i < nrows * 8; i += 32) {
-                        const int r = i >> 3, c = i & 7, j = r / width, q = r - j * width;
-                        const int64_t row = static_cast<int64_t>(ph ? im.first + j : ch.slot[im.first + j] / p.top) * width + q;
-                        cp_async16(b + r * 128 + ((c ^ (r & 7)) << 4), rows + row * pitch + static_cast<int64_t>(s) * 128 + c * 16, 16u);
-                    }
-                    if (kMx) {
-                        const uint32_t fa = b + sp.b_bytes, fb = fa + 2 * mxf4_dev::kScaleTile;
-                        const Weight& w0 = ph ? p.down : p.gate;
-                        const int halves = min(2, w0.kt - 2 * s);
-                        for (int q = 0; q < halves; ++q) {
-                            if (ph) {
-                                cp_async16(fa + q * mxf4_dev::kScaleTile + lane * 16,
-                                           w0.scales + im.expert * w0.scale_se +
-                                               (static_cast<int64_t>(g.tile) * w0.kt + 2 * s + q) * mxf4_dev::kScaleTile + lane * 16,
-                                           16u);
-                            } else {
-                                // 64 gate rows and 64 up rows: half a scale tile of each
-                                const int64_t off = (static_cast<int64_t>(g.tile >> 1) * w0.kt + 2 * s + q) * mxf4_dev::kScaleTile +
-                                                    lane * 16 + (g.tile & 1) * 8;
-                                cp_async8(fa + q * mxf4_dev::kScaleTile + lane * 16, p.gate.scales + im.expert * p.gate.scale_se + off);
-                                cp_async8(fa + q * mxf4_dev::kScaleTile + lane * 16 + 8, p.up.scales + im.expert * p.up.scale_se + off);
-                            }
-                            for (int r = lane; r < nrows; r += 32) {
-                                const int j = r / width, i = r - j * width;
-                                const int64_t row = static_cast<int64_t>(ph ? im.first + j : ch.slot[im.first + j] / p.top) * width + i;
-                                cp_async4(fb + q * mxf4_dev::kScaleTile + (r & 31) * 16 + (r >> 5) * 4,
-                                          scales + (row * words + 2 * s + q) * 4, 4u);
-                            }
-                        }
+                    const uint32_t b = base + st * sp.stage_bytes + 2 * kTileBytes;
+#pragma unroll
+                    for (int i = 0; i < kRows; ++i)
+                        if (src[i]) cp_async16(b + dst[i], src[i] + static_cast<int64_t>(s) * 128, 16u);
+                    if (kMx && ssrc) {
+                        const uint32_t fb = b + sp.b_bytes + 4 * mxf4_dev::kScaleTile + (sr & 31) * 16 + (sr >> 5) * 4;
+                        cp_async4(fb, ssrc + s * 8, 4u);
+                        if (2 * s + 1 < kt) cp_async4(fb + mxf4_dev::kScaleTile, ssrc + s * 8 + 4, 4u);
                     }
                     cp_async_commit();
-                    cp_async_wait<0>();
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(full_b(at_st));
+                    if (++st == sp.stages) st = 0, par ^= 1u;
+                    if (++pend == 3) {
+                        cp_async_wait<2>();
+                        hand_over();
+                    }
                 }
             }
         }
-        cp_async_commit();
-        cp_async_wait<0>();
+        flush();
         if (!ok && lane == 0) fail();
     } else {
         // --------------------------------------------------------- epilogue
@@ -355,32 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
         bool ok = true;
         const int row = threadIdx.x;   // of the tile
         const uint32_t trow = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-        const int sum_rows = max(sp.cap, p.T);
-        // this thread's value of token j of a finished accumulator
-        auto take = [&](uint32_t d, int j, int ph) {
-            float v = 0.f;
-            if (kMx) {
-                uint32_t r[8];
-                asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                             : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                             : "r"(d + j * kPieces)
-                             : "memory");
-                tmem_wait_ld();
-#pragma unroll
-                for (int q = kPieces - 1; q >= 0; --q) v += __uint_as_float(r[q]);   // the small ones first
-            } else if (ph) {
-                uint32_t r[2];
-                asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(d + 2 * j) : "memory");
-                tmem_wait_ld();
-                v = __uint_as_float(r[1]) + __uint_as_float(r[0]);
-            } else {
-                uint32_t r;
-                asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(d + j) : "memory");
-                tmem_wait_ld();
-                v = __uint_as_float(r);
-            }
-            return v;
-        };
+        const int64_t slot_floats = static_cast<int64_t>(max(sp.cap, p.T)) * 256;
         // the four warps go on or leave together
         auto all_of = [&](bool mine) {
             uint32_t r;
@@ -402,9 +430,27 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
             named_bar_sync(1, 128);
             return last_flag != 0;
         };
-        auto slot_of = [&](const Parts& w, int v, int64_t first) {   // a part that began before the tile's end: slot 0
-            return sp.sums + (static_cast<int64_t>(v) * 2 + (w.start(v) > first ? 0 : 1)) * sum_rows * 128;
+        auto slot_of = [&](const Parts& w, int v, int64_t first) {
+            return sp.sums + (static_cast<int64_t>(v) * 2 + (w.start(v) > first ? 0 : 1)) * slot_floats;
         };
+        // hidden value (tile's row, token j of the piece) from its two sums
+        auto hidden = [&](const Segment& g, const Item& im, int j, float gate, float up) {
+            const int f = g.tile * 128 + row;
+            // (past F: zeros, whatever the tokens hold)
+            const float hv = f < p.F ? act_f32(p.act, gate) * up : 0.f;
+            const int64_t r = im.first + j;
+            if (kMx) {
+                split_block(hv, lane, sp.h + r * kPieces * sp.hpitch + ((f - lane) >> 1), sp.hpitch,
+                            sp.hs + r * kPieces * sp.hwords * 4 + ((f - lane) >> 5), sp.hwords * 4);
+            } else if (f < p.fp) {
+                const __half hh = __float2half_rn(hv);
+                const float back = __half2float(hh);
+                __half* dst = reinterpret_cast<__half*>(sp.h + r * 2 * sp.hpitch) + f;
+                dst[0] = hh;
+                dst[sp.hpitch >> 1] = isfinite(back) ? __float2half_rn(hv - back) : __ushort_as_half(0);
+            }
+        };
+        constexpr int kUpWidth = kMx ? kPieces : 1, kDownWidth = kMx ? kPieces : 2;
         for (int ph = 0; ph < 2 && ok; ++ph) {
             const Parts& w = phase[ph];
             const int64_t lo = w.start(part), hi = w.start(part + 1);
@@ -415,78 +461,88 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
                 ok = all_of(mbar_wait(tfull(buf), bpar, abort, p.timeout_ns));
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t d = trow + buf * sp.acc_cols;
+                const uint32_t d = trow + 2 * buf * sp.acc_cols;
+                auto release = [&]() {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(tempty(buf));
+                    if (++buf == 2) buf = 0, bpar ^= 1u;
+                };
                 if (ph == 0) {
                     const int64_t first = at - g.s0;
                     const bool whole = g.s0 == 0 && g.s1 == d_steps;
                     at += g.s1 - g.s0;
-                    float* to = whole ? ex : slot_of(w, part, first);
-                    for (int j = 0; j < im.count; ++j) to[j * 128 + row] = take(d, j, 0);
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(tempty(buf));
-                    if (++buf == 2) buf = 0, bpar ^= 1u;
-                    if (!whole) {
-                        const int v0 = w.of(first), v1 = w.of(first + d_steps - 1);
-                        if (!last_of(&sp.ctl->up[v0], v1 - v0 + 1)) continue;
-                        for (int j = 0; j < im.count; ++j) {
-                            float v = 0.f;
-                            for (int q = v0; q <= v1; ++q) v += ld_cg_f32(slot_of(w, q, first) + j * 128 + row);
-                            ex[j * 128 + row] = v;
+                    float* to = slot_of(w, part, first) + row;
+                    for (int j0 = 0; j0 < im.count; j0 += 4) {
+                        float gate[4], up[4];
+                        take4<kUpWidth>(d + j0 * kUpWidth, gate);
+                        take4<kUpWidth>(d + sp.acc_cols + j0 * kUpWidth, up);
+                        if (j0 + 4 >= im.count) release();
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if (j0 + j >= im.count) break;
+                            if (whole)
+                                hidden(g, im, j0 + j, gate[j], up[j]);
+                            else
+                                to[(j0 + j) * 256] = gate[j], to[(j0 + j) * 256 + 128] = up[j];
                         }
                     }
-                    named_bar_sync(1, 128);
-                    // warps 0, 2 take hidden values 0-31 of the tile, 1, 3 the rest; every other token each
-                    const int f = g.tile * 64 + (warp & 1) * 32 + lane;
-                    for (int j = warp >> 1; j < im.count; j += 2) {
-                        const float* e = ex + j * 128 + (warp & 1) * 32 + lane;
-                        // (past F: zeros, whatever the tokens hold)
-                        const float hv = f < p.F ? act_f32(p.act, e[0]) * e[64] : 0.f;
-                        const int64_t r = im.first + j;
-                        if (kMx) {
-                            split_block(hv, lane, sp.h + r * kPieces * sp.hpitch + ((f - lane) >> 1), sp.hpitch,
-                                        sp.hs + r * kPieces * sp.hwords * 4 + ((f - lane) >> 5), sp.hwords * 4);
-                        } else {
-                            const __half hh = __float2half_rn(hv);
-                            const float back = __half2float(hh);
-                            __half* dst = reinterpret_cast<__half*>(sp.h + r * 2 * sp.hpitch) + f;
-                            dst[0] = hh;
-                            dst[sp.hpitch >> 1] = isfinite(back) ? __float2half_rn(hv - back) : __ushort_as_half(0);
+                    if (whole) continue;
+                    const int v0 = w.of(first), v1 = w.of(first + d_steps - 1);
+                    if (!last_of(&sp.ctl->up[v0], v1 - v0 + 1)) continue;
+                    for (int j0 = 0; j0 < im.count; j0 += 4) {
+                        float gate[4] = {}, up[4] = {};
+                        for (int q = v0; q <= v1; ++q) {
+                            const float* from = slot_of(w, q, first) + row;
+                            float a[4], b[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                a[j] = j0 + j < im.count ? ld_cg_f32(from + (j0 + j) * 256) : 0.f;
+                                b[j] = j0 + j < im.count ? ld_cg_f32(from + (j0 + j) * 256 + 128) : 0.f;
+                            }
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) gate[j] += a[j], up[j] += b[j];
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if (j0 + j >= im.count) break;
+                            hidden(g, im, j0 + j, gate[j], up[j]);
                         }
                     }
-                    named_bar_sync(1, 128);
                 } else {
                     const int64_t per = static_cast<int64_t>(items) * f_steps, first = g.tile * per;
                     at += g.s1 - g.s0;
                     if (!begun)
-                        for (int t = 0; t < p.T; ++t) ysum[t * 128 + row] = 0.f;
+                        for (int t = 0; t < p.T; ++t) ysum[t * 256 + row] = 0.f, ysum[t * 256 + 128 + row] = 0.f;
                     begun = true;
-                    for (int j = 0; j < im.count; ++j) {
-                        float* y = ysum + ch.slot[im.first + j] / p.top * 128 + row;
-                        *y = fmaf(ch.weight[im.first + j], take(d, j, 1), *y);
+                    for (int j0 = 0; j0 < im.count; j0 += 4) {
+                        float a[4], b[4];
+                        take4<kDownWidth>(d + j0 * kDownWidth, a);
+                        take4<kDownWidth>(d + sp.acc_cols + j0 * kDownWidth, b);
+                        if (j0 + 4 >= im.count) release();
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if (j0 + j >= im.count) break;
+                            const float wt = ch.weight[im.first + j0 + j];
+                            float* y = ysum + ch.slot[im.first + j0 + j] / p.top * 256 + row;
+                            y[0] = fmaf(wt, a[j], y[0]);
+                            y[128] = fmaf(wt, b[j], y[128]);
+                        }
                     }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(tempty(buf));
-                    if (++buf == 2) buf = 0, bpar ^= 1u;
                     if (at < hi && at < first + per) continue;   // more of this tile
                     begun = false;
-                    const int col = g.tile * 128 + row;
+                    const int col = g.tile * 256 + row;
                     if (lo <= first && at == first + per) {
-                        if (col < p.D)
-                            for (int t = 0; t < p.T; ++t) p.y[t * p.ldy + col] = __float2half_rn(ysum[t * 128 + row]);
+                        for (int t = 0; t < p.T; ++t) {
+                            if (col < p.D) p.y[t * p.ldy + col] = __float2half_rn(ysum[t * 256 + row]);
+                            if (col + 128 < p.D) p.y[t * p.ldy + col + 128] = __float2half_rn(ysum[t * 256 + 128 + row]);
+                        }
                         continue;
                     }
-                    float* to = slot_of(w, part, first);
-                    for (int t = 0; t < p.T; ++t) to[t * 128 + row] = ysum[t * 128 + row];
+                    float* to = slot_of(w, part, first) + row;
+                    for (int t = 0; t < p.T; ++t) to[t * 256] = ysum[t * 256 + row], to[t * 256 + 128] = ysum[t * 256 + 128 + row];
                     const int v0 = w.of(first), v1 = w.of(first + per - 1);
-                    if (!last_of(&sp.ctl->down[v0], v1 - v0 + 1)) continue;
-                    if (col < p.D)
-                        for (int t = 0; t < p.T; ++t) {
-                            float v = 0.f;
-                            for (int q = v0; q <= v1; ++q) v += ld_cg_f32(slot_of(w, q, first) + t * 128 + row);
-                            p.y[t * p.ldy + col] = __float2half_rn(v);
-                        }
+                    if (last_of(&sp.ctl->down[v0], v1 - v0 + 1) && threadIdx.x == 0) fix[fixes++] = make_int3(g.tile, v0, v1);
                 }
             }
             if (ph == 0 && ok) {
@@ -500,6 +556,31 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
     __syncthreads();
     tc_fence_after();
     if (warp == 5) tmem_dealloc(tmem, sp.tmem_cols);
+    // Shared tiles of y whose last sums this part stored: all threads add them,
+    // 8 parts' loads under way at once.
+    for (int i = 0; i < fixes; ++i) {
+        const int tile = fix[i].x, v0 = fix[i].y, v1 = fix[i].z;
+        const Parts& w = phase[1];
+        const int64_t first = static_cast<int64_t>(tile) * items * f_steps;
+        const int64_t slot_floats = static_cast<int64_t>(max(sp.cap, p.T)) * 256;
+        for (int k = threadIdx.x; k < p.T * 256; k += kThreads) {
+            const int t = k >> 8, col = tile * 256 + (k & 255);
+            if (col >= p.D) continue;
+            float v = 0.f;
+            for (int q0 = v0; q0 <= v1; q0 += 8) {
+                float a[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const int u = min(q0 + q, v1);
+                    a[q] = ld_cg_f32(sp.sums + (static_cast<int64_t>(u) * 2 + (w.start(u) > first ? 0 : 1)) * slot_floats + k);
+                }
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    if (q0 + q <= v1) v += a[q];
+            }
+            p.y[t * p.ldy + col] = __float2half_rn(v);
+        }
+    }
 }
 
 }  // namespace moe_dev

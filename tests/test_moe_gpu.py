@@ -5,6 +5,9 @@ most 2^-20 of the sum of their magnitudes (any order, a few roundings at the
 largest partial sum each), a hidden value by that through the activation (slope
 at most 1.13) and the other factor plus its 2^-21 as two fp16 halves, a routing
 weight by twice its logit's error plus 2^-20, and y by one rounding to fp16.
+With MXFP4 weights the tokens and the hidden values are held as 6 MXFP4 columns:
+each leaves at most 1/5 of the largest remainder of its block of 32, so a value
+is off by at most 5^-6 of its block's largest magnitude.
 """
 import pytest
 import torch
@@ -54,8 +57,16 @@ def held(w):
     return g.mxf4_quantize(w.to(DEV), axis=-2), vals
 
 
-def check(x, router, gate, up, down, top, act, renorm, got):
-    """x .. down on the CPU (weights as the values they stand for)."""
+def held_error(v, columns):
+    """What each value of a narrow side held in MXFP4 columns may be off by."""
+    if not columns:
+        return torch.zeros_like(v)
+    pad = torch.nn.functional.pad(v.abs(), (0, -v.shape[-1] % 32)).view(-1, 32)
+    return (5.0 ** -6 * pad.max(dim=1, keepdim=True).values.expand(-1, 32)).reshape(-1)[:v.shape[-1]]
+
+
+def check(x, router, gate, up, down, top, act, renorm, got, columns=False):
+    """x .. down on the CPU (weights as the values they stand for); `columns`: MXFP4 weights."""
     y, w, ids = (t.cpu() for t in got)
     T, E = x.shape[0], router.shape[1]
     x, router, gate, up, down = (t.double() for t in (x, router, gate, up, down))
@@ -79,10 +90,12 @@ def check(x, router, gate, up, down, top, act, renorm, got):
         for j in range(top):
             e = int(ids[t, j])
             a, u = x[t] @ gate[e], x[t] @ up[e]
-            amag, umag = x[t].abs() @ gate[e].abs(), x[t].abs() @ up[e].abs()
+            dx = held_error(x[t], columns)
+            da = 2.0 ** -20 * (x[t].abs() @ gate[e].abs()) + dx @ gate[e].abs()
+            du = 2.0 ** -20 * (x[t].abs() @ up[e].abs()) + dx @ up[e].abs()
             f = ACT64[act](a)
             h = f * u
-            dh = 2.0 ** -20 * (1.13 * amag * u.abs() + umag * f.abs()) + 2.0 ** -20 * h.abs() + 2.0 ** -24
+            dh = 1.13 * da * (u.abs() + du) + du * f.abs() + 2.0 ** -20 * h.abs() + 2.0 ** -24 + held_error(h, columns)
             o, omag = h @ down[e], h.abs() @ down[e].abs()
             ref += ref_w[t, j] * o
             tol += ref_w[t, j] * (dh @ down[e].abs() + 2.0 ** -20 * omag) + tol_w[t, j] * o.abs()
@@ -107,7 +120,7 @@ def test_layer(T, D, F, E, top, layout):
     else:
         dev, vals = [stored(w, layout) for w in (gate, up, down)], (gate, up, down)
     got = g.moe_few(x.to(DEV), router.to(DEV), *dev, top, act=act, renormalize=renorm)
-    check(x, router, *vals, top, act, renorm, got)
+    check(x, router, *vals, top, act, renorm, got, columns=layout == "mxf4")
     again = g.moe_few(x.to(DEV), router.to(DEV), *dev, top, act=act, renormalize=renorm)
     assert all(torch.equal(a, b) for a, b in zip(got, again))   # no order of arrival in the result
     assert g.gemm_f16_device_status() == 0
