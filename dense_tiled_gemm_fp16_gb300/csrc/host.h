@@ -44,16 +44,14 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 int64_t option(int o);
 uint64_t timeout_ns();
 
-// Launch `kernel` on `stream` with the cluster size (1: none; kCooperative: all
-// blocks resident at once) and, unless GEMM_F16_OPT_PDL is 1, as a programmatic
-// dependent of the kernel before it.
-constexpr int kCooperative = -1;
+// Launch `kernel` on `stream` with the cluster size (1: none) and, unless
+// GEMM_F16_OPT_PDL is 1, as a programmatic dependent of the kernel before it.
 template <typename... Params, typename... Args>
 gemm_f16_status launch_kernel(void (*kernel)(Params...), dim3 grid, unsigned block, size_t smem, int cluster,
                               cudaStream_t stream, const Args&... args)
 {
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[3];
+    cudaLaunchAttribute attr[2];
     cfg.gridDim = grid;
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
@@ -64,11 +62,6 @@ gemm_f16_status launch_kernel(void (*kernel)(Params...), dim3 grid, unsigned blo
         attr[n].val.clusterDim.x = static_cast<unsigned>(cluster);
         attr[n].val.clusterDim.y = 1;
         attr[n].val.clusterDim.z = 1;
-        ++n;
-    }
-    if (cluster == kCooperative) {
-        attr[n].id = cudaLaunchAttributeCooperative;
-        attr[n].val.cooperative = 1;
         ++n;
     }
     if (option(GEMM_F16_OPT_PDL) != 1) {

@@ -108,7 +108,7 @@ moe_dev::Weight weight_of(const moe_f16_weight& w, int64_t E, int64_t in, int64_
 
 constexpr int kMaxDevices = 64;
 constexpr int kMaxSmem = 232448;     // 227 KiB a block
-constexpr int kStaticSmem = 8192;    // more than the stream kernel's own
+constexpr int kStaticSmem = 9216;    // more than the stream kernel's own
 
 // More dynamic shared memory than the default, once a device and kernel.
 bool allow_smem(const void* kernel, int slot, int bytes)
@@ -130,15 +130,23 @@ bool allow_smem(const void* kernel, int slot, int bytes)
     return true;
 }
 
-template <int kLayout>
+template <int kLayout, int kPer>
 gemm_f16_status launch_route(const moe_dev::Params& p, cudaStream_t stream)
 {
     const int chunks = p.dp >> 5, tiles = (p.E + 31) >> 5;
     const int smem = ((chunks / moe_dev::kRouteCluster + 1) * 32 + 8) * 8 * 2 + moe_dev::kWarps * 32 * 8 * 4 + 8 * tiles * 32 * 4;
-    if (!allow_smem(reinterpret_cast<const void*>(moe_dev::moe_route<kLayout>), kLayout, smem)) return GEMM_F16_ERR_LAUNCH;
+    const auto kernel = moe_dev::moe_route<kLayout, kPer>;
+    if (!allow_smem(reinterpret_cast<const void*>(kernel), 2 * kLayout + (kPer > 2), smem)) return GEMM_F16_ERR_LAUNCH;
     const unsigned groups = static_cast<unsigned>((p.T + 7) / 8);
-    return launch_kernel(moe_dev::moe_route<kLayout>, dim3(groups * moe_dev::kRouteCluster), moe_dev::kThreads, smem,
-                         moe_dev::kRouteCluster, stream, p);
+    return launch_kernel(kernel, dim3(groups * moe_dev::kRouteCluster), moe_dev::kThreads, smem, moe_dev::kRouteCluster,
+                         stream, p);
+}
+
+// (most layers have few experts: the choosing warp's code is then short)
+template <int kLayout>
+gemm_f16_status launch_route(const moe_dev::Params& p, cudaStream_t stream)
+{
+    return p.E <= 64 ? launch_route<kLayout, 2>(p, stream) : launch_route<kLayout, moe_dev::kMaxExperts / 32>(p, stream);
 }
 
 template <int kFmt, int kGroups, int kRing>
@@ -156,7 +164,7 @@ gemm_f16_status launch_experts(moe_dev::Params& p, int sms, cudaStream_t stream)
     const int ring = moe_dev::kWarps * kRing * moe_dev::Stage<kFmt>::kBytes;
     const int smem = ring + std::max(2 * moe_dev::kWarps * kGroups * 32 * 16, moe_dev::kWarps * p.T * kOut * 4);
     const auto kernel = moe_dev::moe_experts<kFmt, kGroups, kRing>;
-    if (!allow_smem(reinterpret_cast<const void*>(kernel), 3 + 4 * kFmt + (kGroups > 1) + 2 * (kRing == 2), smem))
+    if (!allow_smem(reinterpret_cast<const void*>(kernel), 8 + (kGroups > 1), smem))
         return GEMM_F16_ERR_LAUNCH;
     return launch_kernel(kernel, dim3(static_cast<unsigned>(sms)), moe_dev::kThreads, smem, 1, stream, p);
 }
@@ -231,9 +239,9 @@ gemm_f16_status launch_stream(const moe_dev::Params& p, const Layout& l, uint8_t
     sp.tmem_cols = need <= 64 ? 64 : need <= 128 ? 128 : need <= 256 ? 256 : 512;
     const int smem = sp.stages * sp.stage_bytes + tail + 1024;
     const auto kernel = moe_dev::moe_stream<kFmt>;
-    if (!allow_smem(reinterpret_cast<const void*>(kernel), 20 + kFmt, kMaxSmem - kStaticSmem)) return GEMM_F16_ERR_LAUNCH;
-    return launch_kernel(kernel, dim3(static_cast<unsigned>(std::min(sms, moe_dev::kMaxParts))), moe_dev::kThreads, smem,
-                         kCooperative, stream, sp);
+    if (!allow_smem(reinterpret_cast<const void*>(kernel), 12 + kFmt, kMaxSmem - kStaticSmem)) return GEMM_F16_ERR_LAUNCH;
+    return launch_kernel(kernel, dim3(static_cast<unsigned>(std::min(sms, moe_dev::kMaxParts))), moe_dev::kThreads, smem, 1,
+                         stream, sp);
 }
 
 }  // namespace

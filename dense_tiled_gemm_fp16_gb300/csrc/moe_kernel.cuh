@@ -159,43 +159,69 @@ __device__ __forceinline__ int expert_row(int mt, int h, int g)
     return kLayout == kOutContiguous ? 8 * (g >> 1) + 2 * (2 * mt + h) + (g & 1) : 16 * mt + 8 * h + g;
 }
 
-// One block of 32 values, one a lane, as kPieces MXFP4 columns: the codes of
-// column q at codes + q * pitch (16 bytes), its scale at scales + q * spitch.
-// Unlike a quantised operand, whose largest magnitudes saturate (6 to 8 times
-// 2^s), a column's scale is a step larger there, so that no remainder is above
-// half a step of the grid, 1/5 of the largest magnitude.
-__device__ __forceinline__ void split_block(float v, int lane, uint8_t* codes, int64_t pitch, uint8_t* scales,
-                                            int64_t spitch)
+// Four blocks of 32 values, a value of each a lane, as kPieces MXFP4 columns: the
+// codes of column q of block j at codes[j] + q * pitch (16 bytes), its scale at
+// scales[j] + q * spitch; blocks from `count` on are not written.  Unlike a
+// quantised operand, whose largest magnitudes saturate (6 to 8 times 2^s), a
+// column's scale is a step larger there, so that no remainder is above half a
+// step of the grid, 1/5 of the largest magnitude.  A column waits for the one
+// before it (a maximum over the lanes, two conversions); four blocks at once
+// hide that, 17 -> 5 us for 64 tokens of 7168 values.
+__device__ __forceinline__ void split_blocks(float* v, int count, int lane, uint8_t* const* codes, int64_t pitch,
+                                             uint8_t* const* scales, int64_t spitch)
 {
-#pragma unroll 2
+#pragma unroll 1
     for (int q = 0; q < kPieces; ++q) {
-        const uint32_t top = __reduce_max_sync(~0u, __float_as_uint(v) & 0x7FFFFFFFu);
-        uint32_t code = mxf4_dev::scale_code<float>(top);
-        uint32_t e = 0;
-        if (code != 255u) {
-            code += (top & 0x7FFFFFu) > 0x400000u && code > 0u;   // above 6 * 2^s: mantissa above 1.5
-            const float t = v * mxf4_dev::pow2f(127 - static_cast<int>(code));
-            uint32_t back;
-            asm("{\n\t.reg .b8 b;\n\t"
-                "cvt.rn.satfinite.e2m1x2.f32 b, %3, %2;\n\t"
-                "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-                "mov.b32 %0, {b, b, b, b};\n\t}"
-                : "=r"(e), "=r"(back)
-                : "f"(t), "f"(0.f));
-            e &= 15u;
-            v -= mxf4_dev::scale_value(code) * __half2float(__ushort_as_half(static_cast<unsigned short>(back)));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t top = __reduce_max_sync(~0u, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+            uint32_t code = mxf4_dev::scale_code<float>(top);
+            uint32_t e = 0;
+            if (code != 255u) {
+                code += (top & 0x7FFFFFu) > 0x400000u && code > 0u;   // above 6 * 2^s: mantissa above 1.5
+                const float t = v[j] * mxf4_dev::pow2f(127 - static_cast<int>(code));
+                uint32_t back;
+                asm("{\n\t.reg .b8 b;\n\t"
+                    "cvt.rn.satfinite.e2m1x2.f32 b, %3, %2;\n\t"
+                    "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+                    "mov.b32 %0, {b, b, b, b};\n\t}"
+                    : "=r"(e), "=r"(back)
+                    : "f"(t), "f"(0.f));
+                e &= 15u;
+                v[j] -= mxf4_dev::scale_value(code) * __half2float(__ushort_as_half(static_cast<unsigned short>(back)));
+            }
+            e |= __shfl_down_sync(~0u, e, 1) << 4;
+            if (j < count) {
+                if ((lane & 1) == 0) codes[j][q * pitch + (lane >> 1)] = static_cast<uint8_t>(e);
+                if (lane == 0) scales[j][q * spitch] = static_cast<uint8_t>(code);
+            }
         }
-        e |= __shfl_down_sync(~0u, e, 1) << 4;
-        if ((lane & 1) == 0) codes[q * pitch + (lane >> 1)] = static_cast<uint8_t>(e);
-        if (lane == 0) scales[q * spitch] = static_cast<uint8_t>(code);
     }
+}
+
+// Eight router elements from `src` on, `step` apart, `n` of them in range.
+template <bool kVector>
+__device__ __forceinline__ uint4 load_eight(const __half* src, int64_t step, int n)
+{
+    if (kVector && n >= 8) return ld_nc_v4(src);
+    uint32_t u[4] = {};
+#pragma unroll 1
+    for (int i = 0; i < min(n, 8); ++i) {
+        const uint32_t v = static_cast<uint32_t>(ld_nc_u16(src + i * step)) << (16 * (i & 1));
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j == i >> 1) u[j] |= v;
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
 // A cluster of 8 CTAs routes 8 tokens: CTA r sums the r-th part of D for all
 // experts and tokens, then takes token r: adds the 8 parts over distributed
-// shared memory and picks its experts.  Bound by latency: the router is read
-// once a cluster, a few 16-byte loads deep a thread.
-template <int kLayout>
+// shared memory and picks its experts.  Bound by latency, not by bytes: the
+// tokens' and the first router loads are under way together, and the code is
+// kept short (every instruction is fetched once, cold).  kPer: experts a lane
+// of the choosing warp looks at.
+template <int kLayout, int kPer>
 __global__ void __launch_bounds__(kThreads) moe_route(const __grid_constant__ Params p)
 {
     extern __shared__ __align__(16) uint8_t smem[];
@@ -206,112 +232,85 @@ __global__ void __launch_bounds__(kThreads) moe_route(const __grid_constant__ Pa
     const int chunks = p.dp >> 5;
     const int c_lo = chunks * rank / kRouteCluster, c_hi = chunks * (rank + 1) / kRouteCluster;
     const int k_lo = c_lo * 32, width = (c_hi - c_lo) * 32;
-    const int tiles = (p.E + 31) >> 5;
+    const int tiles = (p.E + 31) >> 5, ep = tiles * 32;
     // shared: this part's tokens [8][width + 8] fp16, warp sums [16][32][8], logits [8][E rounded up]
     const int xpitch = width + 8;
     __half* xs = reinterpret_cast<__half*>(smem);
     float* red = reinterpret_cast<float*>(smem + ((chunks / kRouteCluster + 1) * 32 + 8) * 8 * 2);
     float* part = red + kWarps * 32 * 8;
-    const int ep = tiles * 32;
 
     griddep_wait();
     griddep_launch_dependents();
     if (blockIdx.x == 0)
         for (int i = threadIdx.x; i < p.nzero; i += kThreads) p.zero[i] = 0;
 
-    for (int i = threadIdx.x; i < 8 * width; i += kThreads) {
-        const int t = i / width, k = i - t * width;
-        __half v = __ushort_as_half(0);
-        if (t < nt) {
-            if (k_lo + k < p.D) v = ld_nc_half(p.x + (t0 + t) * p.sxt + (k_lo + k) * p.sxi);
-            p.xp[static_cast<int64_t>(t0 + t) * p.dp + k_lo + k] = v;
+    // tokens: 64 threads each, 8 values a thread
+    {
+        const int t = threadIdx.x >> 6;
+        const bool vec = p.sxi == 1 && ((reinterpret_cast<uintptr_t>(p.x) | (2 * p.sxt)) & 15) == 0;
+        for (int k = (threadIdx.x & 63) * 8; k < width; k += 512) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (t < nt) {
+                const __half* src = p.x + (t0 + t) * p.sxt + (k_lo + k) * p.sxi;
+                v = vec ? load_eight<true>(src, 1, p.D - k_lo - k) : load_eight<false>(src, p.sxi, p.D - k_lo - k);
+                *reinterpret_cast<uint4*>(p.xp + static_cast<int64_t>(t0 + t) * p.dp + k_lo + k) = v;
+            }
+            *reinterpret_cast<uint4*>(xs + t * xpitch + k) = v;
         }
-        xs[t * xpitch + k] = v;
     }
-    __syncthreads();
 
     const int wt = min(tiles, kWarps), share = kWarps / wt;   // tiles a pass, warps a tile
     for (int pass = 0; pass * wt < tiles; ++pass) {
-        const int tl = warp % wt, mine = warp / wt;
-        const int tile = pass * wt + tl;
+        const int tile = pass * wt + warp % wt, mine = warp / wt, e0 = tile * 32;
+        const bool busy = mine < share && tile < tiles;
         float acc[2][4] = {};
-        if (mine < share && tile < tiles) {
-            const int e0 = tile * 32;
-#pragma unroll 4
-            for (int ch = mine; ch < c_hi - c_lo; ch += share) {
-                const int k0 = k_lo + ch * 32;
-                uint4 w[4];
-                if (kLayout == kInContiguous) {
+        constexpr int kBatch = 4;   // chunks of 32 values whose loads are under way together
+        for (int ch0 = mine; ch0 - mine < c_hi - c_lo; ch0 += kBatch * share) {
+            uint4 w[kBatch][4];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int e = e0 + 8 * q + g, k = k0 + 8 * c;
-                        w[q] = make_uint4(0, 0, 0, 0);
-                        if (e < p.E) {
-                            const __half* src = p.router + e * p.sre + k;
-                            if (k + 8 <= p.D)
-                                w[q] = ld_nc_v4(src);
-                            else {
-                                uint32_t u[4] = {};
-                                for (int i = 0; i < 8; ++i)
-                                    if (k + i < p.D) u[i >> 1] |= static_cast<uint32_t>(ld_nc_u16(src + i)) << (16 * (i & 1));
-                                w[q] = make_uint4(u[0], u[1], u[2], u[3]);
-                            }
-                        }
-                    }
-                } else if (kLayout == kOutContiguous) {
-                    // rows k of the reordered block: quad g's row is value 8 (g / 2) + g % 2 + 2q
+            for (int u = 0; u < kBatch; ++u) {
+                const int ch = ch0 + u * share, k0 = k_lo + ch * 32;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < 4; ++q) {
+                    w[u][q] = make_uint4(0, 0, 0, 0);
+                    if (!busy || ch >= c_hi - c_lo) continue;
+                    if (kLayout == kOutContiguous) {
+                        // rows k of the reordered block: quad g's row is value 8 (g / 2) + g % 2 + 2q
                         const int k = k0 + 8 * (g >> 1) + (g & 1) + 2 * q, e = e0 + 8 * c;
-                        w[q] = make_uint4(0, 0, 0, 0);
-                        if (k < p.D) {
-                            const __half* src = p.router + k * p.sri + e;
-                            if (e + 8 <= p.E)
-                                w[q] = ld_nc_v4(src);
-                            else {
-                                uint32_t u[4] = {};
-                                for (int i = 0; i < 8; ++i)
-                                    if (e + i < p.E) u[i >> 1] |= static_cast<uint32_t>(ld_nc_u16(src + i)) << (16 * (i & 1));
-                                w[q] = make_uint4(u[0], u[1], u[2], u[3]);
-                            }
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int e = e0 + 8 * q + g;
-                        uint32_t u[4] = {};
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int k = k0 + 8 * c + i;
-                            if (e < p.E && k < p.D)
-                                u[i >> 1] |= static_cast<uint32_t>(ld_nc_u16(p.router + k * p.sri + e * p.sre)) << (16 * (i & 1));
-                        }
-                        w[q] = make_uint4(u[0], u[1], u[2], u[3]);
+                        if (k < p.D) w[u][q] = load_eight<true>(p.router + k * p.sri + e, 1, p.E - e);
+                    } else {
+                        const int e = e0 + 8 * q + g, k = k0 + 8 * c;
+                        if (e < p.E)
+                            w[u][q] = load_eight<kLayout == kInContiguous>(p.router + k * p.sri + e * p.sre, p.sri, p.D - k);
                     }
                 }
-                const uint4 b = ld_smem_v4(smem_u32(xs + g * xpitch + ch * 32 + 8 * c));
-                if (kLayout == kOutContiguous) {
-                    // w[q] word j: 8x8 of value rows (q) and expert pairs j; its transpose is
-                    // the operand piece of expert rows j, K piece q
+            }
+            if (pass == 0 && ch0 == mine) __syncthreads();   // the tokens are there
+            if (!busy) continue;
 #pragma unroll
-                    for (int mt = 0; mt < 2; ++mt) {
+            for (int u = 0; u < kBatch; ++u) {
+                const int ch = ch0 + u * share;
+                if (ch >= c_hi - c_lo) break;
+                const uint4 b = ld_smem_v4(smem_u32(xs + g * xpitch + ch * 32 + 8 * c));
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt) {
+                    if (kLayout == kOutContiguous) {
+                        // w[q] word j: 8x8 of value rows (q) and expert pairs j; its transpose is
+                        // the operand piece of expert rows j, K piece q
                         uint32_t a[2][4];
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {
                                 const int j = 2 * mt + h;
-                                a[h][q] = transpose8x8(j == 0 ? w[q].x : j == 1 ? w[q].y : j == 2 ? w[q].z : w[q].w);
+                                a[h][q] = transpose8x8(j == 0 ? w[u][q].x : j == 1 ? w[u][q].y : j == 2 ? w[u][q].z : w[u][q].w);
                             }
                         mma16816(acc[mt], a[0][0], a[1][0], a[0][1], a[1][1], b.x, b.y);
                         mma16816(acc[mt], a[0][2], a[1][2], a[0][3], a[1][3], b.z, b.w);
-                    }
-                } else {
-#pragma unroll
-                    for (int mt = 0; mt < 2; ++mt) {
-                        mma16816(acc[mt], w[2 * mt].x, w[2 * mt + 1].x, w[2 * mt].y, w[2 * mt + 1].y, b.x, b.y);
-                        mma16816(acc[mt], w[2 * mt].z, w[2 * mt + 1].z, w[2 * mt].w, w[2 * mt + 1].w, b.z, b.w);
+                    } else {
+                        const uint4 lo = w[u][2 * mt], hi = w[u][2 * mt + 1];
+                        mma16816(acc[mt], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
+                        mma16816(acc[mt], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
                     }
                 }
             }
@@ -330,45 +329,41 @@ __global__ void __launch_bounds__(kThreads) moe_route(const __grid_constant__ Pa
         }
         __syncthreads();
     }
-    if (p.xq)
-        for (int i = warp; i < nt * (width >> 5); i += kWarps) {
-            const int t = i / (width >> 5), blk = i - t * (width >> 5);
-            const int64_t row = static_cast<int64_t>(t0 + t) * kPieces, at = (k_lo >> 5) + blk;
-            split_block(__half2float(xs[t * xpitch + blk * 32 + lane]), lane, p.xq + row * p.xq_pitch + at * 16, p.xq_pitch,
-                        p.xs + row * p.xs_pitch + at, p.xs_pitch);
-        }
     cluster_sync_all();
+    // this CTA's token: the 8 parts of its logits
+    if (rank < nt)
+        for (int i = threadIdx.x; i < kRouteCluster * ep; i += kThreads)
+            red[i] = ld_cluster_f32(mapa_shared(smem_u32(part + rank * ep + i % ep), static_cast<uint32_t>(i / ep)));
+    __syncthreads();
     if (rank < nt && warp == 0) {
-        float l[kMaxExperts / 32];
-        uint32_t key[kMaxExperts / 32];
+        float l[kPer];
+        uint32_t key[kPer];
 #pragma unroll
-        for (int i = 0; i < kMaxExperts / 32; ++i) {
+        for (int i = 0; i < kPer; ++i) {
             const int e = i * 32 + lane;
             l[i] = 0.f;
             key[i] = 0u;
-            if (i * 32 < ep) {
-                float v = 0.f;
-                const uint32_t at = smem_u32(part + rank * ep + e);
-#pragma unroll
-                for (uint32_t r = 0; r < kRouteCluster; ++r) v += ld_cluster_f32(mapa_shared(at, r));
-                if (e < p.E) l[i] = v, key[i] = order_key(v);
+            if (e < p.E) {
+                for (int r = 0; r < kRouteCluster; ++r) l[i] += red[r * ep + e];
+                key[i] = order_key(l[i]);
             }
         }
-        float best = 0.f, total = 0.f, chosen = 0.f;
+        float best = 0.f, chosen = 0.f;
         int id = 0;   // lane j keeps the j-th choice
+#pragma unroll 1
         for (int j = 0; j < p.top; ++j) {
             uint32_t top = 0u;
 #pragma unroll
-            for (int i = 0; i < kMaxExperts / 32; ++i) top = max(top, key[i]);
+            for (int i = 0; i < kPer; ++i) top = max(top, key[i]);
             top = __reduce_max_sync(~0u, top);
             uint32_t at = 0xFFFFFFFFu;
 #pragma unroll
-            for (int i = kMaxExperts / 32 - 1; i >= 0; --i)
+            for (int i = kPer - 1; i >= 0; --i)
                 if (key[i] == top && i * 32 + lane < p.E) at = i * 32 + lane;
             at = __reduce_min_sync(~0u, at);
             float v = 0.f;
 #pragma unroll
-            for (int i = 0; i < kMaxExperts / 32; ++i)
+            for (int i = 0; i < kPer; ++i)
                 if (i == static_cast<int>(at >> 5)) {
                     v = l[i];
                     if (lane == static_cast<int>(at & 31)) key[i] = 0u;   // (keys of numbers are above 0)
@@ -378,11 +373,11 @@ __global__ void __launch_bounds__(kThreads) moe_route(const __grid_constant__ Pa
             if (lane == j) chosen = v, id = static_cast<int>(at);
         }
         const float mine = lane < p.top ? expf(chosen - best) : 0.f;
-        if (p.renorm) {
-            total = mine;
-        } else {
+        float total = mine;
+        if (!p.renorm) {
+            total = 0.f;
 #pragma unroll
-            for (int i = 0; i < kMaxExperts / 32; ++i)
+            for (int i = 0; i < kPer; ++i)
                 if (i * 32 + lane < p.E) total += expf(l[i] - best);
         }
 #pragma unroll
@@ -390,6 +385,23 @@ __global__ void __launch_bounds__(kThreads) moe_route(const __grid_constant__ Pa
         if (lane < p.top) {
             p.weights[(t0 + rank) * p.top + lane] = mine / total;
             p.ids[(t0 + rank) * p.top + lane] = id;
+        }
+    } else if (p.xq && warp > 0) {
+        // the tokens' part as MXFP4 columns
+        const int blocks = width >> 5;
+        for (int i = (warp - 1) * 4; i < nt * blocks; i += (kWarps - 1) * 4) {
+            float v[4];
+            uint8_t* codes[4];
+            uint8_t* scales[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int n = min(i + j, nt * blocks - 1), t = n / blocks, blk = n - t * blocks;
+                const int64_t row = static_cast<int64_t>(t0 + t) * kPieces, at = (k_lo >> 5) + blk;
+                v[j] = __half2float(xs[t * xpitch + blk * 32 + lane]);
+                codes[j] = p.xq + row * p.xq_pitch + at * 16;
+                scales[j] = p.xs + row * p.xs_pitch + at;
+            }
+            split_blocks(v, nt * blocks - i, lane, codes, p.xq_pitch, scales, p.xs_pitch);
         }
     }
     __syncwarp();

@@ -23,6 +23,12 @@
 // (gate/up, down), wherever that falls: a part's first and last output tile may
 // be shared with its neighbours, whose sums go through the workspace; the part
 // that finishes such a tile last adds them in order.
+//
+// A CTA takes parts by ticket.  All gate/up parts have been taken, by CTAs that
+// run, before any CTA goes on to the down phase and waits for the hidden values,
+// so the wait ends however few CTAs the device holds at once; with one CTA an SM
+// each takes one part of either phase.  The weights of a down part are on their
+// way before the wait.
 #pragma once
 
 #include <cuda.h>
@@ -39,6 +45,7 @@ constexpr int kMaxParts = 160;
 // Counters of one call, zeroed by the routing kernel.
 struct StreamControl {
     int done;                 // finished gate/up parts
+    int ticket[2];            // parts taken
     int up[kMaxParts];        // by the first part of a shared tile: parts that have stored their sums
     int down[kMaxParts];
 };
@@ -121,10 +128,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
     __shared__ __align__(8) uint64_t bars[3 * 16 + 5];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
-    __shared__ int last_flag, fixes;
-    __shared__ int3 fix[2];   // shared tiles of y that this part adds up: tile, first and last part
+    __shared__ int last_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int part = blockIdx.x, parts = gridDim.x;
+    const int parts = gridDim.x;
+    // parts of each phase in the order this CTA takes them: the weights' thread
+    // draws them, `parts` or more ends the list
+    __shared__ volatile int16_t list[2][kMaxParts + 1];
 
     const uint32_t bar0 = smem_u32(bars);
     auto full_a = [&](int s) { return bar0 + 24u * s; };
@@ -147,12 +156,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
         }
         mbar_init(drain, 1);
         abort_flag = 0;
-        fixes = 0;
+
         fence_mbarrier_init();
         tma_prefetch_desc(&sp.gate);
         tma_prefetch_desc(&sp.up);
         tma_prefetch_desc(&sp.down);
     }
+    for (int i = threadIdx.x; i <= kMaxParts; i += kThreads) list[0][i] = list[1][i] = -1;
     if (warp == 5) {
         tmem_alloc(smem_u32(&tmem_slot), sp.tmem_cols);
         tmem_relinquish();
@@ -160,6 +170,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
     tc_fence_before();
     griddep_wait();
     griddep_launch_dependents();
+    int ticket = 0;   // of the weights' thread
+    if (threadIdx.x == 4 * 32) ticket = atomicAdd(&sp.ctl->ticket[0], 1);
     order_choices(p, ch, reinterpret_cast<uint16_t*>(smem), sp.cap);
     fence_proxy_async_smem();   // the counts lay where the copies will write
     __syncthreads();
@@ -197,6 +209,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
         abort_flag = 1;
         atomicExch(p.status, GEMM_F16_ERR_TIMEOUT);
     };
+    // the i-th part of a phase; -1 once the CTA has given up
+    auto part_at = [&](int ph, int i) {
+        int v;
+        while ((v = list[ph][i]) < 0)
+            if (*abort) break;
+        return v;
+    };
     auto columns = [&](int ph, int count) { return kMx ? count * kPieces : ph ? 2 * count : count; };
 
     if (warp == 4) {
@@ -205,7 +224,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
             int n = 0, st = 0;
             uint32_t par = 0;
             bool ok = true;
-            for (int ph = 0; ph < 2 && ok; ++ph) {
+            for (int ph = 0; ph < 2 && ok; ++ph) for (int i = 0; ok; ++i) {
+                const int part = ph == 0 && i == 0 ? ticket : atomicAdd(&sp.ctl->ticket[ph], 1);
+                list[ph][i] = static_cast<int16_t>(min(part, parts));
+                if (part >= parts) break;
                 const int64_t hi = phase[ph].start(part + 1);
                 for (int64_t at = phase[ph].start(part); at < hi && ok;) {
                     const Segment g = segment(ph, at, hi);
@@ -263,7 +285,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
             uint32_t par = 0, bpar = 0;
             bool ok = true;
             const uint32_t tsa = tmem + 4 * sp.acc_cols, tsb = tsa + 16;
-            for (int ph = 0; ph < 2 && ok; ++ph) {
+            for (int ph = 0; ph < 2 && ok; ++ph) for (int i = 0; ok; ++i) {
+                const int part = part_at(ph, i);
+                if (part < 0) ok = false;
+                if (part < 0 || part >= parts) break;
                 const int64_t hi = phase[ph].start(part + 1);
                 const int k64 = ((ph ? p.F : p.D) + 63) >> 6;
                 for (int64_t at = phase[ph].start(part); at < hi && ok;) {
@@ -342,13 +367,19 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
             while (pend) hand_over();
         };
         for (int ph = 0; ph < 2 && ok; ++ph) {
+            bool waited = ph == 0;
+            for (int i = 0; ok; ++i) {
+            const int part = part_at(ph, i);
+            if (part < 0) ok = false;
+            if (part < 0 || part >= parts) break;
             const int64_t lo = phase[ph].start(part), hi = phase[ph].start(part + 1);
             const int width = kMx ? kPieces : ph ? 2 : 1;   // rows of a token
             const uint8_t* rows = ph ? sp.h : sp.x;
             const uint8_t* scales = ph ? sp.hs : sp.xs;
             const int64_t pitch = ph ? sp.hpitch : sp.xpitch, words = ph ? sp.hwords : sp.xwords;
             const int kt = (ph ? p.down : p.gate).kt;
-            if (ph == 1 && lo < hi) {   // every hidden value is there
+            if (!waited && lo < hi) {   // every hidden value is there
+                waited = true;
                 flush();
                 if (lane == 0) {
                     const uint64_t t0 = globaltimer_ns();
@@ -398,6 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
                     }
                 }
             }
+            }
         }
         flush();
         if (!ok && lane == 0) fail();
@@ -430,28 +462,74 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
             named_bar_sync(1, 128);
             return last_flag != 0;
         };
-        auto slot_of = [&](const Parts& w, int v, int64_t first) {
-            return sp.sums + (static_cast<int64_t>(v) * 2 + (w.start(v) > first ? 0 : 1)) * slot_floats;
-        };
-        // hidden value (tile's row, token j of the piece) from its two sums
-        auto hidden = [&](const Segment& g, const Item& im, int j, float gate, float up) {
+        // where part v keeps its sums of a shared tile whose first part is v0: a
+        // part has two at most, the tile it begins in and the one it ends in
+        auto slot_of = [&](int v, int v0) { return sp.sums + (static_cast<int64_t>(v) * 2 + (v == v0)) * slot_floats; };
+        // hidden values (tile's row, tokens j0 .. j0 + 3 of the piece) from their two sums
+        auto hidden = [&](const Segment& g, const Item& im, int j0, const float* gate, const float* up) {
             const int f = g.tile * 128 + row;
-            // (past F: zeros, whatever the tokens hold)
-            const float hv = f < p.F ? act_f32(p.act, gate) * up : 0.f;
-            const int64_t r = im.first + j;
+            float hv[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)   // (past F: zeros, whatever the tokens hold)
+                hv[j] = f < p.F ? act_f32(p.act, gate[j]) * up[j] : 0.f;
             if (kMx) {
-                split_block(hv, lane, sp.h + r * kPieces * sp.hpitch + ((f - lane) >> 1), sp.hpitch,
-                            sp.hs + r * kPieces * sp.hwords * 4 + ((f - lane) >> 5), sp.hwords * 4);
+                uint8_t* codes[4];
+                uint8_t* scales[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int64_t r = static_cast<int64_t>(im.first + min(j0 + j, im.count - 1)) * kPieces;
+                    codes[j] = sp.h + r * sp.hpitch + ((f - lane) >> 1);
+                    scales[j] = sp.hs + r * sp.hwords * 4 + ((f - lane) >> 5);
+                }
+                split_blocks(hv, im.count - j0, lane, codes, sp.hpitch, scales, sp.hwords * 4);
             } else if (f < p.fp) {
-                const __half hh = __float2half_rn(hv);
-                const float back = __half2float(hh);
-                __half* dst = reinterpret_cast<__half*>(sp.h + r * 2 * sp.hpitch) + f;
-                dst[0] = hh;
-                dst[sp.hpitch >> 1] = isfinite(back) ? __float2half_rn(hv - back) : __ushort_as_half(0);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (j0 + j >= im.count) break;
+                    const __half hh = __float2half_rn(hv[j]);
+                    const float back = __half2float(hh);
+                    __half* dst = reinterpret_cast<__half*>(sp.h + static_cast<int64_t>(im.first + j0 + j) * 2 * sp.hpitch) + f;
+                    dst[0] = hh;
+                    dst[sp.hpitch >> 1] = isfinite(back) ? __float2half_rn(hv[j] - back) : __ushort_as_half(0);
+                }
+            }
+        };
+        // the sums of a shared tile of y, by the part that stored its own last: 4
+        // columns a thread, 4 parts' and 2 tokens' loads under way at once
+        auto add_shared = [&](int tile, int v0, int v1) {
+            const int col = tile * 256 + (threadIdx.x & 63) * 4;
+            for (int t0 = threadIdx.x >> 6; t0 < p.T; t0 += 4) {
+                float4 v[2] = {};
+                for (int q0 = v0; q0 <= v1; q0 += 4) {
+                    float4 a[4][2];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            a[q][i] = __ldcg(reinterpret_cast<const float4*>(slot_of(min(q0 + q, v1), v0) + min(t0 + 2 * i, p.T - 1) * 256) +
+                                             (threadIdx.x & 63));
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            if (q0 + q <= v1) v[i].x += a[q][i].x, v[i].y += a[q][i].y, v[i].z += a[q][i].z, v[i].w += a[q][i].w;
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int t = t0 + 2 * i;
+                    if (t >= p.T) break;
+                    const float f[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (col + e < p.D) p.y[t * p.ldy + col + e] = __float2half_rn(f[e]);
+                }
             }
         };
         constexpr int kUpWidth = kMx ? kPieces : 1, kDownWidth = kMx ? kPieces : 2;
-        for (int ph = 0; ph < 2 && ok; ++ph) {
+        for (int ph = 0; ph < 2 && ok; ++ph) for (int i = 0; ok; ++i) {
+            const int part = part_at(ph, i);
+            ok = all_of(part >= 0);
+            if (!ok || part >= parts) break;
             const Parts& w = phase[ph];
             const int64_t lo = w.start(part), hi = w.start(part + 1);
             bool begun = false;   // (down) ysum holds sums of the current tile
@@ -472,28 +550,27 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
                     const int64_t first = at - g.s0;
                     const bool whole = g.s0 == 0 && g.s1 == d_steps;
                     at += g.s1 - g.s0;
-                    float* to = slot_of(w, part, first) + row;
+                    const int v0 = whole ? part : w.of(first), v1 = whole ? part : w.of(first + d_steps - 1);
+                    float* to = slot_of(part, v0) + row;
                     for (int j0 = 0; j0 < im.count; j0 += 4) {
                         float gate[4], up[4];
                         take4<kUpWidth>(d + j0 * kUpWidth, gate);
                         take4<kUpWidth>(d + sp.acc_cols + j0 * kUpWidth, up);
                         if (j0 + 4 >= im.count) release();
+                        if (whole) {
+                            hidden(g, im, j0, gate, up);
+                        } else {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            if (j0 + j >= im.count) break;
-                            if (whole)
-                                hidden(g, im, j0 + j, gate[j], up[j]);
-                            else
-                                to[(j0 + j) * 256] = gate[j], to[(j0 + j) * 256 + 128] = up[j];
+                            for (int j = 0; j < 4; ++j)
+                                if (j0 + j < im.count) to[(j0 + j) * 256] = gate[j], to[(j0 + j) * 256 + 128] = up[j];
                         }
                     }
                     if (whole) continue;
-                    const int v0 = w.of(first), v1 = w.of(first + d_steps - 1);
                     if (!last_of(&sp.ctl->up[v0], v1 - v0 + 1)) continue;
                     for (int j0 = 0; j0 < im.count; j0 += 4) {
                         float gate[4] = {}, up[4] = {};
                         for (int q = v0; q <= v1; ++q) {
-                            const float* from = slot_of(w, q, first) + row;
+                            const float* from = slot_of(q, v0) + row;
                             float a[4], b[4];
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
@@ -503,11 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
 #pragma unroll
                             for (int j = 0; j < 4; ++j) gate[j] += a[j], up[j] += b[j];
                         }
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            if (j0 + j >= im.count) break;
-                            hidden(g, im, j0 + j, gate[j], up[j]);
-                        }
+                        hidden(g, im, j0, gate, up);
                     }
                 } else {
                     const int64_t per = static_cast<int64_t>(items) * f_steps, first = g.tile * per;
@@ -539,10 +612,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
                         }
                         continue;
                     }
-                    float* to = slot_of(w, part, first) + row;
-                    for (int t = 0; t < p.T; ++t) to[t * 256] = ysum[t * 256 + row], to[t * 256 + 128] = ysum[t * 256 + 128 + row];
                     const int v0 = w.of(first), v1 = w.of(first + per - 1);
-                    if (last_of(&sp.ctl->down[v0], v1 - v0 + 1) && threadIdx.x == 0) fix[fixes++] = make_int3(g.tile, v0, v1);
+                    float* to = slot_of(part, v0) + row;
+                    for (int t = 0; t < p.T; ++t) to[t * 256] = ysum[t * 256 + row], to[t * 256 + 128] = ysum[t * 256 + 128 + row];
+                    if (last_of(&sp.ctl->down[v0], v1 - v0 + 1)) add_shared(g.tile, v0, v1);
                 }
             }
             if (ph == 0 && ok) {
@@ -556,31 +629,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
     __syncthreads();
     tc_fence_after();
     if (warp == 5) tmem_dealloc(tmem, sp.tmem_cols);
-    // Shared tiles of y whose last sums this part stored: all threads add them,
-    // 8 parts' loads under way at once.
-    for (int i = 0; i < fixes; ++i) {
-        const int tile = fix[i].x, v0 = fix[i].y, v1 = fix[i].z;
-        const Parts& w = phase[1];
-        const int64_t first = static_cast<int64_t>(tile) * items * f_steps;
-        const int64_t slot_floats = static_cast<int64_t>(max(sp.cap, p.T)) * 256;
-        for (int k = threadIdx.x; k < p.T * 256; k += kThreads) {
-            const int t = k >> 8, col = tile * 256 + (k & 255);
-            if (col >= p.D) continue;
-            float v = 0.f;
-            for (int q0 = v0; q0 <= v1; q0 += 8) {
-                float a[8];
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const int u = min(q0 + q, v1);
-                    a[q] = ld_cg_f32(sp.sums + (static_cast<int64_t>(u) * 2 + (w.start(u) > first ? 0 : 1)) * slot_floats + k);
-                }
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    if (q0 + q <= v1) v += a[q];
-            }
-            p.y[t * p.ldy + col] = __float2half_rn(v);
-        }
-    }
 }
 
 }  // namespace moe_dev
