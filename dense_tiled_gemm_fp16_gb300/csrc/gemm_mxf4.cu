@@ -70,20 +70,23 @@ gemm_f16_status launch_dequantize(const mxf4_dev::DequantParams& p, int64_t batc
                          mxf4_dev::kConvThreads, 0, 1, stream, p);
 }
 
-// Dynamic shared memory above 48 KB is allowed once per device.
-bool allow_smem(int device)
+// Dynamic shared memory above 48 KB is allowed once per device and kernel.
+bool allow_smem(const void* kernel, int slot, int bytes)
 {
     static std::mutex mutex;
-    static bool done[64] = {};
+    static bool done[64][3] = {};
+    int d = 0;
+    if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= 64) {
+        cudaGetLastError();
+        return false;
+    }
     std::lock_guard<std::mutex> lk(mutex);
-    if (device < 0 || device >= 64) return false;
-    if (!done[device]) {
-        if (cudaFuncSetAttribute(mxf4_dev::gemm_mxf4_tile, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem / 2) !=
-            cudaSuccess) {
+    if (!done[d][slot]) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
             cudaGetLastError();
             return false;
         }
-        done[device] = true;
+        done[d][slot] = true;
     }
     return true;
 }
@@ -123,6 +126,68 @@ gemm_f16_status run_quantize(const void* x, int dtype, int64_t sb, int64_t sr, i
                                 : launch_quantize<float>(p, batch, stream);
 }
 
+// Scale tiles as rows of 128 words, two a box.
+bool encode_scales(CUtensorMap* tm, const void* scales, int64_t tiles)
+{
+    const auto encode = tensor_map_encoder();
+    if (!encode) return false;
+    cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(tiles)};
+    cuuint64_t strides[1] = {mxf4_dev::kScaleTile};
+    cuuint32_t box[2] = {128, 2};
+    cuuint32_t estr[2] = {1, 1};
+    return encode(tm, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(scales), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_out(CUtensorMap* tm, void* C, int64_t M, int64_t N, int64_t ldc)
+{
+    const auto encode = tensor_map_encoder();
+    if (!encode) return false;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(M)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(2 * ldc)};
+    cuuint32_t box[2] = {64, 32};
+    cuuint32_t estr[2] = {1, 1};
+    return encode(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, C, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
+template <int kBN>
+gemm_f16_status launch_pair(const Device& dev, const void* A_codes, const void* A_scales, const void* B_codes,
+                            const void* B_scales, const void* bias, int act, void* C, int64_t ldc, int64_t M, int64_t N,
+                            int64_t K, cudaStream_t stream)
+{
+    using Shape = mxf4_dev::PairShape<kBN>;
+    Sizes sa, sb;
+    sizes_of(M, K, 1, &sa);
+    sizes_of(N, K, 1, &sb);
+    mxf4_dev::PairParams p = {};
+    p.bias = static_cast<const __half*>(bias);
+    p.C = static_cast<__half*>(C);
+    p.ldc = ldc, p.M = M, p.N = N;
+    p.kt = static_cast<int32_t>(sa.kt);
+    p.k64 = static_cast<int32_t>(cdiv(K, 64));
+    p.steps = static_cast<int32_t>(cdiv(K, 256));
+    p.act = act;
+    p.tiles_m = static_cast<int32_t>(cdiv(M, 256));
+    p.tiles_n = static_cast<int32_t>(cdiv(N, kBN));
+    p.panel = p.tiles_n <= 16 ? 2 : 8;
+    p.test_stall = option(GEMM_F16_OPT_TEST_STALL) == 1;
+    p.timeout_ns = timeout_ns();
+    p.status = dev.status;
+    p.c_tma = ldc % 8 == 0 && ldc < int64_t(1) << 39 && aligned(C, 16);
+    if (!encode_codes(&p.tmA, A_codes, M, sa.pitch, 128) || !encode_codes(&p.tmB, B_codes, N, sa.pitch, kBN / 2) ||
+        !encode_scales(&p.tmSA, A_scales, sa.row_tiles * sa.kt) || !encode_scales(&p.tmSB, B_scales, sb.row_tiles * sb.kt) ||
+        (p.c_tma && !encode_out(&p.tmC, C, M, N, ldc)))
+        return GEMM_F16_ERR_LAUNCH;
+    if (!allow_smem(reinterpret_cast<const void*>(mxf4_dev::gemm_mxf4_pair<kBN>), kBN == 256 ? 1 : 2, Shape::kSmem))
+        return GEMM_F16_ERR_LAUNCH;
+    const int64_t clusters = std::min<int64_t>(dev.sms / 2, static_cast<int64_t>(p.tiles_m) * p.tiles_n);
+    return launch_kernel(mxf4_dev::gemm_mxf4_pair<kBN>, dim3(static_cast<unsigned>(2 * clusters)), mxf4_dev::kPairThreads,
+                         Shape::kSmem, 2, stream, p);
+}
+
 // The product of checked operands.
 gemm_f16_status product(const Device& dev, const void* A_codes, const void* A_scales, const void* B_codes,
                         const void* B_scales, const void* bias, int act, void* C, int64_t ldc, int64_t M, int64_t N,
@@ -130,6 +195,14 @@ gemm_f16_status product(const Device& dev, const void* A_codes, const void* A_sc
 {
     Sizes sa;
     sizes_of(M, K, 1, &sa);
+    // Pairs once their tiles would occupy most of the device (below that the small tiles
+    // spread better); of the two widths the one whose turns of the clusters
+    // cost less, a 128-wide turn 0.62 of a 256-wide one.
+    const int64_t pairs = dev.sms / 2, wide = cdiv(M, 256) * cdiv(N, 256), narrow = cdiv(M, 256) * cdiv(N, 128);
+    if (M > 64 && N > 64 && narrow * 4 >= pairs * 3 && sa.row_tiles * sa.kt < INT32_MAX && cdiv(N, 128) * sa.kt < INT32_MAX)
+        return cdiv(narrow, pairs) * 0.62 < cdiv(wide, pairs)
+                   ? launch_pair<128>(dev, A_codes, A_scales, B_codes, B_scales, bias, act, C, ldc, M, N, K, stream)
+                   : launch_pair<256>(dev, A_codes, A_scales, B_codes, B_scales, bias, act, C, ldc, M, N, K, stream);
     mxf4_dev::GemmParams p = {};
     // Few rows of A: B's rows take the 128 lanes and A's rows the narrow side.
     p.swapped = M <= 64 && M < N;
@@ -159,9 +232,7 @@ gemm_f16_status product(const Device& dev, const void* A_codes, const void* A_sc
     if (!encode_codes(&p.tmA, p.swapped ? B_codes : A_codes, p.M, sa.pitch, 128) ||
         !encode_codes(&p.tmB, p.swapped ? A_codes : B_codes, p.N, sa.pitch, static_cast<uint32_t>(p.bn)))
         return GEMM_F16_ERR_LAUNCH;
-    int d = 0;
-    cudaGetDevice(&d);
-    if (!allow_smem(d)) return GEMM_F16_ERR_LAUNCH;
+    if (!allow_smem(reinterpret_cast<const void*>(mxf4_dev::gemm_mxf4_tile), 0, kMaxSmem / 2)) return GEMM_F16_ERR_LAUNCH;
     return launch_kernel(mxf4_dev::gemm_mxf4_tile, dim3(static_cast<unsigned>(tiles * cluster)), mxf4_dev::kGemmThreads,
                          p.stages * sbytes + 1024, cluster, stream, p);
 }

@@ -268,4 +268,295 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_mxf4_tile(const __grid_cons
     if (warp == 5) tmem_dealloc(tmem, p.tmem_cols);
 }
 
+// ------------------------------------------------------------------ pairs
+// The form for products of many tiles: persistent clusters of two CTAs, a 256 x
+// kBN tile each, its MMAs over both (cta_group::2), so that each CTA brings half
+// of B's rows.  L2 is what bounds it otherwise: an MMA step of 256 values takes
+// 512 cycles and a CTA then reads 35 KB for it, 70 bytes a cycle, where a CTA
+// alone with a 128 x 256 tile would read 100.
+//
+// Two accumulators of 256 columns and the scales do not fit tensor memory (512
+// columns), so the second begins 24 columns inside the first: a tile's MMAs
+// begin when the epilogue of the one before has those columns in registers,
+// which it reads first.
+struct PairParams {
+    CUtensorMap tmA, tmB;        // codes, boxes of 128 bytes x 128 rows and x kBN / 2 rows
+    CUtensorMap tmSA, tmSB;      // scale tiles: {128 words, tiles}, boxes of two tiles
+    CUtensorMap tmC;             // boxes of 64 columns x 32 rows (c_tma)
+    const __half* bias;
+    __half* C;
+    int64_t ldc, M, N;
+    int32_t kt, k64, steps, act, c_tma;
+    int32_t tiles_m, tiles_n, panel;   // panel: rows of tiles walked column by column
+    int32_t test_stall;
+    uint64_t timeout_ns;
+    int* status;
+};
+
+constexpr int kPairThreads = 320;   // warps 0-7 epilogue, 8 loads, 9 MMA
+constexpr int kEpiBox = 32 * 128;   // bytes of a warp's staged 32 rows x 64 columns
+
+template <int kBN>
+struct PairShape {
+    static constexpr uint32_t kB = kBN / 2 * 128, kSfB = kBN / 128 * kSfBytes;
+    static constexpr uint32_t kStage = kABytes + kB + kSfBytes + kSfB;
+    static constexpr int kStages = kBN == 256 ? 5 : 7;
+    static constexpr uint32_t kSmem = kStages * kStage + 8 * kEpiBox + 1024;
+    static constexpr uint32_t kSfCol = 512 - 8 - 2 * kBN / 32;    // scales of A, then of B
+    static constexpr uint32_t kAcc1 = kBN == 256 ? kSfCol - 256 : 256;
+};
+
+// act of 32 values; one choice for all of them.
+__device__ __forceinline__ void act_all(int act, float* v)
+{
+    if (act == 1) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) v[c] = act_f32(1, v[c]);
+    } else if (act == 2) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) v[c] = act_f32(2, v[c]);
+    } else if (act == 3) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) v[c] = act_f32(3, v[c]);
+    }
+}
+
+// 64 finished columns of a warp's 32 rows from its staging box to C, without TMA.
+__device__ __forceinline__ void store_rows(const PairParams& p, const uint8_t* box, int64_t m0, int64_t n0, int lane)
+{
+    const int cols = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(64), p.N - n0)));
+    for (int r = 0; r < 32 && m0 + r < p.M; ++r) {
+        __half* c = p.C + (m0 + r) * p.ldc + n0;
+        const uint8_t* row = box + r * 128;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int i = lane + 32 * h;
+            if (i < cols) c[i] = *reinterpret_cast<const __half*>(row + (((i >> 3) ^ (r & 7)) << 4) + (i & 7) * 2);
+        }
+    }
+}
+
+template <int kBN>
+__global__ void __launch_bounds__(kPairThreads, 1) gemm_mxf4_pair(const __grid_constant__ PairParams p)
+{
+    using S = PairShape<kBN>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
+    __shared__ __align__(8) uint64_t bars[2 * 8 + 5];
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int abort_flag;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const uint32_t bar0 = smem_u32(bars);
+    auto full = [&](int s) { return bar0 + 16u * s; };
+    auto empty = [&](int s) { return bar0 + 16u * s + 8u; };
+    const uint32_t tfull = bar0 + 128u, room = tfull + 16u, never = room + 8u, drain = never + 8u;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S::kStages; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        mbar_init(tfull, 1);
+        mbar_init(tfull + 8, 1);
+        mbar_init(room, 16);   // every epilogue warp of both CTAs
+        mbar_init(never, 1);
+        mbar_init(drain, 1);
+        abort_flag = 0;
+        fence_mbarrier_init();
+        tma_prefetch_desc(&p.tmA);
+        tma_prefetch_desc(&p.tmB);
+        tma_prefetch_desc(&p.tmSA);
+        tma_prefetch_desc(&p.tmSB);
+        if (p.c_tma) tma_prefetch_desc(&p.tmC);
+    }
+    if (warp == 9) {
+        tmem_alloc_pair(smem_u32(&tmem_slot), 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    griddep_wait();
+    griddep_launch_dependents();
+
+    const volatile int* abort = &abort_flag;
+    auto fail = [&]() {
+        abort_flag = 1;
+        atomicExch(p.status, GEMM_F16_ERR_TIMEOUT);
+    };
+    const int clusters = gridDim.x >> 1;
+    const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
+    auto place = [&](int64_t t, int64_t* m0, int64_t* n0) {
+        const int64_t band = static_cast<int64_t>(p.panel) * p.tiles_n, b = t / band, r = t - b * band;
+        const int64_t rows = min(static_cast<int64_t>(p.panel), p.tiles_m - b * p.panel);
+        *n0 = r / rows * kBN;
+        *m0 = (b * p.panel + r % rows) * 256;
+    };
+
+    if (warp == 8) {
+        if (lane == 0) {
+            int st = 0;
+            uint32_t par = 0;
+            bool ok = true;
+            for (int64_t t = blockIdx.x >> 1; t < tiles && ok; t += clusters) {
+                int64_t m0, n0;
+                place(t, &m0, &n0);
+                const int32_t am = static_cast<int32_t>(m0 + rank * 128), bm = static_cast<int32_t>(n0 + rank * (kBN / 2));
+                const int32_t sa = static_cast<int32_t>(am >> 7) * p.kt, sb = static_cast<int32_t>(n0 >> 7) * p.kt;
+                for (int s = 0; s < p.steps; ++s) {
+                    ok = mbar_wait_cluster(empty(st), par ^ 1u, abort, p.timeout_ns);
+                    if (!ok) break;
+                    const uint32_t a = base + st * S::kStage, b = a + kABytes, fa = b + S::kB, fb = fa + kSfBytes;
+                    const uint32_t bar = mapa_shared(full(st), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(full(st), 2 * S::kStage);
+                    tma_load_2d_pair(a, &p.tmA, s * 128, am, bar);
+                    tma_load_2d_pair(b, &p.tmB, s * 128, bm, bar);
+                    // (past a row tile's last scale tile: another's, or zeros; not used)
+                    tma_load_2d_pair(fa, &p.tmSA, 0, sa + 2 * s, bar);
+#pragma unroll
+                    for (int h = 0; h < kBN / 128; ++h) tma_load_2d_pair(fb + h * kSfBytes, &p.tmSB, 0, sb + h * p.kt + 2 * s, bar);
+                    if (++st == S::kStages) st = 0, par ^= 1u;
+                }
+            }
+            if (!ok) {   // copies in flight land before the pair leaves: far longer than any takes
+                fail();
+                const uint64_t t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 5000000ull) __nanosleep(100000);
+            }
+        }
+    } else if (warp == 9) {
+        if (lane == 0 && rank == 0) {
+            int st = 0, acc = 0;
+            uint32_t par = 0, rpar = 0;
+            bool ok = !p.test_stall || mbar_wait(never, 0, abort, p.timeout_ns);
+            bool first = true;
+            const uint32_t tsa = tmem + S::kSfCol, tsb = tsa + 8;
+            const uint32_t id0 = idesc_mxf4(256, kBN, 0), id1 = idesc_mxf4(256, kBN, 1);
+            for (int64_t t = blockIdx.x >> 1; t < tiles && ok; t += clusters) {
+                if (!first) {   // the tile before last is stored, the last one's shared columns are read
+                    ok = mbar_wait_cluster(room, rpar, abort, p.timeout_ns);
+                    if (!ok) break;
+                    rpar ^= 1u;
+                    tc_fence_after();
+                }
+                first = false;
+                const uint32_t d = tmem + (acc ? S::kAcc1 : 0u);
+                for (int s = 0; s < p.steps; ++s) {
+                    ok = mbar_wait_cluster(full(st), par, abort, p.timeout_ns);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t a = base + st * S::kStage, b = a + kABytes, fa = b + S::kB, fb = fa + kSfBytes;
+                    const uint64_t da = umma_desc_sw128(a, 16, 1024), db = umma_desc_sw128(b, 16, 1024);
+                    const int n64 = min(4, p.k64 - 4 * s);
+                    for (int h = 0; h < (n64 + 1) / 2; ++h) {
+                        tmem_copy_scales_pair(tsa + 4 * h, scale_desc(fa + h * kScaleTile));
+#pragma unroll
+                        for (int j = 0; j < kBN / 128; ++j)
+                            tmem_copy_scales_pair(tsb + (kBN / 32) * h + 4 * j, scale_desc(fb + j * kSfBytes + h * kScaleTile));
+                    }
+                    for (int q = 0; q < n64; ++q)
+                        umma_mxf4_pair(d, da + 2 * q, db + 2 * q, q & 1 ? id1 : id0, tsa + 4 * (q >> 1),
+                                       tsb + (kBN / 32) * (q >> 1), s > 0 || q > 0);
+                    umma_commit_pair_mc(empty(st), 0x3);
+                    if (++st == S::kStages) st = 0, par ^= 1u;
+                }
+                if (!ok) break;
+                umma_commit_pair_mc(tfull + 8 * acc, 0x3);
+                acc ^= 1;
+            }
+            if (!ok) {
+                fail();
+                umma_commit_pair_mc(drain, 0x1);
+                mbar_wait_cluster(drain, 0, nullptr, kDrainNs);
+            }
+        }
+    } else {
+        // epilogue: warps 0-3 the first half of the columns, 4-7 the second; a
+        // warp's lanes are the rows 32 (warp % 4) .. of its CTA's 128
+        constexpr int kHalf = kBN / 2, kBoxes = kHalf / 64;
+        const int half = warp >> 2;
+        const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + half * kHalf;
+        uint8_t* box = smem + S::kStages * S::kStage + warp * kEpiBox;
+        const uint32_t box_at = smem_u32(box), leader_room = mapa_shared(room, 0);
+        int acc = 0;
+        uint32_t tpar = 0;
+        for (int64_t t = blockIdx.x >> 1; t < tiles; t += clusters) {
+            int64_t m0, n0;
+            place(t, &m0, &n0);
+            const bool ok = __all_sync(~0u, mbar_wait_cluster(tfull + 8 * acc, tpar, abort, p.timeout_ns));
+            if (!ok) {
+                if (lane == 0) fail();
+                break;
+            }
+            tc_fence_after();
+            const uint32_t d = trow + (acc ? S::kAcc1 : 0u);
+            const int64_t row0 = m0 + rank * 128 + (warp & 3) * 32;
+            // the columns that the other accumulator shares come first: the last
+            // box of the first accumulator, the first of the second
+            const bool shares = kBN == 256 && half == (acc ? 0 : 1);
+            if (!shares && lane == 0) mbar_arrive_cluster(leader_room);
+#pragma unroll 1
+            for (int i = 0; i < 2 * kBoxes; ++i) {   // 32 columns, half a box, at a time
+                const int b = acc ? i : 2 * kBoxes - 1 - i;
+                uint32_t r[32];
+                tmem_ld_x16(d + b * 32, r);
+                tmem_ld_x16(d + b * 32 + 16, r + 16);
+                tmem_wait_ld();
+                if (shares && i == 0) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(leader_room);
+                }
+                const int64_t n = n0 + half * kHalf + b * 32;
+                float v[32];
+#pragma unroll
+                for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(r[c]);
+                if (p.bias) {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        if (n + c < p.N) v[c] += __half2float(__ldg(p.bias + n + c));
+                }
+                act_all(p.act, v);
+                if (p.c_tma && (i & 1) == 0) {
+                    if (lane == 0) bulk_wait_group_read<0>();   // the box's last store has read it
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    st_smem_v4(box_at + lane * 128 + (((4 * (b & 1) + c) ^ (lane & 7)) << 4),
+                               make_uint4(pack_half2(v[8 * c], v[8 * c + 1]), pack_half2(v[8 * c + 2], v[8 * c + 3]),
+                                          pack_half2(v[8 * c + 4], v[8 * c + 5]), pack_half2(v[8 * c + 6], v[8 * c + 7])));
+                if ((i & 1) == 0) continue;
+                const int64_t nb = n0 + half * kHalf + (b & ~1) * 32;
+                if (p.c_tma) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && nb < p.N && row0 < p.M) {
+                        tma_store_2d(&p.tmC, box_at, static_cast<int32_t>(nb), static_cast<int32_t>(row0));
+                        bulk_commit_group();
+                    }
+                } else {
+                    __syncwarp();
+                    store_rows(p, box, row0, nb, lane);
+                    __syncwarp();
+                }
+            }
+            tc_fence_before();
+            if (acc) tpar ^= 1u;
+            acc ^= 1;
+        }
+        if (p.c_tma && lane == 0) bulk_wait_group_all();
+    }
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync_all();
+    tc_fence_after();
+    if (warp == 9) tmem_dealloc_pair(tmem, 512);
+}
+
 }  // namespace mxf4_dev

@@ -48,4 +48,24 @@ __host__ __device__ constexpr uint32_t idesc_mxf4(uint32_t m, uint32_t n, uint32
            ((2 * half) << 29);
 }
 
+// The forms of a CTA pair (one MMA over 256 rows, each CTA with its 128 rows of
+// A, half the rows of B and the scales of its A rows and of all of B's).
+__device__ __forceinline__ void umma_mxf4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t sfa, uint32_t sfb, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// (each CTA's tile, at the same offset in both, to its own tensor memory)
+__device__ __forceinline__ void tmem_copy_scales_pair(uint32_t taddr, uint64_t desc)
+{
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
 }  // namespace mxf4_dev
