@@ -129,9 +129,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
     __shared__ int last_flag;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const int parts = gridDim.x;
-    // parts of each phase in the order this CTA takes them: the weights' thread
+    // parts of each phase in the order this CTA takes them: the weights' warp
     // draws them, `parts` or more ends the list
     __shared__ volatile int16_t list[2][kMaxParts + 1];
 
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
     tc_fence_before();
     griddep_wait();
     griddep_launch_dependents();
-    int ticket = 0;   // of the weights' thread
+    int ticket = 0;   // of the weights' warp
     if (threadIdx.x == 4 * 32) ticket = atomicAdd(&sp.ctl->ticket[0], 1);
     order_choices(p, ch, reinterpret_cast<uint16_t*>(smem), sp.cap);
     fence_proxy_async_smem();   // the counts lay where the copies will write
@@ -220,13 +220,16 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
 
     if (warp == 4) {
         // ---------------------------------------------------------- weights
-        if (lane == 0) {
-            int n = 0, st = 0;
-            uint32_t par = 0;
-            bool ok = true;
-            for (int ph = 0; ph < 2 && ok; ++ph) for (int i = 0; ok; ++i) {
-                const int part = ph == 0 && i == 0 ? ticket : atomicAdd(&sp.ctl->ticket[ph], 1);
-                list[ph][i] = static_cast<int16_t>(min(part, parts));
+        const bool issue = elect_one();
+        int n = 0, st = 0;
+        uint32_t par = 0;
+        bool ok = true;
+        for (int ph = 0; ph < 2 && ok; ++ph) {
+            for (int i = 0; ok; ++i) {
+                int part = ticket;
+                if (ph || i) part = lane == 0 ? atomicAdd(&sp.ctl->ticket[ph], 1) : 0;
+                part = __shfl_sync(~0u, part, 0);
+                if (lane == 0) list[ph][i] = static_cast<int16_t>(min(part, parts));
                 if (part >= parts) break;
                 const int64_t hi = phase[ph].start(part + 1);
                 for (int64_t at = phase[ph].start(part); at < hi && ok;) {
@@ -238,59 +241,61 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
                     const int o0 = ph ? g.tile * 256 : g.tile * 128, o1 = ph ? o0 + 128 : o0;
                     const Weight& w0 = ph ? p.down : p.gate;
                     const Weight& w1 = ph ? p.down : p.up;
+                    // scales of 128 rows and, but at an odd end, two tiles of K; rows
+                    // 128 on may be past y's last scale tile (and then past its columns)
+                    const bool both = o1 < (ph ? p.D : p.F);
+                    const uint8_t* f0 = kMx ? w0.scales + e * w0.scale_se + static_cast<int64_t>(o0 >> 7) * w0.kt * mxf4_dev::kScaleTile : nullptr;
+                    const uint8_t* f1 = kMx ? w1.scales + e * w1.scale_se + static_cast<int64_t>(o1 >> 7) * w1.kt * mxf4_dev::kScaleTile : nullptr;
                     for (int s = g.s0; s < g.s1; ++s, ++n) {
                         ok = mbar_wait(empty(st), par ^ 1u, abort, p.timeout_ns);
                         if (!ok) break;
                         const uint32_t a = base + st * sp.stage_bytes;
-                        if (kMx) {
-                            // scales of 128 rows and, but at an odd end, two tiles of K; rows
-                            // 128 on may be past y's last scale tile (and then past its columns)
-                            const uint32_t sf = min(2, w0.kt - 2 * s) * mxf4_dev::kScaleTile;
-                            const bool both = o1 < (ph ? p.D : p.F);
-                            const uint32_t fa = a + 2 * kTileBytes + sp.b_bytes;
-                            mbar_arrive_expect_tx(full_a(st), 2 * kTileBytes + (both ? 2 : 1) * sf);
-                            bulk_load(fa, w0.scales + e * w0.scale_se + (static_cast<int64_t>(o0 >> 7) * w0.kt + 2 * s) * mxf4_dev::kScaleTile,
-                                      sf, full_a(st));
-                            if (both)
-                                bulk_load(fa + 2 * mxf4_dev::kScaleTile,
-                                          w1.scales + e * w1.scale_se + (static_cast<int64_t>(o1 >> 7) * w1.kt + 2 * s) * mxf4_dev::kScaleTile,
-                                          sf, full_a(st));
-                        } else {
-                            mbar_arrive_expect_tx(full_a(st), 2 * kTileBytes);
-                        }
-                        if (kFmt == kStreamCols) {
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                tma_load_3d(a + h * (kTileBytes / 2), m0, o0 + 64 * h, s * 64, e, full_a(st));
-                                tma_load_3d(a + kTileBytes + h * (kTileBytes / 2), m1, o1 + 64 * h, s * 64, e, full_a(st));
+                        if (issue) {
+                            if (kMx) {
+                                const uint32_t sf = min(2, w0.kt - 2 * s) * mxf4_dev::kScaleTile;
+                                const uint32_t fa = a + 2 * kTileBytes + sp.b_bytes;
+                                const int64_t off = static_cast<int64_t>(2 * s) * mxf4_dev::kScaleTile;
+                                mbar_arrive_expect_tx(full_a(st), 2 * kTileBytes + (both ? 2 : 1) * sf);
+                                bulk_load(fa, f0 + off, sf, full_a(st));
+                                if (both) bulk_load(fa + 2 * mxf4_dev::kScaleTile, f1 + off, sf, full_a(st));
+                            } else {
+                                mbar_arrive_expect_tx(full_a(st), 2 * kTileBytes);
                             }
-                        } else {
-                            tma_load_3d(a, m0, s * (kMx ? 128 : 64), o0, e, full_a(st));
-                            tma_load_3d(a + kTileBytes, m1, s * (kMx ? 128 : 64), o1, e, full_a(st));
+                            if (kFmt == kStreamCols) {
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    tma_load_3d(a + h * (kTileBytes / 2), m0, o0 + 64 * h, s * 64, e, full_a(st));
+                                    tma_load_3d(a + kTileBytes + h * (kTileBytes / 2), m1, o1 + 64 * h, s * 64, e, full_a(st));
+                                }
+                            } else {
+                                tma_load_3d(a, m0, s * (kMx ? 128 : 64), o0, e, full_a(st));
+                                tma_load_3d(a + kTileBytes, m1, s * (kMx ? 128 : 64), o1, e, full_a(st));
+                            }
                         }
                         if (++st == sp.stages) st = 0, par ^= 1u;
                     }
                 }
             }
-            if (!ok) {   // copies in flight land before the CTA leaves
-                fail();
-                for (int q = 0; q < sp.stages && q < n; ++q)
-                    mbar_wait(full_a(q), ((n - q + sp.stages - 1) / sp.stages - 1) & 1u, nullptr, mxf4_dev::kDrainNs);
-            }
+        }
+        if (!ok) {   // copies in flight land before the CTA leaves
+            if (issue) fail();
+            for (int q = 0; q < sp.stages && q < n; ++q)
+                mbar_wait(full_a(q), ((n - q + sp.stages - 1) / sp.stages - 1) & 1u, nullptr, mxf4_dev::kDrainNs);
         }
     } else if (warp == 5) {
         // -------------------------------------------------------------- MMA
-        if (lane == 0) {
-            int st = 0, buf = 0;
-            uint32_t par = 0, bpar = 0;
-            bool ok = true;
-            const uint32_t tsa = tmem + 4 * sp.acc_cols, tsb = tsa + 16;
-            for (int ph = 0; ph < 2 && ok; ++ph) for (int i = 0; ok; ++i) {
-                const int part = part_at(ph, i);
+        const bool issue = elect_one();
+        int st = 0, buf = 0;
+        uint32_t par = 0, bpar = 0;
+        bool ok = true;
+        const uint32_t tsa = tmem + 4 * sp.acc_cols, tsb = tsa + 16;
+        for (int ph = 0; ph < 2 && ok; ++ph) {
+            const int k64 = ((ph ? p.F : p.D) + 63) >> 6;
+            for (int i = 0; ok; ++i) {
+                const int part = __shfl_sync(~0u, part_at(ph, i), 0);
                 if (part < 0) ok = false;
                 if (part < 0 || part >= parts) break;
                 const int64_t hi = phase[ph].start(part + 1);
-                const int k64 = ((ph ? p.F : p.D) + 63) >> 6;
                 for (int64_t at = phase[ph].start(part); at < hi && ok;) {
                     const Segment g = segment(ph, at, hi);
                     at += g.s1 - g.s0;
@@ -308,43 +313,50 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
                         if (!ok) break;
                         tc_fence_after();
                         const uint32_t a = base + st * sp.stage_bytes, b = a + 2 * kTileBytes;
-                        const int nk = min(4, kMx ? k64 - 4 * s : 4);
-                        if (kMx) {
-                            const uint32_t fa = b + sp.b_bytes, fb = fa + 4 * mxf4_dev::kScaleTile;
-                            for (int q = 0; q < (nk + 1) / 2; ++q) {
-                                const uint32_t at = q * mxf4_dev::kScaleTile;
-                                mxf4_dev::tmem_copy_scales(tsa + 4 * q, mxf4_dev::scale_desc(fa + at));
-                                mxf4_dev::tmem_copy_scales(tsa + 8 + 4 * q, mxf4_dev::scale_desc(fa + 2 * mxf4_dev::kScaleTile + at));
-                                mxf4_dev::tmem_copy_scales(tsb + 4 * q, mxf4_dev::scale_desc(fb + at));
-                            }
-                        }
+                        // (descriptors count 16 bytes: 32 of K, or 16 rows of K, a step; 32 a scale tile)
+                        const uint64_t da = kFmt == kStreamCols ? umma_desc_sw128(a, 8192, 1024) : umma_desc_sw128(a, 16, 1024);
+                        const uint64_t db = umma_desc_sw128(b, 16, 1024);
+                        const uint64_t fa = mxf4_dev::scale_desc(b + sp.b_bytes), fb = fa + 4 * 32;
+                        if (issue) {
+                            const int nk = kMx ? min(4, k64 - 4 * s) : 4;
+                            if (kMx) {
 #pragma unroll
-                        for (int t = 0; t < 2; ++t)
-                            for (int q = 0; q < nk; ++q) {
-                                const uint32_t at = a + t * kTileBytes;
-                                const uint64_t da = kFmt == kStreamCols ? umma_desc_sw128(at + q * 2048, 8192, 1024)
-                                                                        : umma_desc_sw128(at + q * 32, 16, 1024);
-                                const uint64_t db = umma_desc_sw128(b + q * 32, 16, 1024);
-                                const uint32_t acc = s > g.s0 || q > 0;
-                                if (kMx)
-                                    mxf4_dev::umma_mxf4(d + t * sp.acc_cols, da, db, q & 1 ? id1 : id0, tsa + 8 * t + 4 * (q >> 1),
-                                                        tsb + 4 * (q >> 1), acc);
-                                else
-                                    umma_f16(d + t * sp.acc_cols, da, db, id0, acc);
+                                for (int q = 0; q < 2; ++q) {
+                                    if (2 * q >= nk) break;
+                                    mxf4_dev::tmem_copy_scales(tsa + 4 * q, fa + 32 * q);
+                                    mxf4_dev::tmem_copy_scales(tsa + 8 + 4 * q, fa + 64 + 32 * q);
+                                    mxf4_dev::tmem_copy_scales(tsb + 4 * q, fb + 32 * q);
+                                }
                             }
-                        umma_commit(empty(st));
+#pragma unroll
+                            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    if (q >= nk) break;
+                                    const uint64_t at = da + t * (kTileBytes / 16) + q * (kFmt == kStreamCols ? 128 : 2);
+                                    const uint32_t acc = s > g.s0 || q > 0;
+                                    if (kMx)
+                                        mxf4_dev::umma_mxf4(d + t * sp.acc_cols, at, db + 2 * q, q & 1 ? id1 : id0,
+                                                            tsa + 8 * t + 4 * (q >> 1), tsb + 4 * (q >> 1), acc);
+                                    else
+                                        umma_f16(d + t * sp.acc_cols, at, db + 2 * q, id0, acc);
+                                }
+                            umma_commit(empty(st));
+                        }
                         if (++st == sp.stages) st = 0, par ^= 1u;
                     }
                     if (!ok) break;
-                    umma_commit(tfull(buf));
+                    if (issue) umma_commit(tfull(buf));
                     if (++buf == 2) buf = 0, bpar ^= 1u;
                 }
             }
-            if (!ok) {   // MMAs in flight end before the CTA's memory goes
+        }
+        if (!ok) {   // MMAs in flight end before the CTA's memory goes
+            if (issue) {
                 fail();
                 umma_commit(drain);
-                mbar_wait(drain, 0, nullptr, mxf4_dev::kDrainNs);
             }
+            mbar_wait(drain, 0, nullptr, mxf4_dev::kDrainNs);
         }
     } else if (warp >= 6) {
         // ---------------------------------------------------- narrow side

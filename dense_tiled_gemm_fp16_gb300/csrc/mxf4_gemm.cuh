@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_mxf4_tile(const __grid_cons
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const uint32_t bn = p.bn, sbytes = gemm_stage_bytes(p.bn);
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 16u * s; };
@@ -156,62 +156,69 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_mxf4_tile(const __grid_cons
         atomicExch(p.status, GEMM_F16_ERR_TIMEOUT);
     };
     if (warp == 4) {
-        if (lane == 0) {
-            int st = 0;
-            uint32_t ph = 0;
-            const uint8_t* sa = p.sfa + (m0 >> 7) * p.kt * kScaleTile;
-            const uint8_t* sb = p.sfb + (n0 >> 7) * p.kt * kScaleTile;
-            bool ok = true;
-            int issued = 0;
-            for (int s = s_lo; s < s_hi; ++s, ++issued) {
-                ok = mbar_wait(empty(st), ph ^ 1u, abort, p.timeout_ns);
-                if (!ok) break;
-                const uint32_t a = base + st * sbytes, b = a + kABytes, fa = b + bn * 128, fb = fa + kSfBytes;
-                // (an odd last scale tile: the second one is not this row tile's)
-                const uint32_t sf = min(static_cast<int64_t>(2), p.kt - 2 * s) * kScaleTile;
+        const bool issue = elect_one();
+        int st = 0;
+        uint32_t ph = 0;
+        const uint8_t* sa = p.sfa + (m0 >> 7) * p.kt * kScaleTile;
+        const uint8_t* sb = p.sfb + (n0 >> 7) * p.kt * kScaleTile;
+        bool ok = true;
+        int issued = 0;
+        for (int s = s_lo; s < s_hi; ++s, ++issued) {
+            ok = mbar_wait(empty(st), ph ^ 1u, abort, p.timeout_ns);
+            if (!ok) break;
+            const uint32_t a = base + st * sbytes, b = a + kABytes, fa = b + bn * 128, fb = fa + kSfBytes;
+            // (an odd last scale tile: the second one is not this row tile's)
+            const uint32_t sf = min(static_cast<int64_t>(2), p.kt - 2 * s) * kScaleTile;
+            if (issue) {
                 mbar_arrive_expect_tx(full(st), kABytes + bn * 128 + 2 * sf);
                 tma_load_2d(a, &p.tmA, s * 128, static_cast<int32_t>(m0), full(st));
                 tma_load_2d(b, &p.tmB, s * 128, static_cast<int32_t>(n0), full(st));
                 bulk_load(fa, sa + static_cast<int64_t>(s) * kSfBytes, sf, full(st));
                 bulk_load(fb, sb + static_cast<int64_t>(s) * kSfBytes, sf, full(st));
-                if (++st == p.stages) st = 0, ph ^= 1u;
             }
-            if (!ok) {   // copies in flight land before the CTA leaves
-                fail();
-                for (int q = 0; q < p.stages && q < issued; ++q)
-                    mbar_wait(full(q), ((issued - q + p.stages - 1) / p.stages - 1) & 1u, nullptr, kDrainNs);
-            }
+            if (++st == p.stages) st = 0, ph ^= 1u;
+        }
+        if (!ok) {   // copies in flight land before the CTA leaves
+            if (issue) fail();
+            for (int q = 0; q < p.stages && q < issued; ++q)
+                mbar_wait(full(q), ((issued - q + p.stages - 1) / p.stages - 1) & 1u, nullptr, kDrainNs);
         }
     } else if (warp == 5) {
-        if (lane == 0) {
-            int st = 0;
-            uint32_t ph = 0;
-            const uint32_t tsa = tmem + bn, tsb = tsa + 8;
-            const uint32_t id0 = idesc_mxf4(128, bn, 0), id1 = idesc_mxf4(128, bn, 1);
-            bool ok = !p.test_stall || mbar_wait(never, 0, abort, p.timeout_ns);
-            for (int s = s_lo; s < s_hi && ok; ++s) {
-                ok = mbar_wait(full(st), ph, abort, p.timeout_ns);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t a = base + st * sbytes, b = a + kABytes, fa = b + bn * 128, fb = fa + kSfBytes;
-                const uint64_t da = umma_desc_sw128(a, 16, 1024), db = umma_desc_sw128(b, 16, 1024);
+        const bool issue = elect_one();
+        int st = 0;
+        uint32_t ph = 0;
+        const uint32_t tsa = tmem + bn, tsb = tsa + 8;
+        const uint32_t id0 = idesc_mxf4(128, bn, 0), id1 = idesc_mxf4(128, bn, 1);
+        bool ok = !p.test_stall || mbar_wait(never, 0, abort, p.timeout_ns);
+        for (int s = s_lo; s < s_hi && ok; ++s) {
+            ok = mbar_wait(full(st), ph, abort, p.timeout_ns);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t a = base + st * sbytes, b = a + kABytes, fa = b + bn * 128, fb = fa + kSfBytes;
+            const uint64_t da = umma_desc_sw128(a, 16, 1024), db = umma_desc_sw128(b, 16, 1024);
+            const uint64_t dfa = scale_desc(fa), dfb = scale_desc(fb);   // (16-byte units: 32 a tile)
+            if (issue) {
                 const int n64 = min(4, p.k64 - 4 * s);
-                for (int h = 0; h < (n64 + 1) / 2; ++h) {
-                    tmem_copy_scales(tsa + 4 * h, scale_desc(fa + h * kScaleTile));
-                    tmem_copy_scales(tsb + 4 * h, scale_desc(fb + h * kScaleTile));
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (2 * h >= n64) break;
+                    tmem_copy_scales(tsa + 4 * h, dfa + 32 * h);
+                    tmem_copy_scales(tsb + 4 * h, dfb + 32 * h);
                 }
-                for (int q = 0; q < n64; ++q)
-                    umma_mxf4(tmem, da + 2 * q, db + 2 * q, q & 1 ? id1 : id0, tsa + 4 * (q >> 1), tsb + 4 * (q >> 1),
-                              s > s_lo || q > 0);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (q < n64)
+                        umma_mxf4(tmem, da + 2 * q, db + 2 * q, q & 1 ? id1 : id0, tsa + 4 * (q >> 1), tsb + 4 * (q >> 1),
+                                  s > s_lo || q > 0);
                 umma_commit(empty(st));
-                if (++st == p.stages) st = 0, ph ^= 1u;
             }
-            umma_commit(done);
-            if (!ok) {
-                fail();
-                mbar_wait(done, 0, nullptr, kDrainNs);
-            }
+            if (++st == p.stages) st = 0, ph ^= 1u;
         }
+        if (issue) {
+            umma_commit(done);
+            if (!ok) fail();
+        }
+        if (!ok) mbar_wait(done, 0, nullptr, kDrainNs);
     } else {
         const bool ok = mbar_wait(done, 0, abort, p.timeout_ns);
         if (!ok) fail();
@@ -347,7 +354,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_mxf4_pair(const __grid_c
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 16u * s; };
@@ -399,20 +406,21 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_mxf4_pair(const __grid_c
     };
 
     if (warp == 8) {
-        if (lane == 0) {
-            int st = 0;
-            uint32_t par = 0;
-            bool ok = true;
-            for (int64_t t = blockIdx.x >> 1; t < tiles && ok; t += clusters) {
-                int64_t m0, n0;
-                place(t, &m0, &n0);
-                const int32_t am = static_cast<int32_t>(m0 + rank * 128), bm = static_cast<int32_t>(n0 + rank * (kBN / 2));
-                const int32_t sa = static_cast<int32_t>(am >> 7) * p.kt, sb = static_cast<int32_t>(n0 >> 7) * p.kt;
-                for (int s = 0; s < p.steps; ++s) {
-                    ok = mbar_wait_cluster(empty(st), par ^ 1u, abort, p.timeout_ns);
-                    if (!ok) break;
-                    const uint32_t a = base + st * S::kStage, b = a + kABytes, fa = b + S::kB, fb = fa + kSfBytes;
-                    const uint32_t bar = mapa_shared(full(st), 0);
+        const bool issue = elect_one();
+        int st = 0;
+        uint32_t par = 0;
+        bool ok = true;
+        for (int64_t t = blockIdx.x >> 1; t < tiles && ok; t += clusters) {
+            int64_t m0, n0;
+            place(t, &m0, &n0);
+            const int32_t am = static_cast<int32_t>(m0 + rank * 128), bm = static_cast<int32_t>(n0 + rank * (kBN / 2));
+            const int32_t sa = static_cast<int32_t>(am >> 7) * p.kt, sb = static_cast<int32_t>(n0 >> 7) * p.kt;
+            for (int s = 0; s < p.steps; ++s) {
+                ok = mbar_wait_cluster(empty(st), par ^ 1u, abort, p.timeout_ns);
+                if (!ok) break;
+                const uint32_t a = base + st * S::kStage, b = a + kABytes, fa = b + S::kB, fb = fa + kSfBytes;
+                const uint32_t bar = mapa_shared(full(st), 0);
+                if (issue) {
                     if (rank == 0) mbar_arrive_expect_tx(full(st), 2 * S::kStage);
                     tma_load_2d_pair(a, &p.tmA, s * 128, am, bar);
                     tma_load_2d_pair(b, &p.tmB, s * 128, bm, bar);
@@ -420,17 +428,18 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_mxf4_pair(const __grid_c
                     tma_load_2d_pair(fa, &p.tmSA, 0, sa + 2 * s, bar);
 #pragma unroll
                     for (int h = 0; h < kBN / 128; ++h) tma_load_2d_pair(fb + h * kSfBytes, &p.tmSB, 0, sb + h * p.kt + 2 * s, bar);
-                    if (++st == S::kStages) st = 0, par ^= 1u;
                 }
-            }
-            if (!ok) {   // copies in flight land before the pair leaves: far longer than any takes
-                fail();
-                const uint64_t t0 = globaltimer_ns();
-                while (globaltimer_ns() - t0 < 5000000ull) __nanosleep(100000);
+                if (++st == S::kStages) st = 0, par ^= 1u;
             }
         }
+        if (!ok && issue) {   // copies in flight land before the pair leaves: far longer than any takes
+            fail();
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < 5000000ull) __nanosleep(100000);
+        }
     } else if (warp == 9) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
+            const bool issue = elect_one();
             int st = 0, acc = 0;
             uint32_t par = 0, rpar = 0;
             bool ok = !p.test_stall || mbar_wait(never, 0, abort, p.timeout_ns);
@@ -442,7 +451,6 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_mxf4_pair(const __grid_c
                     ok = mbar_wait_cluster(room, rpar, abort, p.timeout_ns);
                     if (!ok) break;
                     rpar ^= 1u;
-                    tc_fence_after();
                 }
                 first = false;
                 const uint32_t d = tmem + (acc ? S::kAcc1 : 0u);
@@ -452,26 +460,35 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_mxf4_pair(const __grid_c
                     tc_fence_after();
                     const uint32_t a = base + st * S::kStage, b = a + kABytes, fa = b + S::kB, fb = fa + kSfBytes;
                     const uint64_t da = umma_desc_sw128(a, 16, 1024), db = umma_desc_sw128(b, 16, 1024);
-                    const int n64 = min(4, p.k64 - 4 * s);
-                    for (int h = 0; h < (n64 + 1) / 2; ++h) {
-                        tmem_copy_scales_pair(tsa + 4 * h, scale_desc(fa + h * kScaleTile));
+                    const uint64_t dfa = scale_desc(fa), dfb = scale_desc(fb);   // (16-byte units: 32 a tile)
+                    if (issue) {
+                        const int n64 = min(4, p.k64 - 4 * s);
 #pragma unroll
-                        for (int j = 0; j < kBN / 128; ++j)
-                            tmem_copy_scales_pair(tsb + (kBN / 32) * h + 4 * j, scale_desc(fb + j * kSfBytes + h * kScaleTile));
+                        for (int h = 0; h < 2; ++h) {
+                            if (2 * h >= n64) break;
+                            tmem_copy_scales_pair(tsa + 4 * h, dfa + 32 * h);
+#pragma unroll
+                            for (int j = 0; j < kBN / 128; ++j)
+                                tmem_copy_scales_pair(tsb + (kBN / 32) * h + 4 * j, dfb + 64 * j + 32 * h);
+                        }
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (q < n64)
+                                umma_mxf4_pair(d, da + 2 * q, db + 2 * q, q & 1 ? id1 : id0, tsa + 4 * (q >> 1),
+                                               tsb + (kBN / 32) * (q >> 1), s > 0 || q > 0);
+                        umma_commit_pair_mc(empty(st), 0x3);
                     }
-                    for (int q = 0; q < n64; ++q)
-                        umma_mxf4_pair(d, da + 2 * q, db + 2 * q, q & 1 ? id1 : id0, tsa + 4 * (q >> 1),
-                                       tsb + (kBN / 32) * (q >> 1), s > 0 || q > 0);
-                    umma_commit_pair_mc(empty(st), 0x3);
                     if (++st == S::kStages) st = 0, par ^= 1u;
                 }
                 if (!ok) break;
-                umma_commit_pair_mc(tfull + 8 * acc, 0x3);
+                if (issue) umma_commit_pair_mc(tfull + 8 * acc, 0x3);
                 acc ^= 1;
             }
             if (!ok) {
-                fail();
-                umma_commit_pair_mc(drain, 0x1);
+                if (issue) {
+                    fail();
+                    umma_commit_pair_mc(drain, 0x1);
+                }
                 mbar_wait_cluster(drain, 0, nullptr, kDrainNs);
             }
         }

@@ -23,6 +23,20 @@ __device__ __forceinline__ uint64_t globaltimer_ns()
     return t;
 }
 
+// Warp-wide issue.  TMA copies and tcgen05 instructions take their operands
+// from uniform registers.  Issued by one thread from code that only it runs, each
+// operand is moved there first, some 70 to 110 cycles an instruction in all;
+// where the whole warp computes them and one elected lane issues, they are
+// computed in place.
+__device__ __forceinline__ int uniform_warp() { return __shfl_sync(~0u, static_cast<int>(threadIdx.x >> 5), 0); }
+
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // ------------------------------------------------------------------ mbarrier
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
 {
