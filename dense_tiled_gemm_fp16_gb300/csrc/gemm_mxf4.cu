@@ -56,18 +56,25 @@ gemm_f16_status launch_quantize(const mxf4_dev::QuantParams& p, int64_t batch, c
     const int64_t tiles = p.row_tiles * p.col_tiles;
     if (tiles > INT32_MAX) return GEMM_F16_ERR_INVALID_VALUE;
     const dim3 grid(static_cast<unsigned>(tiles), 1, static_cast<unsigned>(batch));
-    return launch_kernel(p.sk == 1 ? mxf4_dev::quantize_rows<T> : mxf4_dev::quantize_strided<T>, grid,
-                         mxf4_dev::kConvThreads, 0, 1, stream, p);
+    const bool vec = aligned(p.x, 16) && p.sr * sizeof(T) % 16 == 0 && p.sb * sizeof(T) % 16 == 0;
+    const bool pair = sizeof(T) == 2 && p.sr == 1 && p.sk % 2 == 0 && p.sb % 2 == 0 && aligned(p.x, 4);
+    auto kernel = p.sk != 1 ? mxf4_dev::quantize_strided<T, false>
+                  : vec     ? mxf4_dev::quantize_rows<T, true>
+                            : mxf4_dev::quantize_rows<T, false>;
+    if constexpr (sizeof(T) == 2) {
+        if (p.sk != 1 && pair) kernel = mxf4_dev::quantize_strided<T, true>;
+    }
+    return launch_kernel(kernel, grid, mxf4_dev::kConvThreads, 0, 1, stream, p);
 }
 
 template <typename T>
 gemm_f16_status launch_dequantize(const mxf4_dev::DequantParams& p, int64_t batch, cudaStream_t stream)
 {
-    const int64_t blocks = cdiv(p.rows * p.k, 8 * mxf4_dev::kConvThreads);
+    const int64_t blocks = cdiv(p.rows, mxf4_dev::kDequantRows) * p.col_tiles;
     if (blocks > INT32_MAX) return GEMM_F16_ERR_INVALID_VALUE;
     const dim3 grid(static_cast<unsigned>(blocks), 1, static_cast<unsigned>(batch));
-    return launch_kernel(p.k % 8 == 0 ? mxf4_dev::dequantize<T, true> : mxf4_dev::dequantize<T, false>, grid,
-                         mxf4_dev::kConvThreads, 0, 1, stream, p);
+    return launch_kernel(p.k % 8 == 0 && aligned(p.y, 16) ? mxf4_dev::dequantize<T, true> : mxf4_dev::dequantize<T, false>,
+                         grid, mxf4_dev::kConvThreads, 0, 1, stream, p);
 }
 
 // Dynamic shared memory above 48 KB is allowed once per device and kernel.
@@ -120,7 +127,7 @@ gemm_f16_status run_quantize(const void* x, int dtype, int64_t sb, int64_t sr, i
                              int64_t rows, int64_t k, int64_t batch, const Sizes& s, cudaStream_t stream)
 {
     const mxf4_dev::QuantParams p{x, sb, sr, sk, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales), rows, k,
-                                  s.pitch, s.kt, s.row_tiles, cdiv(k, mxf4_dev::kTileVals)};
+                                  s.pitch, s.kt, s.row_tiles, cdiv(k, sk == 1 ? mxf4_dev::kTileVals : mxf4_dev::kStridedVals)};
     return dtype == MXF4_F16    ? launch_quantize<__half>(p, batch, stream)
            : dtype == MXF4_BF16 ? launch_quantize<__nv_bfloat16>(p, batch, stream)
                                 : launch_quantize<float>(p, batch, stream);
@@ -291,7 +298,7 @@ gemm_f16_status mxf4_dequantize(const void* codes, const void* scales, void* y, 
     if (!device_range_ok(y, bytes) || !device_range_ok(codes, s.code_bytes) || !device_range_ok(scales, s.scale_bytes))
         return GEMM_F16_ERR_INVALID_VALUE;
     const mxf4_dev::DequantParams p{static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), y, rows, k,
-                                    s.pitch, s.kt, s.row_tiles};
+                                    s.pitch, s.kt, s.row_tiles, cdiv(k + 7, mxf4_dev::kTileVals)};
     return dtype == MXF4_F16    ? launch_dequantize<__half>(p, batch, stream)
            : dtype == MXF4_BF16 ? launch_dequantize<__nv_bfloat16>(p, batch, stream)
                                 : launch_dequantize<float>(p, batch, stream);

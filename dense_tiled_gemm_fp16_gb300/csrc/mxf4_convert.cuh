@@ -13,6 +13,13 @@
 namespace mxf4_dev {
 
 constexpr int kTileRows = 128, kTileVals = 256, kConvThreads = 256;
+constexpr int kStridedVals = 256;  // values of a row in a tile of the strided form
+constexpr int kDequantRows = 64;   // rows a block writes
+
+template <bool kValue>
+struct Bool {
+    static constexpr bool value = kValue;
+};
 
 struct QuantParams {
     const void* x;
@@ -22,40 +29,71 @@ struct QuantParams {
     int64_t rows, k, pitch;   // pitch: code bytes a row
     int64_t kt;               // scale tiles along k
     int64_t row_tiles;        // ceil(rows / 128)
-    int64_t col_tiles;        // ceil(k / 256): blocks are numbered columns first
+    int64_t col_tiles;        // tiles along k
 };
 
-// 8 values of one row from `i` on as words of T (2 or 4 bytes a value), values
-// from `k` on zero.  The row has unit stride; `vec` says its start and so every
-// 8th value is 16-byte aligned.
-template <typename T>
-__device__ __forceinline__ void load8(const T* row, int64_t i, int64_t k, bool vec, uint32_t* w)
+// Sixteen bytes from byte `o` (0, 2, .. 14) of 32.
+__device__ __forceinline__ void funnel16(const uint32_t* in, uint32_t o, uint32_t* out)
 {
-    constexpr int kWords = 8 * sizeof(T) / 4;
-    if (vec && i + 8 <= k) {
+    uint32_t w[6], v[5];
 #pragma unroll
-        for (int c = 0; c < kWords / 4; ++c) {
-            const uint4 v = ld_nc_v4(row + i + c * (16 / sizeof(T)));
+    for (int c = 0; c < 6; ++c) w[c] = o & 8u ? in[c + 2] : in[c];
+#pragma unroll
+    for (int c = 0; c < 5; ++c) v[c] = o & 4u ? w[c + 1] : w[c];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) out[c] = __funnelshift_r(v[c], v[c + 1], (o & 2u) * 8u);
+}
+
+// The words of 8 values of a row of unit stride, value `i` first, values from
+// `k` on undefined (mask_tail): aligned 16-byte loads, one more than the values
+// fill where the row starts at another place, each holding at least one of them.
+// kVec: every row starts aligned.
+template <typename T, bool kVec>
+__device__ __forceinline__ void load8(const T* row, int64_t i, int64_t k, uint32_t* w)
+{
+    constexpr int kLoads = sizeof(T) / 2;   // of a row that starts aligned
+    if constexpr (kVec) {
+#pragma unroll
+        for (int c = 0; c < kLoads; ++c) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (i + c * (16 / static_cast<int>(sizeof(T))) < k) v = ld_nc_v4(row + i + c * (16 / sizeof(T)));
             w[4 * c] = v.x, w[4 * c + 1] = v.y, w[4 * c + 2] = v.z, w[4 * c + 3] = v.w;
         }
-        return;
-    }
-#pragma unroll
-    for (int c = 0; c < kWords; ++c) w[c] = 0u;
-    if (sizeof(T) == 4) {
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-            if (i + c < k) w[c] = ld_nc_u32(row + i + c);
     } else {
+        uint32_t t[4 * (kLoads + 1)];
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-            if (i + c < k) w[c >> 1] |= static_cast<uint32_t>(ld_nc_u16(row + i + c)) << (16 * (c & 1));
+        for (int c = 0; c < 4 * (kLoads + 1); ++c) t[c] = 0u;
+        const uintptr_t at = reinterpret_cast<uintptr_t>(row + i);
+        const uint32_t o = at & 15u;
+        const uint4* p = reinterpret_cast<const uint4*>(at - o);
+        const intptr_t bytes = i < k ? static_cast<intptr_t>(min(static_cast<int64_t>(8), k - i)) * static_cast<intptr_t>(sizeof(T)) + o : 0;
+#pragma unroll
+        for (int c = 0; c <= kLoads; ++c)
+            if (16 * c < bytes) {
+                const uint4 v = ld_nc_v4(p + c);
+                t[4 * c] = v.x, t[4 * c + 1] = v.y, t[4 * c + 2] = v.z, t[4 * c + 3] = v.w;
+            }
+#pragma unroll
+        for (int c = 0; c < kLoads; ++c) funnel16(t + 4 * c, o, w + 4 * c);
+    }
+}
+
+// Values from `n` on of 8 set to zero.
+template <typename T>
+__device__ __forceinline__ void mask_tail(uint32_t* w, int64_t n)
+{
+#pragma unroll
+    for (int c = 0; c < 8 * static_cast<int>(sizeof(T)) / 4; ++c) {
+        if (sizeof(T) == 4)
+            w[c] = c < n ? w[c] : 0u;
+        else
+            w[c] = 2 * c + 1 < n ? w[c] : 2 * c < n ? w[c] & 0xFFFFu : 0u;
     }
 }
 
 // Unit stride along k: a warp takes the 256 values of one row, 8 a lane, so its
 // loads and its 128 bytes of codes are contiguous; four lanes share a block.
-template <typename T>
+template <typename T, bool kVec>
 __global__ void __launch_bounds__(kConvThreads) quantize_rows(const QuantParams p)
 {
     __shared__ __align__(16) uint8_t sc[2 * kScaleTile];
@@ -66,38 +104,55 @@ __global__ void __launch_bounds__(kConvThreads) quantize_rows(const QuantParams 
     const T* x = static_cast<const T*>(p.x) + b * p.sb;
     uint8_t* codes = p.codes + b * p.rows * p.pitch;
     uint8_t* scales = p.scales + b * p.row_tiles * p.kt * kScaleTile;
-    const bool vec = (reinterpret_cast<uintptr_t>(x) | (static_cast<uint64_t>(p.sr) * sizeof(T))) % 16 == 0;
     const int64_t i = i0 + lane * 8;
     griddep_wait();
     griddep_launch_dependents();
     constexpr int kUnroll = sizeof(T) == 4 ? 2 : 4;
     constexpr int kWarps = kConvThreads / 32;
+    const T* src = x + (r0 + warp) * p.sr;
+    uint8_t* dst = codes + (r0 + warp) * p.pitch + (i >> 1);
+    // this lane's scale byte: block lane / 4 of the row, tile lane / 16
+    uint8_t* mine = sc + (lane >> 4) * kScaleTile + ((lane >> 2) & 3);
+    const bool some = (i >> 5) < (p.k + 31) / 32;
+    const int64_t step = kWarps * p.sr, cstep = kWarps * p.pitch;
+    auto rows = [&](auto whole) {   // whole: the tile lies inside the matrix
+        constexpr bool kWhole = decltype(whole)::value;
 #pragma unroll 1
-    for (int rr = warp; rr < kTileRows; rr += kWarps * kUnroll) {
-        uint32_t w[kUnroll][8 * sizeof(T) / 4];
+        for (int rr = warp; rr < kTileRows; rr += kWarps * kUnroll) {
+            uint32_t w[kUnroll][8 * sizeof(T) / 4];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int64_t r = r0 + rr + u * kWarps;
-            load8<T>(x + r * p.sr, r < p.rows ? i : p.k, p.k, vec, w[u]);
-        }
+            for (int u = 0; u < kUnroll; ++u) {
+                const int64_t k = kWhole || r0 + rr + u * kWarps < p.rows ? p.k : 0;
+                if (kWhole && kVec) {
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int lr = rr + u * kWarps;
-            const int64_t r = r0 + lr;
-            uint32_t top = top_bits<T>(w[u]);
-            top = max(top, __shfl_xor_sync(~0u, top, 1));
-            top = max(top, __shfl_xor_sync(~0u, top, 2));
-            const bool in = r < p.rows && (i >> 5) < (p.k + 31) / 32;
-            const uint32_t code = in ? scale_code<T>(top) : 0u;
-            if (in) *reinterpret_cast<uint32_t*>(codes + r * p.pitch + (i >> 1)) = codes_of<T>(w[u], code);
-            // lane / 4 is the block in the tile: four scale bytes of one row are one word
-            uint32_t four = code << (8 * ((lane >> 2) & 3));
-            four |= __shfl_xor_sync(~0u, four, 4);
-            four |= __shfl_xor_sync(~0u, four, 8);
-            if ((lane & 15) == 0)
-                *reinterpret_cast<uint32_t*>(sc + (lane >> 4) * kScaleTile + (lr & 31) * 16 + (lr >> 5) * 4) = four;
+                    for (unsigned c = 0; c < sizeof(T) / 2; ++c) {
+                        const uint4 v = ld_nc_v4(src + u * step + i + c * (16 / sizeof(T)));
+                        w[u][4 * c] = v.x, w[u][4 * c + 1] = v.y, w[u][4 * c + 2] = v.z, w[u][4 * c + 3] = v.w;
+                    }
+                } else {
+                    load8<T, kVec>(src + u * step, i, k, w[u]);
+                    if (!kWhole && i + 8 > k) mask_tail<T>(w[u], k - i);
+                }
+            }
+            src += kUnroll * step;
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int lr = rr + u * kWarps;
+                uint32_t top = top_bits<T>(w[u]);
+                top = max(top, __shfl_xor_sync(~0u, top, 1));
+                top = max(top, __shfl_xor_sync(~0u, top, 2));
+                const bool in = kWhole || (some && r0 + lr < p.rows);
+                const uint32_t code = in ? scale_code<T>(top) : 0u;
+                if (in) *reinterpret_cast<uint32_t*>(dst + u * cstep) = codes_of<T>(w[u], code);
+                if ((lane & 3) == 0) mine[(lr & 31) * 16 + (lr >> 5) * 4] = static_cast<uint8_t>(code);
+            }
+            dst += kUnroll * cstep;
         }
-    }
+    };
+    if (r0 + kTileRows <= p.rows && i0 + kTileVals <= p.k)
+        rows(Bool<true>());
+    else
+        rows(Bool<false>());
     __syncthreads();
     if (threadIdx.x < 64) {
         const int t = threadIdx.x >> 5;   // of the two scale tiles
@@ -110,67 +165,85 @@ __global__ void __launch_bounds__(kConvThreads) quantize_rows(const QuantParams 
 
 // Any strides (a transposed view has unit stride along the rows): a lane takes
 // a row and a warp 32 neighbouring rows, so that a unit row stride gives
-// contiguous loads; the codes of the tile are turned in shared memory.
-template <typename T>
+// contiguous loads; the codes of the tile are turned in shared memory.  A tile
+// is wide enough for whole 128-byte lines of codes: with half lines, 64 bytes a
+// row, a 65536 x 7168 fp16 matrix took 1.04 ms instead of 0.39.
+// kPair (16-bit types, unit stride along the rows, rows in aligned pairs): a lane
+// takes two neighbouring rows with each load.
+template <typename T, bool kPair>
 __global__ void __launch_bounds__(kConvThreads) quantize_strided(const QuantParams p)
 {
-    constexpr int kPitch = 128 + 16;   // bytes a row of the staged codes: 16-byte stores spread over the banks
+    constexpr int kPitch = kStridedVals / 2 + 16, kScTiles = kStridedVals / 128;   // bytes a row of the staged codes: 16-byte stores spread over the banks
     __shared__ __align__(16) uint8_t cs[kTileRows * kPitch];
-    __shared__ __align__(16) uint8_t sc[2 * kScaleTile];
+    __shared__ __align__(16) uint8_t sc[kScTiles * kScaleTile];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t rt = blockIdx.x / p.col_tiles;
-    const int64_t r0 = rt * kTileRows, i0 = (blockIdx.x - rt * p.col_tiles) * kTileVals;
+    const int64_t ct = blockIdx.x / p.row_tiles, rt = blockIdx.x - ct * p.row_tiles;   // (neighbours along the rows)
+    const int64_t r0 = rt * kTileRows, i0 = ct * kStridedVals;
     const int64_t b = blockIdx.z;
     const T* x = static_cast<const T*>(p.x) + b * p.sb;
     uint8_t* codes = p.codes + b * p.rows * p.pitch;
     uint8_t* scales = p.scales + b * p.row_tiles * p.kt * kScaleTile;
     griddep_wait();
     griddep_launch_dependents();
-    const int lr = (warp & 3) * 32 + lane;
+    constexpr int kLaneRows = kPair ? 2 : 1, kRowWarps = 4 / kLaneRows;   // warps side by side cover the tile's rows
+    const int lr = (warp % kRowWarps) * 32 * kLaneRows + lane * kLaneRows;
     const int64_t r = r0 + lr;
 #pragma unroll 1
-    for (int blk = warp >> 2; blk < kTileVals / 32; blk += 2) {
+    for (int blk = warp / kRowWarps; blk < kStridedVals / 32; blk += kConvThreads / 32 / kRowWarps) {
         const int64_t i = i0 + blk * 32;
-        uint32_t w[4][8 * sizeof(T) / 4];
+        uint32_t w[kLaneRows][4][8 * sizeof(T) / 4];
+        const T* src = x + r * p.sr + i * p.sk;
+        if constexpr (kPair) {
+            uint32_t v[32];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+            for (int c = 0; c < 32; ++c, src += p.sk) {
+                v[c] = 0u;
+                if (i + c < p.k && r < p.rows) v[c] = r + 1 < p.rows ? ld_nc_u32(src) : ld_nc_u16(src);
+            }
 #pragma unroll
-            for (unsigned c = 0; c < 8 * sizeof(T) / 4; ++c) w[q][c] = 0u;
-            if (r >= p.rows) continue;
+            for (int c = 0; c < 32; c += 2) {
+                w[0][c >> 3][(c & 7) >> 1] = __byte_perm(v[c], v[c + 1], 0x5410);
+                w[1][c >> 3][(c & 7) >> 1] = __byte_perm(v[c], v[c + 1], 0x7632);
+            }
+        } else {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const int64_t j = i + q * 8 + c;
-                if (j >= p.k) continue;
-                const T* src = x + r * p.sr + j * p.sk;
-                if (sizeof(T) == 4)
-                    w[q][c] = ld_nc_u32(src);
-                else
-                    w[q][c >> 1] |= static_cast<uint32_t>(ld_nc_u16(src)) << (16 * (c & 1));
+            for (int q = 0; q < 4; ++q) {
+#pragma unroll
+                for (unsigned c = 0; c < 8 * sizeof(T) / 4; ++c) w[0][q][c] = 0u;
+#pragma unroll
+                for (int c = 0; c < 8; ++c, src += p.sk) {
+                    if (r >= p.rows || i + q * 8 + c >= p.k) continue;
+                    if (sizeof(T) == 4)
+                        w[0][q][c] = ld_nc_u32(src);
+                    else
+                        w[0][q][c >> 1] |= static_cast<uint32_t>(ld_nc_u16(src)) << (16 * (c & 1));
+                }
             }
         }
-        const uint32_t top = max(max(top_bits<T>(w[0]), top_bits<T>(w[1])), max(top_bits<T>(w[2]), top_bits<T>(w[3])));
-        const uint32_t code = r < p.rows && i < p.k ? scale_code<T>(top) : 0u;
-        uint4 c4;
-        c4.x = codes_of<T>(w[0], code), c4.y = codes_of<T>(w[1], code);
-        c4.z = codes_of<T>(w[2], code), c4.w = codes_of<T>(w[3], code);
-        *reinterpret_cast<uint4*>(cs + lr * kPitch + blk * 16) = c4;
-        sc[(blk >> 2) * kScaleTile + lane * 16 + (warp & 3) * 4 + (blk & 3)] = static_cast<uint8_t>(code);
+#pragma unroll
+        for (int h = 0; h < kLaneRows; ++h) {
+            const uint32_t top = max(max(top_bits<T>(w[h][0]), top_bits<T>(w[h][1])), max(top_bits<T>(w[h][2]), top_bits<T>(w[h][3])));
+            const uint32_t code = r + h < p.rows && i < p.k ? scale_code<T>(top) : 0u;
+            uint4 c4;
+            c4.x = codes_of<T>(w[h][0], code), c4.y = codes_of<T>(w[h][1], code);
+            c4.z = codes_of<T>(w[h][2], code), c4.w = codes_of<T>(w[h][3], code);
+            *reinterpret_cast<uint4*>(cs + (lr + h) * kPitch + blk * 16) = c4;
+            sc[(blk >> 2) * kScaleTile + ((lr + h) & 31) * 16 + ((lr + h) >> 5) * 4 + (blk & 3)] = static_cast<uint8_t>(code);
+        }
     }
     __syncthreads();
-    const int64_t bytes = min(p.pitch - (i0 >> 1), static_cast<int64_t>(128));
-    for (int t = threadIdx.x; t < kTileRows * 8; t += kConvThreads) {
-        const int row = t >> 3, c = t & 7;
+    const int64_t bytes = min(p.pitch - (i0 >> 1), static_cast<int64_t>(kStridedVals / 2));
+    constexpr int kWords = kStridedVals / 32;   // 16-byte words of a row's codes
+    for (int t = threadIdx.x; t < kTileRows * kWords; t += kConvThreads) {
+        const int row = t / kWords, c = t % kWords;
         if (r0 + row < p.rows && c * 16 < bytes)
             *reinterpret_cast<uint4*>(codes + (r0 + row) * p.pitch + (i0 >> 1) + c * 16) =
                 *reinterpret_cast<const uint4*>(cs + row * kPitch + c * 16);
     }
-    if (threadIdx.x < 64) {
-        const int t = threadIdx.x >> 5;
-        const int64_t kt = (i0 >> 7) + t;
-        if (kt < p.kt)
-            reinterpret_cast<uint4*>(scales + (rt * p.kt + kt) * kScaleTile)[lane] =
-                reinterpret_cast<const uint4*>(sc + t * kScaleTile)[lane];
-    }
+    const int t = threadIdx.x >> 5;
+    if (t < kScTiles && (i0 >> 7) + t < p.kt)
+        reinterpret_cast<uint4*>(scales + (rt * p.kt + (i0 >> 7) + t) * kScaleTile)[lane] =
+            reinterpret_cast<const uint4*>(sc + t * kScaleTile)[lane];
 }
 
 struct DequantParams {
@@ -178,56 +251,94 @@ struct DequantParams {
     const uint8_t* scales;
     void* y;
     int64_t rows, k, pitch, kt, row_tiles;
+    int64_t col_tiles;   // of 256 values and the 7 that a row may begin before one
 };
 
-// Eight values of a row, 16 (fp32: 32) contiguous bytes a thread.  With k a
-// multiple of 8 the eight share a code word and a scale; otherwise the output's
-// rows start at odd places, and a thread takes 8 values of the flat output,
-// each with its own row, code and scale.
-template <typename T, bool kWhole>
+// A warp writes 256 neighbouring values of a row, 8 a lane, from the first
+// multiple of 8 values of the output's memory on, so that every full store is
+// aligned whatever the row's length; the codes are then taken from any nibble on
+// (two words and a shift), and 8 values may lie in two blocks.
+// kVec: every row starts aligned, so that 8 values are one word of codes.
+template <typename T, bool kVec>
 __global__ void __launch_bounds__(kConvThreads) dequantize(const DequantParams p)
 {
-    const int64_t b = blockIdx.z;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t rt = blockIdx.x / p.col_tiles, b = blockIdx.z;
+    const int64_t c0 = (blockIdx.x - rt * p.col_tiles) * 32 + lane;   // this lane's group of 8
     const uint8_t* codes = p.codes + b * p.rows * p.pitch;
     const uint8_t* scales = p.scales + b * p.row_tiles * p.kt * kScaleTile;
     T* y = static_cast<T*>(p.y) + b * p.rows * p.k;
-    const int64_t n = p.rows * p.k;
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t f = (static_cast<int64_t>(blockIdx.x) * kConvThreads + threadIdx.x) * 8;
-    if (f >= n) return;
-    int64_t r = f / p.k, i = f - r * p.k;
-    T v[8];
-    if (kWhole) {
-        uint32_t h[4];
-        halves_of(*reinterpret_cast<const uint32_t*>(codes + r * p.pitch + (i >> 1)), h);
-        const float s = scale_value(scales[scale_at(r, i >> 5, p.kt)]);
+    constexpr int kUnroll = 4, kWarps = kConvThreads / 32;
+    const int64_t r0 = rt * kDequantRows;
+    T* to = y + (r0 + warp) * p.k;
+    const uint8_t* from = codes + (r0 + warp) * p.pitch;
+    // a tile's 64 rows are half of a scale tile's: place of (row 0, block 0)
+    const uint8_t* srow = scales + (r0 >> 7) * p.kt * kScaleTile + ((r0 >> 5) & 3) * 4;
+    auto place = [&](int lr, int64_t blk) { return srow + (blk >> 2) * kScaleTile + (blk & 3) + (lr & 31) * 16 + (lr >> 5) * 4; };
+#pragma unroll 1
+    for (int rr = warp; rr < kDequantRows; rr += kUnroll * kWarps, to += kUnroll * kWarps * p.k, from += kUnroll * kWarps * p.pitch) {
+        uint32_t w[kUnroll][2], sc[kUnroll][2];
+        int64_t i0[kUnroll];
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-            v[c] = Elem<T>::from_f32(s * Elem<__half>::to_f32(c & 1 ? h[c >> 1] >> 16 : h[c >> 1] & 0xFFFFu));
-    } else {
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            v[c] = Elem<T>::from_f32(0.f);
-            if (f + c < n) {
-                const uint32_t byte = codes[r * p.pitch + (i >> 1)];
-                uint32_t h[4];
-                halves_of(byte >> (4 * (i & 1)) & 15u, h);
-                v[c] = Elem<T>::from_f32(scale_value(scales[scale_at(r, i >> 5, p.kt)]) *
-                                         Elem<__half>::to_f32(h[0] & 0xFFFFu));
+        for (int u = 0; u < kUnroll; ++u) {
+            const int lr = rr + u * kWarps;
+            const int64_t shift = kVec ? 0 : static_cast<int64_t>(reinterpret_cast<uintptr_t>(to + u * kWarps * p.k) / sizeof(T) & 7);
+            const int64_t i = c0 * 8 - shift;
+            i0[u] = r0 + lr < p.rows && i < p.k ? i : p.k;
+            w[u][0] = w[u][1] = sc[u][0] = sc[u][1] = 0u;
+            if (i0[u] >= p.k) continue;
+            const uint32_t* src = reinterpret_cast<const uint32_t*>(from + u * kWarps * p.pitch);
+            if (kVec) {
+                w[u][0] = __ldg(src + c0);
+                sc[u][0] = __ldg(place(lr, i >> 5));
+                continue;
             }
-            if (++i == p.k) i = 0, ++r;
+            const int64_t word = i >> 3, words = p.pitch >> 2;   // (word -1 holds nothing of the row)
+            if (word >= 0) w[u][0] = __ldg(src + word);
+            if (shift != 0 && word + 1 < words) w[u][1] = __ldg(src + word + 1);
+            const int64_t blk = max(i, static_cast<int64_t>(0)) >> 5, last = min(i + 7, p.k - 1) >> 5;
+            sc[u][0] = __ldg(place(lr, blk));
+            sc[u][1] = last != blk ? __ldg(place(lr, last)) : sc[u][0];
         }
-    }
-    // (the batch's matrices start wherever the previous one ends)
-    if (f + 8 <= n && reinterpret_cast<uintptr_t>(y + f) % 16 == 0) {
-        uint4 o[sizeof(T) / 2];
-        memcpy(o, v, sizeof(v));
 #pragma unroll
-        for (unsigned c = 0; c < sizeof(T) / 2; ++c) reinterpret_cast<uint4*>(y + f)[c] = o[c];
-    } else {
-        for (int c = 0; c < 8; ++c)
-            if (f + c < n) y[f + c] = v[c];
+        for (int u = 0; u < kUnroll; ++u) {
+            const int64_t i = i0[u];
+            if (i >= p.k) continue;
+            T* row = to + u * kWarps * p.k;
+            uint32_t h[4];
+            halves_of(kVec ? w[u][0] : __funnelshift_r(w[u][0], w[u][1], 4 * static_cast<uint32_t>(i & 7)), h);
+            T v[8];
+            uint4 o[sizeof(T) / 2];
+            const int turn = kVec ? 8 : 32 - static_cast<int>(i & 31);   // values of the first block
+            if (Elem<T>::kInf == 0x7C00u && sc[u][0] - 103u <= 39u && (kVec || sc[u][1] - 103u <= 39u)) {
+                // fp16 holds the factors (2^-24 to 2^15): one rounding, two values an instruction
+                auto half_scale = [](uint32_t c) { return c >= 113u ? (c - 112u) << 10 : 1u << (c - 103u); };
+                const uint32_t f0 = half_scale(sc[u][0]), f1 = kVec ? f0 : half_scale(sc[u][1]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t f = (2 * c < turn ? f0 : f1) | (2 * c + 1 < turn ? f0 : f1) << 16;
+                    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(h[c]) : "r"(h[c]), "r"(f));
+                }
+                o[0] = make_uint4(h[0], h[1], h[2], h[3]);
+            } else {
+                const float s0 = scale_value(sc[u][0]), s1 = kVec ? s0 : scale_value(sc[u][1]);
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    v[c] = Elem<T>::from_f32((c < turn ? s0 : s1) * Elem<__half>::to_f32(c & 1 ? h[c >> 1] >> 16 : h[c >> 1] & 0xFFFFu));
+                memcpy(o, v, sizeof(v));
+            }
+            if (kVec || (i >= 0 && i + 8 <= p.k)) {
+#pragma unroll
+                for (unsigned c = 0; c < sizeof(T) / 2; ++c) __stcs(reinterpret_cast<uint4*>(row + i) + c, o[c]);
+            } else {
+                memcpy(v, o, sizeof(v));
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    if (i + c >= 0 && i + c < p.k) row[i + c] = v[c];
+            }
+        }
     }
 }
 

@@ -87,15 +87,9 @@ __device__ __forceinline__ uint32_t scale_code(uint32_t top)
 
 // Eight values times 2^-s as e2m1 codes, the first in the low nibble: round to
 // nearest even, magnitudes above 6 saturate.  The products are exact but where
-// they fall below 2^-126, far under the rounding point 0.25.
-template <typename T>
-__device__ __forceinline__ uint32_t codes_of(const uint32_t* w, uint32_t code)
+// they are subnormal, far under the rounding point 0.25.
+__device__ __forceinline__ uint32_t codes_of_f32(const float* v)
 {
-    if (code == 255u) return 0u;
-    const float f = pow2f(127 - static_cast<int>(code));
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = value_of<T>(w, i) * f;
     uint32_t r;
     asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
@@ -106,6 +100,31 @@ __device__ __forceinline__ uint32_t codes_of(const uint32_t* w, uint32_t code)
         : "=r"(r)
         : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
     return r;
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t codes_of(const uint32_t* w, uint32_t code)
+{
+    if (code == 255u) return 0u;
+    uint32_t r;
+    if (Elem<T>::kInf == 0x7C00u && code >= 112u) {
+        // fp16 holds 2^-s up to 2^15 (largest magnitudes from 2^-13 on): two values an instruction
+        const uint32_t f = (142u - code) << 10, ff = f | f << 16;
+        asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t.reg .b32 p0, p1, p2, p3;\n\t"
+            "mul.rn.f16x2 p0, %1, %5;\n\tmul.rn.f16x2 p1, %2, %5;\n\t"
+            "mul.rn.f16x2 p2, %3, %5;\n\tmul.rn.f16x2 p3, %4, %5;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f16x2 b0, p0;\n\tcvt.rn.satfinite.e2m1x2.f16x2 b1, p1;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f16x2 b2, p2;\n\tcvt.rn.satfinite.e2m1x2.f16x2 b3, p3;\n\t"
+            "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+            : "=r"(r)
+            : "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(ff));
+        return r;
+    }
+    const float f = pow2f(127 - static_cast<int>(code));
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = value_of<T>(w, i) * f;
+    return codes_of_f32(v);
 }
 
 // Eight e2m1 codes (a 32-bit word) as four half2, exactly.

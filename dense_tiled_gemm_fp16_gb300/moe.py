@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 
-from .mxf4 import Mxf4Matrix, _empty, _on, _pkg, _stream, _torch
+from .mxf4 import Mxf4Matrix, _empty, _pkg, _run, _stream, _torch
 
 WEIGHT_F16, WEIGHT_MXF4 = 0, 1
 MAX_TOKENS, MAX_EXPERTS, MAX_TOP_K, MAX_DIM = 64, 512, 8, 32768
@@ -108,8 +108,8 @@ def moe_few(x, router, gate, up, down, top_k: int, act="silu", renormalize: bool
     space = _empty(need, t.uint8, device, stream)
     sxt, sxi = x.stride()
     sri, sre = router.stride()
-    _on(device, moe_f16, x.data_ptr(), sxt if T > 1 else D, sxi if D > 1 else 1, router.data_ptr(),
-        sri if D > 1 else (E + 7) // 8 * 8, sre if E > 1 else (D + 7) // 8 * 8, wg, wu, wd, T, D, F, E, top_k,
-        1 if renormalize else 0, code, y.data_ptr(), y.stride(0) if T > 1 else D, probs.data_ptr(), ids.data_ptr(),
-        space.data_ptr(), need, _stream(device, stream))
+    _run(device, "moe_f16", x.data_ptr(), sxt if T > 1 else D, sxi if D > 1 else 1, router.data_ptr(),
+         sri if D > 1 else (E + 7) // 8 * 8, sre if E > 1 else (D + 7) // 8 * 8, wg, wu, wd, T, D, F, E, top_k,
+         1 if renormalize else 0, code, y.data_ptr(), y.stride(0) if T > 1 else D, probs.data_ptr(), ids.data_ptr(),
+         space.data_ptr(), need, _stream(device, stream))
     return y, probs, ids

@@ -31,6 +31,7 @@ def declare(L) -> None:
 # module, and its C mirrors work without torch).
 _g = None
 _t = None
+_fns = {}   # functions of the library that the tensor forms have called
 
 
 def _pkg():
@@ -141,34 +142,43 @@ class Mxf4Matrix:
 
 
 def _dtype_code(dtype) -> int:
-    t = _torch()
+    t = _t or _torch()
     code = F16 if dtype is t.float16 else BF16 if dtype is t.bfloat16 else F32 if dtype is t.float32 else None
     if code is None:
         raise TypeError("MXFP4 conversions take float16, bfloat16 or float32")
     return code
 
 
-def _stream(device, stream):
-    return (stream if stream is not None else _torch().cuda.current_stream(device)).cuda_stream
+def _stream(device, stream) -> int:
+    """Handle of `stream`, or of the device's current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _t._C._cuda_getCurrentRawStream(device.index)
 
 
 def _empty(shape, dtype, device, stream):
     """torch.empty for `stream`: what the allocator hands out is ordered with
     the stream that will write it, the current one unless one is given."""
-    t = _torch()
+    t = _t or _torch()
     if stream is None:
         return t.empty(shape, dtype=dtype, device=device)
     with t.cuda.stream(stream):
         return t.empty(shape, dtype=dtype, device=device)
 
 
-def _on(device, call, *args):
-    """call(*args) with `device` current."""
-    t = _torch()
-    if device.index == t.cuda.current_device():
-        return call(*args)
-    with t.cuda.device(device):
-        return call(*args)
+def _run(device, name: str, *args) -> None:
+    """The library's function `name` with `device` current; raises on a status
+    that is not OK."""
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(_pkg().lib(), name)
+    if device.index == _t.cuda.current_device():
+        st = fn(*args)
+    else:
+        with _t.cuda.device(device):
+            st = fn(*args)
+    if st:
+        _pkg()._check(st, name)
 
 
 def mxf4_quantize(x, axis: int = -1, stream=None) -> Mxf4Matrix:
@@ -194,8 +204,8 @@ def mxf4_quantize(x, axis: int = -1, stream=None) -> Mxf4Matrix:
     data = _empty(nc + ns, _t.uint8, device, stream)
     q = Mxf4Matrix._of(data, ns, rows, k, batch if lead else None, device)
     # (a dimension of one element may carry any stride, a batch of stride 0 repeats)
-    _on(device, mxf4_quantize_ptr, x.data_ptr(), code, sb[0] if batch > 1 else 0, sr if rows > 1 else max(1, k),
-        sk if k > 1 else 1, q.codes_ptr, q.scales_ptr, rows, k, batch, _stream(device, stream))
+    _run(device, "mxf4_quantize", x.data_ptr(), code, sb[0] if batch > 1 else 0, sr if rows > 1 else max(1, k),
+         sk if k > 1 else 1, q.codes_ptr, q.scales_ptr, rows, k, batch, _stream(device, stream))
     return q
 
 
@@ -206,8 +216,8 @@ def mxf4_dequantize(q: Mxf4Matrix, dtype=None, stream=None):
     code = _dtype_code(dtype)
     device = q.device
     y = _empty(q.shape, dtype, device, stream)
-    _on(device, mxf4_dequantize_ptr, q.codes_ptr, q.scales_ptr, y.data_ptr(), code, q.rows, q.k, q.batch or 1,
-        _stream(device, stream))
+    _run(device, "mxf4_dequantize", q.codes_ptr, q.scales_ptr, y.data_ptr(), code, q.rows, q.k, q.batch or 1,
+         _stream(device, stream))
     return y
 
 
@@ -215,7 +225,7 @@ def mxf4_mm(a, b: Mxf4Matrix, bias=None, act="none", out=None, stream=None):
     """fp16 C[m, n] = act(sum_k a[m, k] b[n, k] + bias[n]): b an Mxf4Matrix
     [N, K], a an Mxf4Matrix [M, K] or a float16 tensor [M, K] that is quantised
     on the way; returns C."""
-    g, t = _pkg(), _torch()
+    g, t = _pkg(), _t or _torch()
     if not isinstance(b, Mxf4Matrix) or b.batch is not None:
         raise TypeError("mxf4_mm takes b as an Mxf4Matrix of two dimensions")
     held = isinstance(a, Mxf4Matrix)
@@ -240,13 +250,14 @@ def mxf4_mm(a, b: Mxf4Matrix, bias=None, act="none", out=None, stream=None):
         out = _empty((M, N), t.float16, device, stream)
     raw = _stream(device, stream)
     ldc = out.stride(0) if M > 1 else N
-    bp = 0 if bias is None else bias.data_ptr()
+    bp = None if bias is None else bias.data_ptr()
     if held:
-        _on(device, gemm_mxf4, a.codes_ptr, a.scales_ptr, b.codes_ptr, b.scales_ptr, bp, code, out.data_ptr(), ldc, M,
-            N, K, raw)
+        _run(device, "gemm_mxf4", a.codes_ptr, a.scales_ptr, b.codes_ptr, b.scales_ptr, bp, code, out.data_ptr(), ldc, M,
+             N, K, raw)
     else:
         sm, sk = a.stride()
-        work = _empty(sum(_bytes(M, K, 1)), t.uint8, device, stream)
-        _on(device, gemm_mxf4_a16, a.data_ptr(), sm if M > 1 else max(1, K), sk if K > 1 else 1, work.data_ptr(),
-            b.codes_ptr, b.scales_ptr, bp, code, out.data_ptr(), ldc, M, N, K, raw)
+        nc, ns = _bytes(M, K, 1)
+        work = _empty(nc + ns, t.uint8, device, stream)
+        _run(device, "gemm_mxf4_a16", a.data_ptr(), sm if M > 1 else max(1, K), sk if K > 1 else 1, work.data_ptr(),
+             b.codes_ptr, b.scales_ptr, bp, code, out.data_ptr(), ldc, M, N, K, raw)
     return out
