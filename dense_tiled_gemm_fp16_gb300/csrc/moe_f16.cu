@@ -133,8 +133,7 @@ bool allow_smem(const void* kernel, int slot, int bytes)
 template <int kLayout, int kPer>
 gemm_f16_status launch_route(const moe_dev::Params& p, cudaStream_t stream)
 {
-    const int chunks = p.dp >> 5, tiles = (p.E + 31) >> 5;
-    const int smem = ((chunks / moe_dev::kRouteCluster + 1) * 32 + 8) * 8 * 2 + moe_dev::kWarps * 32 * 8 * 4 + 8 * tiles * 32 * 4;
+    const int smem = moe_dev::RouteShape(p.dp, p.E, kLayout == moe_dev::kOutContiguous).bytes;
     const auto kernel = moe_dev::moe_route<kLayout, kPer>;
     if (!allow_smem(reinterpret_cast<const void*>(kernel), 2 * kLayout + (kPer > 2), smem)) return GEMM_F16_ERR_LAUNCH;
     const unsigned groups = static_cast<unsigned>((p.T + 7) / 8);
@@ -228,16 +227,17 @@ gemm_f16_status launch_stream(const moe_dev::Params& p, const Layout& l, uint8_t
     sp.xwords = static_cast<int32_t>(l.dw / 4);
     sp.hwords = static_cast<int32_t>(l.fw / 4);
     // Tokens of one reading of an expert's weights: all of them for few tokens,
-    // 16 otherwise; fewer leave the shared memory to the weights' ring.
-    sp.cap = p.T <= 4 ? 4 : p.T <= 8 ? 8 : 16;
+    // 16 otherwise, or as many as tensor memory has columns for next to y's sums;
+    // fewer leave the shared memory to the weights' ring.
+    sp.cap = p.T <= 4 ? 4 : p.T <= 8 ? 8 : kMx && p.T > 32 ? 12 : 16;
     sp.b_bytes = static_cast<int32_t>(round_up(kMx ? sp.cap * moe_dev::kPieces : std::max(16, 2 * sp.cap), 8) * 128);
     sp.stage_bytes = 2 * static_cast<int32_t>(moe_dev::kTileBytes) + sp.b_bytes + (kMx ? 6 * mxf4_dev::kScaleTile : 0);
-    const int tail = p.T * 256 * 4;
-    sp.stages = std::min(16, (kMaxSmem - kStaticSmem - 1024 - tail) / sp.stage_bytes);
+    sp.stages = std::min(16, (kMaxSmem - kStaticSmem - 1024) / sp.stage_bytes);
     sp.acc_cols = kMx ? static_cast<uint32_t>(round_up(sp.cap * moe_dev::kPieces, 8)) : 32;
-    const uint32_t need = 4 * sp.acc_cols + (kMx ? 24 : 0);
+    sp.y_col = 4 * sp.acc_cols + (kMx ? 24 : 0);
+    const uint32_t need = sp.y_col + 2 * ((p.T + 7) & ~7);
     sp.tmem_cols = need <= 64 ? 64 : need <= 128 ? 128 : need <= 256 ? 256 : 512;
-    const int smem = sp.stages * sp.stage_bytes + tail + 1024;
+    const int smem = sp.stages * sp.stage_bytes + 1024;
     const auto kernel = moe_dev::moe_stream<kFmt>;
     if (!allow_smem(reinterpret_cast<const void*>(kernel), 12 + kFmt, kMaxSmem - kStaticSmem)) return GEMM_F16_ERR_LAUNCH;
     return launch_kernel(kernel, dim3(static_cast<unsigned>(std::min(sms, moe_dev::kMaxParts))), moe_dev::kThreads, smem, 1,

@@ -54,14 +54,6 @@ __device__ __forceinline__ void mma16816(float* d, uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The 8x8 transpose of 16-bit elements held two a thread, a row a quad.
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t v)
-{
-    uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
-    return r;
-}
-
 __device__ __forceinline__ uint4 ld_smem_v4(uint32_t addr)
 {
     uint4 v;
@@ -150,184 +142,182 @@ __device__ __forceinline__ __half ld_nc_half(const __half* p) { return __ushort_
 // 2 experts contiguous (16-byte words in both).
 enum { kAnyStrides = 0, kInContiguous = 1, kOutContiguous = 2 };
 
-// Expert row of accumulator half `h` (rows g or g + 8) of instruction `mt` in a
-// 32-expert tile: with the experts contiguous, a thread's 16-byte word holds
-// experts 8c .. 8c + 7, whose pairs become the rows of four 8x8 transposes.
-template <int kLayout>
-__device__ __forceinline__ int expert_row(int mt, int h, int g)
-{
-    return kLayout == kOutContiguous ? 8 * (g >> 1) + 2 * (2 * mt + h) + (g & 1) : 16 * mt + 8 * h + g;
-}
-
-// Four blocks of 32 values, a value of each a lane, as kPieces MXFP4 columns: the
-// codes of column q of block j at codes[j] + q * pitch (16 bytes), its scale at
-// scales[j] + q * spitch; blocks from `count` on are not written.  Unlike a
-// quantised operand, whose largest magnitudes saturate (6 to 8 times 2^s), a
-// column's scale is a step larger there, so that no remainder is above half a
-// step of the grid, 1/5 of the largest magnitude.  A column waits for the one
-// before it (a maximum over the lanes, two conversions); four blocks at once
-// hide that, 17 -> 5 us for 64 tokens of 7168 values.
-__device__ __forceinline__ void split_blocks(float* v, int count, int lane, uint8_t* const* codes, int64_t pitch,
-                                             uint8_t* const* scales, int64_t spitch)
+// Four blocks of 32 values as kPieces MXFP4 columns; lane 8j + i holds values 4i
+// .. 4i + 3 of block j in v.  `codes`: this lane's two bytes of column 0, `pitch`
+// bytes to the next column; `scale`: its block's scale of column 0.  Blocks with
+// `on` false are not written.  Unlike a quantised operand, whose largest
+// magnitudes saturate (6 to 8 times 2^s), a column's scale is a step larger
+// there, so that no remainder is above half a step of the grid, 1/5 of the
+// largest magnitude.
+__device__ __forceinline__ void split_blocks(float* v, bool on, int lane, uint8_t* codes, int64_t pitch, uint8_t* scale,
+                                             int64_t spitch)
 {
 #pragma unroll 1
     for (int q = 0; q < kPieces; ++q) {
+        uint32_t top = 0u;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t top = __reduce_max_sync(~0u, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-            uint32_t code = mxf4_dev::scale_code<float>(top);
-            uint32_t e = 0;
-            if (code != 255u) {
-                code += (top & 0x7FFFFFu) > 0x400000u && code > 0u;   // above 6 * 2^s: mantissa above 1.5
-                const float t = v[j] * mxf4_dev::pow2f(127 - static_cast<int>(code));
-                uint32_t back;
-                asm("{\n\t.reg .b8 b;\n\t"
-                    "cvt.rn.satfinite.e2m1x2.f32 b, %3, %2;\n\t"
-                    "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-                    "mov.b32 %0, {b, b, b, b};\n\t}"
-                    : "=r"(e), "=r"(back)
-                    : "f"(t), "f"(0.f));
-                e &= 15u;
-                v[j] -= mxf4_dev::scale_value(code) * __half2float(__ushort_as_half(static_cast<unsigned short>(back)));
-            }
-            e |= __shfl_down_sync(~0u, e, 1) << 4;
-            if (j < count) {
-                if ((lane & 1) == 0) codes[j][q * pitch + (lane >> 1)] = static_cast<uint8_t>(e);
-                if (lane == 0) scales[j][q * spitch] = static_cast<uint8_t>(code);
-            }
+        for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+#pragma unroll
+        for (int s = 1; s < 8; s <<= 1) top = max(top, __shfl_xor_sync(~0u, top, s));
+        uint32_t code = mxf4_dev::scale_code<float>(top), e = 0;
+        if (code != 255u) {
+            code += (top & 0x7FFFFFu) > 0x400000u && code > 0u;   // above 6 * 2^s: mantissa above 1.5
+            const float f = mxf4_dev::pow2f(127 - static_cast<int>(code)), back = mxf4_dev::scale_value(code);
+            uint32_t h0, h1;
+            asm("{\n\t.reg .b8 b0, b1;\n\t"
+                "cvt.rn.satfinite.e2m1x2.f32 b0, %4, %3;\n\t"
+                "cvt.rn.satfinite.e2m1x2.f32 b1, %6, %5;\n\t"
+                "cvt.rn.f16x2.e2m1x2 %1, b0;\n\t"
+                "cvt.rn.f16x2.e2m1x2 %2, b1;\n\t"
+                "mov.b32 %0, {b0, b1, b0, b1};\n\t}"
+                : "=r"(e), "=r"(h0), "=r"(h1)
+                : "f"(v[0] * f), "f"(v[1] * f), "f"(v[2] * f), "f"(v[3] * f));
+            v[0] -= back * __half2float(__ushort_as_half(static_cast<unsigned short>(h0)));
+            v[1] -= back * __half2float(__ushort_as_half(static_cast<unsigned short>(h0 >> 16)));
+            v[2] -= back * __half2float(__ushort_as_half(static_cast<unsigned short>(h1)));
+            v[3] -= back * __half2float(__ushort_as_half(static_cast<unsigned short>(h1 >> 16)));
+        }
+        if (on) {
+            *reinterpret_cast<uint16_t*>(codes + q * pitch) = static_cast<uint16_t>(e);
+            if ((lane & 7) == 0) scale[q * spitch] = static_cast<uint8_t>(code);
         }
     }
 }
 
-// Eight router elements from `src` on, `step` apart, `n` of them in range.
-template <bool kVector>
-__device__ __forceinline__ uint4 load_eight(const __half* src, int64_t step, int n)
+// 16 bytes of fp16 at base + at to shared memory, `n` of the 8 values in range
+// (less: zeros).
+__device__ __forceinline__ void bring_eight(uint32_t dst, const __half* base, int64_t at, int64_t step, bool vector, int n)
 {
-    if (kVector && n >= 8) return ld_nc_v4(src);
+    const __half* src = base + (n > 0 ? at : 0);
+    if (vector) {
+        cp_async16(dst, src, 2 * max(0, min(8, n)));
+        return;
+    }
     uint32_t u[4] = {};
-#pragma unroll 1
     for (int i = 0; i < min(n, 8); ++i) {
         const uint32_t v = static_cast<uint32_t>(ld_nc_u16(src + i * step)) << (16 * (i & 1));
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (j == i >> 1) u[j] |= v;
+        for (int j = 0; j < 4; ++j) u[j] |= j == i >> 1 ? v : 0u;
     }
-    return make_uint4(u[0], u[1], u[2], u[3]);
+    st_smem_v4(dst, make_uint4(u[0], u[1], u[2], u[3]));
 }
+
+template <bool kTrans>
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t* a)
+{
+    if (kTrans)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]) : "r"(addr) : "memory");
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]) : "r"(addr) : "memory");
+}
+
+// How a cluster's CTA lays out its shared memory; the same on the host.
+struct RouteShape {
+    int width, kc, wpitch, xpitch;      // values of D a CTA takes at most, at a time; bytes a row of weights, tokens
+    int x, w, red, part, bytes;         // offsets
+    __host__ __device__ RouteShape(int dp, int experts, bool out_contiguous)
+    {
+        const int ep = (experts + 15) / 16 * 16;
+        width = ((dp >> 5) / kRouteCluster + 1) * 32;
+        const int most = (112 * 1024 / (2 * ep + 16)) / 32 * 32;
+        kc = width < most ? width : most;
+        wpitch = 2 * (out_contiguous ? ep : kc) + 16;
+        xpitch = 2 * width + 16;
+        x = 0;
+        w = x + 8 * xpitch;
+        red = w + (out_contiguous ? kc : ep) * wpitch;
+        part = red + (kWarps * 16 * 8 > kRouteCluster * ep ? kWarps * 16 * 8 : kRouteCluster * ep) * 4;
+        bytes = part + 8 * ep * 4;
+    }
+};
 
 // A cluster of 8 CTAs routes 8 tokens: CTA r sums the r-th part of D for all
 // experts and tokens, then takes token r: adds the 8 parts over distributed
-// shared memory and picks its experts.  Bound by latency, not by bytes: the
-// tokens' and the first router loads are under way together, and the code is
-// kept short (every instruction is fetched once, cold).  kPer: experts a lane
-// of the choosing warp looks at.
+// shared memory and picks its experts.  Bound by latency: the tokens' and the
+// router's parts are brought to shared memory at once, and the loops are not
+// unrolled (every instruction is fetched once, cold: with the loads and the
+// MMAs unrolled in registers this part took 7 us instead of 4).  kPer: experts
+// a lane of the choosing warp looks at.
 template <int kLayout, int kPer>
 __global__ void __launch_bounds__(kThreads) moe_route(const __grid_constant__ Params p)
 {
     extern __shared__ __align__(16) uint8_t smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_ctarank());
     const int t0 = (blockIdx.x / kRouteCluster) * kRouteCluster;
     const int nt = min(kRouteCluster, p.T - t0);
     const int chunks = p.dp >> 5;
     const int c_lo = chunks * rank / kRouteCluster, c_hi = chunks * (rank + 1) / kRouteCluster;
     const int k_lo = c_lo * 32, width = (c_hi - c_lo) * 32;
-    const int tiles = (p.E + 31) >> 5, ep = tiles * 32;
-    // shared: this part's tokens [8][width + 8] fp16, warp sums [16][32][8], logits [8][E rounded up]
-    const int xpitch = width + 8;
-    __half* xs = reinterpret_cast<__half*>(smem);
-    float* red = reinterpret_cast<float*>(smem + ((chunks / kRouteCluster + 1) * 32 + 8) * 8 * 2);
-    float* part = red + kWarps * 32 * 8;
+    const int tiles = (p.E + 15) >> 4, ep = tiles * 16;
+    constexpr bool kOut = kLayout == kOutContiguous;
+    const RouteShape sh(p.dp, p.E, kOut);
+    const uint32_t base = smem_u32(smem);
+    float* red = reinterpret_cast<float*>(smem + sh.red);     // [16 warps][16 experts][8 tokens], then [8 parts][ep]
+    float* part = reinterpret_cast<float*>(smem + sh.part);   // [8 tokens][ep]
 
     griddep_wait();
     griddep_launch_dependents();
     if (blockIdx.x == 0)
         for (int i = threadIdx.x; i < p.nzero; i += kThreads) p.zero[i] = 0;
-
-    // tokens: 64 threads each, 8 values a thread
-    {
+    const bool xvec = p.sxi == 1 && ((reinterpret_cast<uintptr_t>(p.x) | (2 * p.sxt)) & 15) == 0;
+    {   // tokens: 64 threads each, 8 values a thread and turn
         const int t = threadIdx.x >> 6;
-        const bool vec = p.sxi == 1 && ((reinterpret_cast<uintptr_t>(p.x) | (2 * p.sxt)) & 15) == 0;
-        for (int k = (threadIdx.x & 63) * 8; k < width; k += 512) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (t < nt) {
-                const __half* src = p.x + (t0 + t) * p.sxt + (k_lo + k) * p.sxi;
-                v = vec ? load_eight<true>(src, 1, p.D - k_lo - k) : load_eight<false>(src, p.sxi, p.D - k_lo - k);
-                *reinterpret_cast<uint4*>(p.xp + static_cast<int64_t>(t0 + t) * p.dp + k_lo + k) = v;
-            }
-            *reinterpret_cast<uint4*>(xs + t * xpitch + k) = v;
-        }
+#pragma unroll 1
+        for (int k = (threadIdx.x & 63) * 8; k < width; k += 512)
+            bring_eight(base + sh.x + t * sh.xpitch + 2 * k, p.x, (t0 + t) * p.sxt + (k_lo + k) * p.sxi, p.sxi, xvec,
+                        t < nt ? p.D - k_lo - k : 0);
     }
-
-    const int wt = min(tiles, kWarps), share = kWarps / wt;   // tiles a pass, warps a tile
-    for (int pass = 0; pass * wt < tiles; ++pass) {
-        const int tile = pass * wt + warp % wt, mine = warp / wt, e0 = tile * 32;
-        const bool busy = mine < share && tile < tiles;
-        float acc[2][4] = {};
-        constexpr int kBatch = 4;   // chunks of 32 values whose loads are under way together
-        for (int ch0 = mine; ch0 - mine < c_hi - c_lo; ch0 += kBatch * share) {
-            uint4 w[kBatch][4];
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const int ch = ch0 + u * share, k0 = k_lo + ch * 32;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    w[u][q] = make_uint4(0, 0, 0, 0);
-                    if (!busy || ch >= c_hi - c_lo) continue;
-                    if (kLayout == kOutContiguous) {
-                        // rows k of the reordered block: quad g's row is value 8 (g / 2) + g % 2 + 2q
-                        const int k = k0 + 8 * (g >> 1) + (g & 1) + 2 * q, e = e0 + 8 * c;
-                        if (k < p.D) w[u][q] = load_eight<true>(p.router + k * p.sri + e, 1, p.E - e);
-                    } else {
-                        const int e = e0 + 8 * q + g, k = k0 + 8 * c;
-                        if (e < p.E)
-                            w[u][q] = load_eight<kLayout == kInContiguous>(p.router + k * p.sri + e * p.sre, p.sri, p.D - k);
-                    }
+    for (int i = threadIdx.x; i < 8 * ep; i += kThreads) part[i] = 0.f;
+    const int share = tiles < kWarps ? kWarps / tiles : 1;   // warps of a 16-expert tile
+#pragma unroll 1
+    for (int k0 = 0; k0 < width; k0 += sh.kc) {
+        const int kn = min(sh.kc, width - k0);
+        // the router's rows k (experts contiguous) or e (values contiguous)
+        const int words = kOut ? ep / 8 : kn / 8, rows = kOut ? kn : ep;
+#pragma unroll 1
+        for (int i = threadIdx.x; i < rows * words; i += kThreads) {
+            const int r = i / words, c = i - r * words;
+            const int k = k_lo + k0 + (kOut ? r : 8 * c), e = kOut ? 8 * c : r;
+            const bool in = kOut ? k < p.D : e < p.E;
+            bring_eight(base + sh.w + r * sh.wpitch + 16 * c, p.router, k * p.sri + e * p.sre, kOut ? p.sre : p.sri,
+                        kLayout != kAnyStrides, in ? (kOut ? p.E - e : p.D - k) : 0);
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        __syncthreads();
+#pragma unroll 1
+        for (int first = 0; first < tiles; first += kWarps) {
+            const int tile = first + warp / share, mine = warp % share;
+            const int here = min(tiles - first, kWarps / share);   // tiles of this turn
+            float acc[4] = {};
+            if (warp / share < here) {
+                // operand pieces: rows 0-7 and 8-15 of the first 8 values, then of the next 8
+                const int j = lane & 7, piece = lane >> 3;
+                const uint32_t wa = base + sh.w + (kOut ? (j + 8 * (piece >> 1)) * sh.wpitch + (tile * 16 + 8 * (piece & 1)) * 2
+                                                        : (tile * 16 + j + 8 * (piece & 1)) * sh.wpitch + 16 * (piece >> 1));
+                const uint32_t xa = base + sh.x + (lane >> 2) * sh.xpitch + (lane & 3) * 4 + 2 * k0;
+                const uint32_t wstep = kOut ? 16 * sh.wpitch : 32;
+#pragma unroll 2
+                for (int s = mine; s < kn / 16; s += share) {
+                    uint32_t a[4];
+                    ldmatrix4<kOut>(wa + s * wstep, a);
+                    mma16816(acc, a[0], a[1], a[2], a[3], ld_smem_u32(xa + 32 * s), ld_smem_u32(xa + 32 * s + 16));
                 }
             }
-            if (pass == 0 && ch0 == mine) __syncthreads();   // the tokens are there
-            if (!busy) continue;
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const int ch = ch0 + u * share;
-                if (ch >= c_hi - c_lo) break;
-                const uint4 b = ld_smem_v4(smem_u32(xs + g * xpitch + ch * 32 + 8 * c));
-#pragma unroll
-                for (int mt = 0; mt < 2; ++mt) {
-                    if (kLayout == kOutContiguous) {
-                        // w[q] word j: 8x8 of value rows (q) and expert pairs j; its transpose is
-                        // the operand piece of expert rows j, K piece q
-                        uint32_t a[2][4];
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const int j = 2 * mt + h;
-                                a[h][q] = transpose8x8(j == 0 ? w[u][q].x : j == 1 ? w[u][q].y : j == 2 ? w[u][q].z : w[u][q].w);
-                            }
-                        mma16816(acc[mt], a[0][0], a[1][0], a[0][1], a[1][1], b.x, b.y);
-                        mma16816(acc[mt], a[0][2], a[1][2], a[0][3], a[1][3], b.z, b.w);
-                    } else {
-                        const uint4 lo = w[u][2 * mt], hi = w[u][2 * mt + 1];
-                        mma16816(acc[mt], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
-                        mma16816(acc[mt], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
-                    }
-                }
+            for (int i = 0; i < 4; ++i) red[(warp * 16 + (lane >> 2) + 8 * (i >> 1)) * 8 + 2 * (lane & 3) + (i & 1)] = acc[i];
+            __syncthreads();
+            for (int i = threadIdx.x; i < here * 128; i += kThreads) {
+                const int t = i & 7, e = i >> 3;
+                float v = 0.f;
+                for (int m = 0; m < share; ++m) v += red[(((e >> 4) * share + m) * 16 + (e & 15)) * 8 + t];
+                part[t * ep + first * 16 + e] += v;
             }
+            __syncthreads();
         }
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                red[(warp * 32 + expert_row<kLayout>(mt, i >> 1, g)) * 8 + 2 * c + (i & 1)] = acc[mt][i];
-        __syncthreads();
-        for (int i = threadIdx.x; i < wt * 32 * 8; i += kThreads) {
-            const int t = i & 7, e = i >> 3;
-            float v = 0.f;
-            for (int m = 0; m < share; ++m) v += red[((m * wt + (e >> 5)) * 32 + (e & 31)) * 8 + t];
-            if (pass * wt * 32 + e < ep) part[t * ep + pass * wt * 32 + e] = v;
-        }
-        __syncthreads();
     }
     cluster_sync_all();
     // this CTA's token: the 8 parts of its logits
@@ -386,22 +376,29 @@ __global__ void __launch_bounds__(kThreads) moe_route(const __grid_constant__ Pa
             p.weights[(t0 + rank) * p.top + lane] = mine / total;
             p.ids[(t0 + rank) * p.top + lane] = id;
         }
-    } else if (p.xq && warp > 0) {
-        // the tokens' part as MXFP4 columns
-        const int blocks = width >> 5;
-        for (int i = (warp - 1) * 4; i < nt * blocks; i += (kWarps - 1) * 4) {
-            float v[4];
-            uint8_t* codes[4];
-            uint8_t* scales[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int n = min(i + j, nt * blocks - 1), t = n / blocks, blk = n - t * blocks;
+    } else if (warp > 0) {
+        const uint8_t* xs = smem + sh.x;
+        if (p.xq) {   // the tokens' part as MXFP4 columns, four blocks a warp and turn
+            const int blocks = width >> 5, all = nt * blocks;
+#pragma unroll 1
+            for (int i = (warp - 1) * 4; i < all; i += (kWarps - 1) * 4) {
+                const int n = min(i + (lane >> 3), all - 1), t = n / blocks, blk = n - t * blocks;
+                const uint2 u = *reinterpret_cast<const uint2*>(xs + t * sh.xpitch + blk * 64 + (lane & 7) * 8);
+                float v[4];
+                v[0] = __half2float(__ushort_as_half(static_cast<unsigned short>(u.x)));
+                v[1] = __half2float(__ushort_as_half(static_cast<unsigned short>(u.x >> 16)));
+                v[2] = __half2float(__ushort_as_half(static_cast<unsigned short>(u.y)));
+                v[3] = __half2float(__ushort_as_half(static_cast<unsigned short>(u.y >> 16)));
                 const int64_t row = static_cast<int64_t>(t0 + t) * kPieces, at = (k_lo >> 5) + blk;
-                v[j] = __half2float(xs[t * xpitch + blk * 32 + lane]);
-                codes[j] = p.xq + row * p.xq_pitch + at * 16;
-                scales[j] = p.xs + row * p.xs_pitch + at;
+                split_blocks(v, i + (lane >> 3) < all, lane, p.xq + row * p.xq_pitch + at * 16 + (lane & 7) * 2, p.xq_pitch,
+                             p.xs + row * p.xs_pitch + at, p.xs_pitch);
             }
-            split_blocks(v, nt * blocks - i, lane, codes, p.xq_pitch, scales, p.xs_pitch);
+        } else {
+            for (int i = threadIdx.x - 32; i < nt * (width >> 3); i += kThreads - 32) {
+                const int t = i / (width >> 3), k = (i - t * (width >> 3)) * 8;
+                *reinterpret_cast<uint4*>(p.xp + static_cast<int64_t>(t0 + t) * p.dp + k_lo + k) =
+                    *reinterpret_cast<const uint4*>(xs + t * sh.xpitch + 2 * k);
+            }
         }
     }
     __syncwarp();

@@ -62,7 +62,7 @@ struct StreamParams {
     int32_t xpitch, xwords, hpitch, hwords;
     int32_t cap;              // tokens of a piece of an expert's work
     int32_t stages, stage_bytes, b_bytes;   // 3 stages at least
-    uint32_t tmem_cols, acc_cols;
+    uint32_t tmem_cols, acc_cols, y_col;    // y_col: y's sums, a column a token (of T, rounded up to 8) and row tile
 };
 
 // Ranges of a phase, walked alike by every role of a CTA.
@@ -71,6 +71,24 @@ struct Segment {
 };
 
 enum { kStreamRows = 0, kStreamCols = 1, kStreamMxf4 = 2 };
+
+__device__ __forceinline__ void tmem_ld_x1(uint32_t taddr, uint32_t* r)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(*r) : "r"(taddr) : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_x1(uint32_t taddr, uint32_t r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(r) : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t* r)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
 
 // Four tokens' sums of this thread's row: `width` adjacent columns each, the
 // later, smaller ones added first.
@@ -85,12 +103,7 @@ __device__ __forceinline__ void take4(uint32_t taddr, float* v)
                      : "memory");
     } else {
 #pragma unroll
-        for (int i = 0; i < 4 * kWidth; i += 8)
-            asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                         : "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]),
-                           "=r"(r[i + 6]), "=r"(r[i + 7])
-                         : "r"(taddr + i)
-                         : "memory");
+        for (int i = 0; i < 4 * kWidth; i += 8) tmem_ld_x8(taddr + i, r + i);
     }
     tmem_wait_ld();
 #pragma unroll
@@ -128,7 +141,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
     __shared__ __align__(8) uint64_t bars[3 * 16 + 5];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
-    __shared__ int last_flag;
+    __shared__ int last_flag, fixes;
+    __shared__ uint32_t fix[kMaxParts];   // shared tiles of y that this CTA adds up: tile, first and last part
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const int parts = gridDim.x;
     // parts of each phase in the order this CTA takes them: the weights' warp
@@ -142,8 +156,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
     auto tfull = [&](int b) { return bar0 + 24u * 16u + 8u * b; };
     auto tempty = [&](int b) { return bar0 + 24u * 16u + 16u + 8u * b; };
     const uint32_t drain = bar0 + 24u * 16u + 32u;
-    float* ysum = reinterpret_cast<float*>(smem + sp.stages * sp.stage_bytes);   // [T][256]: sums of y's rows
-
     if (threadIdx.x == 0) {
         for (int s = 0; s < sp.stages; ++s) {
             mbar_init(full_a(s), 1);
@@ -156,6 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
         }
         mbar_init(drain, 1);
         abort_flag = 0;
+        fixes = 0;
 
         fence_mbarrier_init();
         tma_prefetch_desc(&sp.gate);
@@ -485,15 +498,19 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
             for (int j = 0; j < 4; ++j)   // (past F: zeros, whatever the tokens hold)
                 hv[j] = f < p.F ? act_f32(p.act, gate[j]) * up[j] : 0.f;
             if (kMx) {
-                uint8_t* codes[4];
-                uint8_t* scales[4];
+                // lane 8j + i takes values 4i .. 4i + 3 of token j0 + j's block (the warp's 32 rows)
+                float v[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int64_t r = static_cast<int64_t>(im.first + min(j0 + j, im.count - 1)) * kPieces;
-                    codes[j] = sp.h + r * sp.hpitch + ((f - lane) >> 1);
-                    scales[j] = sp.hs + r * sp.hwords * 4 + ((f - lane) >> 5);
-                }
-                split_blocks(hv, im.count - j0, lane, codes, sp.hpitch, scales, sp.hwords * 4);
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float o = __shfl_sync(~0u, hv[j], 4 * (lane & 7) + i);
+                        v[i] = j == 0 || lane >> 3 == j ? o : v[i];
+                    }
+                const int j = j0 + (lane >> 3);
+                const int64_t r = static_cast<int64_t>(im.first + min(j, im.count - 1)) * kPieces;
+                split_blocks(v, j < im.count, lane, sp.h + r * sp.hpitch + ((f - lane) >> 1) + (lane & 7) * 2, sp.hpitch,
+                             sp.hs + r * sp.hwords * 4 + ((f - lane) >> 5), sp.hwords * 4);
             } else if (f < p.fp) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -503,37 +520,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
                     __half* dst = reinterpret_cast<__half*>(sp.h + static_cast<int64_t>(im.first + j0 + j) * 2 * sp.hpitch) + f;
                     dst[0] = hh;
                     dst[sp.hpitch >> 1] = isfinite(back) ? __float2half_rn(hv[j] - back) : __ushort_as_half(0);
-                }
-            }
-        };
-        // the sums of a shared tile of y, by the part that stored its own last: 4
-        // columns a thread, 4 parts' and 2 tokens' loads under way at once
-        auto add_shared = [&](int tile, int v0, int v1) {
-            const int col = tile * 256 + (threadIdx.x & 63) * 4;
-            for (int t0 = threadIdx.x >> 6; t0 < p.T; t0 += 4) {
-                float4 v[2] = {};
-                for (int q0 = v0; q0 <= v1; q0 += 4) {
-                    float4 a[4][2];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            a[q][i] = __ldcg(reinterpret_cast<const float4*>(slot_of(min(q0 + q, v1), v0) + min(t0 + 2 * i, p.T - 1) * 256) +
-                                             (threadIdx.x & 63));
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            if (q0 + q <= v1) v[i].x += a[q][i].x, v[i].y += a[q][i].y, v[i].z += a[q][i].z, v[i].w += a[q][i].w;
-                }
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int t = t0 + 2 * i;
-                    if (t >= p.T) break;
-                    const float f[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (col + e < p.D) p.y[t * p.ldy + col + e] = __float2half_rn(f[e]);
                 }
             }
         };
@@ -597,37 +583,62 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
                 } else {
                     const int64_t per = static_cast<int64_t>(items) * f_steps, first = g.tile * per;
                     at += g.s1 - g.s0;
-                    if (!begun)
-                        for (int t = 0; t < p.T; ++t) ysum[t * 256 + row] = 0.f, ysum[t * 256 + 128 + row] = 0.f;
+                    const uint32_t y0 = trow + sp.y_col, y1 = y0 + ((p.T + 7) & ~7);   // this row's, of either row tile
+                    if (!begun) {
+                        const uint32_t zero[8] = {};
+                        for (uint32_t c = y0; c < 2 * y1 - y0; c += 8) mxf4_dev::tmem_st_x8(c, zero);
+                        mxf4_dev::tmem_wait_st();
+                    }
                     begun = true;
                     for (int j0 = 0; j0 < im.count; j0 += 4) {
                         float a[4], b[4];
                         take4<kDownWidth>(d + j0 * kDownWidth, a);
                         take4<kDownWidth>(d + sp.acc_cols + j0 * kDownWidth, b);
                         if (j0 + 4 >= im.count) release();
+                        uint32_t ya[4], yb[4];
+                        int t[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            t[j] = ch.slot[im.first + min(j0 + j, im.count - 1)] / p.top;
+                            tmem_ld_x1(y0 + t[j], &ya[j]);
+                            tmem_ld_x1(y1 + t[j], &yb[j]);
+                        }
+                        tmem_wait_ld();
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             if (j0 + j >= im.count) break;
                             const float wt = ch.weight[im.first + j0 + j];
-                            float* y = ysum + ch.slot[im.first + j0 + j] / p.top * 256 + row;
-                            y[0] = fmaf(wt, a[j], y[0]);
-                            y[128] = fmaf(wt, b[j], y[128]);
+                            tmem_st_x1(y0 + t[j], __float_as_uint(fmaf(wt, a[j], __uint_as_float(ya[j]))));
+                            tmem_st_x1(y1 + t[j], __float_as_uint(fmaf(wt, b[j], __uint_as_float(yb[j]))));
                         }
+                        mxf4_dev::tmem_wait_st();
                     }
                     if (at < hi && at < first + per) continue;   // more of this tile
                     begun = false;
                     const int col = g.tile * 256 + row;
-                    if (lo <= first && at == first + per) {
-                        for (int t = 0; t < p.T; ++t) {
-                            if (col < p.D) p.y[t * p.ldy + col] = __float2half_rn(ysum[t * 256 + row]);
-                            if (col + 128 < p.D) p.y[t * p.ldy + col + 128] = __float2half_rn(ysum[t * 256 + 128 + row]);
-                        }
-                        continue;
-                    }
-                    const int v0 = w.of(first), v1 = w.of(first + per - 1);
+                    const bool whole = lo <= first && at == first + per;
+                    const int v0 = whole ? part : w.of(first), v1 = whole ? part : w.of(first + per - 1);
                     float* to = slot_of(part, v0) + row;
-                    for (int t = 0; t < p.T; ++t) to[t * 256] = ysum[t * 256 + row], to[t * 256 + 128] = ysum[t * 256 + 128 + row];
-                    if (last_of(&sp.ctl->down[v0], v1 - v0 + 1)) add_shared(g.tile, v0, v1);
+                    for (int t0 = 0; t0 < p.T; t0 += 8) {
+                        uint32_t a[8], b[8];
+                        tmem_ld_x8(y0 + t0, a);
+                        tmem_ld_x8(y1 + t0, b);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int t = t0 + j;
+                            if (t >= p.T) break;
+                            if (whole) {
+                                if (col < p.D) p.y[t * p.ldy + col] = __float2half_rn(__uint_as_float(a[j]));
+                                if (col + 128 < p.D) p.y[t * p.ldy + col + 128] = __float2half_rn(__uint_as_float(b[j]));
+                            } else {
+                                to[t * 256] = __uint_as_float(a[j]);
+                                to[t * 256 + 128] = __uint_as_float(b[j]);
+                            }
+                        }
+                    }
+                    if (!whole && last_of(&sp.ctl->down[v0], v1 - v0 + 1) && threadIdx.x == 0)
+                        fix[fixes++] = static_cast<uint32_t>(g.tile) << 16 | static_cast<uint32_t>(v0) << 8 | static_cast<uint32_t>(v1);
                 }
             }
             if (ph == 0 && ok) {
@@ -641,6 +652,40 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
     __syncthreads();
     tc_fence_after();
     if (warp == 5) tmem_dealloc(tmem, sp.tmem_cols);
+    // Shared tiles of y whose last sums this CTA stored: 4 columns a thread, 4
+    // parts' and 2 tokens' loads under way at once.
+    for (int i = 0; i < fixes; ++i) {
+        const int tile = fix[i] >> 16, v0 = fix[i] >> 8 & 255, v1 = fix[i] & 255, c4 = threadIdx.x & 63;
+        const int64_t slot_floats = static_cast<int64_t>(max(sp.cap, p.T)) * 256;
+        for (int t0 = threadIdx.x >> 6; t0 < p.T; t0 += 16) {
+            float4 v[2] = {};
+            for (int q0 = v0; q0 <= v1; q0 += 4) {
+                float4 a[4][2];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int u = min(q0 + q, v1);
+                        a[q][h] = __ldcg(reinterpret_cast<const float4*>(sp.sums + (static_cast<int64_t>(u) * 2 + (u == v0)) * slot_floats +
+                                                                         min(t0 + 8 * h, p.T - 1) * 256) + c4);
+                    }
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (q0 + q <= v1) v[h].x += a[q][h].x, v[h].y += a[q][h].y, v[h].z += a[q][h].z, v[h].w += a[q][h].w;
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int t = t0 + 8 * h, col = tile * 256 + c4 * 4;
+                if (t >= p.T) break;
+                const float f[4] = {v[h].x, v[h].y, v[h].z, v[h].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (col + e < p.D) p.y[t * p.ldy + col + e] = __float2half_rn(f[e]);
+            }
+        }
+    }
 }
 
 }  // namespace moe_dev
