@@ -195,10 +195,11 @@ gemm_f16_status launch_pair(const Device& dev, const void* A_codes, const void* 
                          Shape::kSmem, 2, stream, p);
 }
 
-// The product of checked operands.
+// The product of checked operands; `after_a`: the kernel before is this call's
+// quantisation of A.
 gemm_f16_status product(const Device& dev, const void* A_codes, const void* A_scales, const void* B_codes,
                         const void* B_scales, const void* bias, int act, void* C, int64_t ldc, int64_t M, int64_t N,
-                        int64_t K, cudaStream_t stream)
+                        int64_t K, bool after_a, cudaStream_t stream)
 {
     Sizes sa;
     sizes_of(M, K, 1, &sa);
@@ -228,6 +229,7 @@ gemm_f16_status product(const Device& dev, const void* A_codes, const void* A_sc
     p.timeout_ns = timeout_ns();
     p.status = dev.status;
     p.test_stall = option(GEMM_F16_OPT_TEST_STALL) == 1;
+    p.early = after_a && p.swapped && option(GEMM_F16_OPT_PDL) != 1;
     const uint32_t sbytes = mxf4_dev::gemm_stage_bytes(p.bn);
     // two CTAs an SM, so that one's loads run under the other's last part
     p.stages = static_cast<int32_t>(std::min<int64_t>(16, (kMaxSmem / 2 - 2048) / sbytes));
@@ -321,7 +323,7 @@ gemm_f16_status gemm_mxf4(const void* A_codes, const void* A_scales, const void*
     if (!device_range_ok(A_codes, sa.code_bytes) || !device_range_ok(A_scales, sa.scale_bytes) ||
         !product_memory_ok(B_codes, B_scales, bias, C, N, sb, bytes))
         return GEMM_F16_ERR_INVALID_VALUE;
-    return product(dev, A_codes, A_scales, B_codes, B_scales, bias, act, C, ldc, M, N, K, stream);
+    return product(dev, A_codes, A_scales, B_codes, B_scales, bias, act, C, ldc, M, N, K, false, stream);
 }
 
 gemm_f16_status gemm_mxf4_a16(const void* A, int64_t stride_am, int64_t stride_ak, void* work, const void* B_codes,
@@ -350,7 +352,7 @@ gemm_f16_status gemm_mxf4_a16(const void* A, int64_t stride_am, int64_t stride_a
     uint8_t* codes = scales + sa.scale_bytes;
     st = run_quantize(A, MXF4_F16, 0, stride_am, stride_ak, codes, scales, M, K, 1, sa, stream);
     if (st != GEMM_F16_OK) return st;
-    return product(dev, codes, scales, B_codes, B_scales, bias, act, C, ldc, M, N, K, stream);
+    return product(dev, codes, scales, B_codes, B_scales, bias, act, C, ldc, M, N, K, true, stream);
 }
 
 }  // extern "C"

@@ -34,6 +34,7 @@ struct GemmParams {
     int32_t stages, act;
     int32_t swapped;             // the kernel's A is the caller's B: C[n][m], bias along m
     int32_t bn;                  // rows of the kernel's B a tile takes
+    int32_t early;               // the kernel before this one is the quantisation of the kernel's B
     uint32_t tmem_cols;
     int32_t test_stall;          // failure test: the MMA thread first waits on a barrier nothing arrives on
     uint64_t timeout_ns;
@@ -64,8 +65,8 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
     return v;
 }
 
-// 16 finished sums of row m, columns n .. n + 15, to C.
-__device__ __forceinline__ void store16(const GemmParams& p, int64_t m, int64_t n, float* v)
+// 16 finished sums of row m, columns n .. n + 15, to C; swapped, the first `count`.
+__device__ __forceinline__ void store16(const GemmParams& p, int64_t m, int64_t n, int count, float* v)
 {
     if (m >= p.M) return;
     if (p.swapped) {   // lanes hold neighbouring columns of C
@@ -73,7 +74,7 @@ __device__ __forceinline__ void store16(const GemmParams& p, int64_t m, int64_t 
         __half* c = p.C + m;
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            if (n + i < p.N) c[(n + i) * p.ldc] = __float2half_rn(act_f32(p.act, v[i] + b));
+            if (i < count && n + i < p.N) c[(n + i) * p.ldc] = __float2half_rn(act_f32(p.act, v[i] + b));
         return;
     }
     if (p.bias) {
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_mxf4_tile(const __grid_cons
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
-            mbar_init(full(s), 1);
+            mbar_init(full(s), 2);   // A's bytes and B's
             mbar_init(empty(s), 1);
         }
         mbar_init(done, 1);
@@ -147,7 +148,10 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_mxf4_tile(const __grid_cons
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    griddep_wait();
+    // After a quantisation of this call, which lets this kernel start only when
+    // every kernel before it is done, A is there already: its first slots are
+    // loaded while that kernel runs.  Everything else waits.
+    if (warp != 4 || !p.early) griddep_wait();
     griddep_launch_dependents();
 
     const volatile int* abort = &abort_flag;
@@ -163,18 +167,31 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_mxf4_tile(const __grid_cons
         const uint8_t* sb = p.sfb + (n0 >> 7) * p.kt * kScaleTile;
         bool ok = true;
         int issued = 0;
+        // (an odd last scale tile: the second one is not this row tile's)
+        auto sf_bytes = [&](int s) { return static_cast<uint32_t>(min(static_cast<int64_t>(2), p.kt - 2 * s)) * kScaleTile; };
+        auto load_a = [&](int s, int at) {
+            const uint32_t a = base + at * sbytes, sf = sf_bytes(s);
+            mbar_arrive_expect_tx(full(at), kABytes + sf);
+            tma_load_2d(a, &p.tmA, s * 128, static_cast<int32_t>(m0), full(at));
+            bulk_load(a + kABytes + bn * 128, sa + static_cast<int64_t>(s) * kSfBytes, sf, full(at));
+        };
+        auto load_b = [&](int s, int at) {
+            const uint32_t b = base + at * sbytes + kABytes, sf = sf_bytes(s);
+            mbar_arrive_expect_tx(full(at), bn * 128 + sf);
+            tma_load_2d(b, &p.tmB, s * 128, static_cast<int32_t>(n0), full(at));
+            bulk_load(b + bn * 128 + kSfBytes, sb + static_cast<int64_t>(s) * kSfBytes, sf, full(at));
+        };
+        const int ahead = p.early ? min(p.stages, s_hi - s_lo) : 0;
+        if (issue)
+            for (int q = 0; q < ahead; ++q) load_a(s_lo + q, q);
+        __syncwarp();
+        if (p.early) griddep_wait();
         for (int s = s_lo; s < s_hi; ++s, ++issued) {
             ok = mbar_wait(empty(st), ph ^ 1u, abort, p.timeout_ns);
             if (!ok) break;
-            const uint32_t a = base + st * sbytes, b = a + kABytes, fa = b + bn * 128, fb = fa + kSfBytes;
-            // (an odd last scale tile: the second one is not this row tile's)
-            const uint32_t sf = min(static_cast<int64_t>(2), p.kt - 2 * s) * kScaleTile;
             if (issue) {
-                mbar_arrive_expect_tx(full(st), kABytes + bn * 128 + 2 * sf);
-                tma_load_2d(a, &p.tmA, s * 128, static_cast<int32_t>(m0), full(st));
-                tma_load_2d(b, &p.tmB, s * 128, static_cast<int32_t>(n0), full(st));
-                bulk_load(fa, sa + static_cast<int64_t>(s) * kSfBytes, sf, full(st));
-                bulk_load(fb, sb + static_cast<int64_t>(s) * kSfBytes, sf, full(st));
+                if (issued >= ahead) load_a(s, st);
+                load_b(s, st);
             }
             if (++st == p.stages) st = 0, ph ^= 1u;
         }
@@ -233,7 +250,7 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_mxf4_tile(const __grid_cons
                 float v[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-                store16(p, m, n0 + c, v);
+                store16(p, m, n0 + c, 16, v);
             }
         } else if (ok) {
             // this CTA's part, column by column (lanes hold rows: consecutive words),
@@ -254,18 +271,23 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_mxf4_tile(const __grid_cons
     if (csize > 1) {
         __syncwarp();
         cluster_sync_all();
-        // each CTA finishes a share of the tile's 16-column groups
+        // each CTA finishes a share of the tile's columns, 16 at a time at most
         const bool bad = abort_flag != 0;
         if (warp < 4 && !bad) {
-            for (uint32_t c = 16 * crank; c < bn; c += 16 * csize) {
-                float v[16];
+            const uint32_t c_lo = bn * crank / csize, c_hi = bn * (crank + 1) / csize;
+            for (uint32_t c = c_lo; c < c_hi; c += 16) {
+                const uint32_t count = min(16u, c_hi - c);
+                float v[16] = {};
+#pragma unroll 2
+                for (uint32_t q = 0; q < csize; ++q) {
+                    const uint32_t at = mapa_shared(base + (c * 128 + warp * 32 + lane) * 4, q);
+                    float t[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const uint32_t at = base + ((c + i) * 128 + warp * 32 + lane) * 4;
-                    v[i] = 0.f;
-                    for (uint32_t q = 0; q < csize; ++q) v[i] += ld_cluster_f32(mapa_shared(at, q));
+                    for (uint32_t i = 0; i < 16; ++i) t[i] = i < count ? ld_cluster_f32(at + i * 512) : 0.f;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] += t[i];
                 }
-                store16(p, m0 + warp * 32 + lane, n0 + c, v);
+                store16(p, m0 + warp * 32 + lane, n0 + c, count, v);
             }
         }
         __syncwarp();
