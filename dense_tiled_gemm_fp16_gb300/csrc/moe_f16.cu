@@ -114,7 +114,7 @@ constexpr int kStaticSmem = 9216;    // more than the stream kernel's own
 bool allow_smem(const void* kernel, int slot, int bytes)
 {
     static std::mutex mutex;
-    static int have[kMaxDevices][24] = {};
+    static int have[kMaxDevices][32] = {};
     int d = 0;
     if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= kMaxDevices) {
         cudaGetLastError();
@@ -160,10 +160,10 @@ gemm_f16_status launch_experts(moe_dev::Params& p, int sms, cudaStream_t stream)
         const double fill = static_cast<double>(ranges * s) / (cdiv(ranges * s, sms) * sms);
         if (fill > best + 0.04) best = fill, p.splits = s;
     }
-    const int ring = moe_dev::kWarps * kRing * moe_dev::Stage<kFmt>::kBytes;
+    const int ring = moe_dev::kWarps * kRing * moe_dev::kStepBytes;
     const int smem = ring + std::max(2 * moe_dev::kWarps * kGroups * 32 * 16, moe_dev::kWarps * p.T * kOut * 4);
     const auto kernel = moe_dev::moe_experts<kFmt, kGroups, kRing>;
-    if (!allow_smem(reinterpret_cast<const void*>(kernel), 8 + (kGroups > 1), smem))
+    if (!allow_smem(reinterpret_cast<const void*>(kernel), 16 + 4 * kFmt + (kGroups > 1) + 2 * (kRing == 2), smem))
         return GEMM_F16_ERR_LAUNCH;
     return launch_kernel(kernel, dim3(static_cast<unsigned>(sms)), moe_dev::kThreads, smem, 1, stream, p);
 }
@@ -354,6 +354,10 @@ gemm_f16_status moe_f16(const void* x, int64_t stride_xt, int64_t stride_xi, con
         return launch_stream<moe_dev::kStreamRows>(p, l, base, ws, dev.sms, stream);
     if (cols_aligned(*gate, E) && cols_aligned(*up, E) && cols_aligned(*down, E))
         return launch_stream<moe_dev::kStreamCols>(p, l, base, ws, dev.sms, stream);
+    if (gate->stride_i == 1 && up->stride_i == 1 && down->stride_i == 1)
+        return launch_experts<moe_dev::kF16Rows, 4>(p, dev.sms, stream);
+    if (gate->stride_o == 1 && up->stride_o == 1 && down->stride_o == 1)
+        return launch_experts<moe_dev::kF16Cols, 4>(p, dev.sms, stream);
     return launch_experts<moe_dev::kF16Strided, 4>(p, dev.sms, stream);
 }
 

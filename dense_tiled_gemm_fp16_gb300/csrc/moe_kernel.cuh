@@ -1,18 +1,17 @@
-// A mixture-of-experts layer for a few tokens: the routing kernel and the
-// experts' kernel.
+// A mixture-of-experts layer for a few tokens: the routing kernel, and the
+// experts' kernel for weights at any strides (moe_stream.cuh has the one for
+// weights that TMA can address).
 //
-// With a handful of rows an expert every weight is used a few times at most,
-// so the layer is bound by reading the chosen experts' weights once.  The
-// tensor cores are fed by warps (mma.sync, m16n8k16): a tcgen05 tile would
-// leave 120 of 128 rows empty and stage every byte for it.  The weights take
+// That kernel is bound by the loads that turn unaligned rows into operands, so
+// warps feed the tensor cores themselves (mma.sync, m16n8k16).  The weights take
 // the 16-row side and up to 8 tokens the narrow side; gate and up rows of the
 // same 8 hidden values share one instruction, so that their sums meet in one
-// thread.  Every warp streams its own share of K through a private ring of
-// asynchronous copies: no barrier stands between a warp and its next bytes.
+// thread.  Every warp brings its own share of K through a private ring: no
+// barrier stands between a warp and its next bytes.
 //
 // K is reordered within 32 values, the same on both sides: thread c of a quad
-// holds values 8c .. 8c + 7 of the block, one 16-byte word (or, in MXFP4, one
-// 32-bit word of codes) a row, split over two instructions.
+// holds values 8c .. 8c + 7 of the block, one 16-byte word a row, split over two
+// instructions.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -406,24 +405,20 @@ __global__ void __launch_bounds__(kThreads) moe_route(const __grid_constant__ Pa
 }
 
 // ---------------------------------------------------------------- experts
-// Weight formats of the experts' kernel: fp16 with the contracted axis
-// contiguous, with the other one contiguous, at any strides, and MXFP4.
-enum { kF16Rows = 0, kF16Cols = 1, kF16Strided = 2, kMxf4 = 3 };
+// How the fp16 weights of the any-stride kernel lie: contracted axis contiguous,
+// the other one contiguous (rows that start at any element in both), or neither.
+enum { kF16Rows = 0, kF16Cols = 1, kF16Strided = 2 };
 
-// What a warp does at once.  A step is kVals of K for kTiles 16-row tiles: 2 KB
-// of fp16 in either orientation (64-byte pieces of global rows at least, which
-// is what the copies need to run at the memory's rate), 1 KB of codes.
+// What a warp does at once.  A step is kVals of K for kTiles 16-row tiles, 2 KB
+// of fp16 (64-byte pieces of global rows at least).
 template <int kFmt, bool kUp>
 struct Step {
     static constexpr int kTiles = kFmt == kF16Cols ? (kUp ? 4 : 2) : 1;
-    static constexpr int kVals = kFmt == kF16Cols ? (kUp ? 16 : 32) : kFmt == kMxf4 ? 128 : 64;
+    static constexpr int kVals = kFmt == kF16Cols ? (kUp ? 16 : 32) : 64;
     static constexpr int kOut = (kUp ? 8 : 16) * kTiles;   // hidden values, or columns of y, of a unit
     static constexpr int kWords = kVals / 8;               // 32-bit words of a column a thread holds
 };
-template <int kFmt>
-struct Stage {
-    static constexpr int kBytes = kFmt == kMxf4 ? 1024 + 64 : 2048;   // with the 16 rows' scales
-};
+constexpr int kStepBytes = 2048;
 
 // A step of one projection (down) or of two (up: w0 the gate, w1 the up rows)
 // into a stage: outputs o0 .., values k0 ..; outputs from `rows` and values
@@ -432,68 +427,38 @@ struct Stage {
 //     a pair's rows 0-7 are the gate's, 8-15 the up projection's.
 //   kF16Cols: rows of K; up: 16 of 32 gate and 32 up outputs, down: 32 of 32
 //     outputs.  Two down rows k, k + 16 share 128 bytes.
-//   kMxf4: 16 rows of 128 codes, then their 4 scales each.
 template <int kFmt, bool kUp>
 __device__ __forceinline__ void load_stage(uint32_t dst, const Weight& w0, const Weight& w1, int e, int o0, int rows,
                                            int k0, int K, int lane)
 {
-    if (kFmt == kF16Rows) {
-        const int c = lane & 7, k = k0 + 8 * c;
-        const uint32_t bytes = 2 * max(0, min(8, K - k));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int r = (lane >> 3) + 4 * j;
-            const Weight& w = kUp && j >= 2 ? w1 : w0;
-            const int o = o0 + (kUp ? r & 7 : r);
-            const bool in = o < rows && bytes;
-            const __half* src = reinterpret_cast<const __half*>(w.data) + (in ? e * w.se + o * w.so + k : 0);
-            cp_async16(dst + r * 128 + ((c ^ ((r & 1) << 2)) << 4), src, in ? bytes : 0u);
-        }
-    } else if (kFmt == kF16Strided) {
-        const int c = lane & 7, k = k0 + 8 * c;
-#pragma unroll 1
-        for (int j = 0; j < 4; ++j) {
-            const int r = (lane >> 3) + 4 * j;
-            const Weight& w = kUp && j >= 2 ? w1 : w0;
-            const int o = o0 + (kUp ? r & 7 : r);
-            uint32_t u[4] = {};
-            if (o < rows) {
-                const __half* src = reinterpret_cast<const __half*>(w.data) + e * w.se + o * w.so;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (k + i < K) u[i >> 1] |= static_cast<uint32_t>(ld_nc_u16(src + (k + i) * w.si)) << (16 * (i & 1));
-            }
-            st_smem_v4(dst + r * 128 + ((c ^ ((r & 1) << 2)) << 4), make_uint4(u[0], u[1], u[2], u[3]));
-        }
-    } else if (kFmt == kF16Cols) {
-        const int c = lane & 7;   // 16-byte word of the stage's 128-byte row
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int r = (lane >> 3) + 4 * j;   // of 16 stage rows
+    const int c = lane & 7;   // 16-byte word of the stage's 128-byte row
+#pragma unroll 2
+    for (int j = 0; j < 4; ++j) {
+        const int r = (lane >> 3) + 4 * j;   // of 16 stage rows
+        uint32_t u[4] = {};
+        uint32_t at;
+        if (kFmt == kF16Cols) {
             const Weight& w = kUp && c >= 4 ? w1 : w0;
             const int k = k0 + r + (!kUp && c >= 4 ? 16 : 0), o = o0 + 8 * (c & 3);
-            const uint32_t bytes = k < K ? 2 * max(0, min(8, rows - o)) : 0;
-            const __half* src = reinterpret_cast<const __half*>(w.data) + (bytes ? e * w.se + k * w.si + o : 0);
-            cp_async16(dst + r * 128 + ((c ^ (((r >> 2) << 1) | (r & 1))) << 4), src, bytes);
-        }
-    } else {
-        const int c = lane & 3, k = k0 + 32 * c;
+            const __half* row = reinterpret_cast<const __half*>(w.data) + e * w.se + k * w.si;
+            mxf4_dev::load8<__half, false>(row, o, k < K ? rows : 0, u);
+            if (k >= K || o + 8 > rows) mxf4_dev::mask_tail<__half>(u, k < K ? rows - o : 0);
+            at = r * 128 + ((c ^ (((r >> 2) << 1) | (r & 1))) << 4);
+        } else {
+            const Weight& w = kUp && j >= 2 ? w1 : w0;
+            const int o = o0 + (kUp ? r & 7 : r), k = k0 + 8 * c;
+            const __half* row = reinterpret_cast<const __half*>(w.data) + e * w.se + o * w.so;
+            if (kFmt == kF16Rows) {
+                mxf4_dev::load8<__half, false>(row, k, o < rows ? K : 0, u);
+                if (o >= rows || k + 8 > K) mxf4_dev::mask_tail<__half>(u, o < rows ? K - k : 0);
+            } else if (o < rows) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int r = (lane >> 2) + 8 * j;
-            const Weight& w = kUp && j ? w1 : w0;
-            const int o = o0 + (kUp ? r & 7 : r);
-            const bool in = o < rows && k < K;
-            const uint8_t* src = w.data + (in ? e * w.se + o * w.so + (k >> 1) : 0);
-            cp_async16(dst + r * 64 + ((c ^ ((r >> 1) & 3)) << 4), src, in ? 16u : 0u);
+                for (int i = 0; i < 8; ++i)
+                    if (k + i < K) u[i >> 1] |= static_cast<uint32_t>(ld_nc_u16(row + (k + i) * w.si)) << (16 * (i & 1));
+            }
+            at = r * 128 + ((c ^ ((r & 1) << 2)) << 4);
         }
-        if (lane < 16) {
-            const Weight& w = kUp && lane >= 8 ? w1 : w0;
-            const int o = o0 + (kUp ? lane & 7 : lane);
-            const bool in = o < rows && k0 < K;
-            const uint8_t* src = w.scales + (in ? e * w.scale_se + mxf4_dev::scale_at(o, k0 >> 5, w.kt) : 0);
-            cp_async4(dst + 1024 + lane * 4, src, in ? 4u : 0u);
-        }
+        st_smem_v4(dst + at, make_uint4(u[0], u[1], u[2], u[3]));
     }
 }
 
@@ -562,7 +527,7 @@ __device__ __forceinline__ void mma_stage(float (*acc)[kGroups][4], uint32_t src
             for (int q = 0; q < kGroups; ++q)
                 if (q < groups) mma16816(acc[t][q], a[0], a[1], a[2], a[3], b[q][0], b[q][1]);
         }
-    } else if (kFmt == kF16Cols) {
+    } else {
         // row 8 (j / 2) + j % 2 + 2m of 32 is row j of the m-th quarter of K; K
         // rows from 16 on are the upper words of the stage's rows
         const int j = lane & 7, piece = lane >> 3;
@@ -577,29 +542,6 @@ __device__ __forceinline__ void mma_stage(float (*acc)[kGroups][4], uint32_t src
 #pragma unroll
                 for (int q = 0; q < kGroups; ++q)
                     if (q < groups) mma16816(acc[t][q], a[0], a[1], a[2], a[3], b[q][2 * m], b[q][2 * m + 1]);
-            }
-        }
-    } else {
-        const uint32_t slo = ld_smem_u32(src + 1024 + g * 4), shi = ld_smem_u32(src + 1024 + (g + 8) * 4);
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            const uint32_t at = src + g * 64 + ((h ^ ((g >> 1) & 3)) << 4) + c * 4;
-            uint32_t lo[4], hi[4];
-            mxf4_dev::halves_of(ld_smem_u32(at), lo);
-            mxf4_dev::halves_of(ld_smem_u32(at + 8 * 64), hi);
-            const float s0 = mxf4_dev::scale_value(slo >> (8 * h) & 255u), s1 = mxf4_dev::scale_value(shi >> (8 * h) & 255u);
-#pragma unroll
-            for (int q = 0; q < kGroups; ++q) {
-                if (q < groups) {
-                    // the block's sum, exact products of fp16 values, then its scale
-                    float d[4] = {};
-                    mma16816(d, lo[0], hi[0], lo[1], hi[1], b[q][4 * h], b[q][4 * h + 1]);
-                    mma16816(d, lo[2], hi[2], lo[3], hi[3], b[q][4 * h + 2], b[q][4 * h + 3]);
-                    acc[0][q][0] = fmaf(d[0], s0, acc[0][q][0]);
-                    acc[0][q][1] = fmaf(d[1], s0, acc[0][q][1]);
-                    acc[0][q][2] = fmaf(d[2], s1, acc[0][q][2]);
-                    acc[0][q][3] = fmaf(d[3], s1, acc[0][q][3]);
-                }
             }
         }
     }
@@ -675,7 +617,9 @@ __device__ __forceinline__ void order_choices(const Params& p, Choices& ch, uint
     __syncthreads();
 }
 
-// All experts of the layer.  Two phases, gate/up and down, each cut into
+// All experts of the layer for fp16 weights at strides that TMA cannot address:
+// the chosen experts are read by vector loads that a shift puts in place (or by
+// elements, with no unit stride) into the same products.  Two phases, gate/up and down, each cut into
 // gridDim parts of equal bytes; a CTA takes a part by ticket and, before it
 // starts on a down part, waits until every gate/up part is done.  Tickets of
 // gate/up parts are taken by running CTAs only and are all gone before any CTA
@@ -690,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const __grid_constant
 {
     using Up = Step<kFmt, true>;
     using Down = Step<kFmt, false>;
-    constexpr int kBytes = Stage<kFmt>::kBytes;
+    constexpr int kBytes = kStepBytes;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ Choices sh;
     __shared__ int ticket_slot, last_flag, wait_ok;
@@ -725,7 +669,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const __grid_constant
                                            (warp + ps * kWarps) * kVals, p.D, lane);
                     if (++ps == wsteps) ps = 0, ++pu;
                 }
-                cp_async_commit();
             };
             for (int n = 0; n < kRing - 1; ++n) issue(n);
             int n = 0;
@@ -744,7 +687,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const __grid_constant
 #pragma unroll
                     for (int q = 0; q < kGroups; ++q)
                         load_column<kVals>(col[q], (warp + s * kWarps) * kVals, p.dp, q < groups, b[q]);
-                    cp_async_wait<kRing - 2>();
                     __syncwarp();   // (every lane is done with the stage that is filled next)
                     issue(n + kRing - 1);
                     mma_stage<kFmt, true, kGroups>(acc, ring + (n % kRing) * kBytes, b, groups, lane);
@@ -786,7 +728,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const __grid_constant
                     }
                 }
             }
-            cp_async_wait<0>();
             __syncthreads();
             if (threadIdx.x == 0) {
                 if (!p.test_stall) atom_add_acq_rel_gpu(&p.ctl->done_up, 1);
@@ -828,7 +769,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const __grid_constant
                                         pu / p.splits * kOut, p.D, (pi - it * fsteps) * kVals, p.F, lane);
                 ++pi;
             }
-            cp_async_commit();
         };
         for (int n = 0; n < kRing - 1; ++n) issue(n);
         for (int i = threadIdx.x; i < kWarps * p.T * kOut; i += kThreads) ysum[i] = 0.f;
@@ -893,7 +833,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const __grid_constant
 #pragma unroll
                 for (int q = 0; q < kCols; ++q)
                     load_column<kVals>(col[q], (i - it * fsteps) * kVals, p.fp, q < groups, b[q]);
-                cp_async_wait<kRing - 2>();
                 __syncwarp();   // (every lane is done with the stage that is filled next)
                 issue(n + kRing - 1);
                 mma_stage<kFmt, false, kCols>(acc, ring + (n % kRing) * kBytes, b, groups, lane);
@@ -931,13 +870,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const __grid_constant
                 }
             }
         }
-        cp_async_wait<0>();
         __syncthreads();
         if (threadIdx.x == 0) ticket_slot = atomicAdd(&p.ctl->ticket_down, 1);
         __syncthreads();
         ticket = ticket_slot;
     }
-    cp_async_wait<0>();
 }
 
 }  // namespace moe_dev

@@ -1,4 +1,5 @@
-// The MXFP4 format on the device: places of scales, and values to codes and back.
+// The MXFP4 format on the device: places of scales, and values to codes and back;
+// and vector loads of rows that start at any element.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -138,6 +139,66 @@ __device__ __forceinline__ void halves_of(uint32_t codes, uint32_t* h)
         "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
         : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
         : "r"(codes));
+}
+
+// ------------------------------------------------------- rows at any place
+// Sixteen bytes from byte `o` (0, 2, .. 14) of 32.
+__device__ __forceinline__ void funnel16(const uint32_t* in, uint32_t o, uint32_t* out)
+{
+    uint32_t w[6], v[5];
+#pragma unroll
+    for (int c = 0; c < 6; ++c) w[c] = o & 8u ? in[c + 2] : in[c];
+#pragma unroll
+    for (int c = 0; c < 5; ++c) v[c] = o & 4u ? w[c + 1] : w[c];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) out[c] = __funnelshift_r(v[c], v[c + 1], (o & 2u) * 8u);
+}
+
+// The words of 8 values of a row of unit stride, value `i` first, values from
+// `k` on undefined (mask_tail): aligned 16-byte loads, one more than the values
+// fill where the row starts at another place, each holding at least one of them.
+// kVec: every row starts aligned.
+template <typename T, bool kVec>
+__device__ __forceinline__ void load8(const T* row, int64_t i, int64_t k, uint32_t* w)
+{
+    constexpr int kLoads = sizeof(T) / 2;   // of a row that starts aligned
+    if constexpr (kVec) {
+#pragma unroll
+        for (int c = 0; c < kLoads; ++c) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (i + c * (16 / static_cast<int>(sizeof(T))) < k) v = ld_nc_v4(row + i + c * (16 / sizeof(T)));
+            w[4 * c] = v.x, w[4 * c + 1] = v.y, w[4 * c + 2] = v.z, w[4 * c + 3] = v.w;
+        }
+    } else {
+        uint32_t t[4 * (kLoads + 1)];
+#pragma unroll
+        for (int c = 0; c < 4 * (kLoads + 1); ++c) t[c] = 0u;
+        const uintptr_t at = reinterpret_cast<uintptr_t>(row + i);
+        const uint32_t o = at & 15u;
+        const uint4* p = reinterpret_cast<const uint4*>(at - o);
+        const intptr_t bytes = i < k ? static_cast<intptr_t>(min(static_cast<int64_t>(8), k - i)) * static_cast<intptr_t>(sizeof(T)) + o : 0;
+#pragma unroll
+        for (int c = 0; c <= kLoads; ++c)
+            if (16 * c < bytes) {
+                const uint4 v = ld_nc_v4(p + c);
+                t[4 * c] = v.x, t[4 * c + 1] = v.y, t[4 * c + 2] = v.z, t[4 * c + 3] = v.w;
+            }
+#pragma unroll
+        for (int c = 0; c < kLoads; ++c) funnel16(t + 4 * c, o, w + 4 * c);
+    }
+}
+
+// Values from `n` on of 8 set to zero.
+template <typename T>
+__device__ __forceinline__ void mask_tail(uint32_t* w, int64_t n)
+{
+#pragma unroll
+    for (int c = 0; c < 8 * static_cast<int>(sizeof(T)) / 4; ++c) {
+        if (sizeof(T) == 4)
+            w[c] = c < n ? w[c] : 0u;
+        else
+            w[c] = 2 * c + 1 < n ? w[c] : 2 * c < n ? w[c] & 0xFFFFu : 0u;
+    }
 }
 
 }  // namespace mxf4_dev
