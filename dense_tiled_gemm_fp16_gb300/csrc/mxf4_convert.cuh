@@ -60,6 +60,11 @@ __global__ void __launch_bounds__(kConvThreads) quantize_rows(const QuantParams 
         constexpr bool kWhole = decltype(whole)::value;
 #pragma unroll 1
         for (int rr = warp; rr < kTileRows; rr += kWarps * kUnroll) {
+            if (!kWhole && r0 + rr >= p.rows) {   // (few rows: the rest of the scale tile is padding)
+                if ((lane & 3) == 0)
+                    for (int lr = rr; lr < kTileRows; lr += kWarps) mine[(lr & 31) * 16 + (lr >> 5) * 4] = 0;
+                break;
+            }
             uint32_t w[kUnroll][8 * sizeof(T) / 4];
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {

@@ -28,10 +28,15 @@ def declare(L) -> None:
 
 
 # The package and torch, looked up at the first call (the package imports this
-# module, and its C mirrors work without torch).
+# module, and its C mirrors work without torch), and what the tensor forms take
+# from them: a call of a few microseconds is mostly Python otherwise.
 _g = None
 _t = None
-_fns = {}   # functions of the library that the tensor forms have called
+_codes = {}   # torch dtype -> element type
+_u8 = None    # torch.uint8
+_device = None   # the current device's index
+_raw = None   # the handle of a device's current stream
+_fns = {}     # functions of the library that the tensor forms have called
 
 
 def _pkg():
@@ -43,9 +48,11 @@ def _pkg():
 
 
 def _torch():
-    global _t
+    global _t, _u8, _device, _raw
     if _t is None:
         import torch
+        _codes.update({torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32})
+        _u8, _device, _raw = torch.uint8, torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
         _t = torch
     return _t
 
@@ -142,8 +149,8 @@ class Mxf4Matrix:
 
 
 def _dtype_code(dtype) -> int:
-    t = _t or _torch()
-    code = F16 if dtype is t.float16 else BF16 if dtype is t.bfloat16 else F32 if dtype is t.float32 else None
+    _t or _torch()
+    code = _codes.get(dtype)
     if code is None:
         raise TypeError("MXFP4 conversions take float16, bfloat16 or float32")
     return code
@@ -151,9 +158,7 @@ def _dtype_code(dtype) -> int:
 
 def _stream(device, stream) -> int:
     """Handle of `stream`, or of the device's current one."""
-    if stream is not None:
-        return stream.cuda_stream
-    return _t._C._cuda_getCurrentRawStream(device.index)
+    return _raw(device.index) if stream is None else stream.cuda_stream
 
 
 def _empty(shape, dtype, device, stream):
@@ -172,7 +177,7 @@ def _run(device, name: str, *args) -> None:
     fn = _fns.get(name)
     if fn is None:
         fn = _fns[name] = getattr(_pkg().lib(), name)
-    if device.index == _t.cuda.current_device():
+    if device.index == _device():
         st = fn(*args)
     else:
         with _t.cuda.device(device):
@@ -186,26 +191,33 @@ def mxf4_quantize(x, axis: int = -1, stream=None) -> Mxf4Matrix:
     positive strides) in MXFP4 along `axis`, the one a product will contract: a
     weight [K, N] takes axis=-2 and becomes the [N, K] matrix that mxf4_mm and
     moe_few read."""
-    nd = x.dim()
-    if nd != 2 and nd != 3:
+    shape, strides = x.shape, x.stride()
+    nd = len(shape)
+    if nd == 2:
+        rows, k = shape
+        sr, sk = strides
+        held, batch, sb = None, 1, 0
+    elif nd == 3:
+        held, rows, k = shape
+        sb, sr, sk = strides
+        batch = held
+        if batch == 1:
+            sb = 0
+    else:
         raise ValueError("mxf4_quantize takes a matrix or a batch of matrices")
-    if axis not in (-1, -2, nd - 1, nd - 2):
-        raise ValueError("axis must be one of the two matrix dimensions")
-    code = _dtype_code(x.dtype)
-    if not x.is_cuda:
-        raise ValueError("tensors must be on a CUDA device")
-    *lead, rows, k = x.shape
-    *sb, sr, sk = x.stride()
     if axis == -2 or axis == nd - 2:
         rows, k, sr, sk = k, rows, sk, sr
-    batch = lead[0] if lead else 1
+    elif axis != -1 and axis != nd - 1:
+        raise ValueError("axis must be one of the two matrix dimensions")
+    code = _dtype_code(x.dtype)
     device = x.device
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
     nc, ns = _bytes(rows, k, batch)
-    data = _empty(nc + ns, _t.uint8, device, stream)
-    q = Mxf4Matrix._of(data, ns, rows, k, batch if lead else None, device)
+    q = Mxf4Matrix._of(_empty(nc + ns, _u8, device, stream), ns, rows, k, held, device)
     # (a dimension of one element may carry any stride, a batch of stride 0 repeats)
-    _run(device, "mxf4_quantize", x.data_ptr(), code, sb[0] if batch > 1 else 0, sr if rows > 1 else max(1, k),
-         sk if k > 1 else 1, q.codes_ptr, q.scales_ptr, rows, k, batch, _stream(device, stream))
+    _run(device, "mxf4_quantize", x.data_ptr(), code, sb, sr if rows > 1 else max(1, k), sk if k > 1 else 1, q.codes_ptr,
+         q.scales_ptr, rows, k, batch, _stream(device, stream))
     return q
 
 
