@@ -57,13 +57,9 @@ gemm_f16_status launch_quantize(const mxf4_dev::QuantParams& p, int64_t batch, c
     if (tiles > INT32_MAX) return GEMM_F16_ERR_INVALID_VALUE;
     const dim3 grid(static_cast<unsigned>(tiles), 1, static_cast<unsigned>(batch));
     const bool vec = aligned(p.x, 16) && p.sr * sizeof(T) % 16 == 0 && p.sb * sizeof(T) % 16 == 0;
-    const bool pair = sizeof(T) == 2 && p.sr == 1 && p.sk % 2 == 0 && p.sb % 2 == 0 && aligned(p.x, 4);
-    auto kernel = p.sk != 1 ? mxf4_dev::quantize_strided<T, false>
-                  : vec     ? mxf4_dev::quantize_rows<T, true>
-                            : mxf4_dev::quantize_rows<T, false>;
-    if constexpr (sizeof(T) == 2) {
-        if (p.sk != 1 && pair) kernel = mxf4_dev::quantize_strided<T, true>;
-    }
+    const auto kernel = p.sk != 1 ? mxf4_dev::quantize_strided<T>
+                        : vec     ? mxf4_dev::quantize_rows<T, true>
+                                  : mxf4_dev::quantize_rows<T, false>;
     return launch_kernel(kernel, grid, mxf4_dev::kConvThreads, 0, 1, stream, p);
 }
 
@@ -160,6 +156,9 @@ bool encode_out(CUtensorMap* tm, void* C, int64_t M, int64_t N, int64_t ldc)
            CUDA_SUCCESS;
 }
 
+// C's rows can be stored by TMA.
+bool tma_rows(const void* C, int64_t ldc) { return ldc % 8 == 0 && ldc < int64_t(1) << 39 && aligned(C, 16); }
+
 template <int kBN>
 gemm_f16_status launch_pair(const Device& dev, const void* A_codes, const void* A_scales, const void* B_codes,
                             const void* B_scales, const void* bias, int act, void* C, int64_t ldc, int64_t M, int64_t N,
@@ -183,7 +182,7 @@ gemm_f16_status launch_pair(const Device& dev, const void* A_codes, const void* 
     p.test_stall = option(GEMM_F16_OPT_TEST_STALL) == 1;
     p.timeout_ns = timeout_ns();
     p.status = dev.status;
-    p.c_tma = ldc % 8 == 0 && ldc < int64_t(1) << 39 && aligned(C, 16);
+    p.c_tma = tma_rows(C, ldc);
     if (!encode_codes(&p.tmA, A_codes, M, sa.pitch, 128) || !encode_codes(&p.tmB, B_codes, N, sa.pitch, kBN / 2) ||
         !encode_scales(&p.tmSA, A_scales, sa.row_tiles * sa.kt) || !encode_scales(&p.tmSB, B_scales, sb.row_tiles * sb.kt) ||
         (p.c_tma && !encode_out(&p.tmC, C, M, N, ldc)))
@@ -204,11 +203,15 @@ gemm_f16_status product(const Device& dev, const void* A_codes, const void* A_sc
     Sizes sa;
     sizes_of(M, K, 1, &sa);
     // Pairs once their tiles would occupy most of the device (below that the small tiles
-    // spread better); of the two widths the one whose turns of the clusters
-    // cost less, a 128-wide turn 0.62 of a 256-wide one.
+    // spread better).  Of the two widths the one whose turns of the clusters cost less: a
+    // 128-wide turn takes 0.72 of a 256-wide one (16384 x 2048 x 7168: 107 us, 73 us), 0.62
+    // where rows are stored without TMA and the last turn's stores, which nothing hides, are
+    // longer (3001 x 2000 x 4097, two turns of 256 or three of 128: 18.5 us, 20.2 us; x 1999:
+    // 26.7 us, 24.9 us).
     const int64_t pairs = dev.sms / 2, wide = cdiv(M, 256) * cdiv(N, 256), narrow = cdiv(M, 256) * cdiv(N, 128);
+    const double turn = tma_rows(C, ldc) ? 0.72 : 0.62;
     if (M > 64 && N > 64 && narrow * 4 >= pairs * 3 && sa.row_tiles * sa.kt < INT32_MAX && cdiv(N, 128) * sa.kt < INT32_MAX)
-        return cdiv(narrow, pairs) * 0.62 < cdiv(wide, pairs)
+        return cdiv(narrow, pairs) * turn < cdiv(wide, pairs)
                    ? launch_pair<128>(dev, A_codes, A_scales, B_codes, B_scales, bias, act, C, ldc, M, N, K, stream)
                    : launch_pair<256>(dev, A_codes, A_scales, B_codes, B_scales, bias, act, C, ldc, M, N, K, stream);
     mxf4_dev::GemmParams p = {};

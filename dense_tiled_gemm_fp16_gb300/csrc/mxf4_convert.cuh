@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kConvThreads) quantize_rows(const QuantParams 
     const T* x = static_cast<const T*>(p.x) + b * p.sb;
     uint8_t* codes = p.codes + b * p.rows * p.pitch;
     uint8_t* scales = p.scales + b * p.row_tiles * p.kt * kScaleTile;
-    const int64_t i = i0 + lane * 8;
+    const int i = static_cast<int>(i0) + lane * 8, n = static_cast<int>(p.k);   // (k is below 2^31)
     griddep_wait();
     griddep_launch_dependents();
     constexpr int kUnroll = sizeof(T) == 4 ? 2 : 4;
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kConvThreads) quantize_rows(const QuantParams 
     uint8_t* dst = codes + (r0 + warp) * p.pitch + (i >> 1);
     // this lane's scale byte: block lane / 4 of the row, tile lane / 16
     uint8_t* mine = sc + (lane >> 4) * kScaleTile + ((lane >> 2) & 3);
-    const bool some = (i >> 5) < (p.k + 31) / 32;
+    const bool some = i >> 5 < (n + 31) >> 5;
     const int64_t step = kWarps * p.sr, cstep = kWarps * p.pitch;
     auto rows = [&](auto whole) {   // whole: the tile lies inside the matrix
         constexpr bool kWhole = decltype(whole)::value;
@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kConvThreads) quantize_rows(const QuantParams 
             uint32_t w[kUnroll][8 * sizeof(T) / 4];
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
-                const int64_t k = kWhole || r0 + rr + u * kWarps < p.rows ? p.k : 0;
+                const int k = kWhole || r0 + rr + u * kWarps < p.rows ? n : 0;
                 if (kWhole && kVec) {
 #pragma unroll
                     for (unsigned c = 0; c < sizeof(T) / 2; ++c) {
@@ -113,11 +113,9 @@ __global__ void __launch_bounds__(kConvThreads) quantize_rows(const QuantParams 
 // a row and a warp 32 neighbouring rows, so that a unit row stride gives
 // contiguous loads; the codes of the tile are turned in shared memory.  A tile
 // is wide enough for whole 128-byte lines of codes: with half lines, 64 bytes a
-// row, a 65536 x 7168 fp16 matrix took 1.04 ms instead of 0.39.
-// kPair (16-bit types, unit stride along the rows, rows in aligned pairs): a lane
-// takes two neighbouring rows with each load.
-template <typename T, bool kPair>
-__global__ void __launch_bounds__(kConvThreads) quantize_strided(const QuantParams p)
+// row, a 65536 x 7168 fp16 matrix took 1.04 ms instead of 0.24 (5.0 TB/s).
+template <typename T>
+__global__ void __launch_bounds__(kConvThreads, 4) quantize_strided(const QuantParams p)
 {
     constexpr int kPitch = kStridedVals / 2 + 16, kScTiles = kStridedVals / 128;   // bytes a row of the staged codes: 16-byte stores spread over the banks
     __shared__ __align__(16) uint8_t cs[kTileRows * kPitch];
@@ -131,52 +129,41 @@ __global__ void __launch_bounds__(kConvThreads) quantize_strided(const QuantPara
     uint8_t* scales = p.scales + b * p.row_tiles * p.kt * kScaleTile;
     griddep_wait();
     griddep_launch_dependents();
-    constexpr int kLaneRows = kPair ? 2 : 1, kRowWarps = 4 / kLaneRows;   // warps side by side cover the tile's rows
-    const int lr = (warp % kRowWarps) * 32 * kLaneRows + lane * kLaneRows;
+    const int lr = (warp & 3) * 32 + lane;
     const int64_t r = r0 + lr;
+    auto blocks = [&](auto whole) {   // whole: the tile lies inside the matrix, its strides in 32 bits
+        constexpr bool kWhole = decltype(whole)::value;
 #pragma unroll 1
-    for (int blk = warp / kRowWarps; blk < kStridedVals / 32; blk += kConvThreads / 32 / kRowWarps) {
-        const int64_t i = i0 + blk * 32;
-        uint32_t w[kLaneRows][4][8 * sizeof(T) / 4];
-        const T* src = x + r * p.sr + i * p.sk;
-        if constexpr (kPair) {
+        for (int blk = warp >> 2; blk < kStridedVals / 32; blk += kConvThreads / 128) {
+            const int64_t i = i0 + blk * 32;
+            uint32_t w[4][8 * sizeof(T) / 4];
+            const T* src = x + r * p.sr + i * p.sk;
+            const int left = kWhole ? 32 : static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(32), p.k - i)));
+            const bool row = kWhole || r < p.rows;
+            auto at = [&](int c) { return kWhole ? src + static_cast<uint32_t>(c) * static_cast<uint32_t>(p.sk) : src + c * p.sk; };
             uint32_t v[32];
 #pragma unroll
-            for (int c = 0; c < 32; ++c, src += p.sk) {
-                v[c] = 0u;
-                if (i + c < p.k && r < p.rows) v[c] = r + 1 < p.rows ? ld_nc_u32(src) : ld_nc_u16(src);
-            }
+            for (int c = 0; c < 32; ++c) v[c] = c < left && row ? (sizeof(T) == 4 ? ld_nc_u32(at(c)) : ld_nc_u16(at(c))) : 0u;
 #pragma unroll
             for (int c = 0; c < 32; c += 2) {
-                w[0][c >> 3][(c & 7) >> 1] = __byte_perm(v[c], v[c + 1], 0x5410);
-                w[1][c >> 3][(c & 7) >> 1] = __byte_perm(v[c], v[c + 1], 0x7632);
+                if (sizeof(T) == 4)
+                    w[c >> 3][c & 7] = v[c], w[c >> 3][(c & 7) + 1] = v[c + 1];
+                else
+                    w[c >> 3][(c & 7) >> 1] = __byte_perm(v[c], v[c + 1], 0x5410);
             }
-        } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-#pragma unroll
-                for (unsigned c = 0; c < 8 * sizeof(T) / 4; ++c) w[0][q][c] = 0u;
-#pragma unroll
-                for (int c = 0; c < 8; ++c, src += p.sk) {
-                    if (r >= p.rows || i + q * 8 + c >= p.k) continue;
-                    if (sizeof(T) == 4)
-                        w[0][q][c] = ld_nc_u32(src);
-                    else
-                        w[0][q][c >> 1] |= static_cast<uint32_t>(ld_nc_u16(src)) << (16 * (c & 1));
-                }
-            }
-        }
-#pragma unroll
-        for (int h = 0; h < kLaneRows; ++h) {
-            const uint32_t top = max(max(top_bits<T>(w[h][0]), top_bits<T>(w[h][1])), max(top_bits<T>(w[h][2]), top_bits<T>(w[h][3])));
-            const uint32_t code = r + h < p.rows && i < p.k ? scale_code<T>(top) : 0u;
+            const uint32_t top = max(max(top_bits<T>(w[0]), top_bits<T>(w[1])), max(top_bits<T>(w[2]), top_bits<T>(w[3])));
+            const uint32_t code = kWhole || (row && left > 0) ? scale_code<T>(top) : 0u;
             uint4 c4;
-            c4.x = codes_of<T>(w[h][0], code), c4.y = codes_of<T>(w[h][1], code);
-            c4.z = codes_of<T>(w[h][2], code), c4.w = codes_of<T>(w[h][3], code);
-            *reinterpret_cast<uint4*>(cs + (lr + h) * kPitch + blk * 16) = c4;
-            sc[(blk >> 2) * kScaleTile + ((lr + h) & 31) * 16 + ((lr + h) >> 5) * 4 + (blk & 3)] = static_cast<uint8_t>(code);
+            c4.x = codes_of<T>(w[0], code), c4.y = codes_of<T>(w[1], code);
+            c4.z = codes_of<T>(w[2], code), c4.w = codes_of<T>(w[3], code);
+            *reinterpret_cast<uint4*>(cs + lr * kPitch + blk * 16) = c4;
+            sc[(blk >> 2) * kScaleTile + lane * 16 + (warp & 3) * 4 + (blk & 3)] = static_cast<uint8_t>(code);
         }
-    }
+    };
+    if (r0 + kTileRows <= p.rows && i0 + kStridedVals <= p.k && p.sk < (int64_t(1) << 26))
+        blocks(Bool<true>());
+    else
+        blocks(Bool<false>());
     __syncthreads();
     const int64_t bytes = min(p.pitch - (i0 >> 1), static_cast<int64_t>(kStridedVals / 2));
     constexpr int kWords = kStridedVals / 32;   // 16-byte words of a row's codes
@@ -210,7 +197,8 @@ __global__ void __launch_bounds__(kConvThreads) dequantize(const DequantParams p
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t rt = blockIdx.x / p.col_tiles, b = blockIdx.z;
-    const int64_t c0 = (blockIdx.x - rt * p.col_tiles) * 32 + lane;   // this lane's group of 8
+    const int c0 = static_cast<int>(blockIdx.x - rt * p.col_tiles) * 32 + lane;   // this lane's group of 8
+    const int k = static_cast<int>(p.k), words = static_cast<int>(p.pitch >> 2);   // (k is below 2^31)
     const uint8_t* codes = p.codes + b * p.rows * p.pitch;
     const uint8_t* scales = p.scales + b * p.row_tiles * p.kt * kScaleTile;
     T* y = static_cast<T*>(p.y) + b * p.rows * p.k;
@@ -222,42 +210,42 @@ __global__ void __launch_bounds__(kConvThreads) dequantize(const DequantParams p
     const uint8_t* from = codes + (r0 + warp) * p.pitch;
     // a tile's 64 rows are half of a scale tile's: place of (row 0, block 0)
     const uint8_t* srow = scales + (r0 >> 7) * p.kt * kScaleTile + ((r0 >> 5) & 3) * 4;
-    auto place = [&](int lr, int64_t blk) { return srow + (blk >> 2) * kScaleTile + (blk & 3) + (lr & 31) * 16 + (lr >> 5) * 4; };
+    auto place = [&](int lr, int blk) { return srow + static_cast<int64_t>(blk >> 2) * kScaleTile + (blk & 3) + (lr & 31) * 16 + (lr >> 5) * 4; };
 #pragma unroll 1
     for (int rr = warp; rr < kDequantRows; rr += kUnroll * kWarps, to += kUnroll * kWarps * p.k, from += kUnroll * kWarps * p.pitch) {
         uint32_t w[kUnroll][2], sc[kUnroll][2];
-        int64_t i0[kUnroll];
+        int i0[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int lr = rr + u * kWarps;
-            const int64_t shift = kVec ? 0 : static_cast<int64_t>(reinterpret_cast<uintptr_t>(to + u * kWarps * p.k) / sizeof(T) & 7);
-            const int64_t i = c0 * 8 - shift;
-            i0[u] = r0 + lr < p.rows && i < p.k ? i : p.k;
+            const int shift = kVec ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(to + u * kWarps * p.k) / sizeof(T) & 7);
+            const int i = c0 * 8 - shift;
+            i0[u] = r0 + lr < p.rows && i < k ? i : k;
             w[u][0] = w[u][1] = sc[u][0] = sc[u][1] = 0u;
-            if (i0[u] >= p.k) continue;
+            if (i0[u] >= k) continue;
             const uint32_t* src = reinterpret_cast<const uint32_t*>(from + u * kWarps * p.pitch);
             if (kVec) {
                 w[u][0] = __ldg(src + c0);
                 sc[u][0] = __ldg(place(lr, i >> 5));
                 continue;
             }
-            const int64_t word = i >> 3, words = p.pitch >> 2;   // (word -1 holds nothing of the row)
+            const int word = i >> 3;   // (word -1 holds nothing of the row)
             if (word >= 0) w[u][0] = __ldg(src + word);
             if (shift != 0 && word + 1 < words) w[u][1] = __ldg(src + word + 1);
-            const int64_t blk = max(i, static_cast<int64_t>(0)) >> 5, last = min(i + 7, p.k - 1) >> 5;
+            const int blk = max(i, 0) >> 5, last = min(i + 7, k - 1) >> 5;
             sc[u][0] = __ldg(place(lr, blk));
             sc[u][1] = last != blk ? __ldg(place(lr, last)) : sc[u][0];
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int64_t i = i0[u];
-            if (i >= p.k) continue;
+            const int i = i0[u];
+            if (i >= k) continue;
             T* row = to + u * kWarps * p.k;
             uint32_t h[4];
-            halves_of(kVec ? w[u][0] : __funnelshift_r(w[u][0], w[u][1], 4 * static_cast<uint32_t>(i & 7)), h);
+            halves_of(kVec ? w[u][0] : __funnelshift_r(w[u][0], w[u][1], 4 * (i & 7)), h);
             T v[8];
             uint4 o[sizeof(T) / 2];
-            const int turn = kVec ? 8 : 32 - static_cast<int>(i & 31);   // values of the first block
+            const int turn = kVec ? 8 : 32 - (i & 31);   // values of the first block
             if (Elem<T>::kInf == 0x7C00u && sc[u][0] - 103u <= 39u && (kVec || sc[u][1] - 103u <= 39u)) {
                 // fp16 holds the factors (2^-24 to 2^15): one rounding, two values an instruction
                 auto half_scale = [](uint32_t c) { return c >= 113u ? (c - 112u) << 10 : 1u << (c - 103u); };
@@ -275,14 +263,14 @@ __global__ void __launch_bounds__(kConvThreads) dequantize(const DequantParams p
                     v[c] = Elem<T>::from_f32((c < turn ? s0 : s1) * Elem<__half>::to_f32(c & 1 ? h[c >> 1] >> 16 : h[c >> 1] & 0xFFFFu));
                 memcpy(o, v, sizeof(v));
             }
-            if (kVec || (i >= 0 && i + 8 <= p.k)) {
+            if (kVec || (i >= 0 && i + 8 <= k)) {
 #pragma unroll
                 for (unsigned c = 0; c < sizeof(T) / 2; ++c) __stcs(reinterpret_cast<uint4*>(row + i) + c, o[c]);
             } else {
                 memcpy(v, o, sizeof(v));
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
-                    if (i + c >= 0 && i + c < p.k) row[i + c] = v[c];
+                    if (i + c >= 0 && i + c < k) row[i + c] = v[c];
             }
         }
     }

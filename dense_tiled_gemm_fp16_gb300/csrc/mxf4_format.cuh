@@ -159,7 +159,7 @@ __device__ __forceinline__ void funnel16(const uint32_t* in, uint32_t o, uint32_
 // fill where the row starts at another place, each holding at least one of them.
 // kVec: every row starts aligned.
 template <typename T, bool kVec>
-__device__ __forceinline__ void load8(const T* row, int64_t i, int64_t k, uint32_t* w)
+__device__ __forceinline__ void load8(const T* row, int i, int k, uint32_t* w)
 {
     constexpr int kLoads = sizeof(T) / 2;   // of a row that starts aligned
     if constexpr (kVec) {
@@ -176,7 +176,7 @@ __device__ __forceinline__ void load8(const T* row, int64_t i, int64_t k, uint32
         const uintptr_t at = reinterpret_cast<uintptr_t>(row + i);
         const uint32_t o = at & 15u;
         const uint4* p = reinterpret_cast<const uint4*>(at - o);
-        const intptr_t bytes = i < k ? static_cast<intptr_t>(min(static_cast<int64_t>(8), k - i)) * static_cast<intptr_t>(sizeof(T)) + o : 0;
+        const int bytes = i < k ? min(8, k - i) * static_cast<int>(sizeof(T)) + static_cast<int>(o) : 0;
 #pragma unroll
         for (int c = 0; c <= kLoads; ++c)
             if (16 * c < bytes) {
@@ -190,7 +190,7 @@ __device__ __forceinline__ void load8(const T* row, int64_t i, int64_t k, uint32
 
 // Values from `n` on of 8 set to zero.
 template <typename T>
-__device__ __forceinline__ void mask_tail(uint32_t* w, int64_t n)
+__device__ __forceinline__ void mask_tail(uint32_t* w, int n)
 {
 #pragma unroll
     for (int c = 0; c < 8 * static_cast<int>(sizeof(T)) / 4; ++c) {

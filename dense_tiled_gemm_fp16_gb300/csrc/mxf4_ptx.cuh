@@ -48,6 +48,15 @@ __host__ __device__ constexpr uint32_t idesc_mxf4(uint32_t m, uint32_t n, uint32
            ((2 * half) << 29);
 }
 
+// Arrive on another CTA's barrier after tcgen05 loads that have completed, with
+// tcgen05.fence::before_thread_sync between: nothing in memory is handed over, and
+// a release would wait for the thread's own stores (1 000 to 1 800 cycles where a
+// tile's last stores are in flight).
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr)
+{
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // The forms of a CTA pair (one MMA over 256 rows, each CTA with its 128 rows of
 // A, half the rows of B and the scales of its A rows and of all of B's).
 __device__ __forceinline__ void umma_mxf4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
