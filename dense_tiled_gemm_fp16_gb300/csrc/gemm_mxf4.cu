@@ -204,10 +204,10 @@ gemm_f16_status product(const Device& dev, const void* A_codes, const void* A_sc
     sizes_of(M, K, 1, &sa);
     // Pairs once their tiles would occupy most of the device (below that the small tiles
     // spread better).  Of the two widths the one whose turns of the clusters cost less: a
-    // 128-wide turn takes 0.72 of a 256-wide one (16384 x 2048 x 7168: 107 us, 73 us), 0.62
-    // where rows are stored without TMA and the last turn's stores, which nothing hides, are
-    // longer (3001 x 2000 x 4097, two turns of 256 or three of 128: 18.5 us, 20.2 us; x 1999:
-    // 26.7 us, 24.9 us).
+    // 128-wide turn takes 0.72 of a 256-wide one (16384 x 2048 x 7168: 14 turns in 97 us, 7 in
+    // 68 us), 0.62 where rows are stored without TMA and the last turn's stores, which nothing
+    // hides, are longer (3001 x 2000 x 4097, two turns of 256 or three of 128: 18.0 us, 18.8 us;
+    // x 1999: 25.1 us, 23.3 us).
     const int64_t pairs = dev.sms / 2, wide = cdiv(M, 256) * cdiv(N, 256), narrow = cdiv(M, 256) * cdiv(N, 128);
     const double turn = tma_rows(C, ldc) ? 0.72 : 0.62;
     if (M > 64 && N > 64 && narrow * 4 >= pairs * 3 && sa.row_tiles * sa.kt < INT32_MAX && cdiv(N, 128) * sa.kt < INT32_MAX)

@@ -46,31 +46,48 @@ constexpr uint32_t kABytes = 128 * 128, kSfBytes = 2 * kScaleTile;
 
 __host__ __device__ inline uint32_t gemm_stage_bytes(int bn) { return kABytes + bn * 128 + 2 * kSfBytes; }
 
-// The activations without a branch, so that a thread's 32 values overlap: with
-// erfcf and the full division, whose rare cases branch, 256 threads took 220
-// cycles a SiLU and the epilogue was 9/10 of a product with K = 1000.
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The activations without a branch, so that a thread's 32 values overlap, and of
+// few instructions: with erfcf and the full division, whose rare cases branch, a
+// SiLU took 220 cycles of a warp and the epilogue 9/10 of a product with K = 1000.
 //
 // Phi(x) for x < 0 is erfc(z) / 2 with z = -x / sqrt 2, and erfc(z) exp(z^2) is
 // smooth and falls like 1 / z: t P(t) with t = 1 / (1 + z / 3) and P of degree 7,
 // least relative error over 0 <= z <= 9 (fitted to the function's values in 64
-// bits), is within 1.3e-7 of it.  With the rounding of z^2 the whole is within 2^-18 of
-// x Phi(x) wherever that is not zero in fp16.
+// bits; gelu_factor gives half of P's), is within 1.3e-7 of it.  With the
+// rounding of z^2 and the approximate exponential the whole is within 2^-18 of x
+// Phi(x) wherever that is not zero in fp16.
+__device__ constexpr float gelu_factor(int i)
+{
+    constexpr float f[8] = {0.0940747783f, 0.0931263119f, 0.0966875404f, 0.0410582423f,
+                            0.168501928f,  -0.131988719f, 0.200961143f,  -0.0624212809f};
+    return f[i];
+}
+
 __device__ __forceinline__ float act_f32(int act, float x)
 {
     switch (act) {
     case 1: return x < 0.f ? 0.f : x;
-    case 2: return __fdividef(x, 1.f + __expf(-x));   // (x < -87: the divisor's range gives 0, so does fp16)
+    case 2: return x * rcp(1.f + ex2(-1.44269504f * x));
     case 3: {
-        const float z = fabsf(x) * 0.70710678118654752f, t = __fdividef(1.f, fmaf(z, 1.f / 3.f, 1.f));
-        float q = -0.124842565f;
-        q = fmaf(q, t, 0.401922299f);
-        q = fmaf(q, t, -0.263977448f);
-        q = fmaf(q, t, 0.33700385f);
-        q = fmaf(q, t, 0.0821164811f);
-        q = fmaf(q, t, 0.193375077f);
-        q = fmaf(q, t, 0.186252618f);
-        q = fmaf(q, t, 0.188149561f);
-        const float h = 0.5f * q * t * __expf(-z * z);
+        const float t = rcp(fmaf(fabsf(x), 0.70710678f / 3.f, 1.f));
+        float q = gelu_factor(7);
+#pragma unroll
+        for (int i = 6; i >= 0; --i) q = fmaf(q, t, gelu_factor(i));
+        const float h = q * t * ex2(x * x * (-0.5f * 1.44269504f));
         return x * (x < 0.f ? h : 1.f - h);
     }
     default: return x;
@@ -356,6 +373,52 @@ struct PairShape {
     static constexpr uint32_t kAcc1 = kBN == 256 ? kSfCol - 256 : 256;
 };
 
+// Two fp32 values an instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b)
+{
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+    return v;
+}
+
+__device__ __forceinline__ void unpack2(uint64_t v, float* a, float* b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(v));
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t v;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+    return v;
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t v;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+
+// act_f32's GELU of two values.
+__device__ __forceinline__ void gelu2(float* x0, float* x1)
+{
+    const uint64_t x = pack2(*x0, *x1), one = pack2(1.f, 1.f);
+    auto both = [](float c) { return pack2(c, c); };
+    float a, b;
+    unpack2(fma2(pack2(fabsf(*x0), fabsf(*x1)), both(0.70710678f / 3.f), one), &a, &b);
+    const uint64_t t = pack2(rcp(a), rcp(b));
+    uint64_t q = both(gelu_factor(7));
+#pragma unroll
+    for (int i = 6; i >= 0; --i) q = fma2(q, t, both(gelu_factor(i)));
+    unpack2(mul2(mul2(x, x), both(-0.5f * 1.44269504f)), &a, &b);
+    const uint64_t h = mul2(mul2(q, t), pack2(ex2(a), ex2(b))), r = fma2(h, both(-1.f), one);
+    float h0, h1, r0, r1;
+    unpack2(h, &h0, &h1);
+    unpack2(r, &r0, &r1);
+    unpack2(mul2(x, pack2(*x0 < 0.f ? h0 : r0, *x1 < 0.f ? h1 : r1)), x0, x1);
+}
+
 // act of 32 values; one choice for all of them.
 __device__ __forceinline__ void act_all(int act, float* v)
 {
@@ -367,44 +430,43 @@ __device__ __forceinline__ void act_all(int act, float* v)
         for (int c = 0; c < 32; ++c) v[c] = act_f32(2, v[c]);
     } else if (act == 3) {
 #pragma unroll
-        for (int c = 0; c < 32; ++c) v[c] = act_f32(3, v[c]);
+        for (int c = 0; c < 32; c += 2) gelu2(&v[c], &v[c + 1]);
     }
 }
 
-// 64 finished columns of a warp's 32 rows from its staging box to C, without
-// TMA: two values a lane where C's words are, the odd ones at a row's ends
-// alone; eight rows are read before the first is stored.
+// 64 finished columns of a warp's 32 rows from its staging box to C, where its
+// rows do not begin on 16 bytes: eight lanes a row, 16 aligned bytes of C each,
+// shifted into place from two chunks of the box.  Of a row that begins off values
+// past a boundary the last lane has the last off values and the first 8 - off.
 __device__ __forceinline__ void store_rows(const PairParams& p, uint32_t box, int64_t m0, int64_t n0, int lane)
 {
     if (n0 >= p.N || m0 >= p.M) return;
     const int cols = static_cast<int>(min(static_cast<int64_t>(64), p.N - n0));
     const int rows = static_cast<int>(min(static_cast<int64_t>(32), p.M - m0));
-    for (int r0 = 0; r0 < rows; r0 += 8) {
-        uint16_t* c = reinterpret_cast<uint16_t*>(p.C + (m0 + r0) * p.ldc + n0);
-        uint32_t lo[8], hi[8];   // values i and i + 1 of each row, i = 2 lane - (the row's word offset)
+    uint16_t* c = reinterpret_cast<uint16_t*>(p.C + (m0 + (lane >> 3)) * p.ldc + n0);
+#pragma unroll 4
+    for (int r = lane >> 3; r < 32; r += 4, c += 4 * p.ldc) {
+        const int off = static_cast<int>(reinterpret_cast<uintptr_t>(c) >> 1) & 7, i0 = 8 * (lane & 7) + (-off & 7);
+        uint32_t in[8], out[4];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const int i = 2 * lane - static_cast<int>(reinterpret_cast<uintptr_t>(c + q * p.ldc) >> 1 & 1);
-            auto get = [&](int i) {
-                uint16_t v;
-                asm volatile("ld.shared.u16 %0, [%1];"
-                             : "=h"(v) : "r"(box + (r0 + q) * 128 + (((i >> 3) ^ q) << 4) + (i & 7) * 2) : "memory");
-                return static_cast<uint32_t>(v);
-            };
-            lo[q] = get(max(i, 0));
-            hi[q] = i < 0 ? get(63) : get(i + 1);
-        }
+        for (int h = 0; h < 2; ++h)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(in[4 * h]), "=r"(in[4 * h + 1]), "=r"(in[4 * h + 2]), "=r"(in[4 * h + 3])
+                         : "r"(box + r * 128 + (((((i0 >> 3) + h) ^ r) & 7) << 4)) : "memory");
+        funnel16(in, 2 * (i0 & 7), out);
+        if (r >= rows) continue;
+        if (i0 + 8 <= cols) {
+            *reinterpret_cast<uint4*>(c + i0) = make_uint4(out[0], out[1], out[2], out[3]);
+        } else {
 #pragma unroll
-        for (int q = 0; q < 8; ++q, c += p.ldc) {
-            if (r0 + q >= rows) break;
-            const int i = 2 * lane - static_cast<int>(reinterpret_cast<uintptr_t>(c) >> 1 & 1);
-            if (i >= 0 && i + 1 < cols) {
-                *reinterpret_cast<uint32_t*>(c + i) = lo[q] | hi[q] << 16;
-            } else if (i >= 0) {
-                if (i < cols) c[i] = static_cast<uint16_t>(lo[q]);
-            } else {   // the row's first value, and its last of 64
-                c[0] = static_cast<uint16_t>(lo[q]);
-                if (cols == 64) c[63] = static_cast<uint16_t>(hi[q]);
+            for (int t = 0; t < 4; ++t) {
+                const int i = (i0 + 2 * t) & 63, j = (i + 1) & 63;
+                if (j > i && j < cols) {
+                    *reinterpret_cast<uint32_t*>(c + i) = out[t];
+                } else {
+                    if (i < cols) c[i] = static_cast<uint16_t>(out[t]);
+                    if (j < cols) c[j] = static_cast<uint16_t>(out[t] >> 16);
+                }
             }
         }
     }
@@ -417,6 +479,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_mxf4_pair(const __grid_c
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     __shared__ __align__(8) uint64_t bars[2 * 8 + 5];
+    __shared__ __align__(16) float bias[8][kBN / 2];   // of an epilogue warp's columns
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
 
@@ -578,6 +641,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_mxf4_pair(const __grid_c
         for (int64_t t = blockIdx.x >> 1; t < tiles; t += clusters) {
             int64_t m0, n0;
             place(t, &m0, &n0);
+            if (p.bias) {   // (the warp has met since it read the last tile's)
+                for (int c = lane; c < kHalf; c += 32) {
+                    const int64_t n = n0 + half * kHalf + c;
+                    bias[warp][c] = n < p.N ? __half2float(p.bias[n]) : 0.f;
+                }
+                __syncwarp();
+            }
             const bool ok = __all_sync(~0u, mbar_wait_cluster(tfull + 8 * acc, tpar, abort, p.timeout_ns));
             if (!ok) {
                 if (lane == 0) fail();
@@ -602,14 +672,15 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_mxf4_pair(const __grid_c
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster_relaxed(leader_room);
                 }
-                const int64_t n = n0 + half * kHalf + b * 32;
                 float v[32];
 #pragma unroll
                 for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(r[c]);
                 if (p.bias) {
 #pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        if (n + c < p.N) v[c] += __half2float(__ldg(p.bias + n + c));
+                    for (int c = 0; c < 32; c += 4) {
+                        const float4 f = *reinterpret_cast<const float4*>(&bias[warp][b * 32 + c]);
+                        v[c] += f.x, v[c + 1] += f.y, v[c + 2] += f.z, v[c + 3] += f.w;
+                    }
                 }
                 act_all(p.act, v);
                 if (p.c_tma && (i & 1) == 0) {
