@@ -36,7 +36,7 @@ __device__ __forceinline__ float act_f32(int act, float x)
 {
     switch (act) {
     case 1: return x < 0.f ? 0.f : x;
-    case 2: return x / (1.f + expf(-x));
+    case 2: return __fdividef(x, 1.f + __expf(-x));   // (no branch; x < -87: 0 for a value under 2^-119)
     case 3: return x * (0.5f * erfcf(-x * 0.70710678118654752f));
     default: return x;
     }
@@ -144,23 +144,31 @@ enum { kAnyStrides = 0, kInContiguous = 1, kOutContiguous = 2 };
 // Four blocks of 32 values as kPieces MXFP4 columns; lane 8j + i holds values 4i
 // .. 4i + 3 of block j in v.  `codes`: this lane's two bytes of column 0, `pitch`
 // bytes to the next column; `scale`: its block's scale of column 0.  Blocks with
-// `on` false are not written.  Unlike a quantised operand, whose largest
-// magnitudes saturate (6 to 8 times 2^s), a column's scale is a step larger
-// there, so that no remainder is above half a step of the grid, 1/5 of the
-// largest magnitude.
+// `on` false are not written.
+//
+// Column 0's scale 2^s is the smallest under which the block's largest magnitude
+// does not saturate, so that it is above 3 * 2^s (a quantised operand's is a step
+// smaller for magnitudes of 6 to 8 times 2^s).  e2m1 steps by 2 up to 6, by 1 up
+// to 4: column 0 leaves at most 2^s, 4 steps under 2^(s - 2), and from then on
+// each column leaves at most half of its own unit, 4 steps of one 8 times
+// smaller.  So the scales are known beforehand, s, s - 2, s - 5, s - 8, .., and 6
+// columns leave at most 2^(s - 15), 2^-16.5 of the block's largest magnitude.
+// (A search for each remainder's own largest magnitude took 2.5 times as long.)
 __device__ __forceinline__ void split_blocks(float* v, bool on, int lane, uint8_t* codes, int64_t pitch, uint8_t* scale,
                                              int64_t spitch)
 {
+    uint32_t top = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+#pragma unroll
+    for (int s = 1; s < 8; s <<= 1) top = max(top, __shfl_xor_sync(~0u, top, s));
+    uint32_t code = mxf4_dev::scale_code<float>(top);
+    const bool nan = code == 255u;
+    if (!nan) code += (top & 0x7FFFFFu) > 0x400000u && code > 0u;   // above 6 * 2^s: mantissa above 1.5
 #pragma unroll 1
     for (int q = 0; q < kPieces; ++q) {
-        uint32_t top = 0u;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-#pragma unroll
-        for (int s = 1; s < 8; s <<= 1) top = max(top, __shfl_xor_sync(~0u, top, s));
-        uint32_t code = mxf4_dev::scale_code<float>(top), e = 0;
-        if (code != 255u) {
-            code += (top & 0x7FFFFFu) > 0x400000u && code > 0u;   // above 6 * 2^s: mantissa above 1.5
+        uint32_t e = 0;
+        if (!nan) {
             const float f = mxf4_dev::pow2f(127 - static_cast<int>(code)), back = mxf4_dev::scale_value(code);
             uint32_t h0, h1;
             asm("{\n\t.reg .b8 b0, b1;\n\t"
@@ -180,6 +188,7 @@ __device__ __forceinline__ void split_blocks(float* v, bool on, int lane, uint8_
             *reinterpret_cast<uint16_t*>(codes + q * pitch) = static_cast<uint16_t>(e);
             if ((lane & 7) == 0) scale[q * spitch] = static_cast<uint8_t>(code);
         }
+        if (!nan) code -= min(code, q == 0 ? 2u : 3u);
     }
 }
 

@@ -13,11 +13,10 @@
 // Both operands of an MMA have one type, so the narrow side is held in the
 // weights' format.  fp16: a hidden value is two columns, its fp16 rounding and
 // the fp16 rounding of the rest.  MXFP4: a value is 6 columns, each the e2m1
-// rounding of what the columns before it leave, under a scale that none of the
-// block's 32 values exceeds: a column takes at least 4/5 off the largest
-// remainder, so that 6 leave under 2^-13.9 of the block's largest magnitude,
-// less than a fp16 value's own last place unless it is 8 times smaller.  The
-// epilogue adds the columns in fp32.
+// rounding of what the columns before it leave, which is under 2^-16.5 of the
+// block's largest magnitude in the end (split_blocks): less than a fp16 value's
+// own last place unless it is 50 times smaller.  The epilogue adds the columns in
+// fp32.
 //
 // Work is cut into gridDim parts of equal bytes in each of the two phases
 // (gate/up, down), wherever that falls: a part's first and last output tile may
