@@ -156,8 +156,11 @@ bool encode_out(CUtensorMap* tm, void* C, int64_t M, int64_t N, int64_t ldc)
            CUDA_SUCCESS;
 }
 
-// C's rows can be stored by TMA.
-bool tma_rows(const void* C, int64_t ldc) { return ldc % 8 == 0 && ldc < int64_t(1) << 39 && aligned(C, 16); }
+// C's rows can be stored by TMA, which clips a box to whole 16 bytes.
+bool tma_rows(const void* C, int64_t ldc, int64_t N)
+{
+    return N % 8 == 0 && ldc % 8 == 0 && ldc < int64_t(1) << 39 && aligned(C, 16);
+}
 
 template <int kBN>
 gemm_f16_status launch_pair(const Device& dev, const void* A_codes, const void* A_scales, const void* B_codes,
@@ -182,7 +185,7 @@ gemm_f16_status launch_pair(const Device& dev, const void* A_codes, const void* 
     p.test_stall = option(GEMM_F16_OPT_TEST_STALL) == 1;
     p.timeout_ns = timeout_ns();
     p.status = dev.status;
-    p.c_tma = tma_rows(C, ldc);
+    p.c_tma = tma_rows(C, ldc, N);
     if (!encode_codes(&p.tmA, A_codes, M, sa.pitch, 128) || !encode_codes(&p.tmB, B_codes, N, sa.pitch, kBN / 2) ||
         !encode_scales(&p.tmSA, A_scales, sa.row_tiles * sa.kt) || !encode_scales(&p.tmSB, B_scales, sb.row_tiles * sb.kt) ||
         (p.c_tma && !encode_out(&p.tmC, C, M, N, ldc)))
@@ -202,20 +205,26 @@ gemm_f16_status product(const Device& dev, const void* A_codes, const void* A_sc
 {
     Sizes sa;
     sizes_of(M, K, 1, &sa);
-    // Pairs once their tiles would occupy most of the device (below that the small tiles
-    // spread better).  Of the two widths the one whose turns of the clusters cost less: a
+    // Pairs, but for few tiles with a long K, which small tiles share out: a pair takes
+    // 3.7 us and 0.22 a step, the split form 12 us until its own steps count (1024^3: 4.6
+    // and 11.3 us; 96 x 4096 x 4096: 7.0, 14.9; 128 x 2048 x 8192: 10.6, 12.3; 2048^3: 7.3,
+    // 8.4; 128 x 8192 x 8192: 11.3, 14.1).
+    // Of the two widths the one whose turns of the clusters cost less: a
     // 128-wide turn takes 0.72 of a 256-wide one (16384 x 2048 x 7168: 14 turns in 97 us, 7 in
     // 68 us), 0.62 where rows are stored without TMA and the last turn's stores, which nothing
     // hides, are longer (3001 x 2000 x 4097, two turns of 256 or three of 128: 18.0 us, 18.8 us;
     // x 1999: 25.1 us, 23.3 us).
     const int64_t pairs = dev.sms / 2, wide = cdiv(M, 256) * cdiv(N, 256), narrow = cdiv(M, 256) * cdiv(N, 128);
-    const double turn = tma_rows(C, ldc) ? 0.72 : 0.62;
-    if (M > 64 && N > 64 && narrow * 4 >= pairs * 3 && sa.row_tiles * sa.kt < INT32_MAX && cdiv(N, 128) * sa.kt < INT32_MAX)
+    const double turn = tma_rows(C, ldc, N) ? 0.72 : 0.62;
+    const bool split = narrow * 4 < pairs * 3 && cdiv(K, 256) > 40;
+    if (M > 64 && N > 64 && !split && sa.row_tiles * sa.kt < INT32_MAX && cdiv(N, 128) * sa.kt < INT32_MAX)
         return cdiv(narrow, pairs) * turn < cdiv(wide, pairs)
                    ? launch_pair<128>(dev, A_codes, A_scales, B_codes, B_scales, bias, act, C, ldc, M, N, K, stream)
                    : launch_pair<256>(dev, A_codes, A_scales, B_codes, B_scales, bias, act, C, ldc, M, N, K, stream);
     mxf4_dev::GemmParams p = {};
-    // Few rows of A: B's rows take the 128 lanes and A's rows the narrow side.
+    // Few rows of A: B's rows take the 128 lanes and A's rows the narrow side, as narrow as
+    // they fit (16 x 16384 x 8192: 10.1 us, 18.3 with 64 columns, 23.2 the other way round;
+    // 64 x 8192 x 8192: 11.0 us, 13.5 the other way round).
     p.swapped = M <= 64 && M < N;
     p.bn = !p.swapped ? 128 : M <= 16 ? 16 : M <= 32 ? 32 : 64;
     p.M = p.swapped ? N : M;
@@ -238,8 +247,11 @@ gemm_f16_status product(const Device& dev, const void* A_codes, const void* A_sc
     p.stages = static_cast<int32_t>(std::min<int64_t>(16, (kMaxSmem / 2 - 2048) / sbytes));
     p.tmem_cols = p.bn == 128 ? 256 : p.bn == 64 ? 128 : p.bn == 32 ? 64 : 32;
     const int64_t tiles = cdiv(p.M, 128) * cdiv(p.N, p.bn);
+    // As many CTAs a tile as the device holds at once, while each has 8 steps: their sums
+    // cost 1 to 2 us (1 x 2048 x 2048, 8 steps: 4.7 us by one CTA, 5.9 by 4, 7.0 by 8;
+    // 16 x 4096 x 8192, 32 steps: 11.1, 7.6, 8.8; 16 x 2048 x 16384, 64 steps: 19.0, 9.4, 8.9).
     int cluster = 1;
-    while (cluster < 8 && tiles * cluster * 2 <= 2 * dev.sms && cluster * 2 <= p.steps) cluster *= 2;
+    while (cluster < 8 && tiles * cluster * 2 <= 2 * dev.sms && cluster * 16 <= p.steps) cluster *= 2;
     if (tiles * cluster > INT32_MAX) return GEMM_F16_ERR_INVALID_VALUE;
     if (!encode_codes(&p.tmA, p.swapped ? B_codes : A_codes, p.M, sa.pitch, 128) ||
         !encode_codes(&p.tmB, p.swapped ? A_codes : B_codes, p.N, sa.pitch, static_cast<uint32_t>(p.bn)))

@@ -141,7 +141,8 @@ gemm_f16_status launch_route(const moe_dev::Params& p, cudaStream_t stream)
                          stream, p);
 }
 
-// (most layers have few experts: the choosing warp's code is then short)
+// Up to 64 experts the choosing warp's code is short: with the form for 512, 64 experts took
+// 47.8 us instead of 42.3 (4 tokens, MXFP4) and 8 experts 78.2 instead of 74.9 (1 token, fp16).
 template <int kLayout>
 gemm_f16_status launch_route(const moe_dev::Params& p, cudaStream_t stream)
 {
@@ -226,10 +227,10 @@ gemm_f16_status launch_stream(const moe_dev::Params& p, const Layout& l, uint8_t
     sp.hpitch = static_cast<int32_t>(kMx ? l.fq : 2 * l.fp);
     sp.xwords = static_cast<int32_t>(l.dw / 4);
     sp.hwords = static_cast<int32_t>(l.fw / 4);
-    // Tokens of one reading of an expert's weights: all of them for few tokens,
-    // 16 otherwise, or as many as tensor memory has columns for next to y's sums;
-    // fewer leave the shared memory to the weights' ring.
-    sp.cap = p.T <= 4 ? 4 : p.T <= 8 ? 8 : kMx && p.T > 32 ? 12 : 16;
+    // Tokens of one reading of an expert's weights: 16, or as many as tensor memory
+    // has columns for next to y's sums (4 * 72 + 24 + 128 of 512).  Fewer for few
+    // tokens would leave the weights' ring a stage more, and measured the same.
+    sp.cap = kMx && p.T > 32 ? 12 : 16;
     sp.b_bytes = static_cast<int32_t>(round_up(kMx ? sp.cap * moe_dev::kPieces : std::max(16, 2 * sp.cap), 8) * 128);
     sp.stage_bytes = 2 * static_cast<int32_t>(moe_dev::kTileBytes) + sp.b_bytes + (kMx ? 6 * mxf4_dev::kScaleTile : 0);
     sp.stages = std::min(16, (kMaxSmem - kStaticSmem - 1024) / sp.stage_bytes);

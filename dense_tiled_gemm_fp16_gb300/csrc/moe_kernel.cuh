@@ -88,7 +88,7 @@ struct Weight {
 
 // Counters of one call.
 struct Control {
-    int ticket_up, done_up, ticket_down, unused;
+    int ticket_up, done_up, ticket_down;
 };
 
 struct Params {
@@ -134,8 +134,6 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
 }
-
-__device__ __forceinline__ __half ld_nc_half(const __half* p) { return __ushort_as_half(ld_nc_u16(p)); }
 
 // How the router's elements lie: 0 any strides, 1 contracted axis contiguous,
 // 2 experts contiguous (16-byte words in both).

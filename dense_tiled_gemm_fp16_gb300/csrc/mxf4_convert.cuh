@@ -6,6 +6,11 @@
 // values: the 128 rows fill whole 512-byte scale tiles, which are put together
 // in shared memory and leave in one piece, and 256 values of a row are 128
 // bytes of codes, one full line.
+//
+// Measured on 131072 x 7168 fp16: 335 us (7.1 TB/s), the inverse 344 us (6.9);
+// 65536 x 7168 transposed 239 us (5.0); rows that start anywhere, 65536 x 7001:
+// 240 us (4.8) and 284 us (4.1), bound by the second load and the shift of every
+// 16 bytes (issue 57 and 73 % of cycles).
 #pragma once
 
 #include "mxf4_format.cuh"
