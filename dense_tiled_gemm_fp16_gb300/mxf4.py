@@ -52,7 +52,7 @@ def _torch():
     if _t is None:
         import torch
         _codes.update({torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32})
-        _u8, _device, _raw = torch.uint8, torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
+        _u8, _device, _raw = torch.uint8, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
         _t = torch
     return _t
 
@@ -186,6 +186,13 @@ def _run(device, name: str, *args) -> None:
         _pkg()._check(st, name)
 
 
+def _check_like(x, dtype, device) -> None:
+    if x.dtype is not dtype:
+        raise TypeError("gemm_f16 takes float16 tensors")
+    if x.device != device:
+        raise ValueError("tensors must share one CUDA device")
+
+
 def mxf4_quantize(x, axis: int = -1, stream=None) -> Mxf4Matrix:
     """x (2-D, or 3-D with a leading batch; float16, bfloat16 or float32; any
     positive strides) in MXFP4 along `axis`, the one a product will contract: a
@@ -237,39 +244,41 @@ def mxf4_mm(a, b: Mxf4Matrix, bias=None, act="none", out=None, stream=None):
     """fp16 C[m, n] = act(sum_k a[m, k] b[n, k] + bias[n]): b an Mxf4Matrix
     [N, K], a an Mxf4Matrix [M, K] or a float16 tensor [M, K] that is quantised
     on the way; returns C."""
-    g, t = _pkg(), _t or _torch()
     if not isinstance(b, Mxf4Matrix) or b.batch is not None:
         raise TypeError("mxf4_mm takes b as an Mxf4Matrix of two dimensions")
+    g, f16 = _g or _pkg(), (_t or _torch()).float16
     held = isinstance(a, Mxf4Matrix)
-    if len(a.shape) != 2:
+    shape = a.shape
+    if len(shape) != 2:
         raise ValueError("expected two matrices")
-    M, K = a.shape
-    N = b.rows
+    M, K = shape
+    N, device = b.rows, b.device
     if K != b.k:
         raise ValueError(f"inner dimensions differ: {K} vs {b.k}")
     code = g._act(act)
-    if bias is not None and (bias.dim() != 1 or bias.shape[0] != N or bias.stride(0) != 1):
-        raise ValueError("bias must hold N values with unit stride")
-    device = b.device
-    if out is not None:
-        g._check_out(out, (M, N), "[M, N]")
-    for x in (None if held else a, out, bias):
-        if x is not None and x.dtype is not t.float16:
-            raise TypeError("gemm_f16 takes float16 tensors")
-    if device.type != "cuda" or any(x is not None and x.device != device for x in (a, out, bias)):
+    if not held and a.dtype is not f16:
+        raise TypeError("gemm_f16 takes float16 tensors")
+    if device.type != "cuda" or a.device != device:
         raise ValueError("tensors must share one CUDA device")
+    bp = None
+    if bias is not None:
+        if bias.dim() != 1 or bias.shape[0] != N or bias.stride(0) != 1:
+            raise ValueError("bias must hold N values with unit stride")
+        _check_like(bias, f16, device)
+        bp = bias.data_ptr()
     if out is None:
-        out = _empty((M, N), t.float16, device, stream)
-    raw = _stream(device, stream)
-    ldc = out.stride(0) if M > 1 else N
-    bp = None if bias is None else bias.data_ptr()
+        out, ldc = _empty((M, N), f16, device, stream), N
+    else:
+        g._check_out(out, (M, N), "[M, N]")
+        _check_like(out, f16, device)
+        ldc = out.stride(0) if M > 1 else N
     if held:
         _run(device, "gemm_mxf4", a.codes_ptr, a.scales_ptr, b.codes_ptr, b.scales_ptr, bp, code, out.data_ptr(), ldc, M,
-             N, K, raw)
+             N, K, _stream(device, stream))
     else:
         sm, sk = a.stride()
         nc, ns = _bytes(M, K, 1)
-        work = _empty(nc + ns, t.uint8, device, stream)
+        work = _empty(nc + ns, _u8, device, stream)
         _run(device, "gemm_mxf4_a16", a.data_ptr(), sm if M > 1 else max(1, K), sk if K > 1 else 1, work.data_ptr(),
-             b.codes_ptr, b.scales_ptr, bp, code, out.data_ptr(), ldc, M, N, K, raw)
+             b.codes_ptr, b.scales_ptr, bp, code, out.data_ptr(), ldc, M, N, K, _stream(device, stream))
     return out
