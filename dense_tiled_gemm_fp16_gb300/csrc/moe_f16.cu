@@ -356,10 +356,10 @@ gemm_f16_status moe_f16(const void* x, int64_t stride_xt, int64_t stride_xi, con
     if (cols_aligned(*gate, E) && cols_aligned(*up, E) && cols_aligned(*down, E))
         return launch_stream<moe_dev::kStreamCols>(p, l, base, ws, dev.sms, stream);
     if (gate->stride_i == 1 && up->stride_i == 1 && down->stride_i == 1)
-        return launch_experts<moe_dev::kF16Rows, 4>(p, dev.sms, stream);
+        return launch_experts<moe_dev::kF16Rows, 3>(p, dev.sms, stream);
     if (gate->stride_o == 1 && up->stride_o == 1 && down->stride_o == 1)
-        return launch_experts<moe_dev::kF16Cols, 4>(p, dev.sms, stream);
-    return launch_experts<moe_dev::kF16Strided, 4>(p, dev.sms, stream);
+        return launch_experts<moe_dev::kF16Cols, 3>(p, dev.sms, stream);
+    return launch_experts<moe_dev::kF16Strided, 3>(p, dev.sms, stream);
 }
 
 }  // extern "C"

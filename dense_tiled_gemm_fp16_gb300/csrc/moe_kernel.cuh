@@ -425,48 +425,107 @@ struct Step {
     static constexpr int kOut = (kUp ? 8 : 16) * kTiles;   // hidden values, or columns of y, of a unit
     static constexpr int kWords = kVals / 8;               // 32-bit words of a column a thread holds
 };
-constexpr int kStepBytes = 2048;
+constexpr int kStepBytes = 2560;   // a stage: 2 KB in place, and the words that hold them before
 
-// A step of one projection (down) or of two (up: w0 the gate, w1 the up rows)
-// into a stage: outputs o0 .., values k0 ..; outputs from `rows` and values
-// from K on are zeros.
+// A step of one projection (down) or of two (up: w0 the gate, w1 the up rows);
+// outputs o0 .., values k0 ..; outputs from `rows` and values from K on are zeros.
 //   kF16Rows/kF16Strided: 16 rows of 64 values, word c of row r at c ^ 4 (r & 1);
 //     a pair's rows 0-7 are the gate's, 8-15 the up projection's.
 //   kF16Cols: rows of K; up: 16 of 32 gate and 32 up outputs, down: 32 of 32
 //     outputs.  Two down rows k, k + 16 share 128 bytes.
+// Rows that start anywhere come in two moves: the aligned 16-byte words that
+// hold a run of neighbouring values, one more than they fill, go to the stage
+// asynchronously (fetch_stage); once there, a shift puts them in place (align_stage).
 template <int kFmt, bool kUp>
-__device__ __forceinline__ void load_stage(uint32_t dst, const Weight& w0, const Weight& w1, int e, int o0, int rows,
-                                           int k0, int K, int lane)
-{
-    const int c = lane & 7;   // 16-byte word of the stage's 128-byte row
-#pragma unroll 2
-    for (int j = 0; j < 4; ++j) {
-        const int r = (lane >> 3) + 4 * j;   // of 16 stage rows
-        uint32_t u[4] = {};
-        uint32_t at;
+struct Run {
+    static constexpr int kWords = kFmt == kF16Cols ? 4 : 8;   // words of a run
+    const __half* base;   // of the projection
+    const __half* at;     // the run's first value
+    int n;                // its values in range, possibly more than it has
+    __device__ Run(const Weight& w0, const Weight& w1, int e, int o0, int rows, int k0, int K, int run)
+    {
         if (kFmt == kF16Cols) {
-            const Weight& w = kUp && c >= 4 ? w1 : w0;
-            const int k = k0 + r + (!kUp && c >= 4 ? 16 : 0), o = o0 + 8 * (c & 3);
-            const __half* row = reinterpret_cast<const __half*>(w.data) + e * w.se + k * w.si;
-            mxf4_dev::load8<__half, false>(row, o, k < K ? rows : 0, u);
-            if (k >= K || o + 8 > rows) mxf4_dev::mask_tail<__half>(u, k < K ? rows - o : 0);
-            at = r * 128 + ((c ^ (((r >> 2) << 1) | (r & 1))) << 4);
+            const int half = run & 1, k = k0 + (run >> 1) + (!kUp && half ? 16 : 0);
+            const Weight& w = kUp && half ? w1 : w0;
+            base = reinterpret_cast<const __half*>(w.data);
+            at = base + e * w.se + k * w.si + o0;
+            n = k < K ? rows - o0 : 0;
         } else {
+            const Weight& w = kUp && run >= 8 ? w1 : w0;
+            const int o = o0 + (kUp ? run & 7 : run);
+            base = reinterpret_cast<const __half*>(w.data);
+            at = base + e * w.se + o * w.so + k0;
+            n = o < rows ? K - k0 : 0;
+        }
+    }
+};
+
+// Where word c of stage row r lies.
+template <int kFmt>
+__device__ __forceinline__ uint32_t stage_word(int r, int c)
+{
+    return r * 128 + ((kFmt == kF16Cols ? c ^ (((r >> 2) << 1) | (r & 1)) : c ^ ((r & 1) << 2)) << 4);
+}
+
+template <int kFmt, bool kUp>
+__device__ __forceinline__ void fetch_stage(uint32_t dst, const Weight& w0, const Weight& w1, int e, int o0, int rows,
+                                            int k0, int K, int lane)
+{
+    if constexpr (kFmt == kF16Strided) {   // no neighbouring values: element by element, to their places
+        const int c = lane & 7;
+#pragma unroll 2
+        for (int j = 0; j < 4; ++j) {
+            const int r = (lane >> 3) + 4 * j, o = o0 + (kUp ? r & 7 : r), k = k0 + 8 * c;
             const Weight& w = kUp && j >= 2 ? w1 : w0;
-            const int o = o0 + (kUp ? r & 7 : r), k = k0 + 8 * c;
             const __half* row = reinterpret_cast<const __half*>(w.data) + e * w.se + o * w.so;
-            if (kFmt == kF16Rows) {
-                mxf4_dev::load8<__half, false>(row, k, o < rows ? K : 0, u);
-                if (o >= rows || k + 8 > K) mxf4_dev::mask_tail<__half>(u, o < rows ? K - k : 0);
-            } else if (o < rows) {
+            uint32_t u[4] = {};
+            if (o < rows) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     if (k + i < K) u[i >> 1] |= static_cast<uint32_t>(ld_nc_u16(row + (k + i) * w.si)) << (16 * (i & 1));
             }
-            at = r * 128 + ((c ^ ((r & 1) << 2)) << 4);
+            st_smem_v4(dst + stage_word<kFmt>(r, c), make_uint4(u[0], u[1], u[2], u[3]));
         }
-        st_smem_v4(dst + at, make_uint4(u[0], u[1], u[2], u[3]));
+    } else {
+        constexpr int kWords = Run<kFmt, kUp>::kWords + 1, kAll = 128 / (kWords - 1) * kWords;
+#pragma unroll 1
+        for (int i = lane; i < kAll; i += 32) {
+            const int run = i / kWords, word = i - run * kWords;
+            const Run<kFmt, kUp> v(w0, w1, e, o0, rows, k0, K, run);
+            const uintptr_t at = reinterpret_cast<uintptr_t>(v.at);
+            const int o = static_cast<int>(at & 15u), bytes = 2 * min(v.n, 8 * (kWords - 1));
+            const bool holds = bytes > 0 && 16 * word < o + bytes;
+            const uintptr_t src = holds ? at - o + 16 * word : reinterpret_cast<uintptr_t>(v.base) & ~uintptr_t(15);
+            cp_async16(dst + i * 16, reinterpret_cast<const void*>(src), holds ? 16u : 0u);
+        }
+        cp_async_commit();
     }
+}
+
+template <int kFmt, bool kUp>
+__device__ __forceinline__ void align_stage(uint32_t stage, const Weight& w0, const Weight& w1, int e, int o0, int rows,
+                                            int k0, int K, int lane)
+{
+    if constexpr (kFmt != kF16Strided) {
+        constexpr int kWords = Run<kFmt, kUp>::kWords;
+        const int c = lane & 7;
+        uint32_t u[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = (lane >> 3) + 4 * j, run = kWords == 8 ? r : 2 * r + (c >> 2), word = c & (kWords - 1);
+            const Run<kFmt, kUp> v(w0, w1, e, o0, rows, k0, K, run);
+            const uint32_t from = stage + (run * (kWords + 1) + word) * 16;
+            const uint4 a = ld_smem_v4(from), b = ld_smem_v4(from + 16);
+            const uint32_t in[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            mxf4_dev::funnel16(in, static_cast<uint32_t>(reinterpret_cast<uintptr_t>(v.at)) & 15u, u[j]);
+            if (v.n < 8 * (word + 1)) mxf4_dev::mask_tail<__half>(u[j], v.n - 8 * word);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            st_smem_v4(stage + stage_word<kFmt>((lane >> 3) + 4 * j, c), make_uint4(u[j][0], u[j][1], u[j][2], u[j][3]));
+    }
+    __syncwarp();
 }
 
 // Four 8x8 pieces, each transposed: operand registers of a 16-row tile from
@@ -672,9 +731,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const __grid_constant
             auto issue = [&](int n) {
                 if (n < mine) {
                     const int it = pu / units_each, f0 = (pu - it * units_each) * Up::kOut;
-                    load_stage<kFmt, true>(ring + (n % kRing) * kBytes, p.gate, p.up, sh.item[it].expert, f0, p.F,
-                                           (warp + ps * kWarps) * kVals, p.D, lane);
+                    fetch_stage<kFmt, true>(ring + (n % kRing) * kBytes, p.gate, p.up, sh.item[it].expert, f0, p.F,
+                                            (warp + ps * kWarps) * kVals, p.D, lane);
                     if (++ps == wsteps) ps = 0, ++pu;
+                } else {
+                    cp_async_commit();
                 }
             };
             for (int n = 0; n < kRing - 1; ++n) issue(n);
@@ -694,7 +755,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const __grid_constant
 #pragma unroll
                     for (int q = 0; q < kGroups; ++q)
                         load_column<kVals>(col[q], (warp + s * kWarps) * kVals, p.dp, q < groups, b[q]);
-                    __syncwarp();   // (every lane is done with the stage that is filled next)
+                    cp_async_wait<kRing - 2>();
+                    __syncwarp();   // (and every lane is done with the stage that is filled next)
+                    align_stage<kFmt, true>(ring + (n % kRing) * kBytes, p.gate, p.up, im.expert, f0, p.F,
+                                            (warp + s * kWarps) * kVals, p.D, lane);
                     issue(n + kRing - 1);
                     mma_stage<kFmt, true, kGroups>(acc, ring + (n % kRing) * kBytes, b, groups, lane);
                 }
@@ -772,9 +836,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const __grid_constant
                 if (++pu < u_hi) share(pu, &pi, &pend);
             if (pu < u_hi) {
                 const int it = pi / fsteps;
-                load_stage<kFmt, false>(ring + (n % kRing) * kBytes, p.down, p.down, sh.item[it].expert,
-                                        pu / p.splits * kOut, p.D, (pi - it * fsteps) * kVals, p.F, lane);
+                fetch_stage<kFmt, false>(ring + (n % kRing) * kBytes, p.down, p.down, sh.item[it].expert,
+                                         pu / p.splits * kOut, p.D, (pi - it * fsteps) * kVals, p.F, lane);
                 ++pi;
+            } else {
+                cp_async_commit();
             }
         };
         for (int n = 0; n < kRing - 1; ++n) issue(n);
@@ -840,7 +906,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const __grid_constant
 #pragma unroll
                 for (int q = 0; q < kCols; ++q)
                     load_column<kVals>(col[q], (i - it * fsteps) * kVals, p.fp, q < groups, b[q]);
-                __syncwarp();   // (every lane is done with the stage that is filled next)
+                cp_async_wait<kRing - 2>();
+                __syncwarp();   // (and every lane is done with the stage that is filled next)
+                align_stage<kFmt, false>(ring + (n % kRing) * kBytes, p.down, p.down, im.expert, unit / p.splits * kOut,
+                                         p.D, (i - it * fsteps) * kVals, p.F, lane);
                 issue(n + kRing - 1);
                 mma_stage<kFmt, false, kCols>(acc, ring + (n % kRing) * kBytes, b, groups, lane);
             }
