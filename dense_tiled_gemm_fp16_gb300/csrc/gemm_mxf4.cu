@@ -224,11 +224,12 @@ gemm_f16_status product(const Device& dev, const void* A_codes, const void* A_sc
     mxf4_dev::GemmParams p = {};
     // Few rows of A: B's rows take the 128 lanes and A's rows the narrow side, as narrow as
     // they fit (16 x 16384 x 8192: 10.1 us, 18.3 with 64 columns, 23.2 the other way round;
-    // 64 x 8192 x 8192: 11.0 us, 13.5 the other way round).
+    // 64 x 8192 x 8192: 11.0 us, 13.5 the other way round); the same for few columns
+    // (65536 x 16 x 7168: 41 us, 59 with 128 columns).
     p.swapped = M <= 64 && M < N;
-    p.bn = !p.swapped ? 128 : M <= 16 ? 16 : M <= 32 ? 32 : 64;
     p.M = p.swapped ? N : M;
     p.N = p.swapped ? M : N;
+    p.bn = p.N <= 16 ? 16 : p.N <= 32 ? 32 : p.N <= 64 ? 64 : 128;
     p.sfa = static_cast<const uint8_t*>(p.swapped ? B_scales : A_scales);
     p.sfb = static_cast<const uint8_t*>(p.swapped ? A_scales : B_scales);
     p.kt = sa.kt;

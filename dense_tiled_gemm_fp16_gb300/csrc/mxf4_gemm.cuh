@@ -103,7 +103,7 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
     return v;
 }
 
-// 16 finished sums of row m, columns n .. n + 15, to C; swapped, the first `count`.
+// The first `count` of 16 finished sums of row m, columns n on, to C.
 __device__ __forceinline__ void store16(const GemmParams& p, int64_t m, int64_t n, int count, float* v)
 {
     if (m >= p.M) return;
@@ -125,7 +125,7 @@ __device__ __forceinline__ void store16(const GemmParams& p, int64_t m, int64_t 
         for (int i = 0; i < 16; ++i) v[i] = act_f32(p.act, v[i]);
     }
     __half* c = p.C + m * p.ldc + n;
-    if (n + 16 <= p.N && reinterpret_cast<uintptr_t>(c) % 16 == 0) {
+    if (count == 16 && n + 16 <= p.N && reinterpret_cast<uintptr_t>(c) % 16 == 0) {
         uint4 o[2];
         o[0] = make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]), pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
         o[1] = make_uint4(pack_half2(v[8], v[9]), pack_half2(v[10], v[11]), pack_half2(v[12], v[13]),
@@ -135,7 +135,7 @@ __device__ __forceinline__ void store16(const GemmParams& p, int64_t m, int64_t 
     } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            if (n + i < p.N) c[i] = __float2half_rn(v[i]);
+            if (i < count && n + i < p.N) c[i] = __float2half_rn(v[i]);
     }
 }
 

@@ -1,4 +1,4 @@
-"""MXFP4 products of enough tiles for the CTA-pair kernel: both tile widths, outputs
+"""MXFP4 products by the CTA-pair kernel and of few columns: both tile widths, outputs
 that TMA can store and outputs that it cannot, bias and activation far into
 their tails, launch options.
 
@@ -59,6 +59,19 @@ def test_bias_activation_and_the_output_s_place(M, N, K, act, scale, lead, pitch
     out.fill_(-7.0)
     assert (buf == -7.0).all()   # nothing around the output was written
     assert g.gemm_f16_device_status() == 0
+
+
+@pytest.mark.parametrize("M,N,K", [(96, 96, 10500), (70, 200, 12000), (300, 16, 8192), (1000, 40, 4096), (513, 3, 2100),
+                                   (20000, 33, 300)])
+def test_few_columns_and_long_sums(M, N, K):
+    x, w = _operands(M, N, K, M + N + K, 1)
+    bias = torch.randn(N, generator=torch.Generator().manual_seed(3)).half()
+    buf = torch.full((M + 1, N + 3), -7.0, dtype=torch.float16, device=DEV)
+    out = buf[:M, :N]
+    g.mxf4_mm(x.to(DEV), g.mxf4_quantize(w.to(DEV)), bias=bias.to(DEV), act="silu", out=out)
+    _check(_held(x), _held(w), bias.double().numpy(), "silu", out)
+    out.fill_(-7.0)
+    assert (buf == -7.0).all()
 
 
 def test_activations_of_extreme_sums():
