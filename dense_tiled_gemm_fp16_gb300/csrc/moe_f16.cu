@@ -31,10 +31,6 @@ struct Layout {
     int64_t dq, fq, dw, fw, xq, xs, hq, hs;            // MXFP4 columns: row pitches of codes and of scales
 };
 
-// Most shares of the experts' K: with many tokens the shares' sums cost more
-// than idle CTAs in the last turn.
-int max_splits(int64_t T) { return T <= 16 ? moe_dev::kMaxSplits : 4; }
-
 bool layout_of(int64_t T, int64_t D, int64_t F, int64_t E, int64_t top, Layout* l)
 {
     if (T < 1 || T > MOE_F16_MAX_TOKENS || E < 1 || E > MOE_F16_MAX_EXPERTS || top < 1 || top > MOE_F16_MAX_TOP_K ||
@@ -56,7 +52,7 @@ bool layout_of(int64_t T, int64_t D, int64_t F, int64_t E, int64_t top, Layout* 
     l->xs = take(T * moe_dev::kPieces * l->dw);
     l->hq = take(T * top * moe_dev::kPieces * l->fq);
     l->hs = take(T * top * moe_dev::kPieces * l->fw);
-    l->parts = take(std::max(max_splits(T) * T * l->dp * 4,
+    l->parts = take(std::max(moe_dev::kMaxSplits * T * l->dp * 4,
                              static_cast<int64_t>(moe_dev::kMaxParts) * 2 * std::max<int64_t>(T, 16) * 256 * 4));
     l->bytes = at;
     return true;
@@ -157,7 +153,7 @@ gemm_f16_status launch_experts(moe_dev::Params& p, int sms, cudaStream_t stream)
     const int64_t ranges = cdiv(p.D, kOut);
     p.splits = 1;
     double best = 0;
-    for (int s = 1; s <= max_splits(p.T); ++s) {
+    for (int s = 1; s <= moe_dev::kMaxSplits; ++s) {
         const double fill = static_cast<double>(ranges * s) / (cdiv(ranges * s, sms) * sms);
         if (fill > best + 0.04) best = fill, p.splits = s;
     }
@@ -169,7 +165,8 @@ gemm_f16_status launch_experts(moe_dev::Params& p, int sms, cudaStream_t stream)
     return launch_kernel(kernel, dim3(static_cast<unsigned>(sms)), moe_dev::kThreads, smem, 1, stream, p);
 }
 
-// Pieces of 8 tokens an expert, or of 16 when there are more than 8 in all.
+// Pieces of 8 tokens an expert, or of 16 when there are more than 8 in all (8 of 64
+// experts of 2047 x 1023: 1 token 72 us, 78 with pieces of 16; 8 tokens 196, 221).
 template <int kFmt, int kRing>
 gemm_f16_status launch_experts(moe_dev::Params& p, int sms, cudaStream_t stream)
 {

@@ -9,8 +9,8 @@
 // thread.  Every warp brings its own share of K through a private ring: no
 // barrier stands between a warp and its next bytes.
 //
-// Measured on 16 tokens, 8 of 64 experts of 2047 x 1023, 0.7 GB: 287 us with rows
-// contiguous along k (issue on 59 % of cycles: the shifts), 323 us the other way
+// Measured on 16 tokens, 8 of 64 experts of 2047 x 1023, 0.7 GB: 274 us with rows
+// contiguous along k (issue on 59 % of cycles: the shifts), 321 us the other way
 // (64-byte runs that start anywhere: DRAM reads 2.6 times the bytes).  With loads
 // through registers, waited for before the next step's, they were 360 and 433 us.
 //
@@ -34,7 +34,12 @@ using namespace gemm_f16_dev;
 constexpr int kMaxTokens = 64, kMaxExperts = 512, kMaxTop = 8, kMaxSlots = kMaxTokens * kMaxTop;
 constexpr int kPieces = 6;   // MXFP4 columns that a value of the narrow side is held in
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kMaxSplits = 8, kMaxRanges = 2048;   // ranges of 16 columns at least, 32768 in all
+// Shares of the experts' K that a range of y's columns is cut into at most, where the
+// ranges alone leave CTAs idle: more cost more in sums than they fill (8 of 64 experts of
+// 2047 x 1023, rows contiguous along k and the other way: 1 token 51 and 58 us with up to
+// 4 shares, 72 and 65 with 8, 51 and 67 with none; 16 tokens 274 and 321, 287 and 337, 274
+// and 412).
+constexpr int kMaxSplits = 4, kMaxRanges = 2048;   // ranges of 16 columns at least, 32768 in all
 constexpr int kRouteCluster = 8;   // CTAs that share a router product, and tokens of a group
 
 __device__ __forceinline__ float act_f32(int act, float x)
