@@ -52,6 +52,25 @@ __device__ __forceinline__ float act_f32(int act, float x)
     }
 }
 
+// A hidden value for fp16 weights: its rounding to fp16 and 2^11 times what that
+// leaves, in fp16 too.  What is left is at most half the first one's last place,
+// 2^-11 of the power of two below the value, so that the second neither
+// overflows (16 * 2^11 at most) nor, down to values of 2^-14, falls under its own
+// type: the pair is within 2^-23 of the value, or 2^-36 where that is less.
+// (Without the factor the second half lost bits below 2^-3 and all of them
+// below 2^-14: outputs of 2^-12 from hidden values of 2^-17 were 2.2e-3 off.)
+constexpr float kLowScale = 2048.f;
+
+__device__ __forceinline__ void split_hidden(float h, __half* hi, __half* lo)
+{
+    *hi = __float2half_rn(h);
+    const float back = __half2float(*hi);
+    *lo = isfinite(back) ? __float2half_rn((h - back) * kLowScale) : __ushort_as_half(0);
+}
+
+// The sum of the two halves' products.
+__device__ __forceinline__ float join_hidden(float hi, float lo) { return fmaf(lo, 1.f / kLowScale, hi); }
+
 // D (+)= A * B, m16n8k16, fp16 in, fp32 sums.
 __device__ __forceinline__ void mma16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1)
@@ -123,7 +142,7 @@ struct Params {
     int32_t* counts;       // [column ranges]: finished shares
     float* parts;          // [splits][T][dp]: their sums
     __half* xp;            // [T][dp]: the tokens, packed, zeros past D
-    __half* hp;            // [T * top][2][fp]: the hidden values as high and low halves, by expert
+    __half* hp;            // [T * top][2][fp]: the hidden values as split_hidden's halves, by expert
     int32_t test_stall;
     uint64_t timeout_ns;
     int* status;
@@ -815,12 +834,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const __grid_constant
                             if (j < im.count) {
                                 // (past F: zeros, whatever the tokens hold)
                                 const float hv = f < p.F ? act_f32(p.act, i ? v.y : v.x) * (i ? v.w : v.z) : 0.f;
-                                const __half hi = __float2half_rn(hv);
-                                const float back = __half2float(hi);
-                                const __half lo = isfinite(back) ? __float2half_rn(hv - back) : __ushort_as_half(0);
                                 __half* dst = p.hp + static_cast<int64_t>(im.first + j) * 2 * p.fp + f;
-                                dst[0] = hi;
-                                dst[p.fp] = lo;
+                                split_hidden(hv, dst, dst + p.fp);
                             }
                         }
                     }
@@ -916,8 +931,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts(const __grid_constant
                         float* to = mysum + sh.slot[im.first + j] / p.top * kOut;
 #pragma unroll
                         for (int t = 0; t < kTiles; ++t) {
-                            to[16 * t + g] = fmaf(w, acc[t][q][0] + acc[t][q][1], to[16 * t + g]);
-                            to[16 * t + g + 8] = fmaf(w, acc[t][q][2] + acc[t][q][3], to[16 * t + g + 8]);
+                            to[16 * t + g] = fmaf(w, join_hidden(acc[t][q][0], acc[t][q][1]), to[16 * t + g]);
+                            to[16 * t + g + 8] = fmaf(w, join_hidden(acc[t][q][2], acc[t][q][3]), to[16 * t + g + 8]);
                         }
                     }
                 }

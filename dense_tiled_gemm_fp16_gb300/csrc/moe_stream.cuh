@@ -12,7 +12,7 @@
 //
 // Both operands of an MMA have one type, so the narrow side is held in the
 // weights' format.  fp16: a hidden value is two columns, its fp16 rounding and
-// the fp16 rounding of the rest.  MXFP4: a value is 6 columns, each the e2m1
+// that of 2^11 times the rest (split_hidden).  MXFP4: a value is 6 columns, each the e2m1
 // rounding of what the columns before it leave, which is under 2^-16.5 of the
 // block's largest magnitude in the end (split_blocks): less than a fp16 value's
 // own last place unless it is 50 times smaller.  The epilogue adds the columns in
@@ -95,7 +95,7 @@ __device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t* r)
 }
 
 // Four tokens' sums of this thread's row: `width` adjacent columns each, the
-// later, smaller ones added first.
+// later, smaller ones added first; two are the halves of hidden values.
 template <int kWidth>
 __device__ __forceinline__ void take4(uint32_t taddr, float* v)
 {
@@ -112,9 +112,13 @@ __device__ __forceinline__ void take4(uint32_t taddr, float* v)
     tmem_wait_ld();
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        v[j] = __uint_as_float(r[j * kWidth + kWidth - 1]);
+        if constexpr (kWidth == 2) {
+            v[j] = join_hidden(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+        } else {
+            v[j] = __uint_as_float(r[j * kWidth + kWidth - 1]);
 #pragma unroll
-        for (int q = kWidth - 2; q >= 0; --q) v[j] += __uint_as_float(r[j * kWidth + q]);
+            for (int q = kWidth - 2; q >= 0; --q) v[j] += __uint_as_float(r[j * kWidth + q]);
+        }
     }
 }
 
@@ -519,11 +523,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if (j0 + j >= im.count) break;
-                    const __half hh = __float2half_rn(hv[j]);
-                    const float back = __half2float(hh);
                     __half* dst = reinterpret_cast<__half*>(sp.h + static_cast<int64_t>(im.first + j0 + j) * 2 * sp.hpitch) + f;
-                    dst[0] = hh;
-                    dst[sp.hpitch >> 1] = isfinite(back) ? __float2half_rn(hv[j] - back) : __ushort_as_half(0);
+                    split_hidden(hv[j], dst, dst + (sp.hpitch >> 1));
                 }
             }
         };

@@ -12,8 +12,9 @@
  *   y[t]     = fp16(sum_j w[t, j] * (h[t, j] down_e))
  *
  * x, router and the experts' fp16 weights are fp16 at any positive strides;
- * products are exact, sums fp32.  Between the projections h is held as the sum
- * of two fp16 values (22 bits or so); a magnitude past the fp16 range becomes
+ * products are exact, sums fp32.  With fp16 weights h is held between the
+ * projections as an fp16 value plus 2^-11 times another, within 2^-23 of
+ * itself or 2^-36 where that is less; a magnitude past the fp16 range becomes
  * an infinity, as in the library's products.  An expert that no token chose is
  * not read.
  */
