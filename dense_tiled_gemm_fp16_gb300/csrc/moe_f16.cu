@@ -224,17 +224,14 @@ gemm_f16_status launch_stream(const moe_dev::Params& p, const Layout& l, uint8_t
     sp.hpitch = static_cast<int32_t>(kMx ? l.fq : 2 * l.fp);
     sp.xwords = static_cast<int32_t>(l.dw / 4);
     sp.hwords = static_cast<int32_t>(l.fw / 4);
-    // Tokens of one reading of an expert's weights: 16, or as many as tensor memory
-    // has columns for next to y's sums (4 * 72 + 24 + 128 of 512).  Fewer for few
-    // tokens would leave the weights' ring a stage more, and measured the same.
-    sp.cap = kMx && p.T > 32 ? 12 : 16;
+    const moe_dev::StreamShape shape(kMx, p.T);
+    sp.cap = shape.cap;
     sp.b_bytes = static_cast<int32_t>(round_up(kMx ? sp.cap * moe_dev::kPieces : std::max(16, 2 * sp.cap), 8) * 128);
     sp.stage_bytes = 2 * static_cast<int32_t>(moe_dev::kTileBytes) + sp.b_bytes + (kMx ? 6 * mxf4_dev::kScaleTile : 0);
     sp.stages = std::min(16, (kMaxSmem - kStaticSmem - 1024) / sp.stage_bytes);
-    sp.acc_cols = kMx ? static_cast<uint32_t>(round_up(sp.cap * moe_dev::kPieces, 8)) : 32;
-    sp.y_col = 4 * sp.acc_cols + (kMx ? 24 : 0);
-    const uint32_t need = sp.y_col + 2 * ((p.T + 7) & ~7);
-    sp.tmem_cols = need <= 64 ? 64 : need <= 128 ? 128 : need <= 256 ? 256 : 512;
+    sp.acc_cols = shape.acc_cols;
+    sp.y_col = shape.y_col;
+    sp.tmem_cols = shape.alloc;
     const int smem = sp.stages * sp.stage_bytes + 1024;
     const auto kernel = moe_dev::moe_stream<kFmt>;
     if (!allow_smem(reinterpret_cast<const void*>(kernel), 12 + kFmt, kMaxSmem - kStaticSmem)) return GEMM_F16_ERR_LAUNCH;

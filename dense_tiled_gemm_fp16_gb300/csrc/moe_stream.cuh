@@ -45,6 +45,32 @@ namespace moe_dev {
 constexpr int kLoadWarps = 10;  // warps 6 .. 15 bring the narrow side
 constexpr uint32_t kTileBytes = 128 * 128;
 constexpr int kMaxParts = 160;
+constexpr uint32_t kTmemCols = 512;
+
+// A call's shares of tensor memory, in columns: two accumulators a row tile,
+// the scales (MXFP4), and y's sums, a column a token (rounded up to 8) and row tile.
+struct StreamShape {
+    int cap;                                  // tokens of a piece: of one reading of an expert's weights
+    uint32_t acc_cols, y_col, need, alloc;    // an accumulator, where y's sums begin, all, as allocated
+    // Pieces of 16 tokens, or with MXFP4 and more than 32 tokens as many as there are
+    // columns for next to y's sums (4 * 72 + 24 + 128).  Smaller ones for few tokens
+    // would leave the weights' ring a stage more, and measured the same.
+    __host__ __device__ constexpr StreamShape(bool mx, int tokens)
+        : cap(mx && tokens > 32 ? 12 : 16), acc_cols(mx ? (cap * kPieces + 7) / 8 * 8 : 32),
+          y_col(4 * acc_cols + (mx ? 24 : 0)), need(y_col + 2 * ((tokens + 7) & ~7)),
+          alloc(need <= 64 ? 64 : need <= 128 ? 128 : need <= 256 ? 256 : kTmemCols)
+    {
+    }
+};
+
+// Columns past the allocation would be an illegal access, so no number of tokens may need more.
+constexpr bool every_call_fits()
+{
+    for (int t = 1; t <= kMaxTokens; ++t)
+        if (StreamShape(false, t).need > kTmemCols || StreamShape(true, t).need > kTmemCols) return false;
+    return true;
+}
+static_assert(every_call_fits(), "the expert stream's columns fit tensor memory");
 
 // Counters of one call, zeroed by the routing kernel.
 struct StreamControl {
