@@ -445,6 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
                     while (ok && ld_acquire_gpu(&sp.ctl->done) < parts)
                         ok = !*abort && globaltimer_ns() - t0 <= p.timeout_ns;
                 }
+                __syncwarp();   // the other lanes' reads come after lane 0's acquire (a shuffle orders no memory)
                 ok = __shfl_sync(~0u, ok, 0);
                 if (!ok) break;
             }
