@@ -256,7 +256,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
         abort_flag = 1;
         atomicExch(p.status, GEMM_F16_ERR_TIMEOUT);
     };
-    // the i-th part of a phase; -1 once the CTA has given up
+    // The lanes of a warp wait for themselves and may see a wait's limit pass, or the
+    // CTA give up, at different times: before they next meet in a warp-wide
+    // instruction they agree, and all go on only if each does.
+    // The i-th part of a phase; -1 once the CTA has given up.
     auto part_at = [&](int ph, int i) {
         int v;
         while ((v = list[ph][i]) < 0)
@@ -272,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
         uint32_t par = 0;
         bool ok = true;
         for (int ph = 0; ph < 2 && ok; ++ph) {
-            for (int i = 0; ok; ++i) {
+            for (int i = 0; (ok = __all_sync(~0u, ok)); ++i) {
                 int part = ticket;
                 if (ph || i) part = lane == 0 ? atomicAdd(&sp.ctl->ticket[ph], 1) : 0;
                 part = __shfl_sync(~0u, part, 0);
@@ -338,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
         const uint32_t tsa = tmem + 4 * sp.acc_cols, tsb = tsa + 16;
         for (int ph = 0; ph < 2 && ok; ++ph) {
             const int k64 = ((ph ? p.F : p.D) + 63) >> 6;
-            for (int i = 0; ok; ++i) {
+            for (int i = 0; (ok = __all_sync(~0u, ok)); ++i) {
                 const int part = __shfl_sync(~0u, part_at(ph, i), 0);
                 if (part < 0) ok = false;
                 if (part < 0 || part >= parts) break;
@@ -428,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
         for (int ph = 0; ph < 2 && ok; ++ph) {
             bool waited = ph == 0;
             for (int i = 0; ok; ++i) {
-            const int part = part_at(ph, i);
+            const int part = __shfl_sync(~0u, part_at(ph, i), 0);
             if (part < 0) ok = false;
             if (part < 0 || part >= parts) break;
             const int64_t lo = phase[ph].start(part), hi = phase[ph].start(part + 1);

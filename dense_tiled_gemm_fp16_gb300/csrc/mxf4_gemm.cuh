@@ -277,7 +277,8 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_mxf4_tile(const __grid_cons
         }
         if (!ok) mbar_wait(done, 0, nullptr, kDrainNs);
     } else {
-        const bool ok = mbar_wait(done, 0, abort, p.timeout_ns);
+        // (a warp's lanes read tensor memory together or not at all)
+        const bool ok = __all_sync(~0u, mbar_wait(done, 0, abort, p.timeout_ns));
         if (!ok) fail();
         tc_fence_after();
         const int64_t m = m0 + warp * 32 + lane;
