@@ -216,13 +216,15 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
     }
     tc_fence_before();
     griddep_wait();
-    griddep_launch_dependents();
     int ticket = 0;   // of the weights' warp
     if (threadIdx.x == 4 * 32) ticket = atomicAdd(&sp.ctl->ticket[0], 1);
     order_choices(p, ch, reinterpret_cast<uint16_t*>(smem), sp.cap);
     fence_proxy_async_smem();   // the counts lay where the copies will write
     __syncthreads();
     tc_fence_after();
+    // Only now that this CTA has its tensor memory: a kernel that started in between
+    // could take it and then wait for this one.
+    griddep_launch_dependents();
     const uint32_t tmem = tmem_slot;
     const int items = ch.items;
 
