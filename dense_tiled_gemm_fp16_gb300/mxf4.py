@@ -106,14 +106,21 @@ def _bytes(rows: int, k: int, batch: int):
 
 class Mxf4Matrix:
     """A matrix [rows, k], or a batch [batch, rows, k], held in MXFP4 along k:
-    ``codes`` and ``scales`` are the byte arrays include/gemm_mxf4.h lays out,
-    ``codes_ptr`` and ``scales_ptr`` their device addresses."""
+    ``codes`` and ``scales`` are the byte arrays include/gemm_mxf4.h lays out
+    (contiguous uint8), ``codes_ptr`` and ``scales_ptr`` their device addresses."""
 
     __slots__ = ("_data", "_split", "rows", "k", "batch", "device", "codes_ptr", "scales_ptr")
 
     def __init__(self, codes, scales, rows: int, k: int, batch=None):
+        u8 = (_t or _torch()).uint8
+        if codes.dtype is not u8 or scales.dtype is not u8:
+            raise TypeError("codes and scales must be uint8 tensors")
+        if min(rows, k, 1 if batch is None else batch) < 1:
+            raise ValueError("a matrix has at least one row, one value and, in a batch, one matrix")
         if (codes.numel(), scales.numel()) != _bytes(rows, k, batch or 1) or codes.device != scales.device:
             raise ValueError("codes and scales do not hold a matrix of these sizes")
+        if not codes.is_contiguous() or not scales.is_contiguous():   # (only their base addresses go on)
+            raise ValueError("codes and scales must be contiguous")
         self._data, self._split = (codes, scales), None
         self.rows, self.k, self.batch, self.device = rows, k, batch, codes.device
         self.codes_ptr, self.scales_ptr = codes.data_ptr(), scales.data_ptr()
