@@ -95,9 +95,9 @@ def moe_few(x, router, gate, up, down, top_k: int, act="silu", renormalize: bool
     wg, wu, wd = _weight(gate, D, F, E, "gate"), _weight(up, D, F, E, "up"), _weight(down, F, D, E, "down")
     if out is not None:
         g._check_out(out, (T, D), "[T, D]")
-    for v in (x, router, out):
+    for name, v in (("x", x), ("router", router), ("out", out)):
         if v is not None and v.dtype is not t.float16:
-            raise TypeError("gemm_f16 takes float16 tensors")
+            raise TypeError(f"moe_few takes {name} as a float16 tensor")
     device = x.device
     if device.type != "cuda" or any(v is not None and v.device != device for v in (router, gate, up, down, out)):
         raise ValueError("tensors must share one CUDA device")

@@ -193,9 +193,9 @@ def _run(device, name: str, *args) -> None:
         _pkg()._check(st, name)
 
 
-def _check_like(x, dtype, device) -> None:
+def _check_like(x, dtype, device, name: str) -> None:
     if x.dtype is not dtype:
-        raise TypeError("gemm_f16 takes float16 tensors")
+        raise TypeError(f"mxf4_mm takes {name} as a float16 tensor")
     if x.device != device:
         raise ValueError("tensors must share one CUDA device")
 
@@ -264,20 +264,20 @@ def mxf4_mm(a, b: Mxf4Matrix, bias=None, act="none", out=None, stream=None):
         raise ValueError(f"inner dimensions differ: {K} vs {b.k}")
     code = g._act(act)
     if not held and a.dtype is not f16:
-        raise TypeError("gemm_f16 takes float16 tensors")
+        raise TypeError("mxf4_mm takes a as a float16 tensor or an Mxf4Matrix")
     if device.type != "cuda" or a.device != device:
         raise ValueError("tensors must share one CUDA device")
     bp = None
     if bias is not None:
         if bias.dim() != 1 or bias.shape[0] != N or bias.stride(0) != 1:
             raise ValueError("bias must hold N values with unit stride")
-        _check_like(bias, f16, device)
+        _check_like(bias, f16, device, "bias")
         bp = bias.data_ptr()
     if out is None:
         out, ldc = _empty((M, N), f16, device, stream), N
     else:
         g._check_out(out, (M, N), "[M, N]")
-        _check_like(out, f16, device)
+        _check_like(out, f16, device, "out")
         ldc = out.stride(0) if M > 1 else N
     if held:
         _run(device, "gemm_mxf4", a.codes_ptr, a.scales_ptr, b.codes_ptr, b.scales_ptr, bp, code, out.data_ptr(), ldc, M,
