@@ -241,6 +241,8 @@ def mxf4_dequantize(q: Mxf4Matrix, dtype=None, stream=None):
         dtype = _torch().float16
     code = _dtype_code(dtype)
     device = q.device
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
     y = _empty(q.shape, dtype, device, stream)
     _run(device, "mxf4_dequantize", q.codes_ptr, q.scales_ptr, y.data_ptr(), code, q.rows, q.k, q.batch or 1,
          _stream(device, stream))

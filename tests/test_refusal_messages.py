@@ -26,6 +26,12 @@ def test_product():
         g.mxf4_mm(z(3, 64, dtype=torch.float32), q)
 
 
+def test_inverse_of_a_host_matrix():
+    q = g.Mxf4Matrix(z(4 * 32, dtype=torch.uint8), z(512, dtype=torch.uint8), 4, 64)
+    with pytest.raises(ValueError, match="CUDA device"):
+        g.mxf4_dequantize(q)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("which", ["bias", "out"])
 def test_product_on_the_device(which):
