@@ -226,7 +226,7 @@ gemm_f16_status launch_stream(const moe_dev::Params& p, const Layout& l, uint8_t
     sp.hwords = static_cast<int32_t>(l.fw / 4);
     const moe_dev::StreamShape shape(kMx, p.T);
     sp.cap = shape.cap;
-    sp.b_bytes = static_cast<int32_t>(round_up(kMx ? sp.cap * moe_dev::kPieces : std::max(16, 2 * sp.cap), 8) * 128);
+    sp.b_bytes = static_cast<int32_t>((kMx ? sp.cap * moe_dev::kPieces : 2 * sp.cap) * 128);
     sp.stage_bytes = 2 * static_cast<int32_t>(moe_dev::kTileBytes) + sp.b_bytes + (kMx ? 6 * mxf4_dev::kScaleTile : 0);
     sp.stages = std::min(16, (kMaxSmem - kStaticSmem - 1024) / sp.stage_bytes);
     sp.acc_cols = shape.acc_cols;

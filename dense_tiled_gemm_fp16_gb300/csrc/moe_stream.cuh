@@ -12,11 +12,10 @@
 //
 // Both operands of an MMA have one type, so the narrow side is held in the
 // weights' format.  fp16: a hidden value is two columns, its fp16 rounding and
-// that of 2^11 times the rest (split_hidden).  MXFP4: a value is 6 columns, each the e2m1
-// rounding of what the columns before it leave, which is under 2^-16.5 of the
-// block's largest magnitude in the end (split_blocks): less than a fp16 value's
-// own last place unless it is 50 times smaller.  The epilogue adds the columns in
-// fp32.
+// that of 2^11 times the rest (split_hidden).  MXFP4: a value is 8 columns, each the e2m1
+// rounding of what the columns before it leave, which is under 2^-22.5 of the
+// block's largest magnitude in the end (split_blocks).  The epilogue adds the
+// columns in fp32.
 //
 // Work is cut into gridDim parts of equal bytes in each of the two phases
 // (gate/up, down), wherever that falls: a part's first and last output tile may
@@ -52,11 +51,11 @@ constexpr uint32_t kTmemCols = 512;
 struct StreamShape {
     int cap;                                  // tokens of a piece: of one reading of an expert's weights
     uint32_t acc_cols, y_col, need, alloc;    // an accumulator, where y's sums begin, all, as allocated
-    // Pieces of 16 tokens, or with MXFP4 and more than 32 tokens as many as there are
-    // columns for next to y's sums (4 * 72 + 24 + 128).  Smaller ones for few tokens
-    // would leave the weights' ring a stage more, and measured the same.
+    // Pieces of 16 tokens, with MXFP4 as many as there are columns for next to the scales
+    // and y's sums: 14 for 16 tokens, 13 for 32, 11 for 64.
     __host__ __device__ constexpr StreamShape(bool mx, int tokens)
-        : cap(mx && tokens > 32 ? 12 : 16), acc_cols(mx ? (cap * kPieces + 7) / 8 * 8 : 32),
+        : cap(mx ? static_cast<int>((kTmemCols - 24 - 2 * ((tokens + 7) & ~7)) / (4 * kPieces)) : 16),
+          acc_cols(mx ? cap * kPieces : 32),
           y_col(4 * acc_cols + (mx ? 24 : 0)), need(y_col + 2 * ((tokens + 7) & ~7)),
           alloc(need <= 64 ? 64 : need <= 128 ? 128 : need <= 256 ? 256 : kTmemCols)
     {
@@ -463,7 +462,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
                     const int j = r / width;
                     return static_cast<int64_t>(ph ? im.first + j : ch.slot[im.first + j] / p.top) * width + r - j * width;
                 };
-                constexpr int kRows = (16 * (kMx ? kPieces : 2) + 4 * kLoadWarps - 1) / (4 * kLoadWarps);   // a lane's rows
+                // a lane's rows (no call has larger pieces than one for a token)
+                constexpr int kRows = (StreamShape(kMx, 1).cap * (kMx ? kPieces : 2) + 4 * kLoadWarps - 1) / (4 * kLoadWarps);
                 const uint8_t* src[kRows];
                 uint32_t dst[kRows];
 #pragma unroll

@@ -15,8 +15,11 @@
  * products are exact, sums fp32.  With fp16 weights h is held between the
  * projections as an fp16 value plus 2^-11 times another, within 2^-23 of
  * itself or 2^-36 where that is less; a magnitude past the fp16 range becomes
- * an infinity, as in the library's products.  An expert that no token chose is
- * not read.
+ * an infinity, as in the library's products.  With MXFP4 weights x and h are
+ * held as sums of 8 MXFP4 values, within 2^-22.5 of the largest magnitude among
+ * the 32 values that share a block with them (i / 32); h keeps fp32's range
+ * there, and an infinity or a NaN makes its whole block, and so the token's y,
+ * NaN.  An expert that no token chose is not read.
  */
 #ifndef MOE_F16_H
 #define MOE_F16_H
