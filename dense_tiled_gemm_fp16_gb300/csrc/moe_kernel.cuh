@@ -9,10 +9,12 @@
 // thread.  Every warp brings its own share of K through a private ring: no
 // barrier stands between a warp and its next bytes.
 //
-// Measured on 16 tokens, 8 of 64 experts of 2047 x 1023, 0.7 GB: 274 us with rows
-// contiguous along k (issue on 59 % of cycles: the shifts), 321 us the other way
-// (64-byte runs that start anywhere: DRAM reads 2.6 times the bytes).  With loads
-// through registers, waited for before the next step's, they were 360 and 433 us.
+// Measured on 16 tokens, 8 of 64 experts of 2047 x 1023, 0.7 GB: 274 to 282 us with
+// rows contiguous along k (issue on 59 % of cycles: the shifts), 299 to 321 us the
+// other way (64-byte runs that start anywhere: DRAM reads 2.6 times the bytes).  With
+// loads through registers, waited for before the next step's, they were 360 and 433.
+// Projections of different orders share no unit stride and are read value by
+// value: 561 us where 2048 x 1024 in one order streams in 133.
 //
 // K is reordered within 32 values, the same on both sides: thread c of a quad
 // holds values 8c .. 8c + 7 of the block, one 16-byte word a row, split over two

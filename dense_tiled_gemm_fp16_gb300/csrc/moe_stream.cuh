@@ -1,8 +1,9 @@
 // The experts' kernel of the mixture-of-experts layer for weights that TMA can
 // address: fp16 in either orientation, and MXFP4.
 //
-// The layer is bound by reading the chosen experts' weights once, so the kernel
-// is built around that stream: one thread a CTA keeps a ring of 32 KB pairs of
+// The layer is bound by reading the chosen experts' weights, once for every piece
+// of 11 to 16 tokens (StreamShape) that chose one, so the kernel is built around that
+// stream: one thread a CTA keeps a ring of 32 KB pairs of
 // weight tiles in flight by TMA, the tensor cores take them from shared memory
 // as the 128-row side (tcgen05.mma), and a few token columns are the narrow
 // side.  No instruction is spent per weight: MXFP4 codes are multiplied as they
@@ -29,9 +30,11 @@
 // way before the wait.
 //
 // Measured, both kernels: 64 tokens, 8 of 64 experts of 7168 x 2048 in MXFP4, 1.5 GB:
-// 278 us (5.4 TB/s, 0.95 of the copy rate within a phase); 16 tokens, 8 of 64 of 2048 x
-// 1024 in fp16, 0.7 GB: 129 us; 4 tokens in MXFP4, 88 MB: 42 us, latency for the most
-// part (routing 7 us, first weights 5, exchange between the phases 8, last sums 4).
+// 288 to 291 us (5.2 TB/s); 16 tokens, 8 of 64 of 2048 x 1024 in fp16, 0.7 GB: 128 us; 4
+// tokens in MXFP4, 88 MB: 42 us, latency for the most part (routing 7 us, first
+// weights 5, exchange between the phases 8, last sums 4).  Experts with several
+// pieces: 64 tokens, 4 of 8 of 4096 x 2048 (37 tokens the most) 149 us in fp16 and 93 in
+// MXFP4, all 8 (64 each) 260 and 122, where one reading takes 59 and 16.
 #pragma once
 
 #include <cuda.h>

@@ -7,10 +7,10 @@
 // in shared memory and leave in one piece, and 256 values of a row are 128
 // bytes of codes, one full line.
 //
-// Measured on 131072 x 7168 fp16: 335 us (7.1 TB/s), the inverse 344 us (6.9);
-// 65536 x 7168 transposed 239 us (5.0); rows that start anywhere, 65536 x 7001:
-// 240 us (4.8) and 284 us (4.1), bound by the second load and the shift of every
-// 16 bytes (issue 57 and 73 % of cycles).
+// Measured on 131072 x 7168 fp16: 336 us (7.1 TB/s), the inverse 349 us (6.8), fp32
+// 577 us (7.4); 65536 x 7168 transposed 241 us (4.9), fp32 312 us (6.8); rows that
+// start anywhere, 65536 x 7001: 244 us (4.8) and 286 us (4.1), bound by the second
+// load and the shift of every 16 bytes (issue 57 and 73 % of cycles).
 #pragma once
 
 #include "mxf4_format.cuh"

@@ -1,4 +1,4 @@
-// The MXFP4 format on the device: places of scales, and values to codes and back;
+// The MXFP4 format on the device: scales, values to codes and back;
 // and vector loads of rows that start at any element.
 #pragma once
 
@@ -14,12 +14,6 @@ namespace mxf4_dev {
 using namespace gemm_f16_dev;
 
 constexpr int kScaleTile = 512;   // bytes: 128 rows x 4 blocks
-
-// Place of (row, block) in a matrix's scales, `kt` scale tiles per 128 rows.
-__host__ __device__ inline int64_t scale_at(int64_t row, int64_t blk, int64_t kt)
-{
-    return ((row >> 7) * kt + (blk >> 2)) * kScaleTile + (row & 31) * 16 + ((row >> 5) & 3) * 4 + (blk & 3);
-}
 
 // 2^e exactly, -126 <= e <= 127.
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }

@@ -142,8 +142,9 @@ __device__ __forceinline__ void store16(const GemmParams& p, int64_t m, int64_t 
 // One 128 x bn tile a cluster, its K slots dealt to the cluster's CTAs in
 // contiguous parts; with more than one CTA the parts are summed by rank over
 // distributed shared memory (a fixed order, no workspace and no atomics).
-// Bound by the length of one cold chain: 16 x 16384 x 8192, 71 MB of weights,
-// takes 15.9 us with cold caches (4.5 TB/s), 9.9 us with the weights in L2.
+// Bound by the length of one cold chain: 16 x 16384 x 8192, 71 MB of weights
+// in 256 CTAs of 16 steps, takes 15.8 us with cold caches (4.5 TB/s), 9.9 us with
+// the weights in L2.
 __global__ void __launch_bounds__(kGemmThreads) gemm_mxf4_tile(const __grid_constant__ GemmParams p)
 {
     extern __shared__ uint8_t smem_raw[];
@@ -350,8 +351,9 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_mxf4_tile(const __grid_cons
 // begin when the epilogue of the one before has those columns in registers,
 // which it reads first: 1 200 cycles from a tile's last MMA to the next one's first.
 //
-// 131072 x 2048 x 7168: 497 us, 7.7 PFLOP/s; 8192^3 149 us, 7.4; 4096^3 24.5 us, the
-// last of its 4 turns a third full.
+// 131072 x 2048 x 7168: 496 us in short runs (7.8 PFLOP/s), 557 to 576 us in long ones;
+// 8192^3 152 us, 7.2; 4096^3 27 us, the last of its 4 turns a third full.  8192 x 8192 x
+// 1024 with bias and GELU: 70 us, the epilogue's (33 us without).
 struct PairParams {
     CUtensorMap tmA, tmB;        // codes, boxes of 128 bytes x 128 rows and x kBN / 2 rows
     CUtensorMap tmSA, tmSB;      // scale tiles: {128 words, tiles}, boxes of two tiles

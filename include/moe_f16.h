@@ -39,8 +39,10 @@ extern "C" {
 /* One projection of every expert: E matrices [in, out].
  * MOE_F16_WEIGHT_F16: data is fp16, element (e, i, o) at e * stride_e +
  *   i * stride_i + o * stride_o elements; scales NULL.  Fastest with one of
- *   stride_i, stride_o 1, the other strides multiples of 8 and data 16-byte
- *   aligned.
+ *   stride_i, stride_o 1, the same one in all three projections, the other
+ *   strides multiples of 8 and data 16-byte aligned; where one projection's are
+ *   not, all three are read the slower way (2 to 3 times the time), and value by
+ *   value (4 times) where they share no unit stride.
  * MOE_F16_WEIGHT_MXF4: data and scales are the codes and scales of E MXFP4
  *   matrices of `out` rows with `in` values each (gemm_mxf4.h); the strides are
  *   not read. */
