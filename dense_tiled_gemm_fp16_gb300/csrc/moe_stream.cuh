@@ -263,7 +263,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
     // The lanes of a warp wait for themselves and may see a wait's limit pass, or the
     // CTA give up, at different times: before they next meet in a warp-wide
     // instruction they agree, and all go on only if each does.
-    // The i-th part of a phase; -1 once the CTA has given up.
+    // The i-th part of a phase; -1 once the CTA has given up, or when the weights' warp,
+    // which names a part as soon as the one before is on its way, has not by the limit.
     auto part_at = [&](int ph, int i) {
         int v;
         while ((v = list[ph][i]) < 0)
@@ -435,9 +436,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
         for (int ph = 0; ph < 2 && ok; ++ph) {
             bool waited = ph == 0;
             for (int i = 0; ok; ++i) {
-            const int part = __shfl_sync(~0u, part_at(ph, i), 0);
-            if (part < 0) ok = false;
-            if (part < 0 || part >= parts) break;
+            const int part = part_at(ph, i);
+            ok = __all_sync(~0u, part >= 0);
+            if (!ok || part >= parts) break;
             const int64_t lo = phase[ph].start(part), hi = phase[ph].start(part + 1);
             const int width = kMx ? kPieces : ph ? 2 : 1;   // rows of a token
             const uint8_t* rows = ph ? sp.h : sp.x;
