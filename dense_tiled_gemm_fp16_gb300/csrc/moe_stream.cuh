@@ -266,9 +266,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream(const __grid_constant_
     // The i-th part of a phase; -1 once the CTA has given up, or when the weights' warp,
     // which names a part as soon as the one before is on its way, has not by the limit.
     auto part_at = [&](int ph, int i) {
-        int v;
+        int v = list[ph][i];
+        if (v >= 0) return v;
+        const uint64_t t0 = globaltimer_ns();
         while ((v = list[ph][i]) < 0)
-            if (*abort) break;
+            if (*abort || globaltimer_ns() - t0 > p.timeout_ns) break;
         return v;
     };
     auto columns = [&](int ph, int count) { return kMx ? count * kPieces : ph ? 2 * count : count; };
