@@ -30,7 +30,7 @@
 // way before the wait.
 //
 // Measured, both kernels: 64 tokens, 8 of 64 experts of 7168 x 2048 in MXFP4, 1.5 GB:
-// 288 to 291 us (5.2 TB/s); 16 tokens, 8 of 64 of 2048 x 1024 in fp16, 0.7 GB: 128 us; 4
+// 288 to 295 us (5.2 TB/s); 16 tokens, 8 of 64 of 2048 x 1024 in fp16, 0.7 GB: 128 us; 4
 // tokens in MXFP4, 88 MB: 42 us, latency for the most part (routing 7 us, first
 // weights 5, exchange between the phases 8, last sums 4).  Experts with several
 // pieces: 64 tokens, 4 of 8 of 4096 x 2048 (37 tokens the most) 149 us in fp16 and 93 in
