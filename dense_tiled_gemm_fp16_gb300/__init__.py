@@ -16,7 +16,9 @@ the current stream from the tensors: ``matmul``, ``bmm``, ``grouped_mm``,
 
 ``mxf4.py`` binds the MXFP4 matrices of ``include/gemm_mxf4.h`` (``mxf4_quantize``,
 ``mxf4_dequantize``, ``mxf4_mm``); ``moe.py`` the mixture-of-experts layer for a
-few tokens of ``include/moe_f16.h`` (``moe_few``).
+few tokens of ``include/moe_f16.h`` (``moe_few``); ``fp8.py`` the 8-bit matrices of
+``include/gemm_fp8.h`` (``fp8_quantize``, ``fp8_dequantize``, ``fp8_mm``,
+``fp8_grouped_mm``).
 """
 from __future__ import annotations
 
@@ -25,7 +27,9 @@ import os
 import threading
 
 from . import ledger  # noqa: F401  (pure-Python cost ledger)
-from . import moe, mxf4
+from . import fp8, moe, mxf4
+from .fp8 import (Fp8Matrix, fp8_dequantize, fp8_dequantize_ptr, fp8_grouped_mm, fp8_mm, fp8_quantize,  # noqa: F401
+                  fp8_quantize_ptr, fp8_sizes, gemm_fp8, gemm_fp8_a16, gemm_fp8_grouped, gemm_fp8_grouped_a16)
 from .moe import MoeWeight, moe_f16, moe_f16_workspace_size, moe_few  # noqa: F401
 from .mxf4 import (Mxf4Matrix, gemm_mxf4, gemm_mxf4_a16, mxf4_dequantize, mxf4_dequantize_ptr, mxf4_mm, mxf4_quantize,  # noqa: F401
                    mxf4_quantize_ptr, mxf4_sizes)
@@ -153,6 +157,7 @@ def lib():
                 L.gemm_f16_fused_get_plan.argtypes = [P, I64, I64, P, I64, I64, P, P, P, I, P, I64, I64, I64, I64,
                                                       ctypes.POINTER(Plan)]
                 L.gemm_f16_fused_get_plan.restype = ctypes.c_int
+                fp8.declare(L)
                 mxf4.declare(L)
                 moe.declare(L)
                 _lib = L

@@ -1,0 +1,223 @@
+// Quantisation to 8 bits and its inverse: streaming kernels, bound by HBM (2 or 4
+// bytes a value in, 1 + 1/128 out, and back).
+//
+// A block of threads takes a tile of 128 rows x 512 values: whole 512-byte scale
+// tiles, put together in shared memory, and whole 128-byte lines of codes.
+#pragma once
+
+#include "fp8_format.cuh"
+
+namespace fp8_dev {
+
+constexpr int kTileRows = 128, kTileVals = 512, kConvThreads = 256;
+constexpr int kDequantRows = 32;   // rows a block writes
+
+struct QuantParams {
+    const void* x;
+    int64_t sb, sr, sk;   // element strides
+    uint8_t* codes;
+    uint8_t* scales;
+    int64_t rows, k, pitch;   // pitch: code bytes a row
+    int64_t kt, row_tiles;
+    int64_t tile_rows;        // rows of a tile that a block takes: 128, or fewer of few rows
+};
+
+// Unit stride along k: 16 lanes take a block of 128 values, 8 a lane; a warp's 256
+// values are contiguous, half of a tile's width.  Rows of a tile that another block
+// of threads takes (tile_rows < 128) are left to it; the one with the matrix's last
+// row also writes the padding rows' scales.
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kConvThreads) quantize_rows(const QuantParams p)
+{
+    constexpr int kUnroll = sizeof(T) == 4 ? 2 : 4, kStep = kConvThreads / 64;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t parts = (p.rows + p.tile_rows - 1) / p.tile_rows;
+    const int64_t ct = blockIdx.x / parts, part = blockIdx.x - ct * parts;
+    const int64_t r0 = part * p.tile_rows, b = blockIdx.z;
+    const T* x = static_cast<const T*>(p.x) + b * p.sb;
+    uint8_t* codes = p.codes + b * p.rows * p.pitch;
+    uint8_t* scales = p.scales + b * p.row_tiles * p.kt * kScaleTile;
+    const int n = static_cast<int>(p.k), i = static_cast<int>(ct) * kTileVals + (warp & 1) * 256 + lane * 8;
+    const int block = i >> 7;   // this lane's block of its rows
+    const bool some = block < (n + kBlock - 1) / kBlock;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t end = min(p.rows, r0 + p.tile_rows);
+#pragma unroll 1
+    for (int64_t r = r0 + (warp >> 1); r < end; r += kStep * kUnroll) {
+        uint32_t w[kUnroll][8 * sizeof(T) / 4];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int k = r + u * kStep < end ? n : 0;
+            mxf4_dev::load8<T, kVec>(x + (r + u * kStep) * p.sr, i, k, w[u]);
+            if (i + 8 > k) mxf4_dev::mask_tail<T>(w[u], k - i);
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int64_t row = r + u * kStep;
+            uint32_t top = mxf4_dev::top_bits<T>(w[u]);
+#pragma unroll
+            for (int d = 1; d < 16; d *= 2) top = max(top, __shfl_xor_sync(~0u, top, d));
+            if (row >= end) continue;
+            const uint32_t code = some ? scale_code<T>(top) : 0u;
+            const uint2 c = codes8<T>(w[u], code);
+            if (i + 8 <= p.pitch) *reinterpret_cast<uint2*>(codes + row * p.pitch + i) = c;
+            if ((lane & 15) == 0) scales[scale_at(row, block, p.kt)] = static_cast<uint8_t>(code);
+        }
+    }
+    if (end == p.rows)   // padding rows of the last scale tile
+        for (int64_t r = p.rows + (warp >> 1); r < p.row_tiles * 128; r += kStep)
+            if ((lane & 15) == 0) scales[scale_at(r, block, p.kt)] = 0;
+}
+
+// Any strides (a transposed view has unit stride along the rows): a lane takes a
+// block of a row and a warp 32 neighbouring rows, so that a unit row stride gives
+// contiguous loads; the codes, 128 bytes a row, are turned in shared memory.
+template <typename T>
+__global__ void __launch_bounds__(kConvThreads) quantize_strided(const QuantParams p)
+{
+    constexpr int kPitch = kBlock + 16;   // bytes a row of the staged codes: 16-byte stores spread over the banks
+    constexpr int kWords = kBlock * sizeof(T) / 4;
+    __shared__ __align__(16) uint8_t cs[2][kTileRows * kPitch];
+    __shared__ __align__(16) uint8_t sc[kScaleTile];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = warp >> 2;
+    const int64_t ct = blockIdx.x / p.row_tiles, rt = blockIdx.x - ct * p.row_tiles;   // (neighbours along the rows)
+    const int64_t r0 = rt * kTileRows, b = blockIdx.z;
+    const T* x = static_cast<const T*>(p.x) + b * p.sb;
+    uint8_t* codes = p.codes + b * p.rows * p.pitch;
+    uint8_t* scales = p.scales + b * p.row_tiles * p.kt * kScaleTile;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lr = (warp & 3) * 32 + lane;
+    const int64_t r = r0 + lr;
+#pragma unroll 1
+    for (int it = 0; it < 2; ++it) {
+        const int blk = 2 * it + half;   // of the tile's four
+        const int64_t i = ct * kTileVals + blk * kBlock;
+        const int left = r < p.rows ? static_cast<int>(max(int64_t(0), min(int64_t(kBlock), p.k - i))) : 0;
+        const T* src = x + r * p.sr + i * p.sk;
+        uint32_t w[kWords];
+#pragma unroll
+        for (int c = 0; c < kBlock; ++c) {
+            const uint32_t v = c < left ? (sizeof(T) == 4 ? ld_nc_u32(src + c * p.sk) : ld_nc_u16(src + c * p.sk)) : 0u;
+            if (sizeof(T) == 4)
+                w[c] = v;
+            else
+                w[c >> 1] = c & 1 ? w[c >> 1] | v << 16 : v;
+        }
+        uint32_t top = 0;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) top = max(top, mxf4_dev::top_bits<T>(w + c * kWords / 16));
+        const uint32_t code = left > 0 ? scale_code<T>(top) : 0u;
+#pragma unroll
+        for (int c = 0; c < 16; c += 2) {
+            const uint2 a = codes8<T>(w + c * kWords / 16, code), d = codes8<T>(w + (c + 1) * kWords / 16, code);
+            *reinterpret_cast<uint4*>(cs[half] + lr * kPitch + c * 8) = make_uint4(a.x, a.y, d.x, d.y);
+        }
+        sc[lane * 16 + (warp & 3) * 4 + blk] = static_cast<uint8_t>(code);
+        __syncthreads();
+        for (int t = threadIdx.x & 127; t < kTileRows * 8; t += 128) {
+            const int row = t >> 3, c = t & 7;
+            if (r0 + row < p.rows && i + c * 16 < p.pitch)
+                *reinterpret_cast<uint4*>(codes + (r0 + row) * p.pitch + i + c * 16) =
+                    *reinterpret_cast<const uint4*>(cs[half] + row * kPitch + c * 16);
+        }
+        __syncthreads();
+    }
+    if (warp == 0)
+        reinterpret_cast<uint4*>(scales + (rt * p.kt + ct) * kScaleTile)[lane] = reinterpret_cast<const uint4*>(sc)[lane];
+}
+
+struct DequantParams {
+    const uint8_t* codes;
+    const uint8_t* scales;
+    void* y;
+    int64_t rows, k, pitch, kt, row_tiles;
+    int64_t col_tiles;   // of 256 values and the 7 that a row may begin before one
+};
+
+// A warp writes 256 neighbouring values of a row, 8 a lane, from the first multiple
+// of 8 values of the output's memory on, so that every full store is aligned
+// whatever the row's length; the codes are then taken from any byte on (three words
+// and a shift), and 8 values may lie in two blocks.
+// kVec: every row starts aligned, so that 8 values are 8 aligned bytes of codes.
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kConvThreads) dequantize(const DequantParams p)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t rt = blockIdx.x / p.col_tiles, b = blockIdx.z;
+    const int64_t c0 = (blockIdx.x - rt * p.col_tiles) * 32 + lane;   // this lane's group of 8
+    const uint8_t* codes = p.codes + b * p.rows * p.pitch;
+    const uint8_t* scales = p.scales + b * p.row_tiles * p.kt * kScaleTile;
+    T* y = static_cast<T*>(p.y) + b * p.rows * p.k;
+    griddep_wait();
+    griddep_launch_dependents();
+    constexpr int kUnroll = 4, kWarps = kConvThreads / 32;
+    const int64_t k = p.k, words = p.pitch >> 2, r0 = rt * kDequantRows + warp;
+    uint32_t w[kUnroll][3], sc[kUnroll][2];
+    int64_t at[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+        const int64_t r = r0 + u * kWarps;
+        const int shift = kVec ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(y + r * k) / sizeof(T) & 7);
+        const int64_t i = c0 * 8 - shift;
+        at[u] = r < p.rows && i < k ? i : k;
+        w[u][0] = w[u][1] = w[u][2] = sc[u][0] = sc[u][1] = 0u;
+        if (at[u] >= k) continue;
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(codes + r * p.pitch);
+        if (kVec) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(src) + c0);
+            w[u][0] = v.x, w[u][1] = v.y;
+            sc[u][0] = __ldg(scales + scale_at(r, i >> 7, p.kt));
+            continue;
+        }
+        const int64_t word = i >> 2;   // (words -1 and -2 hold nothing of the row)
+#pragma unroll
+        for (int c = 0; c < 3; ++c)
+            if (word + c >= 0 && word + c < words) w[u][c] = __ldg(src + word + c);
+        const int64_t first = max(i, int64_t(0)) >> 7, last = min(i + 7, k - 1) >> 7;
+        sc[u][0] = __ldg(scales + scale_at(r, first, p.kt));
+        sc[u][1] = last != first ? __ldg(scales + scale_at(r, last, p.kt)) : sc[u][0];
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+        const int64_t i = at[u];
+        if (i >= k) continue;
+        T* row = y + (r0 + u * kWarps) * k;
+        uint32_t h[4];
+        const uint32_t o = 8 * static_cast<uint32_t>(i & 3);
+        halves_of(kVec ? w[u][0] : __funnelshift_r(w[u][0], w[u][1], o), h);
+        halves_of(kVec ? w[u][1] : __funnelshift_r(w[u][1], w[u][2], o), h + 2);
+        T v[8];
+        uint4 out[sizeof(T) / 2];
+        const int turn = kVec ? 8 : static_cast<int>(kBlock - (i & (kBlock - 1)));   // values of the first block
+        if (Elem<T>::kInf == 0x7C00u && sc[u][0] - 103u <= 39u && (kVec || sc[u][1] - 103u <= 39u)) {
+            // fp16 holds the factors (2^-24 to 2^15): one rounding, two values an instruction
+            auto half_scale = [](uint32_t c) { return c >= 113u ? (c - 112u) << 10 : 1u << (c - 103u); };
+            const uint32_t f0 = half_scale(sc[u][0]), f1 = kVec ? f0 : half_scale(sc[u][1]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint32_t f = (2 * c < turn ? f0 : f1) | (2 * c + 1 < turn ? f0 : f1) << 16;
+                asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(h[c]) : "r"(h[c]), "r"(f));
+            }
+            out[0] = make_uint4(h[0], h[1], h[2], h[3]);
+        } else {
+            const float s0 = scale_value(sc[u][0]), s1 = kVec ? s0 : scale_value(sc[u][1]);
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                v[c] = Elem<T>::from_f32((c < turn ? s0 : s1) * Elem<__half>::to_f32(c & 1 ? h[c >> 1] >> 16 : h[c >> 1] & 0xFFFFu));
+            memcpy(out, v, sizeof(v));
+        }
+        if (kVec || (i >= 0 && i + 8 <= k)) {
+#pragma unroll
+            for (unsigned c = 0; c < sizeof(T) / 2; ++c) __stcs(reinterpret_cast<uint4*>(row + i) + c, out[c]);
+        } else {
+            memcpy(v, out, sizeof(v));
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                if (i + c >= 0 && i + c < k) row[i + c] = v[c];
+        }
+    }
+}
+
+}  // namespace fp8_dev
