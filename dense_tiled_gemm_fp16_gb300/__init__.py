@@ -18,7 +18,9 @@ the current stream from the tensors: ``matmul``, ``bmm``, ``grouped_mm``,
 ``mxf4_dequantize``, ``mxf4_mm``); ``moe.py`` the mixture-of-experts layer for a
 few tokens of ``include/moe_f16.h`` (``moe_few``); ``fp8.py`` the 8-bit matrices of
 ``include/gemm_fp8.h`` (``fp8_quantize``, ``fp8_dequantize``, ``fp8_mm``,
-``fp8_grouped_mm``).
+``fp8_grouped_mm``); ``norm.py`` the norm of ``include/rms_norm.h`` (``rms_norm``);
+``route.py`` the expert order of ``include/moe_route.h`` (``moe_sort``,
+``moe_gather``, ``moe_combine``, ``moe_combine_grad``).
 """
 from __future__ import annotations
 
@@ -27,12 +29,15 @@ import os
 import threading
 
 from . import ledger  # noqa: F401  (pure-Python cost ledger)
-from . import fp8, moe, mxf4
+from . import fp8, moe, mxf4, norm, route
 from .fp8 import (Fp8Matrix, fp8_dequantize, fp8_dequantize_ptr, fp8_grouped_mm, fp8_mm, fp8_quantize,  # noqa: F401
                   fp8_quantize_ptr, fp8_sizes, gemm_fp8, gemm_fp8_a16, gemm_fp8_grouped, gemm_fp8_grouped_a16)
 from .moe import MoeWeight, moe_f16, moe_f16_workspace_size, moe_few  # noqa: F401
 from .mxf4 import (Mxf4Matrix, gemm_mxf4, gemm_mxf4_a16, mxf4_dequantize, mxf4_dequantize_ptr, mxf4_mm, mxf4_quantize,  # noqa: F401
                    mxf4_quantize_ptr, mxf4_sizes)
+from .norm import rms_norm, rms_norm_ptr  # noqa: F401
+from .route import (MoeOrder, moe_combine, moe_combine_grad, moe_combine_grad_ptr, moe_combine_ptr, moe_gather,  # noqa: F401
+                    moe_gather_fp8_ptr, moe_gather_ptr, moe_sort, moe_sort_ptr, moe_sort_workspace_size)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgemm_f16.so")
@@ -160,6 +165,8 @@ def lib():
                 fp8.declare(L)
                 mxf4.declare(L)
                 moe.declare(L)
+                norm.declare(L)
+                route.declare(L)
                 _lib = L
     return _lib
 
