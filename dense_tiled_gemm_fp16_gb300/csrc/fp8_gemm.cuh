@@ -361,8 +361,8 @@ __global__ void __launch_bounds__(kTileThreads) gemm_fp8_tile(const __grid_const
 //
 // Gate/up (kGated): the 256 lanes hold 128 rows of either weight, 16 of one and 16 of
 // the other by turns, so that a thread of the epilogue holds both values of an output.
-constexpr int kPairThreads = 352;   // warps 0-7 epilogue, 8 loads, 9 MMA, 10 scales
 constexpr int kStages = 6, kSets = 4, kMaxGroups = 512;
+constexpr int kPairThreads = 320 + 32 * kSets;   // warps 0-7 epilogue, 8 loads, 9 MMA, the others scales
 constexpr uint32_t kStageBytes = 2 * kABytes, kSetBytes = 3 * kScaleTile, kBoxBytes = 32 * 64;
 constexpr uint32_t kPairSmem = kStages * kStageBytes + 8 * kBoxBytes + kSets * kSetBytes + 1024;
 constexpr uint32_t kSfCol = 496, kAcc1 = 240;   // scales of the weights (4), of A (8); the second accumulator
@@ -445,6 +445,22 @@ __device__ __forceinline__ void choose_tiles(const PairParams& p, Groups& g, int
         at += __shfl_sync(~0u, sum, 31);
     }
     if (lane == 0) g.tile0[p.groups] = at;
+}
+
+// Loads that are issued where they stand (the plain ones may be moved down to the use of
+// their values, past the waits between).
+__device__ __forceinline__ uint4 ld_now_v4(const void* p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint32_t ld_now_u32(const void* p)
+{
+    uint32_t v;
+    asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
 }
 
 struct Tile {
@@ -604,40 +620,45 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
             const uint64_t t0 = globaltimer_ns();
             while (globaltimer_ns() - t0 < 5000000ull) __nanosleep(100000);
         }
-    } else if (warp == 10) {
-        // 16 bytes a lane of each tile: the words of rows lane, lane + 32, + 64, + 96
-        int st = 0;
+    } else if (warp >= 10) {
+        // A warp for each of the kSets sets in shared memory: the fence that hands a set over
+        // waits for the loads under way, some 2500 cycles from DRAM, while a 256 x 256 tile
+        // uses a set up in 2048.
+        // 16 bytes a lane of each tile: the words of rows lane, lane + 32, + 64, + 96.
+        const int st = warp - 10;
         uint32_t par = 0;
         bool ok = true;
-        for (int t = blockIdx.x >> 1; t < tiles && ok; t += clusters) {
+        int q = st;
+        for (int t = blockIdx.x >> 1; t < tiles && ok; t += clusters, q -= static_cast<int>(p.kt)) {
+            if (q >= p.kt) continue;
             const Tile o = place(p, groups, t);
-            const int wn = (o.w * 2 + static_cast<int>(rank)) * kRows;
-            const int first = (o.row + lane) & 127;   // (a half further is the next tile's same place)
+            const int wn = (o.w * 2 + static_cast<int>(rank)) * kRows, first = (o.row + lane) & 31;
             const int turn = ((o.row & 127) + lane) >> 5;   // words that the first tile's line lacks: 0 .. 4
-            for (int q = 0; q < static_cast<int>(p.kt); ++q) {
+            const int64_t matrix = static_cast<int64_t>(o.group) * p.w_tiles * p.kt * kScaleTile;
+            for (; q < p.kt && ok; q += kSets) {
+                const uint4 none = make_uint4(0u, 0u, 0u, 0u);
                 auto line = [&](const uint8_t* scales, int64_t tile, int64_t count, int r) {
-                    return tile < count ? ld_nc_v4(scales + (tile * p.kt + q) * kScaleTile + (r & 31) * 16)
-                                        : make_uint4(0u, 0u, 0u, 0u);
+                    return tile < count ? ld_now_v4(scales + (tile * p.kt + q) * kScaleTile + r * 16) : none;
                 };
                 uint4 w, x[3];
                 if (kGated) {
-                    const uint8_t* from = (lane & 16 ? p.su : p.sw) + (static_cast<int64_t>(o.group) * p.w_tiles * p.kt + q) * kScaleTile;
+                    const uint8_t* from = (lane & 16 ? p.su : p.sw) + matrix;
                     uint32_t v[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int r = wn + 16 * j + (lane & 15);
-                        v[j] = r < p.n ? ld_nc_u32(from + scale_at(r, 0, p.kt)) : 0u;
+                        v[j] = r < p.n ? ld_now_u32(from + scale_at(r, 4 * q, p.kt)) : 0u;
                     }
                     w = make_uint4(v[0], v[1], v[2], v[3]);
                 } else {
-                    w = line(p.sw + static_cast<int64_t>(o.group) * p.w_tiles * p.kt * kScaleTile, wn >> 7, p.w_tiles, lane);
+                    w = line(p.sw + matrix, wn >> 7, p.w_tiles, lane);
                 }
 #pragma unroll
-                for (int h = 0; h < 3; ++h)
-                    x[h] = h == 0 || o.width > 128 * (h - 1) ? line(p.sx, (o.row >> 7) + h, p.x_tiles, first)
-                                                            : make_uint4(0u, 0u, 0u, 0u);
+                for (int h = 0; h < 3; ++h)   // (a tile further is the next one's same line)
+                    x[h] = h == 0 || o.width > 128 * (h - 1) ? line(p.sx, (o.row >> 7) + h, p.x_tiles, first) : none;
                 ok = __all_sync(~0u, mbar_wait_cluster(sempty(st), par ^ 1u, abort, p.timeout_ns));
                 if (!ok) break;
+                par ^= 1u;
                 const uint32_t at = sets + st * kSetBytes + lane * 16;
                 st_smem_v4(at, w);
 #pragma unroll
@@ -653,7 +674,6 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(mapa_shared(sfull(st), 0));
-                if (++st == kSets) st = 0, par ^= 1u;
             }
         }
         if (!ok && lane == 0) fail();
@@ -674,34 +694,40 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
                 }
                 begun = true;
                 const uint32_t d = tmem + (acc ? kAcc1 : 0u);
+                ok = mbar_wait_cluster(sfull(set), spar, abort, p.timeout_ns) &&
+                     mbar_wait_cluster(full(st), par, abort, p.timeout_ns);
                 for (int s = 0; s < p.steps && ok; ++s) {
-                    if ((s & 3) == 0) {
-                        ok = mbar_wait_cluster(sfull(set), spar, abort, p.timeout_ns);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t df = scale_desc(sets + set * kSetBytes);   // (16-byte units: 32 a tile)
-                        if (issue) {
-                            tmem_copy_scales_pair(tsw, df);
-                            tmem_copy_scales_pair(tsx, df + 32);
-                            if (o.width > 128) tmem_copy_scales_pair(tsx + 4, df + 64);
-                            umma_commit_pair_mc(sempty(set), 0x3);
-                        }
-                        if (++set == kSets) set = 0, spar ^= 1u;
-                    }
-                    ok = mbar_wait_cluster(full(st), par, abort, p.timeout_ns);
-                    if (!ok) break;
                     tc_fence_after();
                     const uint32_t a = base + st * kStageBytes;
                     const uint64_t da = umma_desc_sw128(a, 16, 1024), db = umma_desc_sw128(a + kABytes, 16, 1024);
-                    const uint32_t id = idesc_mxf8(256, o.width, s & 3);
+                    const uint32_t id = idesc_mxf8(256, o.width, s & 3), done = empty(st);
                     const int n32 = min(4, p.k32 - 4 * s);
+                    const bool copies = (s & 3) == 0;
+                    const uint64_t df = scale_desc(sets + set * kSetBytes);   // (16-byte units: 32 a tile)
+                    const uint32_t read = sempty(set);
+                    auto mma = [&](int q) { umma_mxf8_pair(d, da + 2 * q, db + 2 * q, id, tsw, tsx, s > 0 || q > 0); };
                     if (issue) {
+                        if (copies) {
+                            tmem_copy_scales_pair(tsw, df);
+                            tmem_copy_scales_pair(tsx, df + 32);
+                            if (o.width > 128) tmem_copy_scales_pair(tsx + 4, df + 64);
+                            umma_commit_pair_mc(read, 0x3);
+                        }
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            if (q < n32) umma_mxf8_pair(d, da + 2 * q, db + 2 * q, id, tsw, tsx, s > 0 || q > 0);
-                        umma_commit_pair_mc(empty(st), 0x3);
+                        for (int q = 0; q < 3; ++q)
+                            if (q < n32) mma(q);
                     }
+                    // the next step's waits while these run (the stage and the set that they wait
+                    // for were emptied by earlier steps than this one)
+                    if (copies && ++set == kSets) set = 0, spar ^= 1u;
                     if (++st == kStages) st = 0, par ^= 1u;
+                    if (s + 1 < p.steps)
+                        ok = (((s + 1) & 3) != 0 || mbar_wait_cluster(sfull(set), spar, abort, p.timeout_ns)) &&
+                             mbar_wait_cluster(full(st), par, abort, p.timeout_ns);
+                    if (issue) {
+                        if (n32 == 4) mma(3);
+                        umma_commit_pair_mc(done, 0x3);
+                    }
                 }
                 if (!ok) break;
                 if (issue) umma_commit_pair_mc(tfull + 8 * acc, 0x3);
