@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kTileThreads) gemm_fp8_tile(const __grid_const
 // ------------------------------------------------------------------ pairs
 // Persistent clusters of two CTAs, one tile at a time, its MMAs over both
 // (cta_group::2).  The weights' rows take the 256 lanes and A's rows the columns, in
-// every product: a tile's columns are then as many as its rows need (32 to 256, a
+// every product: a tile's columns are then as many as its rows need (32 to 224, a
 // number in the instruction descriptor), so that one kernel serves groups of any
 // number of rows, which the host does not know.
 //
@@ -354,18 +354,19 @@ __global__ void __launch_bounds__(kTileThreads) gemm_fp8_tile(const __grid_const
 // then leaves out.  A's scales begin at any row, so a warp puts their words in the
 // order of the scale tiles as it loads them, one set for 512 values of k.
 //
-// Two accumulators of 256 columns and the scales do not fit tensor memory (512
-// columns): the second begins 16 columns inside a first one of 256, and a tile's
-// MMAs begin when the epilogue of the one before has those columns in registers,
-// which it reads first.
+// At most 224 columns, so that two accumulators and the scales fit tensor memory (512
+// columns) side by side and a tile's MMAs follow the last one's without a pause: with
+// two of 256, which have to share some, 1200 cycles passed between them (a 256-wide
+// tile takes 512 cycles a step, one of 224 takes 448).
 //
 // Gate/up (kGated): the 256 lanes hold 128 rows of either weight, 16 of one and 16 of
 // the other by turns, so that a thread of the epilogue holds both values of an output.
-constexpr int kStages = 6, kSets = 4, kMaxGroups = 512;
+constexpr int kMaxStages = 10, kSets = 4, kMaxGroups = 512;
 constexpr int kPairThreads = 320 + 32 * kSets;   // warps 0-7 epilogue, 8 loads, 9 MMA, the others scales
-constexpr uint32_t kStageBytes = 2 * kABytes, kSetBytes = 3 * kScaleTile, kBoxBytes = 32 * 64;
-constexpr uint32_t kPairSmem = kStages * kStageBytes + 8 * kBoxBytes + kSets * kSetBytes + 1024;
-constexpr uint32_t kSfCol = 496, kAcc1 = 240;   // scales of the weights (4), of A (8); the second accumulator
+constexpr uint32_t kSlotBytes = 12 * kABytes, kSetBytes = 3 * kScaleTile, kBoxBytes = 32 * 64;   // kSlotBytes: all stages
+constexpr uint32_t kPairSmem = kSlotBytes + 8 * kBoxBytes + kSets * kSetBytes + 1024;
+constexpr int kMaxWidth = 224;                  // columns of a tile
+constexpr uint32_t kSfCol = 496, kAcc1 = 256;   // scales of the weights (4), of A (8); the second accumulator
 
 struct PairParams {
     CUtensorMap tmW, tmU;        // weight codes {pitch, n, groups}, boxes of 128 bytes x 128 rows (kGated: 16)
@@ -379,6 +380,7 @@ struct PairParams {
     uint16_t* C;
     int64_t ldc, rows, n;
     int32_t groups, tiles_w, panel;   // panel: weight tiles walked together
+    int32_t width;               // W; 0: of the groups' choice
     int32_t k32, steps, act, bf16, vec;   // vec: C's rows take 16-byte stores
     int32_t test_stall;
     uint64_t timeout_ns;
@@ -392,17 +394,30 @@ struct Groups {
     int width;                   // W
 };
 
-__device__ __forceinline__ int parts_of(int rows, int w) { return (rows + w - 1) / w; }
-__device__ __forceinline__ int width_of(int rows, int parts) { return parts ? ((rows + parts - 1) / parts + 31) & ~31 : 0; }
+__host__ __device__ inline int parts_of(int rows, int w) { return (rows + w - 1) / w; }
+__host__ __device__ inline int width_of(int rows, int parts) { return parts ? ((rows + parts - 1) / parts + 31) & ~31 : 0; }
 
-// By one warp.  Counts below zero are taken as zero, rows past the matrix as absent.
 // A turn of the clusters costs its widest tile's columns and about 64 more, for the
 // weights' load and the tile's own start.
+__host__ __device__ inline int64_t cost_of(int tiles, int widest, int clusters)
+{
+    return static_cast<int64_t>((tiles + clusters - 1) / clusters) * (widest + 64);
+}
+
+// By one warp.  Counts below zero are taken as zero, rows past the matrix as absent.
 __device__ __forceinline__ void choose_tiles(const PairParams& p, Groups& g, int clusters, int lane)
 {
+    if (!p.group_rows) {
+        if (lane == 0) {
+            const int rows = static_cast<int>(p.rows);
+            g.row0[0] = g.tile0[0] = 0, g.row0[1] = rows;
+            g.tile0[1] = parts_of(rows, p.width) * p.tiles_w, g.width = p.width;
+        }
+        return;
+    }
     int64_t before = 0;
     for (int i = lane; i - lane < p.groups; i += 32) {
-        int64_t n = i >= p.groups ? 0 : p.group_rows ? max(0, p.group_rows[i]) : p.rows, sum = n;
+        int64_t n = i >= p.groups ? 0 : max(0, p.group_rows[i]), sum = n;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
             const int64_t up = __shfl_up_sync(~0u, sum, d);
@@ -415,8 +430,7 @@ __device__ __forceinline__ void choose_tiles(const PairParams& p, Groups& g, int
     __syncwarp();
     // a lane in four takes a width and a quarter of the groups
     const int w = 32 * ((lane & 7) + 1);
-    int64_t tiles = 0;
-    int widest = 0;
+    int tiles = 0, widest = 0;
     for (int i = lane >> 3; i < p.groups; i += 4) {
         const int r = g.row0[i + 1] - g.row0[i], parts = parts_of(r, w);
         tiles += parts;
@@ -427,10 +441,10 @@ __device__ __forceinline__ void choose_tiles(const PairParams& p, Groups& g, int
         tiles += __shfl_xor_sync(~0u, tiles, d);
         widest = max(widest, __shfl_xor_sync(~0u, widest, d));
     }
-    int64_t cost = (tiles * p.tiles_w + clusters - 1) / clusters * (widest + 64) * 16 + (7 - (lane & 7));
+    int64_t cost = w > kMaxWidth ? INT64_MAX : cost_of(tiles * p.tiles_w, widest, clusters) * 16 + (7 - (lane & 7));
 #pragma unroll
     for (int d = 1; d < 8; d *= 2) cost = min(cost, __shfl_xor_sync(~0u, cost, d));
-    const int width = 32 * (8 - static_cast<int>(cost & 15));
+    const int width = p.width ? p.width : 32 * (8 - static_cast<int>(cost & 15));
     if (lane == 0) g.width = width;
     int at = 0;
     for (int i = lane; i - lane < p.groups; i += 32) {
@@ -462,6 +476,51 @@ __device__ __forceinline__ uint32_t ld_now_u32(const void* p)
     asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
     return v;
 }
+
+// The pair's instructions for the lane that `on` is set in.  A predicate instead of a
+// branch: in a branch that not all lanes take every operand is moved to a uniform register
+// for each instruction, 60 cycles and more, and a step's six instructions and waits took
+// 660 cycles whatever the tile's width.
+__device__ __forceinline__ void umma_mxf8_pair_if(uint32_t on, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                                  uint32_t idesc, uint32_t sfa, uint32_t sfb, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(on)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_copy_scales_pair_if(uint32_t on, uint32_t taddr, uint64_t desc)
+{
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+                 "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr), "l"(desc), "r"(on)
+                 : "memory");
+}
+
+__device__ __forceinline__ void umma_commit_pair_mc_if(uint32_t on, uint32_t bar, uint16_t cta_mask)
+{
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+            bar),
+        "h"(cta_mask), "r"(on)
+        : "memory");
+}
+
+// Whether the phase with the given parity is over, without waiting.
+__device__ __forceinline__ uint32_t mbar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok;
+}
+
+// Rows of A's copy for a CTA's half of a tile's columns: 16, 32, 64 or 128.
+__device__ __forceinline__ int box_rows(int width) { return width <= 32 ? 16 : width <= 64 ? 32 : width <= 128 ? 64 : 128; }
 
 struct Tile {
     int group, row, width, rows, w;   // A's first row, the columns, those that are the group's; weight tile
@@ -529,7 +588,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
     constexpr int kN = kGated ? 16 : 32;            // columns of C a warp holds
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    __shared__ __align__(8) uint64_t bars[2 * kStages + 2 * kSets + 5];
+    __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2 * kSets + 6];
     __shared__ Groups groups;
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
@@ -539,13 +598,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 16u * s; };
     auto empty = [&](int s) { return bar0 + 16u * s + 8u; };
-    auto sfull = [&](int s) { return bar0 + 16u * (kStages + s); };
-    auto sempty = [&](int s) { return bar0 + 16u * (kStages + s) + 8u; };
-    const uint32_t tfull = bar0 + 16u * (kStages + kSets), room = tfull + 16u, never = room + 8u, drain = never + 8u;
-    const uint32_t boxes = base + kStages * kStageBytes, sets = boxes + 8 * kBoxBytes;
+    auto sfull = [&](int s) { return bar0 + 16u * (kMaxStages + s); };
+    auto sempty = [&](int s) { return bar0 + 16u * (kMaxStages + s) + 8u; };
+    const uint32_t tfull = bar0 + 16u * (kMaxStages + kSets), tempty = tfull + 16u, never = tempty + 16u, drain = never + 8u;
+    const uint32_t boxes = base + kSlotBytes, sets = boxes + 8 * kBoxBytes;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < kMaxStages; ++s) {
             mbar_init(full(s), 1);
             mbar_init(empty(s), 1);
         }
@@ -553,9 +612,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
             mbar_init(sfull(s), 2);   // the scale warps of both CTAs
             mbar_init(sempty(s), 1);
         }
-        mbar_init(tfull, 1);
-        mbar_init(tfull + 8, 1);
-        mbar_init(room, 16);   // every epilogue warp of both CTAs
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(tfull + 8 * a, 1);
+            mbar_init(tempty + 8 * a, 16);   // every epilogue warp of both CTAs
+        }
         mbar_init(never, 1);
         mbar_init(drain, 1);
         abort_flag = 0;
@@ -576,7 +636,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
     cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    const int tiles = groups.tile0[p.groups];
+    const int tiles = __shfl_sync(~0u, groups.tile0[p.groups], 0);
+    // as many stages as fit: a tile of few columns brings little for its 16 KB of weights
+    const uint32_t stage_bytes = kABytes + box_rows(__shfl_sync(~0u, groups.width, 0)) * 128u;
+    const int stages = static_cast<int>(min(kSlotBytes / stage_bytes, static_cast<uint32_t>(kMaxStages)));
 
     const volatile int* abort = &abort_flag;
     auto fail = [&]() {
@@ -591,13 +654,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
         bool ok = true;
         for (int t = blockIdx.x >> 1; t < tiles && ok; t += clusters) {
             const Tile o = place(p, groups, t);
-            const int half = o.width >> 1, box = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
-            const uint32_t xbytes = 128u * (16u << box);
+            const int half = o.width >> 1, rows = box_rows(o.width), box = 27 - __clz(rows);   // 16 << box rows
+            const uint32_t xbytes = 128u * rows;
             const int32_t wn = (o.w * 2 + static_cast<int>(rank)) * kRows, xr = o.row + static_cast<int>(rank) * half;
             for (int s = 0; s < p.steps; ++s) {
-                ok = mbar_wait_cluster(empty(st), par ^ 1u, abort, p.timeout_ns);
+                ok = mbar_wait(empty(st), par ^ 1u, abort, p.timeout_ns);
                 if (!ok) break;
-                const uint32_t a = base + st * kStageBytes;
+                const uint32_t a = base + st * stage_bytes;
                 const uint32_t bar = mapa_shared(full(st), 0);
                 if (issue) {
                     if (rank == 0) mbar_arrive_expect_tx(full(st), 2 * (kABytes + xbytes));
@@ -612,7 +675,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
                     }
                     tma_load_2d_pair(a + kABytes, &p.tmX[box], s * 128, xr, bar);
                 }
-                if (++st == kStages) st = 0, par ^= 1u;
+                if (++st == stages) st = 0, par ^= 1u;
             }
         }
         if (!ok && issue) {   // copies in flight land before the pair leaves: far longer than any takes
@@ -656,7 +719,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
 #pragma unroll
                 for (int h = 0; h < 3; ++h)   // (a tile further is the next one's same line)
                     x[h] = h == 0 || o.width > 128 * (h - 1) ? line(p.sx, (o.row >> 7) + h, p.x_tiles, first) : none;
-                ok = __all_sync(~0u, mbar_wait_cluster(sempty(st), par ^ 1u, abort, p.timeout_ns));
+                ok = __all_sync(~0u, mbar_wait(sempty(st), par ^ 1u, abort, p.timeout_ns));
                 if (!ok) break;
                 par ^= 1u;
                 const uint32_t at = sets + st * kSetBytes + lane * 16;
@@ -680,58 +743,54 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
     } else if (warp == 9) {
         if (rank == 0) {
             const bool issue = elect_one();
-            int st = 0, acc = 0, set = 0;
-            uint32_t par = 0, spar = 0, rpar = 0;
+            int st = 0, acc = 0, set = 0, t = blockIdx.x >> 1, s = 0;
+            uint32_t par = 0, spar = 0, tpar = 0;
             bool ok = !p.test_stall || mbar_wait(never, 0, abort, p.timeout_ns);
-            bool begun = false;
             const uint32_t tsw = tmem + kSfCol, tsx = tsw + 4;
-            for (int t = blockIdx.x >> 1; t < tiles && ok; t += clusters) {
-                const Tile o = place(p, groups, t);
-                if (begun) {   // the tile before last is stored, the last one's shared columns are read
-                    ok = mbar_wait_cluster(room, rpar, abort, p.timeout_ns);
-                    if (!ok) break;
-                    rpar ^= 1u;
+            int width = 0;
+            // what step s of tile t waits for: the accumulator's last tile read, the scales, the operands
+            auto ready = [&]() {
+                if (s == 0) width = __shfl_sync(~0u, place(p, groups, t).width, 0);
+                return __all_sync(~0u, (s != 0 || mbar_wait(tempty + 8 * acc, tpar ^ 1u, abort, p.timeout_ns)) &&
+                                           ((s & 3) != 0 || mbar_wait_cluster(sfull(set), spar, abort, p.timeout_ns)) &&
+                                           mbar_wait(full(st), par, abort, p.timeout_ns)) != 0;
+            };
+            if (ok && t < tiles) ok = ready();
+            while (ok && t < tiles) {
+                tc_fence_after();
+                const uint32_t d = tmem + (acc ? kAcc1 : 0u), a = base + st * stage_bytes;
+                const uint64_t da = umma_desc_sw128(a, 16, 1024), db = umma_desc_sw128(a + kABytes, 16, 1024);
+                const uint32_t id = idesc_mxf8(256, width, s & 3), done = empty(st), read = sempty(set), over = tfull + 8 * acc;
+                const uint64_t df = scale_desc(sets + set * kSetBytes);   // (16-byte units: 32 a tile)
+                const int n32 = min(4, p.k32 - 4 * s);
+                const bool copies = (s & 3) == 0, last = s + 1 == p.steps, more = s > 0;
+                if (copies && ++set == kSets) set = 0, spar ^= 1u;
+                if (++st == stages) st = 0, par ^= 1u;
+                // the next step's barriers, asked here and looked at when this step's first
+                // instructions are out: an answer takes some 100 cycles
+                const uint32_t there = mbar_test(full(st), par) & ((s & 3) == 3 ? mbar_test(sfull(set), spar) : 1u);
+                auto mma = [&](int q) {
+                    umma_mxf8_pair_if(issue && q < n32, d, da + 2 * q, db + 2 * q, id, tsw, tsx, more || q > 0);
+                };
+                if (copies) {
+                    tmem_copy_scales_pair_if(issue, tsw, df);
+                    tmem_copy_scales_pair_if(issue, tsx, df + 32);
+                    if (width > 128) tmem_copy_scales_pair_if(issue, tsx + 4, df + 64);
+                    umma_commit_pair_mc_if(issue, read, 0x3);
                 }
-                begun = true;
-                const uint32_t d = tmem + (acc ? kAcc1 : 0u);
-                ok = mbar_wait_cluster(sfull(set), spar, abort, p.timeout_ns) &&
-                     mbar_wait_cluster(full(st), par, abort, p.timeout_ns);
-                for (int s = 0; s < p.steps && ok; ++s) {
-                    tc_fence_after();
-                    const uint32_t a = base + st * kStageBytes;
-                    const uint64_t da = umma_desc_sw128(a, 16, 1024), db = umma_desc_sw128(a + kABytes, 16, 1024);
-                    const uint32_t id = idesc_mxf8(256, o.width, s & 3), done = empty(st);
-                    const int n32 = min(4, p.k32 - 4 * s);
-                    const bool copies = (s & 3) == 0;
-                    const uint64_t df = scale_desc(sets + set * kSetBytes);   // (16-byte units: 32 a tile)
-                    const uint32_t read = sempty(set);
-                    auto mma = [&](int q) { umma_mxf8_pair(d, da + 2 * q, db + 2 * q, id, tsw, tsx, s > 0 || q > 0); };
-                    if (issue) {
-                        if (copies) {
-                            tmem_copy_scales_pair(tsw, df);
-                            tmem_copy_scales_pair(tsx, df + 32);
-                            if (o.width > 128) tmem_copy_scales_pair(tsx + 4, df + 64);
-                            umma_commit_pair_mc(read, 0x3);
-                        }
 #pragma unroll
-                        for (int q = 0; q < 3; ++q)
-                            if (q < n32) mma(q);
-                    }
-                    // the next step's waits while these run (the stage and the set that they wait
-                    // for were emptied by earlier steps than this one)
-                    if (copies && ++set == kSets) set = 0, spar ^= 1u;
-                    if (++st == kStages) st = 0, par ^= 1u;
-                    if (s + 1 < p.steps)
-                        ok = (((s + 1) & 3) != 0 || mbar_wait_cluster(sfull(set), spar, abort, p.timeout_ns)) &&
-                             mbar_wait_cluster(full(st), par, abort, p.timeout_ns);
-                    if (issue) {
-                        if (n32 == 4) mma(3);
-                        umma_commit_pair_mc(done, 0x3);
-                    }
+                for (int q = 0; q < 3; ++q) mma(q);
+                // (what the next step waits for hangs on earlier steps than this one, and on the
+                // tile before)
+                if (++s == p.steps) {
+                    s = 0, t += clusters;
+                    if (acc) tpar ^= 1u;
+                    acc ^= 1;
                 }
-                if (!ok) break;
-                if (issue) umma_commit_pair_mc(tfull + 8 * acc, 0x3);
-                acc ^= 1;
+                if (t < tiles && (last || !__all_sync(~0u, there))) ok = ready();
+                mma(3);
+                umma_commit_pair_mc_if(issue, done, 0x3);
+                if (last) umma_commit_pair_mc_if(issue, over, 0x3);
             }
             if (!ok) {
                 if (issue) {
@@ -746,7 +805,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
         // ones, 4-7 the odd ones; a warp's lanes are the weight rows 32 (warp % 4) on
         const int half = warp >> 2;
         const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        const uint32_t box = boxes + warp * kBoxBytes, leader_room = mapa_shared(room, 0);
+        const uint32_t box = boxes + warp * kBoxBytes, leader_empty = mapa_shared(tempty, 0);
         int acc = 0;
         uint32_t tpar = 0;
         for (int t = blockIdx.x >> 1; t < tiles; t += clusters) {
@@ -760,29 +819,24 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
                     if (n < p.n) bias[i] = widen(p.bias[n], p.bf16);
                 }
             }
-            const bool ok = __all_sync(~0u, mbar_wait_cluster(tfull + 8 * acc, tpar, abort, p.timeout_ns));
+            const bool ok = __all_sync(~0u, mbar_wait(tfull + 8 * acc, tpar, abort, p.timeout_ns));
             if (!ok) {
                 if (lane == 0) fail();
                 break;
             }
             tc_fence_after();
             const uint32_t d = trow + (acc ? kAcc1 : 0u);
-            const int chunks = o.width >> 5, last = chunks - 1 - ((chunks - 1 - half) & 1);   // of this warp's parity
-            // the columns that the other accumulator shares come first: 224 to 255 of the
-            // first one, 0 to 31 of the second
-            const bool shares = acc ? half == 0 : half == 1 && chunks == 8;
-            if (!shares && lane == 0) mbar_arrive_cluster_relaxed(leader_room);
+            const int chunks = o.width >> 5;
 #pragma unroll 1
-            for (int i = half; i < chunks; i += 2) {
-                const int b = acc ? i : last + half - i;
+            for (int b = half; b < chunks; b += 2) {
                 float v[32];
                 tmem_ld_16x256b_x4(d + b * 32, v);
                 tmem_ld_16x256b_x4(d + b * 32 + (16u << 16), v + 16);
                 tmem_wait_ld();
-                if (shares && i == half) {
+                if (b + 2 >= chunks) {   // the accumulator's columns are read
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster_relaxed(leader_room);
+                    if (lane == 0) mbar_arrive_cluster_relaxed(leader_empty + 8 * acc);
                 }
                 const int left = o.rows - b * 32;   // rows of C among the 32
                 if (left <= 0 || n0 >= p.n) continue;
@@ -828,7 +882,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
                 }
                 __syncwarp();
             }
-            tc_fence_before();
+            if (half >= chunks && lane == 0) mbar_arrive_cluster_relaxed(leader_empty + 8 * acc);
             if (acc) tpar ^= 1u;
             acc ^= 1;
         }

@@ -198,6 +198,15 @@ gemm_f16_status launch_pair(const Product& q, const Device& dev, const Sizes& sa
     const auto kernel = gated ? fp8_dev::gemm_fp8_pair<true> : fp8_dev::gemm_fp8_pair<false>;
     if (!allow_smem(reinterpret_cast<const void*>(kernel), gated ? 1 : 2, fp8_dev::kPairSmem)) return GEMM_F16_ERR_LAUNCH;
     const int64_t clusters = std::min<int64_t>(dev.sms / 2, tiles);
+    // Unless it is forced: with groups the kernel finds the width, by the same rule.
+    p.width = static_cast<int32_t>(std::min<int64_t>(option(GEMM_F16_OPT_MAX_STAGES) * 32, fp8_dev::kMaxWidth));
+    int64_t best = p.width || q.groups ? 0 : INT64_MAX;
+    for (int w = fp8_dev::kMaxWidth; w && best; w -= 32) {
+        const int rows = static_cast<int>(q.m), parts = fp8_dev::parts_of(rows, w);
+        const int64_t cost = fp8_dev::cost_of(static_cast<int>(parts * tiles_w), fp8_dev::width_of(rows, parts),
+                                              static_cast<int>(clusters));
+        if (cost < best) best = cost, p.width = w;
+    }
     return launch_kernel(kernel, dim3(static_cast<unsigned>(2 * clusters)), fp8_dev::kPairThreads, fp8_dev::kPairSmem, 2,
                          stream, p);
 }
