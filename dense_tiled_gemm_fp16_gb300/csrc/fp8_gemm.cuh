@@ -370,7 +370,7 @@ constexpr uint32_t kSfCol = 496, kAcc1 = 256;   // scales of the weights (4), of
 
 struct PairParams {
     CUtensorMap tmW, tmU;        // weight codes {pitch, n, groups}, boxes of 128 bytes x 128 rows (kGated: 16)
-    CUtensorMap tmX[4];          // A's codes {pitch, rows}, boxes of 128 bytes x 16, 32, 64 and 128 rows
+    CUtensorMap tmX[7];          // A's codes {pitch, rows}, boxes of 128 bytes x 16, 32, .. 112 rows (one group: of its width's)
     const uint8_t* sw;           // scale tiles of the weights, of the second ones, and of A
     const uint8_t* su;
     const uint8_t* sx;
@@ -391,7 +391,9 @@ struct PairParams {
 struct Groups {
     int row0[kMaxGroups + 1];    // rows past the last group's end belong to none
     int tile0[kMaxGroups + 1];   // tiles before the group: its parts x tiles_w
-    int width;                   // W
+    int parts[kMaxGroups];       // of its rows
+    uint8_t width[kMaxGroups];   // columns of each part, at most
+    int widest;                  // of all groups
 };
 
 __host__ __device__ inline int parts_of(int rows, int w) { return (rows + w - 1) / w; }
@@ -411,7 +413,8 @@ __device__ __forceinline__ void choose_tiles(const PairParams& p, Groups& g, int
         if (lane == 0) {
             const int rows = static_cast<int>(p.rows);
             g.row0[0] = g.tile0[0] = 0, g.row0[1] = rows;
-            g.tile0[1] = parts_of(rows, p.width) * p.tiles_w, g.width = p.width;
+            g.parts[0] = parts_of(rows, p.width), g.tile0[1] = g.parts[0] * p.tiles_w;
+            g.width[0] = static_cast<uint8_t>(g.widest = p.width);
         }
         return;
     }
@@ -445,10 +448,17 @@ __device__ __forceinline__ void choose_tiles(const PairParams& p, Groups& g, int
 #pragma unroll
     for (int d = 1; d < 8; d *= 2) cost = min(cost, __shfl_xor_sync(~0u, cost, d));
     const int width = p.width ? p.width : 32 * (8 - static_cast<int>(cost & 15));
-    if (lane == 0) g.width = width;
     int at = 0;
+    widest = 0;
     for (int i = lane; i - lane < p.groups; i += 32) {
-        const int n = i < p.groups ? parts_of(g.row0[i + 1] - g.row0[i], width) * p.tiles_w : 0;
+        int n = 0;
+        if (i < p.groups) {
+            const int rows = g.row0[i + 1] - g.row0[i], parts = parts_of(rows, width), w = width_of(rows, parts);
+            g.parts[i] = parts;
+            g.width[i] = static_cast<uint8_t>(w);
+            widest = max(widest, w);
+            n = parts * p.tiles_w;
+        }
         int sum = n;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
@@ -458,7 +468,8 @@ __device__ __forceinline__ void choose_tiles(const PairParams& p, Groups& g, int
         if (i < p.groups) g.tile0[i] = at + sum - n;
         at += __shfl_sync(~0u, sum, 31);
     }
-    if (lane == 0) g.tile0[p.groups] = at;
+    widest = __reduce_max_sync(~0u, widest);
+    if (lane == 0) g.tile0[p.groups] = at, g.widest = max(widest, 32);
 }
 
 // Loads that are issued where they stand (the plain ones may be moved down to the use of
@@ -519,30 +530,33 @@ __device__ __forceinline__ uint32_t mbar_test(uint32_t bar, uint32_t parity)
     return ok;
 }
 
-// Rows of A's copy for a CTA's half of a tile's columns: 16, 32, 64 or 128.
-__device__ __forceinline__ int box_rows(int width) { return width <= 32 ? 16 : width <= 64 ? 32 : width <= 128 ? 64 : 128; }
-
 struct Tile {
     int group, row, width, rows, w;   // A's first row, the columns, those that are the group's; weight tile
 };
 
-// Inside a group: bands of `panel` weight tiles, in a band one part of the rows
-// after the other, so that the clusters at work share both operands in L2.
-__device__ __forceinline__ Tile place(const PairParams& p, const Groups& g, int t)
+// The last group that begins at tile t or before (an empty one has no tile).
+__device__ __forceinline__ int group_of(const PairParams& p, const Groups& g, int t)
 {
-    int lo = 0, hi = p.groups;   // the last group that begins at t or before (an empty one has no tile)
+    int lo = 0, hi = p.groups;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (g.tile0[mid] <= t) lo = mid;
         else hi = mid;
     }
-    const int r0 = g.row0[lo], rows = g.row0[lo + 1] - r0, parts = parts_of(rows, g.width);
-    const int i = t - g.tile0[lo], band = i / (p.panel * parts), j = i - band * p.panel * parts;
-    const int in_band = min(p.panel, p.tiles_w - band * p.panel), part = j / in_band;
+    return lo;
+}
+
+// Inside a group: bands of `panel` weight tiles, in a band one part of the rows
+// after the other, so that the clusters at work share both operands in L2.
+__device__ __forceinline__ Tile place(const PairParams& p, const Groups& g, int t)
+{
     Tile o;
-    o.group = lo;
+    o.group = group_of(p, g, t);
+    const int r0 = g.row0[o.group], rows = g.row0[o.group + 1] - r0, all = p.panel * g.parts[o.group];
+    const int i = t - g.tile0[o.group], band = i / all, j = i - band * all;
+    const int in_band = min(p.panel, p.tiles_w - band * p.panel), part = j / in_band;
     o.w = band * p.panel + (j - part * in_band);
-    o.width = width_of(rows, parts);
+    o.width = g.width[o.group];
     o.row = r0 + part * o.width;
     o.rows = min(o.width, rows - part * o.width);
     return o;
@@ -638,7 +652,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
     const uint32_t tmem = tmem_slot;
     const int tiles = __shfl_sync(~0u, groups.tile0[p.groups], 0);
     // as many stages as fit: a tile of few columns brings little for its 16 KB of weights
-    const uint32_t stage_bytes = kABytes + box_rows(__shfl_sync(~0u, groups.width, 0)) * 128u;
+    const uint32_t stage_bytes = kABytes + __shfl_sync(~0u, groups.widest, 0) * 64u;
     const int stages = static_cast<int>(min(kSlotBytes / stage_bytes, static_cast<uint32_t>(kMaxStages)));
 
     const volatile int* abort = &abort_flag;
@@ -654,8 +668,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
         bool ok = true;
         for (int t = blockIdx.x >> 1; t < tiles && ok; t += clusters) {
             const Tile o = place(p, groups, t);
-            const int half = o.width >> 1, rows = box_rows(o.width), box = 27 - __clz(rows);   // 16 << box rows
-            const uint32_t xbytes = 128u * rows;
+            const int half = o.width >> 1, box = (o.width >> 5) - 1;
+            const uint32_t xbytes = 128u * half;
             const int32_t wn = (o.w * 2 + static_cast<int>(rank)) * kRows, xr = o.row + static_cast<int>(rank) * half;
             for (int s = 0; s < p.steps; ++s) {
                 ok = mbar_wait(empty(st), par ^ 1u, abort, p.timeout_ns);
@@ -747,10 +761,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
             uint32_t par = 0, spar = 0, tpar = 0;
             bool ok = !p.test_stall || mbar_wait(never, 0, abort, p.timeout_ns);
             const uint32_t tsw = tmem + kSfCol, tsx = tsw + 4;
-            int width = 0;
+            auto width_at = [&](int u) {
+                return u < tiles ? __shfl_sync(~0u, static_cast<int>(groups.width[group_of(p, groups, u)]), 0) : 0;
+            };
+            int width = width_at(t), next_width = 0;
             // what step s of tile t waits for: the accumulator's last tile read, the scales, the operands
             auto ready = [&]() {
-                if (s == 0) width = __shfl_sync(~0u, place(p, groups, t).width, 0);
                 return __all_sync(~0u, (s != 0 || mbar_wait(tempty + 8 * acc, tpar ^ 1u, abort, p.timeout_ns)) &&
                                            ((s & 3) != 0 || mbar_wait_cluster(sfull(set), spar, abort, p.timeout_ns)) &&
                                            mbar_wait(full(st), par, abort, p.timeout_ns)) != 0;
@@ -768,7 +784,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
                 if (++st == stages) st = 0, par ^= 1u;
                 // the next step's barriers, asked here and looked at when this step's first
                 // instructions are out: an answer takes some 100 cycles
-                const uint32_t there = mbar_test(full(st), par) & ((s & 3) == 3 ? mbar_test(sfull(set), spar) : 1u);
+                uint32_t there = mbar_test(full(st), par);
+                if (last || (s & 3) == 3) there &= mbar_test(sfull(set), spar);
+                if (last) there &= mbar_test(tempty + 8 * (acc ^ 1), tpar ^ 1u ^ acc);
                 auto mma = [&](int q) {
                     umma_mxf8_pair_if(issue && q < n32, d, da + 2 * q, db + 2 * q, id, tsw, tsx, more || q > 0);
                 };
@@ -782,12 +800,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
                 for (int q = 0; q < 3; ++q) mma(q);
                 // (what the next step waits for hangs on earlier steps than this one, and on the
                 // tile before)
+                if (s == 0) next_width = width_at(t + clusters);
                 if (++s == p.steps) {
-                    s = 0, t += clusters;
+                    s = 0, t += clusters, width = next_width;
                     if (acc) tpar ^= 1u;
                     acc ^= 1;
                 }
-                if (t < tiles && (last || !__all_sync(~0u, there))) ok = ready();
+                if (t < tiles && !__all_sync(~0u, there)) ok = ready();
                 mma(3);
                 umma_commit_pair_mc_if(issue, done, 0x3);
                 if (last) umma_commit_pair_mc_if(issue, over, 0x3);

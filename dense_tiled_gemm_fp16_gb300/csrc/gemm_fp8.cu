@@ -193,20 +193,25 @@ gemm_f16_status launch_pair(const Product& q, const Device& dev, const Sizes& sa
     if (!encode_codes(&p.tmW, q.b_codes, q.n, p.groups, sb.pitch, box) ||
         (gated && !encode_codes(&p.tmU, q.u_codes, q.n, p.groups, sb.pitch, box)))
         return GEMM_F16_ERR_LAUNCH;
-    for (int i = 0; i < 4; ++i)
-        if (!encode_codes(&p.tmX[i], q.a_codes, q.m, 0, sa.pitch, 16u << i)) return GEMM_F16_ERR_LAUNCH;
     const auto kernel = gated ? fp8_dev::gemm_fp8_pair<true> : fp8_dev::gemm_fp8_pair<false>;
     if (!allow_smem(reinterpret_cast<const void*>(kernel), gated ? 1 : 2, fp8_dev::kPairSmem)) return GEMM_F16_ERR_LAUNCH;
     const int64_t clusters = std::min<int64_t>(dev.sms / 2, tiles);
     // Unless it is forced: with groups the kernel finds the width, by the same rule.
-    p.width = static_cast<int32_t>(std::min<int64_t>(option(GEMM_F16_OPT_MAX_STAGES) * 32, fp8_dev::kMaxWidth));
-    int64_t best = p.width || q.groups ? 0 : INT64_MAX;
-    for (int w = fp8_dev::kMaxWidth; w && best; w -= 32) {
-        const int rows = static_cast<int>(q.m), parts = fp8_dev::parts_of(rows, w);
-        const int64_t cost = fp8_dev::cost_of(static_cast<int>(parts * tiles_w), fp8_dev::width_of(rows, parts),
-                                              static_cast<int>(clusters));
-        if (cost < best) best = cost, p.width = w;
+    p.width = static_cast<int32_t>(std::min<int64_t>(option(GEMM_F16_OPT_TILE_N), fp8_dev::kMaxWidth));
+    if (!q.groups) {
+        const int rows = static_cast<int>(q.m);
+        int64_t best = p.width ? 0 : INT64_MAX;
+        for (int w = fp8_dev::kMaxWidth; w && best; w -= 32) {
+            const int parts = fp8_dev::parts_of(rows, w);
+            const int64_t cost = fp8_dev::cost_of(static_cast<int>(parts * tiles_w), fp8_dev::width_of(rows, parts),
+                                                  static_cast<int>(clusters));
+            if (cost < best) best = cost, p.width = w;
+        }
+        p.width = fp8_dev::width_of(rows, fp8_dev::parts_of(rows, p.width));
     }
+    for (int i = 0; i < 7; ++i)
+        if ((q.groups || p.width == 32 * (i + 1)) && !encode_codes(&p.tmX[i], q.a_codes, q.m, 0, sa.pitch, 16u * (i + 1)))
+            return GEMM_F16_ERR_LAUNCH;
     return launch_kernel(kernel, dim3(static_cast<unsigned>(2 * clusters)), fp8_dev::kPairThreads, fp8_dev::kPairSmem, 2,
                          stream, p);
 }
