@@ -756,60 +756,68 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
         if (!ok && lane == 0) fail();
     } else if (warp == 9) {
         if (rank == 0) {
-            const bool issue = elect_one();
-            int st = 0, acc = 0, set = 0, t = blockIdx.x >> 1, s = 0;
+            const uint32_t issue = elect_one();
+            int st = 0, acc = 0, set = 0, t = blockIdx.x >> 1;
             uint32_t par = 0, spar = 0, tpar = 0;
             bool ok = !p.test_stall || mbar_wait(never, 0, abort, p.timeout_ns);
-            const uint32_t tsw = tmem + kSfCol, tsx = tsw + 4;
+            const uint32_t tsw = tmem + kSfCol, tsx = tsw + 4, step16 = stage_bytes >> 4;
+            const uint64_t desc0 = umma_desc_sw128(base, 16, 1024), sets0 = scale_desc(sets);   // (in 16-byte units)
             auto width_at = [&](int u) {
                 return u < tiles ? __shfl_sync(~0u, static_cast<int>(groups.width[group_of(p, groups, u)]), 0) : 0;
             };
-            int width = width_at(t), next_width = 0;
-            // what step s of tile t waits for: the accumulator's last tile read, the scales, the operands
-            auto ready = [&]() {
-                return __all_sync(~0u, (s != 0 || mbar_wait(tempty + 8 * acc, tpar ^ 1u, abort, p.timeout_ns)) &&
-                                           ((s & 3) != 0 || mbar_wait_cluster(sfull(set), spar, abort, p.timeout_ns)) &&
+            int width = width_at(t);
+            // waits for the operands at hand, for their scales and for an accumulator that has been read
+            auto ready = [&](bool scales, bool room) {
+                return __all_sync(~0u, (!room || mbar_wait(tempty + 8 * acc, tpar ^ 1u, abort, p.timeout_ns)) &&
+                                           (!scales || mbar_wait_cluster(sfull(set), spar, abort, p.timeout_ns)) &&
                                            mbar_wait(full(st), par, abort, p.timeout_ns)) != 0;
             };
-            if (ok && t < tiles) ok = ready();
+            if (ok && t < tiles) ok = ready(true, true);
             while (ok && t < tiles) {
-                tc_fence_after();
-                const uint32_t d = tmem + (acc ? kAcc1 : 0u), a = base + st * stage_bytes;
-                const uint64_t da = umma_desc_sw128(a, 16, 1024), db = umma_desc_sw128(a + kABytes, 16, 1024);
-                const uint32_t id = idesc_mxf8(256, width, s & 3), done = empty(st), read = sempty(set), over = tfull + 8 * acc;
-                const uint64_t df = scale_desc(sets + set * kSetBytes);   // (16-byte units: 32 a tile)
-                const int n32 = min(4, p.k32 - 4 * s);
-                const bool copies = (s & 3) == 0, last = s + 1 == p.steps, more = s > 0;
-                if (copies && ++set == kSets) set = 0, spar ^= 1u;
-                if (++st == stages) st = 0, par ^= 1u;
-                // the next step's barriers, asked here and looked at when this step's first
-                // instructions are out: an answer takes some 100 cycles
-                uint32_t there = mbar_test(full(st), par);
-                if (last || (s & 3) == 3) there &= mbar_test(sfull(set), spar);
-                if (last) there &= mbar_test(tempty + 8 * (acc ^ 1), tpar ^ 1u ^ acc);
-                auto mma = [&](int q) {
-                    umma_mxf8_pair_if(issue && q < n32, d, da + 2 * q, db + 2 * q, id, tsw, tsx, more || q > 0);
+                const uint32_t d = tmem + (acc ? kAcc1 : 0u), id0 = idesc_mxf8(256, width, 0), over = tfull + 8 * acc;
+                const int next_width = width_at(t + clusters);
+                // one slot, the `byte`-th of its set; n32 instructions
+                auto step = [&](int s, int byte, int n32) {
+                    tc_fence_after();
+                    const uint64_t da = desc0 + st * step16, db = da + (kABytes >> 4);
+                    const uint32_t id = id0 | idesc_mxf8(0, 0, byte), done = empty(st);
+                    const bool last = s + 1 == p.steps, fresh = last || byte == 3;
+                    if (byte == 0) {
+                        const uint64_t df = sets0 + set * (kSetBytes >> 4);
+                        tmem_copy_scales_pair_if(issue, tsw, df);
+                        tmem_copy_scales_pair_if(issue, tsx, df + 32);
+                        if (width > 128) tmem_copy_scales_pair_if(issue, tsx + 4, df + 64);
+                        umma_commit_pair_mc_if(issue, sempty(set), 0x3);
+                        if (++set == kSets) set = 0, spar ^= 1u;
+                    }
+                    if (++st == stages) st = 0, par ^= 1u;
+                    // the next slot's barriers, asked here and looked at when this one's first
+                    // instructions are out: an answer takes some 100 cycles
+                    uint32_t there = mbar_test(full(st), par);
+                    if (fresh) there &= mbar_test(sfull(set), spar);
+                    if (last) there &= mbar_test(tempty + 8 * (acc ^ 1), tpar ^ 1u ^ acc);
+                    auto mma = [&](int q) {
+                        umma_mxf8_pair_if(n32 > q ? issue : 0u, d, da + 2 * q, db + 2 * q, id, tsw, tsx, s > 0 || q > 0);
+                    };
+                    mma(0), mma(1), mma(2);
+                    // (what the next slot waits for hangs on earlier ones than this, and on the tile before)
+                    if (last) {
+                        t += clusters, width = next_width;
+                        if (acc) tpar ^= 1u;
+                        acc ^= 1;
+                    }
+                    if (!__all_sync(~0u, there) && t < tiles) ok = ready(fresh, last);
+                    mma(3);
+                    umma_commit_pair_mc_if(issue, done, 0x3);
+                    if (last) umma_commit_pair_mc_if(issue, over, 0x3);
                 };
-                if (copies) {
-                    tmem_copy_scales_pair_if(issue, tsw, df);
-                    tmem_copy_scales_pair_if(issue, tsx, df + 32);
-                    if (width > 128) tmem_copy_scales_pair_if(issue, tsx + 4, df + 64);
-                    umma_commit_pair_mc_if(issue, read, 0x3);
-                }
+                int s = 0;
+                for (; s + 4 <= p.steps - 1 && ok; s += 4) {   // whole sets
 #pragma unroll
-                for (int q = 0; q < 3; ++q) mma(q);
-                // (what the next step waits for hangs on earlier steps than this one, and on the
-                // tile before)
-                if (s == 0) next_width = width_at(t + clusters);
-                if (++s == p.steps) {
-                    s = 0, t += clusters, width = next_width;
-                    if (acc) tpar ^= 1u;
-                    acc ^= 1;
+                    for (int b = 0; b < 4; ++b)
+                        if (ok) step(s + b, b, 4);
                 }
-                if (t < tiles && !__all_sync(~0u, there)) ok = ready();
-                mma(3);
-                umma_commit_pair_mc_if(issue, done, 0x3);
-                if (last) umma_commit_pair_mc_if(issue, over, 0x3);
+                for (; s < p.steps && ok; ++s) step(s, s & 3, min(4, p.k32 - 4 * s));
             }
             if (!ok) {
                 if (issue) {
