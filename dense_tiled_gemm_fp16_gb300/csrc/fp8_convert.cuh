@@ -12,6 +12,11 @@ namespace fp8_dev {
 constexpr int kTileRows = 128, kTileVals = 512, kConvThreads = 256;
 constexpr int kDequantRows = 32;   // rows a block writes
 
+template <bool kValue>
+struct Bool {
+    static constexpr bool value = kValue;
+};
+
 struct QuantParams {
     const void* x;
     int64_t sb, sr, sk;   // element strides
@@ -22,14 +27,15 @@ struct QuantParams {
     int64_t tile_rows;        // rows of a tile that a block takes: 128, or fewer of few rows
 };
 
-// Unit stride along k: 16 lanes take a block of 128 values, 8 a lane; a warp's 256
-// values are contiguous, half of a tile's width.  Rows of a tile that another block
-// of threads takes (tile_rows < 128) are left to it; the one with the matrix's last
-// row also writes the padding rows' scales.
+// Unit stride along k: a warp takes the 512 values of a row of the tile, 8 a lane twice,
+// so that its loads and stores are contiguous, 16 lanes share a block and the row's four
+// scales make one word.  Rows of a scale tile that another block of threads takes
+// (tile_rows < 128) are left to it; the one with the matrix's last row also writes the
+// padding rows' scales.
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kConvThreads) quantize_rows(const QuantParams p)
 {
-    constexpr int kUnroll = sizeof(T) == 4 ? 2 : 4, kStep = kConvThreads / 64;
+    constexpr int kUnroll = sizeof(T) == 4 ? 1 : 2, kWarps = kConvThreads / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t parts = (p.rows + p.tile_rows - 1) / p.tile_rows;
     const int64_t ct = blockIdx.x / parts, part = blockIdx.x - ct * parts;
@@ -37,37 +43,52 @@ __global__ void __launch_bounds__(kConvThreads) quantize_rows(const QuantParams 
     const T* x = static_cast<const T*>(p.x) + b * p.sb;
     uint8_t* codes = p.codes + b * p.rows * p.pitch;
     uint8_t* scales = p.scales + b * p.row_tiles * p.kt * kScaleTile;
-    const int n = static_cast<int>(p.k), i = static_cast<int>(ct) * kTileVals + (warp & 1) * 256 + lane * 8;
-    const int block = i >> 7;   // this lane's block of its rows
-    const bool some = block < (n + kBlock - 1) / kBlock;
+    const int n = static_cast<int>(p.k), i = static_cast<int>(ct) * kTileVals + lane * 8;   // (k is below 2^31)
     griddep_wait();
     griddep_launch_dependents();
     const int64_t end = min(p.rows, r0 + p.tile_rows);
+    auto rows = [&](auto whole) {   // whole: no value of the tile is past the row's end
+        constexpr bool kWhole = decltype(whole)::value;
 #pragma unroll 1
-    for (int64_t r = r0 + (warp >> 1); r < end; r += kStep * kUnroll) {
-        uint32_t w[kUnroll][8 * sizeof(T) / 4];
+        for (int64_t r = r0 + warp; r < end; r += kWarps * kUnroll) {
+            uint32_t w[kUnroll][2][8 * sizeof(T) / 4];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int k = r + u * kStep < end ? n : 0;
-            mxf4_dev::load8<T, kVec>(x + (r + u * kStep) * p.sr, i, k, w[u]);
-            if (i + 8 > k) mxf4_dev::mask_tail<T>(w[u], k - i);
+            for (int u = 0; u < kUnroll; ++u) {
+                const T* row = x + (r + u * kWarps) * p.sr;
+                const int k = r + u * kWarps < end ? n : 0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    mxf4_dev::load8<T, kVec>(row, i + 256 * h, k, w[u][h]);
+                    if (!kWhole && i + 256 * h + 8 > k) mxf4_dev::mask_tail<T>(w[u][h], k - i - 256 * h);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int64_t row = r + u * kWarps;
+                if (row >= end) break;
+                uint32_t word = 0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t top = mxf4_dev::top_bits<T>(w[u][h]);
+#pragma unroll
+                    for (int d = 1; d < 16; d *= 2) top = max(top, __shfl_xor_sync(~0u, top, d));
+                    const bool some = kWhole || ((i + 256 * h) & ~(kBlock - 1)) < n;
+                    const uint32_t code = some ? scale_code<T>(top) : 0u;
+                    const uint2 c = codes8<T>(w[u][h], code);
+                    if (kWhole || i + 256 * h + 8 <= p.pitch) *reinterpret_cast<uint2*>(codes + row * p.pitch + i + 256 * h) = c;
+                    word |= (code | __shfl_xor_sync(~0u, code, 16) << 8) << (16 * h);
+                }
+                if (lane == 0) *reinterpret_cast<uint32_t*>(scales + scale_at(row, 4 * ct, p.kt)) = word;
+            }
         }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int64_t row = r + u * kStep;
-            uint32_t top = mxf4_dev::top_bits<T>(w[u]);
-#pragma unroll
-            for (int d = 1; d < 16; d *= 2) top = max(top, __shfl_xor_sync(~0u, top, d));
-            if (row >= end) continue;
-            const uint32_t code = some ? scale_code<T>(top) : 0u;
-            const uint2 c = codes8<T>(w[u], code);
-            if (i + 8 <= p.pitch) *reinterpret_cast<uint2*>(codes + row * p.pitch + i) = c;
-            if ((lane & 15) == 0) scales[scale_at(row, block, p.kt)] = static_cast<uint8_t>(code);
-        }
-    }
+    };
+    if ((ct + 1) * kTileVals <= p.k)
+        rows(Bool<true>());
+    else
+        rows(Bool<false>());
     if (end == p.rows)   // padding rows of the last scale tile
-        for (int64_t r = p.rows + (warp >> 1); r < p.row_tiles * 128; r += kStep)
-            if ((lane & 15) == 0) scales[scale_at(r, block, p.kt)] = 0;
+        for (int64_t r = p.rows + threadIdx.x; r < p.row_tiles * 128; r += kConvThreads)
+            *reinterpret_cast<uint32_t*>(scales + scale_at(r, 4 * ct, p.kt)) = 0u;
 }
 
 // Any strides (a transposed view has unit stride along the rows): a lane takes a

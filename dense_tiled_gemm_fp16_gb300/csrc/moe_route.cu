@@ -17,9 +17,9 @@ namespace {
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 // Parts of the choices that moe_sort counts by themselves: one block each, at most 152,
-// so that every block can add up all counts.  One block alone takes 4096 choices in less
-// than the second kernel costs.
-constexpr int64_t kFewChoices = 4096, kMaxParts = 152;
+// so that every block can add up all counts.  One block alone takes 1024 choices at
+// once; 4096 took it 18 us, two kernels 10.
+constexpr int64_t kFewChoices = 1024, kMaxParts = 152;
 
 bool sort_parts(int64_t tokens, int64_t top, int64_t experts, int64_t* part, int64_t* parts)
 {
@@ -76,6 +76,10 @@ bool sizes_ok(int dtype, const int32_t* rows, int64_t tokens, int64_t top, int64
 }
 
 bool takes_vectors(const void* p, int64_t stride) { return !p || (aligned(p, 16) && stride % 8 == 0); }
+
+// Blocks along a row; one that starts up to 7 values past a 16-byte boundary reaches
+// that much further.
+int32_t chunks_of(int64_t d, bool vec) { return static_cast<int32_t>(cdiv(d + (vec ? 0 : 7), route_dev::kChunk)); }
 
 gemm_f16_status launch_rows(void (*kernel)(const route_dev::RowParams), const route_dev::RowParams& p, int64_t blocks,
                             cudaStream_t stream)
@@ -139,8 +143,8 @@ gemm_f16_status moe_gather(const void* x, int dtype, int64_t stride_x, const int
     route_dev::RowParams p = {};
     p.x = static_cast<const uint16_t*>(x), p.out = static_cast<uint16_t*>(out), p.rows = rows;
     p.sx = stride_x, p.so = stride_out, p.tokens = tokens, p.d = d, p.places = n;
-    p.top = static_cast<int32_t>(top_k), p.chunks = static_cast<int32_t>(cdiv(d, route_dev::kChunk));
     const bool vec = d % 8 == 0 && takes_vectors(x, stride_x) && takes_vectors(out, stride_out);
+    p.top = static_cast<int32_t>(top_k), p.chunks = chunks_of(d, vec);
     return launch_rows(vec ? route_dev::gather_rows<true> : route_dev::gather_rows<false>, p, tokens * p.chunks, stream);
 }
 
@@ -188,8 +192,8 @@ gemm_f16_status moe_combine(const void* y, int dtype, int64_t stride_y, const in
     route_dev::RowParams p = {};
     p.x = static_cast<const uint16_t*>(y), p.out = static_cast<uint16_t*>(out), p.rows = rows, p.weights = weights;
     p.sx = stride_y, p.so = stride_out, p.tokens = tokens, p.d = d, p.places = n;
-    p.top = static_cast<int32_t>(top_k), p.chunks = static_cast<int32_t>(cdiv(d, route_dev::kChunk));
     const bool vec = d % 8 == 0 && takes_vectors(y, stride_y) && takes_vectors(out, stride_out), half = dtype == FP8_F16;
+    p.top = static_cast<int32_t>(top_k), p.chunks = chunks_of(d, vec);
     return launch_rows(half ? (vec ? route_dev::combine_rows<__half, true> : route_dev::combine_rows<__half, false>)
                             : (vec ? route_dev::combine_rows<__nv_bfloat16, true> : route_dev::combine_rows<__nv_bfloat16, false>),
                        p, tokens * p.chunks, stream);

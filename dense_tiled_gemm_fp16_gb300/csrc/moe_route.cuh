@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_count(const SortParams p)
 // The places.  Every block adds up the counts of all parts and of those before its own
 // (at most 152 of them), then goes through its choices 1024 at a time: a warp finds the
 // lanes of the same expert, and the warps' counts are added up in order.  One part
-// (few choices) is counted here.
+// (1024 choices at most) is counted here.
 __global__ void __launch_bounds__(kSortThreads) sort_place(const SortParams p)
 {
     constexpr int kWarps = kSortThreads / 32;
@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place(const SortParams p)
     __shared__ uint16_t count[kWarps][kMaxExperts + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, buckets = p.experts + 1;
     for (int e = threadIdx.x; e < buckets; e += kSortThreads) total[e] = next[e] = 0;
-    for (int i = threadIdx.x; i < kWarps * (kMaxExperts + 1); i += kSortThreads) (&count[0][0])[i] = 0;
+    for (int e = lane; e < buckets; e += 32) count[warp][e] = 0;
     griddep_wait();
     griddep_launch_dependents();
     __syncthreads();
@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place(const SortParams p)
         const int e = threadIdx.x & (width - 1), lots = kSortThreads / width;
         if (e < buckets) {
             int all = 0, before = 0;
-#pragma unroll 8
+#pragma unroll 16
             for (int c = threadIdx.x / width; c < p.parts; c += lots) {
                 const int n = p.counts[static_cast<int64_t>(c) * buckets + e];
                 all += n;
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place(const SortParams p)
         __syncthreads();
         for (int b = threadIdx.x; b < buckets; b += kSortThreads) {
             int at = 0;   // of this expert, in the warps before
-#pragma unroll 8
+#pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const int n = count[w][b];
                 count[w][b] = static_cast<uint16_t>(at);
@@ -125,8 +125,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_place(const SortParams p)
             p.order[place] = e < p.experts ? static_cast<int>(i) : -1;
         }
         __syncthreads();
+        if (base + kSortThreads >= hi) break;   // (of the whole block)
         for (int b = threadIdx.x; b < buckets; b += kSortThreads) next[b] += total[b];
-        for (int k = threadIdx.x; k < kWarps * buckets; k += kSortThreads) count[k / buckets][k % buckets] = 0;
+        for (int b = lane; b < buckets; b += 32) count[warp][b] = 0;
         __syncthreads();
     }
 }
@@ -144,7 +145,9 @@ struct RowParams {
     int32_t top, chunks;     // chunks: blocks along a row
 };
 
-constexpr int kRowThreads = 256, kChunk = kRowThreads * 8;   // values of a row a block takes at a time
+// Blocks of 128 threads, so that an SM always has some with their loads under way (256:
+// combining 16384 tokens of 8 choices of 7168 values took 388 us, this 321).
+constexpr int kRowThreads = 128, kChunk = kRowThreads * 8;   // values of a row a block takes at a time
 
 // (a place outside the rows, which no order of this library holds, is taken as none)
 __device__ __forceinline__ int64_t place_of(const RowParams& p, int64_t t, int j)
@@ -154,7 +157,8 @@ __device__ __forceinline__ int64_t place_of(const RowParams& p, int64_t t, int j
 }
 
 // A token's row is read once and written to each of its places: the other way round, by
-// place, the rows would be read top times from a matrix that L2 does not hold.
+// place, the rows would be read top times from a matrix that L2 does not hold.  Where
+// rows start anywhere a thread takes the values of 16 aligned bytes of each place's row.
 template <bool kVec>
 __global__ void __launch_bounds__(kRowThreads) gather_rows(const RowParams p)
 {
@@ -162,19 +166,25 @@ __global__ void __launch_bounds__(kRowThreads) gather_rows(const RowParams p)
     griddep_wait();
     griddep_launch_dependents();
     uint32_t w[4];
-    row_dev::load8<kVec>(p.x + t * p.sx, i, p.d, w);
+    if (kVec) row_dev::load8<true>(p.x + t * p.sx, i, p.d, w);
 #pragma unroll 8
     for (int j = 0; j < p.top; ++j) {
         const int64_t r = place_of(p, t, j);
-        if (r >= 0) row_dev::store8<kVec>(p.out + r * p.so, i, p.d, w);
+        if (r < 0) continue;
+        uint16_t* out = p.out + r * p.so;
+        const int o = kVec ? 0 : row_dev::lead_of(out);
+        if (!kVec) row_dev::load8<false>(p.x + t * p.sx, i - o, p.d, w);
+        row_dev::store8<kVec>(out, i - o, p.d, w);
     }
 }
 
 // The sum is in the order of the choices, in fp32, rounded once.
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kRowThreads) combine_rows(const RowParams p)
+__global__ void __launch_bounds__(kRowThreads, 8) combine_rows(const RowParams p)
 {
-    const int64_t t = blockIdx.x / p.chunks, i = (blockIdx.x - t * p.chunks) * kChunk + threadIdx.x * 8;
+    const int64_t t = blockIdx.x / p.chunks;
+    uint16_t* out = p.out + t * p.so;
+    const int64_t i = (blockIdx.x - t * p.chunks) * kChunk + threadIdx.x * 8 - (kVec ? 0 : row_dev::lead_of(out));
     griddep_wait();
     griddep_launch_dependents();
     float s[8] = {};
@@ -186,8 +196,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_rows(const RowParams p)
         for (int j = 0; j < kAtOnce; ++j) {
             const int64_t r = j0 + j < p.top ? place_of(p, t, j0 + j) : -1;
             f[j] = r < 0 ? 0.f : p.weights ? p.weights[t * p.top + j0 + j] : 1.f;
-            row_dev::load8<kVec>(p.x + r * p.sx, i, r < 0 ? 0 : p.d, v[j]);
-            if (r < 0) f[j] = 0.f;
+            row_dev::load8<kVec>(p.x + r * p.sx, i, r < 0 ? -8 : p.d, v[j]);
         }
 #pragma unroll
         for (int j = 0; j < kAtOnce; ++j) {
@@ -202,19 +211,20 @@ __global__ void __launch_bounds__(kRowThreads) combine_rows(const RowParams p)
     uint32_t o[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) o[c] = row_dev::narrow2<T>(s[2 * c], s[2 * c + 1]);
-    row_dev::store8<kVec>(p.out + t * p.so, i, p.d, o);
+    row_dev::store8<kVec>(out, i, p.d, o);
 }
 
 // out[place(t, j)] = w[t, j] dy[t], dweights[t, j] = dy[t] . y[place(t, j)]; a choice
 // without a place has a weight's gradient of zero.  A block a token, so that the dot
 // products are added up in one order.
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kRowThreads) combine_grad_rows(const RowParams p)
+__global__ void __launch_bounds__(kRowThreads, 5) combine_grad_rows(const RowParams p)
 {
-    constexpr int kAtOnce = 8;
+    constexpr int kAtOnce = kVec ? 8 : 4;
     __shared__ float part[kRowThreads / 32][kAtOnce];
     const int64_t t = blockIdx.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint16_t* dout = p.x + t * p.sx;
     griddep_wait();
     griddep_launch_dependents();
     for (int j0 = 0; j0 < p.top; j0 += kAtOnce) {
@@ -225,15 +235,18 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_rows(const RowParams
             at[j] = j0 + j < p.top ? place_of(p, t, j0 + j) : -1;
             f[j] = at[j] < 0 ? 0.f : p.weights[t * p.top + j0 + j];
         }
-        for (int64_t i0 = 0; i0 < p.d; i0 += kChunk) {   // (all lanes of a warp together)
-            const int64_t i = i0 + threadIdx.x * 8;
+        for (int64_t i = threadIdx.x * 8; i < p.d + (kVec ? 0 : 7); i += kChunk) {
             uint32_t g[4], v[kAtOnce][4];
-            row_dev::load8<kVec>(p.x + t * p.sx, i, p.d, g);
+            if (kVec) row_dev::load8<true>(dout, i, p.d, g);
+            // rows that start anywhere: the values of 16 aligned bytes of dy's row
+            auto lead = [&](int j) { return kVec || at[j] < 0 ? 0 : row_dev::lead_of(p.out + at[j] * p.so); };
 #pragma unroll
-            for (int j = 0; j < kAtOnce; ++j) row_dev::load8<kVec>(p.y + at[j] * p.sy, i, at[j] < 0 ? 0 : p.d, v[j]);
+            for (int j = 0; j < kAtOnce; ++j)
+                row_dev::load8<kVec>(p.y + at[j] * p.sy, i - lead(j), at[j] < 0 ? -8 : p.d, v[j]);
 #pragma unroll
             for (int j = 0; j < kAtOnce; ++j) {
                 if (at[j] < 0) continue;
+                if (!kVec) row_dev::load8<false>(dout, i - lead(j), p.d, g);
                 uint32_t o[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -242,7 +255,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_rows(const RowParams
                     dot[j] = fmaf(a.y, b.y, dot[j]);
                     o[c] = row_dev::narrow2<T>(f[j] * a.x, f[j] * a.y);
                 }
-                row_dev::store8<kVec>(p.out + at[j] * p.so, i, p.d, o);
+                row_dev::store8<kVec>(p.out + at[j] * p.so, i - lead(j), p.d, o);
             }
         }
 #pragma unroll

@@ -26,14 +26,19 @@ gemm_f16_status launch(const norm_dev::Params& p, bool vec, cudaStream_t stream)
 template <typename T>
 gemm_f16_status choose(const norm_dev::Params& p, bool vec, int sms, cudaStream_t stream)
 {
+    // As many threads as leave few of them without values; of more than 1024 values a row
+    // takes whole blocks.
     if (p.d <= 256) return launch<T, 32, 1>(p, vec, stream);
+    if (p.d <= 512) return launch<T, 32, 2>(p, vec, stream);
     if (p.d <= 1024) return launch<T, 32, 4>(p, vec, stream);
     // a row that would be most of a block's time: more threads on it
     if (p.rows <= sms && p.d > 2048 && p.d <= 8192) return launch<T, 1024, 1>(p, vec, stream);
     if (p.d <= 2048) return launch<T, 256, 1>(p, vec, stream);
     if (p.d <= 4096) return launch<T, 256, 2>(p, vec, stream);
+    if (p.d <= 6144) return launch<T, 256, 3>(p, vec, stream);
     if (p.d <= 8192) return launch<T, 256, 4>(p, vec, stream);
-    if (p.d <= 16384) return launch<T, 1024, 2>(p, vec, stream);
+    if (p.d <= 12288) return launch<T, 512, 3>(p, vec, stream);
+    if (p.d <= 16384) return launch<T, 512, 4>(p, vec, stream);
     return launch<T, 1024, 4>(p, vec, stream);
 }
 

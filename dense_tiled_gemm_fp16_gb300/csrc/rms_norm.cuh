@@ -35,12 +35,51 @@ __global__ void __launch_bounds__(kThreads < 256 ? 256 : kThreads) rms_norm(cons
 {
     constexpr int kBlock = kThreads < 256 ? 256 : kThreads, kWarps = kThreads / 32;
     __shared__ float part[kBlock / 32];
+    __shared__ uint4 edge[kVec ? 1 : kVecs * kBlock / 32];
     const int t = threadIdx.x % kThreads;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * (kBlock / kThreads) + threadIdx.x / kThreads;
     const bool in = row < p.rows;   // (of whole warps, and of whole blocks where a row takes more than one)
     const int64_t d = in ? p.d : 0;
     griddep_wait();
     griddep_launch_dependents();
+
+    // A row's values to memory.  Where it starts off a 16-byte boundary a thread writes the
+    // aligned 16 bytes that end in its own values: the ones before come from the lane
+    // before, of a warp's first lane through shared memory.  (Writing them one by one
+    // there, 15 stores of 2 bytes a warp, took three times as long.)
+    auto store_row = [&](uint16_t* out, uint32_t (&w)[kVecs][4]) {
+        if constexpr (kVec) {
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v) row_dev::store8<true>(out, (v * kThreads + t) * 8, d, w[v]);
+        } else {
+            const int o = row_dev::lead_of(out), lane = threadIdx.x & 31;
+            const int first = (threadIdx.x / kThreads) * kVecs * kWarps;   // of this row's edges
+            if (kWarps > 1) __syncthreads();   // (the last row of values has been read)
+            if (lane == 31)
+#pragma unroll
+                for (int v = 0; v < kVecs; ++v)
+                    edge[first + v * kWarps + (t >> 5)] = make_uint4(w[v][0], w[v][1], w[v][2], w[v][3]);
+            if (kWarps > 1) __syncthreads();
+            else __syncwarp();
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v) {
+                const int i = (v * kThreads + t) * 8;
+                uint32_t prev[4], mine[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) prev[c] = __shfl_up_sync(~0u, w[v][c], 1);
+                if (lane == 0 && i > 0) {
+                    const uint4 e = edge[first + v * kWarps + (t >> 5) - 1];
+                    prev[0] = e.x, prev[1] = e.y, prev[2] = e.z, prev[3] = e.w;
+                }
+                row_dev::shift8(prev, w[v], o, mine);
+                row_dev::store8<false>(out, i - o, d, mine);
+                // the last o of the last thread, where the row goes on to there
+                if (v == kVecs - 1 && t == kThreads - 1 && i + 8 - o < d)
+                    row_dev::store_some(out + i, w[v], 8 - o, static_cast<int>(min(static_cast<int64_t>(8), d - i)));
+            }
+            __syncwarp();
+        }
+    };
 
     uint32_t h[kVecs][4];
 #pragma unroll
@@ -56,8 +95,8 @@ __global__ void __launch_bounds__(kThreads < 256 ? 256 : kThreads) rms_norm(cons
                 const float2 a = row_dev::widen2<T>(h[v][c]), b = row_dev::widen2<T>(r[v][c]);
                 h[v][c] = row_dev::narrow2<T>(a.x + b.x, a.y + b.y);
             }
-            row_dev::store8<kVec>(p.sum + row * p.ss, (v * kThreads + t) * 8, d, h[v]);
         }
+        store_row(p.sum + row * p.ss, h);
     }
     float s = 0.f;
 #pragma unroll
@@ -90,10 +129,9 @@ __global__ void __launch_bounds__(kThreads < 256 ? 256 : kThreads) rms_norm(cons
             y[2 * c] = a.x * r * b.x, y[2 * c + 1] = a.y * r * b.y;
         }
         if (p.y) {
-            uint32_t o[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) o[c] = row_dev::narrow2<T>(y[2 * c], y[2 * c + 1]);
-            row_dev::store8<kVec>(p.y + row * p.sy, i, d, o);
+            for (int c = 0; c < 4; ++c) h[v][c] = row_dev::narrow2<T>(y[2 * c], y[2 * c + 1]);
+            if (kVec) row_dev::store8<true>(p.y + row * p.sy, i, d, h[v]);
         } else {
             uint32_t top = 0;
 #pragma unroll
@@ -110,12 +148,16 @@ __global__ void __launch_bounds__(kThreads < 256 ? 256 : kThreads) rms_norm(cons
                 p.scales[fp8_dev::scale_at(row, i >> 7, p.kt)] = static_cast<uint8_t>(code);
         }
     }
-    if (!p.y) {   // the scale tiles' padding: blocks past the row's, rows past the last
+    if (p.y) {
+        if (!kVec) store_row(p.y + row * p.sy, h);
+    } else {   // the scale tiles' padding: blocks past the row's, rows past the last
         const int64_t blocks = (p.d + 127) >> 7;
         if (in && t < 4 * p.kt - blocks) p.scales[fp8_dev::scale_at(row, blocks + t, p.kt)] = 0;
-        if (row == p.rows - 1)
-            for (int64_t q = p.rows; q < p.row_tiles * 128; ++q)
-                for (int64_t b = t; b < 4 * p.kt; b += kThreads) p.scales[fp8_dev::scale_at(q, b, p.kt)] = 0;
+        if (row == p.rows - 1) {
+            const int kt = static_cast<int>(p.kt), words = static_cast<int>(p.row_tiles * 128 - p.rows) * kt;
+            for (int q = t; q < words; q += kThreads)
+                *reinterpret_cast<uint32_t*>(p.scales + fp8_dev::scale_at(p.rows + q / kt, 4 * (q % kt), p.kt)) = 0u;
+        }
     }
 }
 

@@ -33,17 +33,16 @@ def rms_norm_ptr(x: int, dtype: int, stride_x: int, residual: int, stride_residu
              "rms_norm")
 
 
-def _rows(v, like, name: str) -> int:
-    """The row stride of v, which has the shape, type and device of `like` and contiguous rows."""
-    if v.shape != like.shape or v.dtype is not like.dtype:
+def _rows(v, shape, dtype, device, name: str) -> int:
+    """The row stride of v, a matrix of that shape, type and device with contiguous rows."""
+    if v.shape != shape or v.dtype is not dtype:
         raise ValueError(f"{name} must have x's shape and type")
-    if v.device != like.device:
+    if v.device != device:
         raise ValueError("tensors must share one CUDA device")
-    d = v.shape[1]
     s, unit = v.stride()
-    if unit != 1 and d > 1:
+    if unit != 1 and shape[1] > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return s if v.shape[0] > 1 else max(d, 1)
+    return s if shape[0] > 1 else max(shape[1], 1)
 
 
 def rms_norm(x, weight, eps: float = 1e-6, residual=None, quantize: bool = False, out=None, sum_out=None, stream=None):
@@ -53,35 +52,46 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, quantize: bool = False
     Returns y [rows, d] of x's type, or with `quantize` the Fp8Matrix of it, and
     with a residual (y, h), h the sum rounded to x's type; `sum_out` receives h and
     may be x or residual itself."""
-    if x.dim() != 2:
+    shape, dtype, device = x.shape, x.dtype, x.device
+    if len(shape) != 2:
         raise ValueError("rms_norm takes x [rows, d]")
-    code = _dtype_code(x.dtype, "x", BF16)
-    device = x.device
-    rows, d = x.shape
-    sx = _rows(x, x, "x")
-    if weight.dim() != 1 or weight.shape[0] != d or weight.dtype is not x.dtype or (d > 1 and weight.stride(0) != 1):
+    code = _dtype_code(dtype, "x", BF16)
+    rows, d = shape
+    sx, unit = x.stride()
+    if unit != 1 and d > 1:
+        raise ValueError("x must have contiguous rows")
+    if rows < 2:
+        sx = max(d, 1)
+    if weight.shape != shape[1:] or weight.dtype is not dtype or (d > 1 and weight.stride(0) != 1):
         raise ValueError("weight must hold d values of x's type with unit stride")
     if weight.device != device:
         raise ValueError("tensors must share one CUDA device")
-    if residual is None and sum_out is not None:
-        raise ValueError("sum_out needs a residual")
-    if quantize and out is not None:
-        raise ValueError("out is for an output that is not quantized")
-    sr = _rows(residual, x, "residual") if residual is not None else 0
-    ss = _rows(sum_out, x, "sum_out") if sum_out is not None else d
-    sy = _rows(out, x, "out") if out is not None else d
     _cuda(device)
-    h, q = sum_out, None
-    if residual is not None and h is None:
-        h = _empty((rows, d), x.dtype, device, stream)
+    h, hp, rp, sr, ss, sy = None, None, None, 0, d, d
+    if residual is not None:
+        sr = _rows(residual, shape, dtype, device, "residual")
+        if sum_out is None:
+            h = _empty(shape, dtype, device, stream)
+        else:
+            h, ss = sum_out, _rows(sum_out, shape, dtype, device, "sum_out")
+        hp, rp = h.data_ptr(), residual.data_ptr()
+    elif sum_out is not None:
+        raise ValueError("sum_out needs a residual")
+    yp = cp = sp = None
     if quantize:
+        if out is not None:
+            raise ValueError("out is for an output that is not quantized")
         if rows < 1 or d < 1:
             raise ValueError("a matrix in 8 bits has at least one row and one value")
-        y = q = Fp8Matrix._new(rows, d, None, device, stream)
+        y = Fp8Matrix._new(rows, d, None, device, stream)
+        cp, sp = y.codes_ptr, y.scales_ptr
     else:
-        y = _empty((rows, d), x.dtype, device, stream) if out is None else out
+        if out is None:
+            y = _empty(shape, dtype, device, stream)
+        else:
+            y, sy = out, _rows(out, shape, dtype, device, "out")
+        yp = y.data_ptr()
     if rows:
-        _run(device, "rms_norm", x.data_ptr(), code, sx, None if residual is None else residual.data_ptr(), sr,
-             weight.data_ptr(), eps, None if h is None else h.data_ptr(), ss, None if q else y.data_ptr(), sy,
-             q.codes_ptr if q else None, q.scales_ptr if q else None, rows, d, _stream(device, stream))
+        _run(device, "rms_norm", x.data_ptr(), code, sx, rp, sr, weight.data_ptr(), eps, hp, ss, yp, sy, cp, sp, rows, d,
+             _stream(device, stream))
     return y if residual is None else (y, h)

@@ -82,6 +82,9 @@ def moe_combine_grad_ptr(dout: int, dtype: int, stride_dout: int, y: int, stride
 
 
 # ------------------------------------------------------------ torch helpers
+_FEW = 1024   # choices that moe_sort orders without a workspace
+
+
 class MoeOrder(NamedTuple):
     """Where (token, expert) choices stand, int32 on the device: rows [T, top_k],
     the place of each choice (-1: no expert's); order [T * top_k], the choice t *
@@ -95,17 +98,15 @@ class MoeOrder(NamedTuple):
 def moe_sort(ids, experts: int, stream=None) -> MoeOrder:
     """The order of the choices ids [T, top_k] (int32, contiguous) by expert, of one
     expert by token.  An id outside 0 .. experts - 1 is no expert's."""
-    t = _torch()
-    if ids.dim() != 2 or ids.dtype is not t.int32 or not ids.is_contiguous():
+    t, shape, device = _torch(), ids.shape, ids.device
+    if len(shape) != 2 or ids.dtype is not t.int32 or not ids.is_contiguous():
         raise TypeError("moe_sort takes ids as a contiguous int32 tensor [T, top_k]")
-    T, top = ids.shape
-    device = ids.device
+    T, top = shape
+    n = T * top
     _cuda(device)
-    need = moe_sort_workspace_size(T, top, experts)
-    rows = _empty((T, top), t.int32, device, stream)
-    order = _empty((T * top,), t.int32, device, stream)
-    groups = _empty((experts,), t.int32, device, stream)
-    space = _empty((need,), t.uint8, device, stream) if need else None
+    need = moe_sort_workspace_size(T, top, experts) if n > _FEW or not 1 <= experts <= MAX_EXPERTS else 0
+    rows, order, groups = (_empty(size, t.int32, device, stream) for size in (shape, n, experts))
+    space = _empty(need, t.uint8, device, stream) if need else None
     _run(device, "moe_sort", ids.data_ptr() or None, T, top, experts, rows.data_ptr() or None, order.data_ptr() or None,
          groups.data_ptr(), space.data_ptr() if need else None, need, _stream(device, stream))
     return MoeOrder(rows, order, groups)
@@ -114,17 +115,18 @@ def moe_sort(ids, experts: int, stream=None) -> MoeOrder:
 def _places(order: MoeOrder, device):
     """(T, top_k) of an order on `device`."""
     rows = order.rows
-    if rows.dim() != 2 or rows.dtype is not _torch().int32 or not rows.is_contiguous():
+    shape = rows.shape
+    if len(shape) != 2 or rows.dtype is not _torch().int32 or not rows.is_contiguous():
         raise TypeError("an order's rows are a contiguous int32 tensor [T, top_k]")
     if rows.device != device:
         raise ValueError("tensors must share one CUDA device")
     _cuda(device)
-    return rows.shape
+    return shape
 
 
 def _matrix(v, shape, dtype, device, name: str) -> int:
     """The row stride of v, a matrix of that shape, type and device with contiguous rows."""
-    if tuple(v.shape) != shape or v.dtype is not dtype:
+    if v.shape != shape or v.dtype is not dtype:
         raise ValueError(f"{name} must be {list(shape)} of type {dtype}")
     if v.device != device:
         raise ValueError("tensors must share one CUDA device")
@@ -135,7 +137,7 @@ def _matrix(v, shape, dtype, device, name: str) -> int:
 
 
 def _weights(w, shape, device) -> None:
-    if tuple(w.shape) != tuple(shape) or w.dtype is not _torch().float32 or not w.is_contiguous():
+    if w.shape != shape or w.dtype is not _torch().float32 or not w.is_contiguous():
         raise TypeError("weights must be a contiguous float32 tensor [T, top_k]")
     if w.device != device:
         raise ValueError("tensors must share one CUDA device")
@@ -159,9 +161,11 @@ def moe_gather(x, order: MoeOrder, out=None, stream=None):
         return q
     code, d = _dtype_code(x.dtype, "x", BF16), x.shape[1]
     sx = _matrix(x, (T, d), x.dtype, device, "x")
+    so = d
     if out is None:
         out = _empty((T * top, d), x.dtype, device, stream)
-    so = _matrix(out, (T * top, d), x.dtype, device, "out")
+    else:
+        so = _matrix(out, (T * top, d), x.dtype, device, "out")
     if T:
         _run(device, "moe_gather", x.data_ptr(), code, sx, order.rows.data_ptr(), T, top, d, out.data_ptr(), so,
              _stream(device, stream))
@@ -180,9 +184,11 @@ def moe_combine(y, order: MoeOrder, weights=None, out=None, stream=None):
     sy = _matrix(y, (T * top, d), y.dtype, device, "y")
     if weights is not None:
         _weights(weights, (T, top), device)
+    so = d
     if out is None:
         out = _empty((T, d), y.dtype, device, stream)
-    so = _matrix(out, (T, d), y.dtype, device, "out")
+    else:
+        so = _matrix(out, (T, d), y.dtype, device, "out")
     if T:
         _run(device, "moe_combine", y.data_ptr(), code, sy, order.rows.data_ptr(),
              None if weights is None else weights.data_ptr(), T, top, d, out.data_ptr(), so, _stream(device, stream))
@@ -202,9 +208,11 @@ def moe_combine_grad(dout, y, order: MoeOrder, weights, out=None, stream=None):
     sy = _matrix(y, (T * top, d), y.dtype, device, "y")
     sg = _matrix(dout, (T, d), y.dtype, device, "dout")
     _weights(weights, (T, top), device)
+    so = d
     if out is None:
         out = _empty((T * top, d), y.dtype, device, stream)
-    so = _matrix(out, (T * top, d), y.dtype, device, "out")
+    else:
+        so = _matrix(out, (T * top, d), y.dtype, device, "out")
     dw = _empty((T, top), weights.dtype, device, stream)
     if T:
         _run(device, "moe_combine_grad", dout.data_ptr(), code, sg, y.data_ptr(), sy, order.rows.data_ptr(),
