@@ -357,7 +357,8 @@ __global__ void __launch_bounds__(kTileThreads) gemm_fp8_tile(const __grid_const
 // At most 224 columns, so that two accumulators and the scales fit tensor memory (512
 // columns) side by side and a tile's MMAs follow the last one's without a pause: with
 // two of 256, which have to share some, 1200 cycles passed between them (a 256-wide
-// tile takes 512 cycles a step, one of 224 takes 448).
+// tile takes 512 cycles a step, one of 224 takes 448).  256 where no cluster has a second
+// tile.
 //
 // Gate/up (kGated): the 256 lanes hold 128 rows of either weight, 16 of one and 16 of
 // the other by turns, so that a thread of the epilogue holds both values of an output.
@@ -365,12 +366,12 @@ constexpr int kMaxStages = 10, kSets = 4, kMaxGroups = 512;
 constexpr int kPairThreads = 320 + 32 * kSets;   // warps 0-7 epilogue, 8 loads, 9 MMA, the others scales
 constexpr uint32_t kSlotBytes = 12 * kABytes, kSetBytes = 3 * kScaleTile, kBoxBytes = 32 * 64;   // kSlotBytes: all stages
 constexpr uint32_t kPairSmem = kSlotBytes + 8 * kBoxBytes + kSets * kSetBytes + 1024;
-constexpr int kMaxWidth = 224;                  // columns of a tile
+constexpr int kMaxWidth = 224, kOneWidth = 256; // columns of a tile; of a cluster's only one
 constexpr uint32_t kSfCol = 496, kAcc1 = 256;   // scales of the weights (4), of A (8); the second accumulator
 
 struct PairParams {
     CUtensorMap tmW, tmU;        // weight codes {pitch, n, groups}, boxes of 128 bytes x 128 rows (kGated: 16)
-    CUtensorMap tmX[7];          // A's codes {pitch, rows}, boxes of 128 bytes x 16, 32, .. 112 rows (one group: of its width's)
+    CUtensorMap tmX[8];          // A's codes {pitch, rows}, boxes of 128 bytes x 16, 32, .. 128 rows (one group: of its width's)
     const uint8_t* sw;           // scale tiles of the weights, of the second ones, and of A
     const uint8_t* su;
     const uint8_t* sx;
@@ -392,7 +393,7 @@ struct Groups {
     int row0[kMaxGroups + 1];    // rows past the last group's end belong to none
     int tile0[kMaxGroups + 1];   // tiles before the group: its parts x tiles_w
     int parts[kMaxGroups];       // of its rows
-    uint8_t width[kMaxGroups];   // columns of each part, at most
+    uint16_t width[kMaxGroups];  // columns of each part, at most
     int widest;                  // of all groups
 };
 
@@ -414,7 +415,7 @@ __device__ __forceinline__ void choose_tiles(const PairParams& p, Groups& g, int
             const int rows = static_cast<int>(p.rows);
             g.row0[0] = g.tile0[0] = 0, g.row0[1] = rows;
             g.parts[0] = parts_of(rows, p.width), g.tile0[1] = g.parts[0] * p.tiles_w;
-            g.width[0] = static_cast<uint8_t>(g.widest = p.width);
+            g.width[0] = static_cast<uint16_t>(g.widest = p.width);
         }
         return;
     }
@@ -444,7 +445,7 @@ __device__ __forceinline__ void choose_tiles(const PairParams& p, Groups& g, int
         tiles += __shfl_xor_sync(~0u, tiles, d);
         widest = max(widest, __shfl_xor_sync(~0u, widest, d));
     }
-    int64_t cost = w > kMaxWidth ? INT64_MAX : cost_of(tiles * p.tiles_w, widest, clusters) * 16 + (7 - (lane & 7));
+    int64_t cost = w > kMaxWidth && tiles * p.tiles_w > clusters ? INT64_MAX : cost_of(tiles * p.tiles_w, widest, clusters) * 16 + (7 - (lane & 7));
 #pragma unroll
     for (int d = 1; d < 8; d *= 2) cost = min(cost, __shfl_xor_sync(~0u, cost, d));
     const int width = p.width ? p.width : 32 * (8 - static_cast<int>(cost & 15));
@@ -455,7 +456,7 @@ __device__ __forceinline__ void choose_tiles(const PairParams& p, Groups& g, int
         if (i < p.groups) {
             const int rows = g.row0[i + 1] - g.row0[i], parts = parts_of(rows, width), w = width_of(rows, parts);
             g.parts[i] = parts;
-            g.width[i] = static_cast<uint8_t>(w);
+            g.width[i] = static_cast<uint16_t>(w);
             widest = max(widest, w);
             n = parts * p.tiles_w;
         }

@@ -23,7 +23,7 @@ struct Sizes {
 bool sizes_of(int64_t rows, int64_t k, int64_t batch, Sizes* s)
 {
     if (rows < 1 || k < 1 || batch < 1 || rows > GEMM_F16_MAX_DIM || k > GEMM_F16_MAX_DIM) return false;
-    s->pitch = cdiv(k, 16) * 16;
+    s->pitch = cdiv(k, 128) * 128;
     s->kt = cdiv(k, 512);
     s->row_tiles = cdiv(rows, 128);
     if (__builtin_mul_overflow(rows * s->pitch, batch, &s->code_bytes)) return false;
@@ -201,15 +201,16 @@ gemm_f16_status launch_pair(const Product& q, const Device& dev, const Sizes& sa
     if (!q.groups) {
         const int rows = static_cast<int>(q.m);
         int64_t best = p.width ? 0 : INT64_MAX;
-        for (int w = fp8_dev::kMaxWidth; w && best; w -= 32) {
+        for (int w = fp8_dev::kOneWidth; w && best; w -= 32) {
             const int parts = fp8_dev::parts_of(rows, w);
+            if (w > fp8_dev::kMaxWidth && parts * tiles_w > clusters) continue;
             const int64_t cost = fp8_dev::cost_of(static_cast<int>(parts * tiles_w), fp8_dev::width_of(rows, parts),
                                                   static_cast<int>(clusters));
             if (cost < best) best = cost, p.width = w;
         }
         p.width = fp8_dev::width_of(rows, fp8_dev::parts_of(rows, p.width));
     }
-    for (int i = 0; i < 7; ++i)
+    for (int i = 0; i < 8; ++i)
         if ((q.groups || p.width == 32 * (i + 1)) && !encode_codes(&p.tmX[i], q.a_codes, q.m, 0, sa.pitch, 16u * (i + 1)))
             return GEMM_F16_ERR_LAUNCH;
     return launch_kernel(kernel, dim3(static_cast<unsigned>(2 * clusters)), fp8_dev::kPairThreads, fp8_dev::kPairSmem, 2,

@@ -168,7 +168,7 @@ gemm_f16_status moe_gather_fp8(const void* codes, const void* scales, const int3
     route_dev::Fp8RowParams p = {};
     p.codes = static_cast<const uint8_t*>(codes), p.scales = static_cast<const uint8_t*>(scales);
     p.out_codes = static_cast<uint8_t*>(out_codes), p.out_scales = static_cast<uint8_t*>(out_scales);
-    p.rows = rows, p.tokens = tokens, p.places = n, p.pitch = cdiv(k, 16) * 16, p.kt = cdiv(k, 512);
+    p.rows = rows, p.tokens = tokens, p.places = n, p.pitch = cdiv(k, 128) * 128, p.kt = cdiv(k, 512);
     p.top = static_cast<int32_t>(top_k), p.chunks = static_cast<int32_t>(cdiv(p.pitch, 16 * route_dev::kRowThreads));
     const int64_t blocks = tokens * p.chunks + 1;   // the last one: padding
     if (blocks > INT32_MAX) return GEMM_F16_ERR_INVALID_VALUE;

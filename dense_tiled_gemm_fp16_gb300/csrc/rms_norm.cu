@@ -96,7 +96,7 @@ extern "C" gemm_f16_status rms_norm(const void* x, int dtype, int64_t stride_x, 
     p.codes = static_cast<uint8_t*>(codes);
     p.scales = static_cast<uint8_t*>(scales);
     p.sx = stride_x, p.sr = stride_residual, p.ss = stride_sum, p.sy = stride_y;
-    p.rows = rows, p.d = d, p.pitch = cdiv(d, 16) * 16, p.kt = cdiv(d, 512), p.row_tiles = cdiv(rows, 128);
+    p.rows = rows, p.d = d, p.pitch = cdiv(d, 128) * 128, p.kt = cdiv(d, 512), p.row_tiles = cdiv(rows, 128);
     p.eps = eps;
     bool vec = d % 8 == 0 && aligned(weight, 16);
     for (const Range& r : in)

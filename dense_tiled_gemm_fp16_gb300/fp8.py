@@ -96,7 +96,7 @@ def gemm_fp8_grouped_a16(A: int, a_dtype: int, stride_am: int, stride_ak: int, w
 # ------------------------------------------------------------ torch helpers
 def _bytes(rows: int, k: int, batch: int):
     """fp8_sizes without its checks: (codes, scales)."""
-    return batch * rows * ((k + 15) >> 4) * 16, batch * ((rows + 127) >> 7) * ((k + 511) >> 9) * 512
+    return batch * rows * ((k + 127) >> 7) * 128, batch * ((rows + 127) >> 7) * ((k + 511) >> 9) * 512
 
 
 class Fp8Matrix:

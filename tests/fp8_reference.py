@@ -54,6 +54,6 @@ def scales_plain(tiled, rows, k):
 
 def codes_plain(codes, rows, k):
     """[rows, k] of one matrix's codes, checking that the padding is zero."""
-    c = codes.reshape(rows, -(-k // 16) * 16)
+    c = codes.reshape(rows, -(-k // 128) * 128)
     assert not c[:, k:].any()
     return c[:, :k]
