@@ -372,6 +372,7 @@ constexpr uint32_t kSfCol = 496, kAcc1 = 256;   // scales of the weights (4), of
 struct PairParams {
     CUtensorMap tmW, tmU;        // weight codes {pitch, n, groups}, boxes of 128 bytes x 128 rows (kGated: 16)
     CUtensorMap tmX[8];          // A's codes {pitch, rows}, boxes of 128 bytes x 16, 32, .. 128 rows (one group: of its width's)
+    CUtensorMap tmC;             // boxes of a warp's columns x 32 rows (c_tma)
     const uint8_t* sw;           // scale tiles of the weights, of the second ones, and of A
     const uint8_t* su;
     const uint8_t* sx;
@@ -382,7 +383,7 @@ struct PairParams {
     int64_t ldc, rows, n;
     int32_t groups, tiles_w, panel;   // panel: weight tiles walked together
     int32_t width;               // W; 0: of the groups' choice
-    int32_t k32, steps, act, bf16, vec;   // vec: C's rows take 16-byte stores
+    int32_t k32, steps, act, bf16, c_tma;   // c_tma: C's rows take 16-byte stores, and TMA's
     int32_t test_stall;
     uint64_t timeout_ns;
     int* status;
@@ -637,6 +638,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
         fence_mbarrier_init();
         tma_prefetch_desc(&p.tmW);
         if (kGated) tma_prefetch_desc(&p.tmU);
+        if (p.c_tma) tma_prefetch_desc(&p.tmC);
     }
     if (warp == 9) {
         tmem_alloc_pair(smem_u32(&tmem_slot), 512);
@@ -877,8 +879,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
                     for (int c = 0; c < 32; ++c) v[c] += bias[2 * (c >> 4) + ((c >> 1) & 1)];
                     act_all(p.act, v);
                 }
-                // to the box as rows of C: row tok at tok * 2 kN, its 16-byte parts shifted so
-                // that eight rows fall on different banks
+                // to the box as rows of C: row tok at tok * 2 kN, its 16-byte parts shifted as TMA's
+                // swizzles have it, so that eight rows fall on different banks
+                if (lane == 0) bulk_wait_group_read<0>();   // the box's last store has read it
+                __syncwarp();
                 auto part = [&](int tok, int c) {
                     return box + tok * (2 * kN) + ((c ^ (kGated ? (tok >> 2) & 1 : (tok >> 1) & 3)) << 4);
                 };
@@ -892,9 +896,18 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
                         stmatrix_x4_trans(part(8 * c + (lane & 7), lane >> 3), two(4 * c), two(4 * c + 2), two(16 + 4 * c),
                                           two(16 + 4 * c + 2));
                 }
+                if (p.c_tma && left >= 32) {   // (TMA leaves out columns past C's, not rows past the group's)
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(&p.tmC, box, static_cast<int32_t>(n0), o.row + b * 32);
+                        bulk_commit_group();
+                    }
+                    continue;
+                }
                 __syncwarp();
                 uint16_t* to = p.C + (static_cast<int64_t>(o.row) + b * 32) * p.ldc + n0;
-                if (p.vec && n0 + kN <= p.n) {
+                if (p.c_tma && n0 + kN <= p.n) {
                     constexpr int kParts = kN / 8, kPass = 32 / kParts;   // 16-byte parts of a row, rows a pass
                     const int c = lane % kParts;
 #pragma unroll
@@ -914,6 +927,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
             if (acc) tpar ^= 1u;
             acc ^= 1;
         }
+        if (lane == 0) bulk_wait_group_all();
     }
     tc_fence_before();
     __syncwarp();

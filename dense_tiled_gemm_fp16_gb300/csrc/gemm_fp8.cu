@@ -48,6 +48,20 @@ bool encode_codes(CUtensorMap* tm, const void* codes, int64_t rows, int64_t batc
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// C, boxes of 32 rows x the columns of an epilogue's warp: 32, of a gated product 16.
+bool encode_out(CUtensorMap* tm, void* C, int64_t M, int64_t N, int64_t ldc, bool gated)
+{
+    const auto encode = tensor_map_encoder();
+    if (!encode) return false;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(M)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(2 * ldc)};
+    cuuint32_t box[2] = {gated ? 16u : 32u, 32};
+    cuuint32_t estr[2] = {1, 1};
+    return encode(tm, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, C, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  gated ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Dynamic shared memory above 48 KB is allowed once per device and kernel.
 bool allow_smem(const void* kernel, int slot, int bytes)
 {
@@ -185,7 +199,7 @@ gemm_f16_status launch_pair(const Product& q, const Device& dev, const Sizes& sa
     p.steps = static_cast<int32_t>(cdiv(q.k, 128));
     p.act = q.act;
     p.bf16 = q.dtype == FP8_BF16;
-    p.vec = q.ldc % 8 == 0 && aligned(q.c, 16);
+    p.c_tma = q.n % 8 == 0 && q.ldc % 8 == 0 && q.ldc < int64_t(1) << 39 && aligned(q.c, 16);
     p.test_stall = option(GEMM_F16_OPT_TEST_STALL) == 1;
     p.timeout_ns = timeout_ns();
     p.status = dev.status;
@@ -193,6 +207,7 @@ gemm_f16_status launch_pair(const Product& q, const Device& dev, const Sizes& sa
     if (!encode_codes(&p.tmW, q.b_codes, q.n, p.groups, sb.pitch, box) ||
         (gated && !encode_codes(&p.tmU, q.u_codes, q.n, p.groups, sb.pitch, box)))
         return GEMM_F16_ERR_LAUNCH;
+    if (p.c_tma && !encode_out(&p.tmC, q.c, q.m, q.n, q.ldc, gated)) return GEMM_F16_ERR_LAUNCH;
     const auto kernel = gated ? fp8_dev::gemm_fp8_pair<true> : fp8_dev::gemm_fp8_pair<false>;
     if (!allow_smem(reinterpret_cast<const void*>(kernel), gated ? 1 : 2, fp8_dev::kPairSmem)) return GEMM_F16_ERR_LAUNCH;
     const int64_t clusters = std::min<int64_t>(dev.sms / 2, tiles);
