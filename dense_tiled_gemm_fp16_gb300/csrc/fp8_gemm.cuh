@@ -900,7 +900,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        tma_store_2d(&p.tmC, box, static_cast<int32_t>(n0), o.row + b * 32);
+                        // (first out of L2: the operands stay)
+                        tma_store_2d_l2(&p.tmC, box, static_cast<int32_t>(n0), o.row + b * 32, 1);
                         bulk_commit_group();
                     }
                     continue;

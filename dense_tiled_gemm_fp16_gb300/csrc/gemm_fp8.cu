@@ -194,7 +194,9 @@ gemm_f16_status launch_pair(const Product& q, const Device& dev, const Sizes& sa
     const int64_t tiles_w = cdiv(q.n, gated ? 128 : 256), tiles = (cdiv(q.m, 32) + p.groups) * tiles_w;
     if (tiles > INT32_MAX) return GEMM_F16_ERR_INVALID_VALUE;   // (an upper bound of their number)
     p.tiles_w = static_cast<int32_t>(tiles_w);
-    p.panel = 8;
+    // Weight tiles of at most 32 MB walked together, so that A's rows come from DRAM once
+    // (131072 x 7168 x 2048 in 8 groups: 1405 us with 8 tiles, 1349 with all 28).
+    p.panel = static_cast<int32_t>(std::min<int64_t>(tiles_w, std::max<int64_t>(8, (int64_t(32) << 20) / (256 * sb.pitch))));
     p.k32 = static_cast<int32_t>(cdiv(q.k, 32));
     p.steps = static_cast<int32_t>(cdiv(q.k, 128));
     p.act = q.act;
