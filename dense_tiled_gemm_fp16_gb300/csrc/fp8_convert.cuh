@@ -12,11 +12,6 @@ namespace fp8_dev {
 constexpr int kTileRows = 128, kTileVals = 512, kConvThreads = 256;
 constexpr int kDequantRows = 32;   // rows a block writes
 
-template <bool kValue>
-struct Bool {
-    static constexpr bool value = kValue;
-};
-
 struct QuantParams {
     const void* x;
     int64_t sb, sr, sk;   // element strides

@@ -14,6 +14,11 @@ using mxf4_dev::scale_value;
 
 constexpr int kBlock = 128;   // values that share a scale
 
+template <bool kValue>
+struct Bool {
+    static constexpr bool value = kValue;
+};
+
 // Scale code of a block whose largest magnitude has the bits `top`: s + 127 for the
 // smallest s with |x| <= 448 * 2^s (448 = 1.75 * 2^8 is e4m3's largest), 255 (NaN)
 // with an infinity or a NaN among them.  Being no smaller than the largest value

@@ -13,14 +13,16 @@ namespace {
 
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-template <typename T, int kThreads, int kVecs>
+template <typename T, int kThreads, int kVecs, bool kBoth = true>   // kBoth: aligned rows come here, too
 gemm_f16_status launch(const norm_dev::Params& p, bool vec, cudaStream_t stream)
 {
     constexpr int kBlock = kThreads < 256 ? 256 : kThreads;
     const int64_t blocks = cdiv(p.rows, kBlock / kThreads);
     if (blocks > INT32_MAX) return GEMM_F16_ERR_INVALID_VALUE;
-    return launch_kernel(vec ? norm_dev::rms_norm<T, kThreads, kVecs, true> : norm_dev::rms_norm<T, kThreads, kVecs, false>,
-                         dim3(static_cast<unsigned>(blocks)), kBlock, 0, 1, stream, p);
+    auto kernel = norm_dev::rms_norm<T, kThreads, kVecs, false>;
+    if constexpr (kBoth)
+        if (vec) kernel = norm_dev::rms_norm<T, kThreads, kVecs, true>;
+    return launch_kernel(kernel, dim3(static_cast<unsigned>(blocks)), kBlock, 0, 1, stream, p);
 }
 
 template <typename T>
@@ -28,18 +30,20 @@ gemm_f16_status choose(const norm_dev::Params& p, bool vec, int sms, cudaStream_
 {
     // As many threads as leave few of them without values; of more than 1024 values a row
     // takes whole blocks.
-    if (p.d <= 256) return launch<T, 32, 1>(p, vec, stream);
-    if (p.d <= 512) return launch<T, 32, 2>(p, vec, stream);
-    if (p.d <= 1024) return launch<T, 32, 4>(p, vec, stream);
+    const int64_t d = p.d + (vec ? 0 : 7);   // (a row that starts up to 7 values past a boundary)
+    if (d <= 256) return launch<T, 32, 1>(p, vec, stream);
+    if (d <= 512) return launch<T, 32, 2>(p, vec, stream);
+    if (d <= 1024) return launch<T, 32, 4>(p, vec, stream);
     // a row that would be most of a block's time: more threads on it
-    if (p.rows <= sms && p.d > 2048 && p.d <= 8192) return launch<T, 1024, 1>(p, vec, stream);
-    if (p.d <= 2048) return launch<T, 256, 1>(p, vec, stream);
-    if (p.d <= 4096) return launch<T, 256, 2>(p, vec, stream);
-    if (p.d <= 6144) return launch<T, 256, 3>(p, vec, stream);
-    if (p.d <= 8192) return launch<T, 256, 4>(p, vec, stream);
-    if (p.d <= 12288) return launch<T, 512, 3>(p, vec, stream);
-    if (p.d <= 16384) return launch<T, 512, 4>(p, vec, stream);
-    return launch<T, 1024, 4>(p, vec, stream);
+    if (p.rows <= sms && d > 2048 && d <= 8192) return launch<T, 1024, 1>(p, vec, stream);
+    if (d <= 2048) return launch<T, 256, 1>(p, vec, stream);
+    if (d <= 4096) return launch<T, 256, 2>(p, vec, stream);
+    if (d <= 6144) return launch<T, 256, 3>(p, vec, stream);
+    if (d <= 8192) return launch<T, 256, 4>(p, vec, stream);
+    if (d <= 12288) return launch<T, 512, 3>(p, vec, stream);
+    if (d <= 16384) return launch<T, 512, 4>(p, vec, stream);
+    if (d <= 32768) return launch<T, 1024, 4>(p, vec, stream);
+    return launch<T, 1024, 5, false>(p, vec, stream);
 }
 
 }  // namespace

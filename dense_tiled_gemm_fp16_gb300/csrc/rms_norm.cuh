@@ -14,6 +14,7 @@
 namespace norm_dev {
 
 using namespace gemm_f16_dev;
+using fp8_dev::Bool;
 
 struct Params {
     const uint16_t* x;
@@ -43,51 +44,68 @@ __global__ void __launch_bounds__(kThreads < 256 ? 256 : kThreads) rms_norm(cons
     griddep_wait();
     griddep_launch_dependents();
 
-    // A row's values to memory.  Where it starts off a 16-byte boundary a thread writes the
-    // aligned 16 bytes that end in its own values: the ones before come from the lane
-    // before, of a warp's first lane through shared memory.  (Writing them one by one
-    // there, 15 stores of 2 bytes a warp, took three times as long.)
-    auto store_row = [&](uint16_t* out, uint32_t (&w)[kVecs][4]) {
-        if constexpr (kVec) {
+    // Where rows start anywhere a thread takes the values of 16 aligned bytes of x's row,
+    // `lead` before a multiple of eight, where residual and sum mostly have theirs, too.
+    // Then the values move to their multiples of eight, so that the sum of squares has
+    // one order wherever the rows lie, and y's go back on their way out.
+    const int lead = kVec ? 0 : row_dev::lead_of(p.x + row * p.sx);
+    auto at = [&](int v, int before) { return (v * kThreads + t) * 8 - before; };
+
+    // The values' neighbours: of the thread before (kNext: after), of a warp's end through
+    // shared memory.  By all threads of a row.
+    auto neighbours = [&](auto next, uint32_t (&w)[kVecs][4], uint32_t (&n)[kVecs][4]) {
+        constexpr bool kNext = decltype(next)::value;
+        const int lane = threadIdx.x & 31, first = (threadIdx.x / kThreads) * kVecs * kWarps;   // of this row's edges
+        if (kWarps > 1) __syncthreads();   // (the last edges have been read)
+        if (lane == (kNext ? 0 : 31))
 #pragma unroll
-            for (int v = 0; v < kVecs; ++v) row_dev::store8<true>(out, (v * kThreads + t) * 8, d, w[v]);
-        } else {
-            const int o = row_dev::lead_of(out), lane = threadIdx.x & 31;
-            const int first = (threadIdx.x / kThreads) * kVecs * kWarps;   // of this row's edges
-            if (kWarps > 1) __syncthreads();   // (the last row of values has been read)
-            if (lane == 31)
+            for (int v = 0; v < kVecs; ++v)
+                edge[first + v * kWarps + (t >> 5)] = make_uint4(w[v][0], w[v][1], w[v][2], w[v][3]);
+        if (kWarps > 1) __syncthreads();
+        else __syncwarp();
 #pragma unroll
-                for (int v = 0; v < kVecs; ++v)
-                    edge[first + v * kWarps + (t >> 5)] = make_uint4(w[v][0], w[v][1], w[v][2], w[v][3]);
-            if (kWarps > 1) __syncthreads();
-            else __syncwarp();
+        for (int v = 0; v < kVecs; ++v) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) n[v][c] = kNext ? __shfl_down_sync(~0u, w[v][c], 1) : __shfl_up_sync(~0u, w[v][c], 1);
+            if (lane == (kNext ? 31 : 0)) {
+                const int e = v * kWarps + (t >> 5) + (kNext ? 1 : -1);
+                const uint4 x = e >= 0 && e < kVecs * kWarps ? edge[first + e] : make_uint4(0u, 0u, 0u, 0u);
+                n[v][0] = x.x, n[v][1] = x.y, n[v][2] = x.z, n[v][3] = x.w;
+            }
+        }
+        __syncwarp();
+    };
+
+    // Values that begin `from` before multiples of eight.
+    auto store_row = [&](uint16_t* out, uint32_t (&w)[kVecs][4], int from) {
+        const int o = kVec ? 0 : (row_dev::lead_of(out) - from) & 7;   // (the same in all of a row's threads, and a row of several warps is a block)
+        if (o == 0) {
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v) row_dev::store8<kVec>(out, at(v, from), d, w[v]);
+        } else if constexpr (!kVec) {
+            // 16 aligned bytes that end in the thread's own values
+            uint32_t before[kVecs][4];
+            neighbours(Bool<false>(), w, before);
 #pragma unroll
             for (int v = 0; v < kVecs; ++v) {
-                const int i = (v * kThreads + t) * 8;
-                uint32_t prev[4], mine[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) prev[c] = __shfl_up_sync(~0u, w[v][c], 1);
-                if (lane == 0 && i > 0) {
-                    const uint4 e = edge[first + v * kWarps + (t >> 5) - 1];
-                    prev[0] = e.x, prev[1] = e.y, prev[2] = e.z, prev[3] = e.w;
-                }
-                row_dev::shift8(prev, w[v], o, mine);
+                uint32_t mine[4];
+                row_dev::take8(before[v], w[v], 8 - o, mine);
+                const int i = at(v, from);
                 row_dev::store8<false>(out, i - o, d, mine);
                 // the last o of the last thread, where the row goes on to there
                 if (v == kVecs - 1 && t == kThreads - 1 && i + 8 - o < d)
                     row_dev::store_some(out + i, w[v], 8 - o, static_cast<int>(min(static_cast<int64_t>(8), d - i)));
             }
-            __syncwarp();
         }
     };
 
     uint32_t h[kVecs][4];
 #pragma unroll
-    for (int v = 0; v < kVecs; ++v) row_dev::load8<kVec>(p.x + row * p.sx, (v * kThreads + t) * 8, d, h[v]);
+    for (int v = 0; v < kVecs; ++v) row_dev::load8<kVec>(p.x + row * p.sx, at(v, lead), d, h[v]);
     if (p.residual) {
         uint32_t r[kVecs][4];
 #pragma unroll
-        for (int v = 0; v < kVecs; ++v) row_dev::load8<kVec>(p.residual + row * p.sr, (v * kThreads + t) * 8, d, r[v]);
+        for (int v = 0; v < kVecs; ++v) row_dev::load8<kVec>(p.residual + row * p.sr, at(v, lead), d, r[v]);
 #pragma unroll
         for (int v = 0; v < kVecs; ++v) {
 #pragma unroll
@@ -96,7 +114,18 @@ __global__ void __launch_bounds__(kThreads < 256 ? 256 : kThreads) rms_norm(cons
                 h[v][c] = row_dev::narrow2<T>(a.x + b.x, a.y + b.y);
             }
         }
-        store_row(p.sum + row * p.ss, h);
+        store_row(p.sum + row * p.ss, h, lead);
+    }
+    if constexpr (!kVec) {
+        uint32_t after[kVecs][4];
+        neighbours(Bool<true>(), h, after);
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v) {
+            uint32_t mine[4];
+            row_dev::take8(h[v], after[v], lead, mine);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) h[v][c] = mine[c];
+        }
     }
     float s = 0.f;
 #pragma unroll
@@ -119,7 +148,7 @@ __global__ void __launch_bounds__(kThreads < 256 ? 256 : kThreads) rms_norm(cons
     const float r = 1.f / sqrtf(s / static_cast<float>(p.d) + p.eps);
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
-        const int i = (v * kThreads + t) * 8;
+        const int i = at(v, 0);
         uint32_t w[4];
         row_dev::load8<kVec>(p.weight, i, p.d, w);
         float y[8];
@@ -149,7 +178,7 @@ __global__ void __launch_bounds__(kThreads < 256 ? 256 : kThreads) rms_norm(cons
         }
     }
     if (p.y) {
-        if (!kVec) store_row(p.y + row * p.sy, h);
+        if (!kVec) store_row(p.y + row * p.sy, h, 0);
     } else {   // the scale tiles' padding: blocks past the row's, rows past the last
         const int64_t blocks = (p.d + 127) >> 7;
         if (in && t < 4 * p.kt - blocks) p.scales[fp8_dev::scale_at(row, blocks + t, p.kt)] = 0;

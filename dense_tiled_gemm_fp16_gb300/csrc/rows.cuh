@@ -30,6 +30,11 @@ __device__ __forceinline__ void load8(const uint16_t* row, int64_t i, int64_t d,
         const uintptr_t at = reinterpret_cast<uintptr_t>(row + i);
         const int o = static_cast<int>(at & 15u);
         const uint4* p = reinterpret_cast<const uint4*>(at - o);
+        if (o == 0 && hi - lo == 8) {
+            const uint4 v = *p;
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+            return;
+        }
         uint32_t t[8] = {};
         if (2 * lo + o < 16) {
             const uint4 a = p[0];
@@ -70,18 +75,11 @@ __device__ __forceinline__ void store8(uint16_t* row, int64_t i, int64_t d, cons
         store_some(row + i, w, i < 0 ? static_cast<int>(-i) : 0, static_cast<int>(min(static_cast<int64_t>(8), d - i)));
 }
 
-// The values that end in a row's boundary from those that begin at multiples of eight:
-// with `o` the row's lead, the last o of the eight before (`prev`) and the first 8 - o
-// of these.
-__device__ __forceinline__ void shift8(const uint32_t* prev, const uint32_t* w, int o, uint32_t* out)
+// Eight values from `o` on (0 to 7) of the sixteen in a and b.
+__device__ __forceinline__ void take8(const uint32_t* a, const uint32_t* b, int o, uint32_t* out)
 {
-    const uint32_t in[8] = {prev[0], prev[1], prev[2], prev[3], w[0], w[1], w[2], w[3]};
-    if (o == 0) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) out[c] = w[c];
-    } else {
-        funnel16(in, 16 - 2 * o, out);
-    }
+    const uint32_t in[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    funnel16(in, 2 * o, out);
 }
 
 // The two values of a word in fp32, and back with one rounding.
