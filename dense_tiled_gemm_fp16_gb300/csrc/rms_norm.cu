@@ -13,37 +13,33 @@ namespace {
 
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-template <typename T, int kThreads, int kVecs, bool kBoth = true>   // kBoth: aligned rows come here, too
-gemm_f16_status launch(const norm_dev::Params& p, bool vec, cudaStream_t stream)
+template <typename T, int kMost, int kVecs>
+gemm_f16_status launch(const norm_dev::Params& p, bool vec, int threads, cudaStream_t stream)
 {
-    constexpr int kBlock = kThreads < 256 ? 256 : kThreads;
-    const int64_t blocks = cdiv(p.rows, kBlock / kThreads);
+    const int64_t blocks = kMost == 256 ? cdiv(p.rows, kMost / 32) : p.rows;
     if (blocks > INT32_MAX) return GEMM_F16_ERR_INVALID_VALUE;
-    auto kernel = norm_dev::rms_norm<T, kThreads, kVecs, false>;
-    if constexpr (kBoth)
-        if (vec) kernel = norm_dev::rms_norm<T, kThreads, kVecs, true>;
-    return launch_kernel(kernel, dim3(static_cast<unsigned>(blocks)), kBlock, 0, 1, stream, p);
+    return launch_kernel(vec ? norm_dev::rms_norm<T, kMost, kVecs, true> : norm_dev::rms_norm<T, kMost, kVecs, false>,
+                         dim3(static_cast<unsigned>(blocks)), static_cast<unsigned>(threads), 0, 1, stream, p);
 }
 
 template <typename T>
 gemm_f16_status choose(const norm_dev::Params& p, bool vec, int sms, cudaStream_t stream)
 {
-    // As many threads as leave few of them without values; of more than 1024 values a row
-    // takes whole blocks.
     const int64_t d = p.d + (vec ? 0 : 7);   // (a row that starts up to 7 values past a boundary)
-    if (d <= 256) return launch<T, 32, 1>(p, vec, stream);
-    if (d <= 512) return launch<T, 32, 2>(p, vec, stream);
-    if (d <= 1024) return launch<T, 32, 4>(p, vec, stream);
-    // a row that would be most of a block's time: more threads on it
-    if (p.rows <= sms && d > 2048 && d <= 8192) return launch<T, 1024, 1>(p, vec, stream);
-    if (d <= 2048) return launch<T, 256, 1>(p, vec, stream);
-    if (d <= 4096) return launch<T, 256, 2>(p, vec, stream);
-    if (d <= 6144) return launch<T, 256, 3>(p, vec, stream);
-    if (d <= 8192) return launch<T, 256, 4>(p, vec, stream);
-    if (d <= 12288) return launch<T, 512, 3>(p, vec, stream);
-    if (d <= 16384) return launch<T, 512, 4>(p, vec, stream);
-    if (d <= 32768) return launch<T, 1024, 4>(p, vec, stream);
-    return launch<T, 1024, 5, false>(p, vec, stream);
+    if (d <= 256) return launch<T, 256, 1>(p, vec, 256, stream);
+    if (d <= 512) return launch<T, 256, 2>(p, vec, 256, stream);
+    if (d <= 1024) return launch<T, 256, 4>(p, vec, 256, stream);
+    auto threads = [&](int vecs) { return static_cast<int>(cdiv(d, 256 * vecs) * 32); };
+    // few rows: as many threads as a row has work for
+    if (p.rows <= sms && threads(1) <= 1024) return launch<T, 1024, 1>(p, vec, threads(1), stream);
+    // otherwise 2 to 4 times 8 values a thread, whichever leaves the fewest without
+    int vecs = 4;
+    for (int v = 3; v >= 2; --v)
+        if (v * threads(v) < vecs * threads(vecs)) vecs = v;
+    if (threads(4) > 288) return launch<T, 832, 5>(p, vec, threads(5), stream);
+    return vecs == 4   ? launch<T, 288, 4>(p, vec, threads(4), stream)
+           : vecs == 3 ? launch<T, 384, 3>(p, vec, threads(3), stream)
+                       : launch<T, 576, 2>(p, vec, threads(2), stream);
 }
 
 }  // namespace

@@ -4,7 +4,7 @@
 //   y = h / sqrt(mean(h^2) + eps) * weight, rounded once, to their type or to 8 bits
 //
 // Bound by HBM: a row is read once, kept in registers over the sum of its squares
-// (fp32: eight values a lane in order, then a tree), and written once.  Sixteen lanes
+// (fp32), and written once.  Sixteen lanes
 // hold a block of 128 values, so the 8-bit form's scales are four shuffles away.
 #pragma once
 
@@ -29,17 +29,18 @@ struct Params {
     float eps;
 };
 
-// A row takes kThreads threads of kVecs x 8 values each; a block of 256 threads (or
-// more, where a row takes more) has 256 / kThreads rows.
-template <typename T, int kThreads, int kVecs, bool kVec>
-__global__ void __launch_bounds__(kThreads < 256 ? 256 : kThreads) rms_norm(const Params p)
+// kMost 256: a warp a row, eight rows a block.  Otherwise a block of at most kMost threads
+// a row.  A thread takes kVecs times 8 values.
+template <typename T, int kMost, int kVecs, bool kVec>
+__global__ void __launch_bounds__(kMost) rms_norm(const Params p)
 {
-    constexpr int kBlock = kThreads < 256 ? 256 : kThreads, kWarps = kThreads / 32;
-    __shared__ float part[kBlock / 32];
-    __shared__ uint4 edge[kVec ? 1 : kVecs * kBlock / 32];
-    const int t = threadIdx.x % kThreads;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kBlock / kThreads) + threadIdx.x / kThreads;
-    const bool in = row < p.rows;   // (of whole warps, and of whole blocks where a row takes more than one)
+    constexpr bool kWarpRow = kMost == 256;
+    __shared__ float part[kVecs * kMost / 32];
+    __shared__ uint4 edge[kVec ? 1 : kVecs * kMost / 32];
+    const int threads = kWarpRow ? 32 : blockDim.x, warps = kWarpRow ? 1 : threads >> 5;
+    const int t = kWarpRow ? threadIdx.x & 31 : threadIdx.x;
+    const int64_t row = kWarpRow ? static_cast<int64_t>(blockIdx.x) * (kMost / 32) + (threadIdx.x >> 5) : blockIdx.x;
+    const bool in = row < p.rows;   // (of whole warps; a block's row always is)
     const int64_t d = in ? p.d : 0;
     griddep_wait();
     griddep_launch_dependents();
@@ -49,27 +50,27 @@ __global__ void __launch_bounds__(kThreads < 256 ? 256 : kThreads) rms_norm(cons
     // Then the values move to their multiples of eight, so that the sum of squares has
     // one order wherever the rows lie, and y's go back on their way out.
     const int lead = kVec ? 0 : row_dev::lead_of(p.x + row * p.sx);
-    auto at = [&](int v, int before) { return (v * kThreads + t) * 8 - before; };
+    auto at = [&](int v, int before) { return (v * threads + t) * 8 - before; };
 
     // The values' neighbours: of the thread before (kNext: after), of a warp's end through
     // shared memory.  By all threads of a row.
     auto neighbours = [&](auto next, uint32_t (&w)[kVecs][4], uint32_t (&n)[kVecs][4]) {
         constexpr bool kNext = decltype(next)::value;
-        const int lane = threadIdx.x & 31, first = (threadIdx.x / kThreads) * kVecs * kWarps;   // of this row's edges
-        if (kWarps > 1) __syncthreads();   // (the last edges have been read)
+        const int lane = threadIdx.x & 31, first = kWarpRow ? (threadIdx.x >> 5) * kVecs : 0;   // of this row's edges
+        if (!kWarpRow) __syncthreads();   // (the last edges have been read)
         if (lane == (kNext ? 0 : 31))
 #pragma unroll
             for (int v = 0; v < kVecs; ++v)
-                edge[first + v * kWarps + (t >> 5)] = make_uint4(w[v][0], w[v][1], w[v][2], w[v][3]);
-        if (kWarps > 1) __syncthreads();
-        else __syncwarp();
+                edge[first + v * warps + (t >> 5)] = make_uint4(w[v][0], w[v][1], w[v][2], w[v][3]);
+        if (kWarpRow) __syncwarp();
+        else __syncthreads();
 #pragma unroll
         for (int v = 0; v < kVecs; ++v) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) n[v][c] = kNext ? __shfl_down_sync(~0u, w[v][c], 1) : __shfl_up_sync(~0u, w[v][c], 1);
             if (lane == (kNext ? 31 : 0)) {
-                const int e = v * kWarps + (t >> 5) + (kNext ? 1 : -1);
-                const uint4 x = e >= 0 && e < kVecs * kWarps ? edge[first + e] : make_uint4(0u, 0u, 0u, 0u);
+                const int e = v * warps + (t >> 5) + (kNext ? 1 : -1);
+                const uint4 x = e >= 0 && e < kVecs * warps ? edge[first + e] : make_uint4(0u, 0u, 0u, 0u);
                 n[v][0] = x.x, n[v][1] = x.y, n[v][2] = x.z, n[v][3] = x.w;
             }
         }
@@ -93,7 +94,7 @@ __global__ void __launch_bounds__(kThreads < 256 ? 256 : kThreads) rms_norm(cons
                 const int i = at(v, from);
                 row_dev::store8<false>(out, i - o, d, mine);
                 // the last o of the last thread, where the row goes on to there
-                if (v == kVecs - 1 && t == kThreads - 1 && i + 8 - o < d)
+                if (v == kVecs - 1 && t == threads - 1 && i + 8 - o < d)
                     row_dev::store_some(out + i, w[v], 8 - o, static_cast<int>(min(static_cast<int64_t>(8), d - i)));
             }
         }
@@ -127,23 +128,32 @@ __global__ void __launch_bounds__(kThreads < 256 ? 256 : kThreads) rms_norm(cons
             for (int c = 0; c < 4; ++c) h[v][c] = mine[c];
         }
     }
-    float s = 0.f;
+    // One order for every form and place: 256 values, eight a lane, by a warp's tree, then
+    // the sums of all such chunks by a tree over 32 lanes.
+    float s = 0.f, chunk[kVecs];
 #pragma unroll
-    for (int v = 0; v < kVecs; ++v)
+    for (int v = 0; v < kVecs; ++v) {
+        chunk[v] = 0.f;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             const float2 a = row_dev::widen2<T>(h[v][c]);
-            s = fmaf(a.x, a.x, s);
-            s = fmaf(a.y, a.y, s);
+            chunk[v] = fmaf(a.x, a.x, chunk[v]);
+            chunk[v] = fmaf(a.y, a.y, chunk[v]);
         }
 #pragma unroll
-    for (int k = 16; k; k /= 2) s += __shfl_xor_sync(~0u, s, k);
-    if (kWarps > 1) {
-        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
-        __syncthreads();
-        s = part[(threadIdx.x & 31) % kWarps];
+        for (int k = 16; k; k /= 2) chunk[v] += __shfl_xor_sync(~0u, chunk[v], k);
+    }
+    if constexpr (kWarpRow) {
+        s = kVecs == 4 ? (chunk[0] + chunk[kVecs / 2]) + (chunk[1 % kVecs] + chunk[3 % kVecs])
+                       : kVecs == 2 ? chunk[0] + chunk[1 % kVecs] : chunk[0];
+    } else {
+        if ((t & 31) == 0)
 #pragma unroll
-        for (int k = kWarps / 2; k; k /= 2) s += __shfl_xor_sync(~0u, s, k);
+            for (int v = 0; v < kVecs; ++v) part[v * warps + (t >> 5)] = chunk[v];
+        __syncthreads();
+        for (int k = t & 31; k < kVecs * warps; k += 32) s += part[k];
+#pragma unroll
+        for (int k = 16; k; k /= 2) s += __shfl_xor_sync(~0u, s, k);
     }
     const float r = 1.f / sqrtf(s / static_cast<float>(p.d) + p.eps);
 #pragma unroll
@@ -184,7 +194,7 @@ __global__ void __launch_bounds__(kThreads < 256 ? 256 : kThreads) rms_norm(cons
         if (in && t < 4 * p.kt - blocks) p.scales[fp8_dev::scale_at(row, blocks + t, p.kt)] = 0;
         if (row == p.rows - 1) {
             const int kt = static_cast<int>(p.kt), words = static_cast<int>(p.row_tiles * 128 - p.rows) * kt;
-            for (int q = t; q < words; q += kThreads)
+            for (int q = t; q < words; q += threads)
                 *reinterpret_cast<uint32_t*>(p.scales + fp8_dev::scale_at(p.rows + q / kt, 4 * (q % kt), p.kt)) = 0u;
         }
     }
