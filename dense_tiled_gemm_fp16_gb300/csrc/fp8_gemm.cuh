@@ -364,8 +364,8 @@ __global__ void __launch_bounds__(kTileThreads) gemm_fp8_tile(const __grid_const
 // the other by turns, so that a thread of the epilogue holds both values of an output.
 constexpr int kMaxStages = 10, kSets = 4, kMaxGroups = 512;
 constexpr int kPairThreads = 320 + 32 * kSets;   // warps 0-7 epilogue, 8 loads, 9 MMA, the others scales
-constexpr uint32_t kSlotBytes = 12 * kABytes, kSetBytes = 3 * kScaleTile, kBoxBytes = 32 * 64;   // kSlotBytes: all stages
-constexpr uint32_t kPairSmem = kSlotBytes + 8 * kBoxBytes + kSets * kSetBytes + 1024;
+constexpr uint32_t kSlotBytes = 6 * (kABytes + 64 * 224), kSetBytes = 3 * kScaleTile, kBoxBytes = 32 * 64;   // kSlotBytes: all stages
+constexpr uint32_t kPairSmem = kSlotBytes + 16 * kBoxBytes + kSets * kSetBytes + 1024;
 constexpr int kMaxWidth = 224, kOneWidth = 256; // columns of a tile; of a cluster's only one
 constexpr uint32_t kSfCol = 496, kAcc1 = 256;   // scales of the weights (4), of A (8); the second accumulator
 
@@ -567,18 +567,15 @@ __device__ __forceinline__ Tile place(const PairParams& p, const Groups& g, int 
 
 // 16 lanes x 32 columns: of 8 columns each, registers 0 and 1 hold row lane / 4, columns
 // 2 (lane % 4) and the next, registers 2 and 3 the row 8 further.
-__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, float* v)
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, float* r)
 {
-    uint32_t r[16];
     asm volatile(
         "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
         : "r"(taddr)
         : "memory");
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // Four 8 x 8 matrices of 16-bit values, each stored transposed: lane 8 i + j gives the
@@ -618,7 +615,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
     auto sfull = [&](int s) { return bar0 + 16u * (kMaxStages + s); };
     auto sempty = [&](int s) { return bar0 + 16u * (kMaxStages + s) + 8u; };
     const uint32_t tfull = bar0 + 16u * (kMaxStages + kSets), tempty = tfull + 16u, never = tempty + 16u, drain = never + 8u;
-    const uint32_t boxes = base + kSlotBytes, sets = boxes + 8 * kBoxBytes;
+    const uint32_t boxes = base + kSlotBytes, sets = boxes + 16 * kBoxBytes;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kMaxStages; ++s) {
@@ -836,7 +833,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
         // ones, 4-7 the odd ones; a warp's lanes are the weight rows 32 (warp % 4) on
         const int half = warp >> 2;
         const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        const uint32_t box = boxes + warp * kBoxBytes, leader_empty = mapa_shared(tempty, 0);
+        const uint32_t box0 = boxes + warp * 2 * kBoxBytes, leader_empty = mapa_shared(tempty, 0);
+        uint32_t turn = 0;
         int acc = 0;
         uint32_t tpar = 0;
         for (int t = blockIdx.x >> 1; t < tiles; t += clusters) {
@@ -858,19 +856,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
             tc_fence_after();
             const uint32_t d = trow + (acc ? kAcc1 : 0u);
             const int chunks = o.width >> 5;
-#pragma unroll 1
-            for (int b = half; b < chunks; b += 2) {
-                float v[32];
+            auto load = [&](int b, float* v) {
                 tmem_ld_16x256b_x4(d + b * 32, v);
                 tmem_ld_16x256b_x4(d + b * 32 + (16u << 16), v + 16);
-                tmem_wait_ld();
-                if (b + 2 >= chunks) {   // the accumulator's columns are read
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster_relaxed(leader_empty + 8 * acc);
-                }
+            };
+            auto finish = [&](int b, float* v) {
                 const int left = o.rows - b * 32;   // rows of C among the 32
-                if (left <= 0 || n0 >= p.n) continue;
+                if (left <= 0 || n0 >= p.n) return;
+                const uint32_t box = box0 + (turn ^= kBoxBytes);
                 if (kGated) {
                     act_all<16>(p.act, v);
 #pragma unroll
@@ -882,7 +875,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
                 }
                 // to the box as rows of C: row tok at tok * 2 kN, its 16-byte parts shifted as TMA's
                 // swizzles have it, so that eight rows fall on different banks
-                if (lane == 0) bulk_wait_group_read<0>();   // the box's last store has read it
+                if (lane == 0) bulk_wait_group_read<1>();   // the box's last store, the one before last, has read it
                 __syncwarp();
                 auto part = [&](int tok, int c) {
                     return box + tok * (2 * kN) + ((c ^ (kGated ? (tok >> 2) & 1 : (tok >> 1) & 3)) << 4);
@@ -905,7 +898,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
                         tma_store_2d_l2(&p.tmC, box, static_cast<int32_t>(n0), o.row + b * 32, 1);
                         bulk_commit_group();
                     }
-                    continue;
+                    return;
                 }
                 __syncwarp();
                 uint16_t* to = p.C + (static_cast<int64_t>(o.row) + b * 32) * p.ldc + n0;
@@ -924,6 +917,20 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
                     }
                 }
                 __syncwarp();
+            };
+#pragma unroll 1
+            for (int b = half; b < chunks; b += 4) {   // twice 32 columns for one wait
+                float v[32], w[32];
+                load(b, v);
+                if (b + 2 < chunks) load(b + 2, w);
+                tmem_wait_ld();
+                if (b + 4 >= chunks) {   // the accumulator's columns are read
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster_relaxed(leader_empty + 8 * acc);
+                }
+                finish(b, v);
+                if (b + 2 < chunks) finish(b + 2, w);
             }
             if (half >= chunks && lane == 0) mbar_arrive_cluster_relaxed(leader_empty + 8 * acc);
             if (acc) tpar ^= 1u;
