@@ -643,13 +643,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
         tmem_relinquish_pair();
     }
     griddep_wait();
-    griddep_launch_dependents();
     const int clusters = gridDim.x >> 1;
     if (warp == 0) choose_tiles(p, groups, clusters, lane);
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();
     tc_fence_after();
+    griddep_launch_dependents();   // (this CTA has its tensor memory)
     const uint32_t tmem = tmem_slot;
     const int tiles = __shfl_sync(~0u, groups.tile0[p.groups], 0);
     // as many stages as fit: a tile of few columns brings little for its 16 KB of weights
