@@ -8,6 +8,7 @@
 // hold a block of 128 values, so the 8-bit form's scales are four shuffles away.
 #pragma once
 
+#include "activation.cuh"
 #include "fp8_format.cuh"
 #include "rows.cuh"
 
@@ -15,6 +16,19 @@ namespace norm_dev {
 
 using namespace gemm_f16_dev;
 using fp8_dev::Bool;
+
+using mxf4_dev::fma2;
+using mxf4_dev::mul2;
+using mxf4_dev::pack2;
+using mxf4_dev::unpack2;
+
+// The larger one, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 
 struct Params {
     const uint16_t* x;
@@ -31,8 +45,10 @@ struct Params {
 
 // kMost 256: a warp a row, eight rows a block.  Otherwise a block of at most kMost threads
 // a row.  A thread takes kVecs times 8 values.
+// (At least three blocks of the largest an SM for rows that start anywhere, three times
+// eight values a thread: 32768 x 4097 in bf16 with a residual 233 us, 276 without.)
 template <typename T, int kMost, int kVecs, bool kVec>
-__global__ void __launch_bounds__(kMost) rms_norm(const Params p)
+__global__ void __launch_bounds__(kMost, kVecs == 3 && !kVec ? 3 : 0) rms_norm(const Params p)
 {
     constexpr bool kWarpRow = kMost == 256;
     __shared__ float part[kVecs * kMost / 32];
@@ -110,10 +126,7 @@ __global__ void __launch_bounds__(kMost) rms_norm(const Params p)
 #pragma unroll
         for (int v = 0; v < kVecs; ++v) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float2 a = row_dev::widen2<T>(h[v][c]), b = row_dev::widen2<T>(r[v][c]);
-                h[v][c] = row_dev::narrow2<T>(a.x + b.x, a.y + b.y);
-            }
+            for (int c = 0; c < 4; ++c) h[v][c] = row_dev::add2<T>(h[v][c], r[v][c]);
         }
         store_row(p.sum + row * p.ss, h, lead);
     }
@@ -128,18 +141,21 @@ __global__ void __launch_bounds__(kMost) rms_norm(const Params p)
             for (int c = 0; c < 4; ++c) h[v][c] = mine[c];
         }
     }
-    // One order for every form and place: 256 values, eight a lane, by a warp's tree, then
-    // the sums of all such chunks by a tree over 32 lanes.
+    // One order for every form and place: 256 values, eight a lane (even and odd ones apart),
+    // by a warp's tree, then the sums of all such chunks by a tree over 32 lanes.
     float s = 0.f, chunk[kVecs];
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
-        chunk[v] = 0.f;
+        uint64_t two = 0;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             const float2 a = row_dev::widen2<T>(h[v][c]);
-            chunk[v] = fmaf(a.x, a.x, chunk[v]);
-            chunk[v] = fmaf(a.y, a.y, chunk[v]);
+            const uint64_t both = pack2(a.x, a.y);
+            two = fma2(both, both, two);
         }
+        float even, odd;
+        unpack2(two, &even, &odd);
+        chunk[v] = even + odd;
 #pragma unroll
         for (int k = 16; k; k /= 2) chunk[v] += __shfl_xor_sync(~0u, chunk[v], k);
     }
@@ -165,23 +181,31 @@ __global__ void __launch_bounds__(kMost) rms_norm(const Params p)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             const float2 a = row_dev::widen2<T>(h[v][c]), b = row_dev::widen2<T>(w[c]);
-            y[2 * c] = a.x * r * b.x, y[2 * c + 1] = a.y * r * b.y;
+            unpack2(mul2(mul2(pack2(a.x, a.y), pack2(r, r)), pack2(b.x, b.y)), &y[2 * c], &y[2 * c + 1]);
         }
         if (p.y) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) h[v][c] = row_dev::narrow2<T>(y[2 * c], y[2 * c + 1]);
             if (kVec) row_dev::store8<true>(p.y + row * p.sy, i, d, h[v]);
         } else {
-            uint32_t top = 0;
+            if (i + 8 > p.d) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                if (i + c >= p.d) y[c] = 0.f;   // (an infinite r times nothing)
-                top = max(top, __float_as_uint(y[c]) & 0x7FFFFFFFu);
+                for (int c = 0; c < 8; ++c)
+                    if (i + c >= p.d) y[c] = 0.f;   // (an infinite r times nothing)
             }
+            float top = 0.f;
 #pragma unroll
-            for (int k = 1; k < 16; k *= 2) top = max(top, __shfl_xor_sync(~0u, top, k));
-            const uint32_t code = fp8_dev::scale_code<float>(top);
-            const uint2 q = fp8_dev::codes8<float>(reinterpret_cast<const uint32_t*>(y), code);
+            for (int c = 0; c < 8; ++c) top = max_nan(top, fabsf(y[c]));
+#pragma unroll
+            for (int k = 1; k < 16; k *= 2) top = max_nan(top, __shfl_xor_sync(~0u, top, k));
+            const uint32_t code = fp8_dev::scale_code_f32(top);
+            uint2 q = make_uint2(0u, 0u);
+            if (code != 255u) {
+                const float f = fp8_dev::inverse_scale(code);
+#pragma unroll
+                for (int c = 0; c < 8; c += 2) unpack2(mul2(pack2(y[c], y[c + 1]), pack2(f, f)), &y[c], &y[c + 1]);
+                q = make_uint2(fp8_dev::e4m3_of(y[0], y[1], y[2], y[3]), fp8_dev::e4m3_of(y[4], y[5], y[6], y[7]));
+            }
             if (in && i + 8 <= p.pitch) *reinterpret_cast<uint2*>(p.codes + row * p.pitch + i) = q;
             if (in && (t & 15) == 0 && i < p.d)
                 p.scales[fp8_dev::scale_at(row, i >> 7, p.kt)] = static_cast<uint8_t>(code);

@@ -89,6 +89,18 @@ __device__ __forceinline__ float2 widen2(uint32_t w)
     return make_float2(Elem<T>::to_f32(w & 0xFFFFu), Elem<T>::to_f32(w >> 16));
 }
 
+// The sum of two such pairs, rounded once.
+template <typename T>
+__device__ __forceinline__ uint32_t add2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    if constexpr (Elem<T>::kInf == 0x7C00u)
+        asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else
+        asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 template <typename T>
 __device__ __forceinline__ uint32_t narrow2(float a, float b);
 template <>
