@@ -1,5 +1,6 @@
 // Quantisation to 8 bits and its inverse: streaming kernels, bound by HBM (2 or 4
-// bytes a value in, 1 + 1/128 out, and back).
+// bytes a value in, 1 + 1/128 out, and back; the inverse of 131072 x 7168 to fp16 takes 409
+// us, 6.9 TB/s).
 //
 // A block of threads takes a tile of 128 rows x 512 values: whole 512-byte scale
 // tiles, put together in shared memory, and whole 128-byte lines of codes.
@@ -27,10 +28,16 @@ struct QuantParams {
 // scales make one word.  Rows of a scale tile that another block of threads takes
 // (tile_rows < 128) are left to it; the one with the matrix's last row also writes the
 // padding rows' scales.
+//
+// One row at a time and full occupancy keep more loads under way than several rows and
+// less of it: 131072 x 7168 in fp16 565 us with four rows a warp, 445 with two, 409 so
+// (6.9 TB/s); fp32 has the bytes under way with half the occupancy (32768 x 7168: 175 us,
+// 6.7 TB/s).  Rows that start anywhere, 32768 x 4097 in bf16: 89 us (4.5 TB/s), by the second
+// load and the shift of every 16 bytes.
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kConvThreads) quantize_rows(const QuantParams p)
+__global__ void __launch_bounds__(kConvThreads, sizeof(T) == 4 ? 4 : 8) quantize_rows(const QuantParams p)
 {
-    constexpr int kUnroll = sizeof(T) == 4 ? 1 : 2, kWarps = kConvThreads / 32;
+    constexpr int kWarps = kConvThreads / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t parts = (p.rows + p.tile_rows - 1) / p.tile_rows;
     const int64_t ct = blockIdx.x / parts, part = blockIdx.x - ct * parts;
@@ -45,36 +52,25 @@ __global__ void __launch_bounds__(kConvThreads) quantize_rows(const QuantParams 
     auto rows = [&](auto whole) {   // whole: no value of the tile is past the row's end
         constexpr bool kWhole = decltype(whole)::value;
 #pragma unroll 1
-        for (int64_t r = r0 + warp; r < end; r += kWarps * kUnroll) {
-            uint32_t w[kUnroll][2][8 * sizeof(T) / 4];
+        for (int64_t r = r0 + warp; r < end; r += kWarps) {
+            uint32_t w[2][8 * sizeof(T) / 4], word = 0;
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const T* row = x + (r + u * kWarps) * p.sr;
-                const int k = r + u * kWarps < end ? n : 0;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    mxf4_dev::load8<T, kVec>(row, i + 256 * h, k, w[u][h]);
-                    if (!kWhole && i + 256 * h + 8 > k) mxf4_dev::mask_tail<T>(w[u][h], k - i - 256 * h);
-                }
+            for (int h = 0; h < 2; ++h) {
+                mxf4_dev::load8<T, kVec>(x + r * p.sr, i + 256 * h, n, w[h]);
+                if (!kWhole && i + 256 * h + 8 > n) mxf4_dev::mask_tail<T>(w[h], n - i - 256 * h);
             }
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int64_t row = r + u * kWarps;
-                if (row >= end) break;
-                uint32_t word = 0;
+            for (int h = 0; h < 2; ++h) {
+                uint32_t top = mxf4_dev::top_bits<T>(w[h]);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t top = mxf4_dev::top_bits<T>(w[u][h]);
-#pragma unroll
-                    for (int d = 1; d < 16; d *= 2) top = max(top, __shfl_xor_sync(~0u, top, d));
-                    const bool some = kWhole || ((i + 256 * h) & ~(kBlock - 1)) < n;
-                    const uint32_t code = some ? scale_code<T>(top) : 0u;
-                    const uint2 c = codes8<T>(w[u][h], code);
-                    if (kWhole || i + 256 * h + 8 <= p.pitch) *reinterpret_cast<uint2*>(codes + row * p.pitch + i + 256 * h) = c;
-                    word |= (code | __shfl_xor_sync(~0u, code, 16) << 8) << (16 * h);
-                }
-                if (lane == 0) *reinterpret_cast<uint32_t*>(scales + scale_at(row, 4 * ct, p.kt)) = word;
+                for (int d = 1; d < 16; d *= 2) top = max(top, __shfl_xor_sync(~0u, top, d));
+                const bool some = kWhole || ((i + 256 * h) & ~(kBlock - 1)) < n;
+                const uint32_t code = some ? scale_code<T>(top) : 0u;
+                const uint2 c = codes8<T>(w[h], code);
+                if (kWhole || i + 256 * h + 8 <= p.pitch) *reinterpret_cast<uint2*>(codes + r * p.pitch + i + 256 * h) = c;
+                word |= (code | __shfl_xor_sync(~0u, code, 16) << 8) << (16 * h);
             }
+            if (lane == 0) *reinterpret_cast<uint32_t*>(scales + scale_at(r, 4 * ct, p.kt)) = word;
         }
     };
     if ((ct + 1) * kTileVals <= p.k)
