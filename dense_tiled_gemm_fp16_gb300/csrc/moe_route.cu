@@ -194,8 +194,16 @@ gemm_f16_status moe_combine(const void* y, int dtype, int64_t stride_y, const in
     p.sx = stride_y, p.so = stride_out, p.tokens = tokens, p.d = d, p.places = n;
     const bool vec = d % 8 == 0 && takes_vectors(y, stride_y) && takes_vectors(out, stride_out), half = dtype == FP8_F16;
     p.top = static_cast<int32_t>(top_k), p.chunks = chunks_of(d, vec);
-    return launch_rows(half ? (vec ? route_dev::combine_rows<__half, true> : route_dev::combine_rows<__half, false>)
-                            : (vec ? route_dev::combine_rows<__nv_bfloat16, true> : route_dev::combine_rows<__nv_bfloat16, false>),
+    auto kernel = [&](auto type, auto vectors) {
+        using T = decltype(type);
+        constexpr bool kVec = decltype(vectors)::value;
+        return top_k <= 2   ? route_dev::combine_rows<T, kVec, 2>
+               : top_k <= 4 ? route_dev::combine_rows<T, kVec, 4>
+                            : route_dev::combine_rows<T, kVec, 8>;
+    };
+    using fp8_dev::Bool;
+    return launch_rows(half ? (vec ? kernel(__half(), Bool<true>()) : kernel(__half(), Bool<false>()))
+                            : (vec ? kernel(__nv_bfloat16(), Bool<true>()) : kernel(__nv_bfloat16(), Bool<false>())),
                        p, tokens * p.chunks, stream);
 }
 
@@ -221,9 +229,16 @@ gemm_f16_status moe_combine_grad(const void* dout, int dtype, int64_t stride_dou
     p.top = static_cast<int32_t>(top_k);
     const bool vec = d % 8 == 0 && takes_vectors(dout, stride_dout) && takes_vectors(y, stride_y) && takes_vectors(dy, stride_dy);
     const bool half = dtype == FP8_F16;
-    return launch_rows(half ? (vec ? route_dev::combine_grad_rows<__half, true> : route_dev::combine_grad_rows<__half, false>)
-                            : (vec ? route_dev::combine_grad_rows<__nv_bfloat16, true>
-                                   : route_dev::combine_grad_rows<__nv_bfloat16, false>),
+    auto kernel = [&](auto type, auto vectors) {
+        using T = decltype(type);
+        constexpr bool kVec = decltype(vectors)::value;   // (rows that start anywhere: two loads each)
+        return top_k <= 2           ? route_dev::combine_grad_rows<T, kVec, 2>
+               : top_k <= 4 || !kVec ? route_dev::combine_grad_rows<T, kVec, 4>
+                                     : route_dev::combine_grad_rows<T, kVec, kVec ? 8 : 4>;
+    };
+    using fp8_dev::Bool;
+    return launch_rows(half ? (vec ? kernel(__half(), Bool<true>()) : kernel(__half(), Bool<false>()))
+                            : (vec ? kernel(__nv_bfloat16(), Bool<true>()) : kernel(__nv_bfloat16(), Bool<false>())),
                        p, tokens, stream);
 }
 

@@ -48,6 +48,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_count(const SortParams p)
         p.counts[static_cast<int64_t>(blockIdx.x) * (p.experts + 1) + e] = count[e];
 }
 
+// Both kernels are latency: 131072 choices of 64 experts 3.5 + 8.6 us, 1024 by one block 6.
+//
 // The places.  Every block adds up the counts of all parts and of those before its own
 // (at most 152 of them), then goes through its choices 1024 at a time: a warp finds the
 // lanes of the same expert, and the warps' counts are added up in order.  One part
@@ -159,6 +161,7 @@ __device__ __forceinline__ int64_t place_of(const RowParams& p, int64_t t, int j
 // A token's row is read once and written to each of its places: the other way round, by
 // place, the rows would be read top times from a matrix that L2 does not hold.  Where
 // rows start anywhere a thread takes the values of 16 aligned bytes of each place's row.
+// 16384 tokens of 8 choices, 7168 values: 312 us (6.8 TB/s), 2049 values 159 us (3.8).
 template <bool kVec>
 __global__ void __launch_bounds__(kRowThreads) gather_rows(const RowParams p)
 {
@@ -178,9 +181,14 @@ __global__ void __launch_bounds__(kRowThreads) gather_rows(const RowParams p)
     }
 }
 
-// The sum is in the order of the choices, in fp32, rounded once.
-template <typename T, bool kVec>
-__global__ void __launch_bounds__(kRowThreads, 8) combine_rows(const RowParams p)
+// The sum is in the order of the choices, in fp32, rounded once.  kAtOnce: choices whose
+// rows are under way together, the more blocks an SM the fewer they are (16384 tokens of 2
+// choices of 4097 values: 94 us, 187 with room for eight).
+//
+// 16384 tokens of 8 choices, 7168 values: 309 us (6.8 TB/s); 2049 values, rows that start
+// anywhere, 238 us (2.5), by the second load and the shift of every 16 bytes.
+template <typename T, bool kVec, int kAtOnce>
+__global__ void __launch_bounds__(kRowThreads, kAtOnce == 8 ? 8 : kAtOnce == 4 ? 10 : 12) combine_rows(const RowParams p)
 {
     const int64_t t = blockIdx.x / p.chunks;
     uint16_t* out = p.out + t * p.so;
@@ -188,7 +196,6 @@ __global__ void __launch_bounds__(kRowThreads, 8) combine_rows(const RowParams p
     griddep_wait();
     griddep_launch_dependents();
     float s[8] = {};
-    constexpr int kAtOnce = 8;
     for (int j0 = 0; j0 < p.top; j0 += kAtOnce) {
         uint32_t v[kAtOnce][4];
         float f[kAtOnce];
@@ -216,11 +223,11 @@ __global__ void __launch_bounds__(kRowThreads, 8) combine_rows(const RowParams p
 
 // out[place(t, j)] = w[t, j] dy[t], dweights[t, j] = dy[t] . y[place(t, j)]; a choice
 // without a place has a weight's gradient of zero.  A block a token, so that the dot
-// products are added up in one order.
-template <typename T, bool kVec>
-__global__ void __launch_bounds__(kRowThreads, 5) combine_grad_rows(const RowParams p)
+// products are added up in one order.  16384 tokens of 8 choices, 7168 values: 579 us (6.9
+// TB/s); 2049 values 341 us (3.4).
+template <typename T, bool kVec, int kAtOnce>
+__global__ void __launch_bounds__(kRowThreads, kAtOnce == 8 ? 5 : kAtOnce == 4 ? 7 : 10) combine_grad_rows(const RowParams p)
 {
-    constexpr int kAtOnce = kVec ? 8 : 4;
     __shared__ float part[kRowThreads / 32][kAtOnce];
     const int64_t t = blockIdx.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
