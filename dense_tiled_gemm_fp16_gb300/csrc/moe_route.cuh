@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kRowThreads) gather_rows(const RowParams p)
 // 16384 tokens of 8 choices, 7168 values: 309 us (6.8 TB/s); 2049 values, rows that start
 // anywhere, 238 us (2.5), by the second load and the shift of every 16 bytes.
 template <typename T, bool kVec, int kAtOnce>
-__global__ void __launch_bounds__(kRowThreads, kAtOnce == 8 ? 8 : kAtOnce == 4 ? 10 : 12) combine_rows(const RowParams p)
+__global__ void __launch_bounds__(kRowThreads, kAtOnce == 8 ? 8 : kAtOnce == 4 ? 10 : kVec ? 12 : 14) combine_rows(const RowParams p)
 {
     const int64_t t = blockIdx.x / p.chunks;
     uint16_t* out = p.out + t * p.so;
