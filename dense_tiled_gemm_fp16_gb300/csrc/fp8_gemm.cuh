@@ -524,6 +524,16 @@ __device__ __forceinline__ void umma_commit_pair_mc_if(uint32_t on, uint32_t bar
         : "memory");
 }
 
+__device__ __forceinline__ void tma_store_2d_if(uint32_t on, const void* tmap, uint32_t src, int32_t x, int32_t y, uint64_t policy)
+{
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.global.shared::cta.bulk_group.L2::cache_hint [%0, {%1, %2}], [%3], %4;\n\t"
+        "@q cp.async.bulk.commit_group;\n\t}" ::"l"(reinterpret_cast<uint64_t>(tmap)),
+        "r"(x), "r"(y), "r"(src), "l"(policy), "r"(on)
+        : "memory");
+}
+
 // Whether the phase with the given parity is over, without waiting.
 __device__ __forceinline__ uint32_t mbar_test(uint32_t bar, uint32_t parity)
 {
@@ -556,7 +566,7 @@ __device__ __forceinline__ Tile place(const PairParams& p, const Groups& g, int 
     Tile o;
     o.group = group_of(p, g, t);
     const int r0 = g.row0[o.group], rows = g.row0[o.group + 1] - r0, all = p.panel * g.parts[o.group];
-    const int i = t - g.tile0[o.group], band = i / all, j = i - band * all;
+    const int i = t - g.tile0[o.group], band = i < all ? 0 : i / all, j = i - band * all;
     const int in_band = min(p.panel, p.tiles_w - band * p.panel), part = j / in_band;
     o.w = band * p.panel + (j - part * in_band);
     o.width = g.width[o.group];
@@ -834,18 +844,19 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
         const int half = warp >> 2;
         const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const uint32_t box0 = boxes + warp * 2 * kBoxBytes, leader_empty = mapa_shared(tempty, 0);
+        const uint64_t policy = l2_policy(1);   // C first out of L2: the operands stay
         uint32_t turn = 0;
         int acc = 0;
         uint32_t tpar = 0;
         for (int t = blockIdx.x >> 1; t < tiles; t += clusters) {
             const Tile o = place(p, groups, t);
             const int64_t n0 = static_cast<int64_t>(o.w * 2 + static_cast<int>(rank)) * kRows + (warp & 3) * kN;
-            float bias[4] = {};
+            uint16_t bias[4] = {};   // (as they are, so that nothing waits for them here)
             if (!kGated && p.bias) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int64_t n = n0 + 8 * i + (lane >> 2);
-                    if (n < p.n) bias[i] = widen(p.bias[n], p.bf16);
+                    if (n < p.n) bias[i] = ld_nc_u16(p.bias + n);
                 }
             }
             const bool ok = __all_sync(~0u, mbar_wait(tfull + 8 * acc, tpar, abort, p.timeout_ns));
@@ -869,8 +880,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
 #pragma unroll
                     for (int c = 0; c < 16; ++c) v[c] *= v[16 + c];
                 } else {
+                    if (p.bias) {
+                        float f[4];
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) v[c] += bias[2 * (c >> 4) + ((c >> 1) & 1)];
+                        for (int i = 0; i < 4; ++i) f[i] = widen(bias[i], p.bf16);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) v[c] += f[2 * (c >> 4) + ((c >> 1) & 1)];
+                    }
                     act_all(p.act, v);
                 }
                 // to the box as rows of C: row tok at tok * 2 kN, its 16-byte parts shifted as TMA's
@@ -893,11 +909,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
                 if (p.c_tma && left >= 32) {   // (TMA leaves out columns past C's, not rows past the group's)
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) {
-                        // (first out of L2: the operands stay)
-                        tma_store_2d_l2(&p.tmC, box, static_cast<int32_t>(n0), o.row + b * 32, 1);
-                        bulk_commit_group();
-                    }
+                    tma_store_2d_if(lane == 0, &p.tmC, box, static_cast<int32_t>(n0), o.row + b * 32, policy);
                     return;
                 }
                 __syncwarp();
