@@ -354,11 +354,9 @@ __global__ void __launch_bounds__(kTileThreads) gemm_fp8_tile(const __grid_const
 // then leaves out.  A's scales begin at any row, so a warp puts their words in the
 // order of the scale tiles as it loads them, one set for 512 values of k.
 //
-// At most 224 columns, so that two accumulators and the scales fit tensor memory (512
-// columns) side by side and a tile's MMAs follow the last one's without a pause: with
-// two of 256, which have to share some, 1200 cycles passed between them (a 256-wide
-// tile takes 512 cycles a step, one of 224 takes 448).  256 where no cluster has a second
-// tile.
+// Up to 224 columns two accumulators and the scales fit tensor memory (512 columns), and a
+// tile's MMAs follow the last one's without a pause.  Tiles of 256 columns have one, which
+// the epilogue reads before the next tile's MMAs begin.
 //
 // Gate/up (kGated): the 256 lanes hold 128 rows of either weight, 16 of one and 16 of
 // the other by turns, so that a thread of the epilogue holds both values of an output.
@@ -366,7 +364,7 @@ constexpr int kMaxStages = 10, kSets = 4, kMaxGroups = 512;
 constexpr int kPairThreads = 320 + 32 * kSets;   // warps 0-7 epilogue, 8 loads, 9 MMA, the others scales
 constexpr uint32_t kSlotBytes = 6 * (kABytes + 64 * 224), kSetBytes = 3 * kScaleTile, kBoxBytes = 32 * 64;   // kSlotBytes: all stages
 constexpr uint32_t kPairSmem = kSlotBytes + 16 * kBoxBytes + kSets * kSetBytes + 1024;
-constexpr int kMaxWidth = 224, kOneWidth = 256; // columns of a tile; of a cluster's only one
+constexpr int kMaxWidth = 256, kTwoWidth = 224; // columns of a tile; of one that has two accumulators
 constexpr uint32_t kSfCol = 496, kAcc1 = 256;   // scales of the weights (4), of A (8); the second accumulator
 
 struct PairParams {
@@ -401,12 +399,14 @@ struct Groups {
 __host__ __device__ inline int parts_of(int rows, int w) { return (rows + w - 1) / w; }
 __host__ __device__ inline int width_of(int rows, int parts) { return parts ? ((rows + parts - 1) / parts + 31) & ~31 : 0; }
 
-// What a turn of the clusters costs: a step of 128 values brings 16 KB of weights and 64
-// bytes a column to either CTA, at 64 bytes a cycle 256 + W cycles, which is more than its
-// 2 W cycles of MMA (measured: 321 cycles at W = 64, 376 at 128, 485 at 224).
-__host__ __device__ inline int64_t cost_of(int tiles, int widest, int clusters)
+// What the clusters' turns cost in cycles: a step of 128 values brings 16 KB of weights and
+// 64 bytes a column to either CTA, at 64 bytes a cycle 256 + W cycles, which is no less
+// than its 2 W cycles of MMA (measured: 321 cycles at W = 64, 376 at 128, 485 at 224), and a
+// tile costs some 600 more, with one accumulator 3000.
+__host__ __device__ inline int64_t cost_of(int tiles, int widest, int clusters, int steps)
 {
-    return static_cast<int64_t>((tiles + clusters - 1) / clusters) * (widest + 256);
+    const int turns = (tiles + clusters - 1) / clusters;
+    return turns * (static_cast<int64_t>(steps) * (widest + 256) + (widest > 224 && turns > 1 ? 3000 : 600));
 }
 
 // By one warp.  Counts below zero are taken as zero, rows past the matrix as absent.
@@ -447,7 +447,7 @@ __device__ __forceinline__ void choose_tiles(const PairParams& p, Groups& g, int
         tiles += __shfl_xor_sync(~0u, tiles, d);
         widest = max(widest, __shfl_xor_sync(~0u, widest, d));
     }
-    int64_t cost = w > kMaxWidth && tiles * p.tiles_w > clusters ? INT64_MAX : cost_of(tiles * p.tiles_w, widest, clusters) * 16 + (7 - (lane & 7));
+    int64_t cost = cost_of(tiles * p.tiles_w, widest, clusters, p.steps) * 16 + (7 - (lane & 7));
 #pragma unroll
     for (int d = 1; d < 8; d *= 2) cost = min(cost, __shfl_xor_sync(~0u, cost, d));
     const int width = p.width ? p.width : 32 * (8 - static_cast<int>(cost & 15));
@@ -665,6 +665,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
     // as many stages as fit: a tile of few columns brings little for its 16 KB of weights
     const uint32_t stage_bytes = kABytes + __shfl_sync(~0u, groups.widest, 0) * 64u;
     const int stages = static_cast<int>(min(kSlotBytes / stage_bytes, static_cast<uint32_t>(kMaxStages)));
+    const bool two = stage_bytes <= kABytes + kTwoWidth * 64u;   // accumulators
 
     const volatile int* abort = &abort_flag;
     auto fail = [&]() {
@@ -806,7 +807,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
                     // instructions are out: an answer takes some 100 cycles
                     uint32_t there = mbar_test(full(st), par);
                     if (fresh) there &= mbar_test(sfull(set), spar);
-                    if (last) there &= mbar_test(tempty + 8 * (acc ^ 1), tpar ^ 1u ^ acc);
+                    if (last && two) there &= mbar_test(tempty + 8 * (acc ^ 1), tpar ^ 1u ^ acc);
                     auto mma = [&](int q) {
                         umma_mxf8_pair_if(n32 > q ? issue : 0u, d, da + 2 * q, db + 2 * q, id, tsw, tsx, s > 0 || q > 0);
                     };
@@ -814,13 +815,15 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
                     // (what the next slot waits for hangs on earlier ones than this, and on the tile before)
                     if (last) {
                         t += clusters, width = next_width;
-                        if (acc) tpar ^= 1u;
-                        acc ^= 1;
+                        if (acc || !two) tpar ^= 1u;
+                        if (two) acc ^= 1;
                     }
-                    if (!__all_sync(~0u, there) && t < tiles) ok = ready(fresh, last);
+                    const bool one = last && !two;   // the accumulator's own tile has to end first
+                    if (!one && !__all_sync(~0u, there) && t < tiles) ok = ready(fresh, last);
                     mma(3);
                     umma_commit_pair_mc_if(issue, done, 0x3);
                     if (last) umma_commit_pair_mc_if(issue, over, 0x3);
+                    if (one && t < tiles) ok = ready(true, true);
                 };
                 int s = 0;
                 for (; s + 4 <= p.steps - 1 && ok; s += 4) {   // whole sets
@@ -945,8 +948,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
                 if (b + 2 < chunks) finish(b + 2, w);
             }
             if (half >= chunks && lane == 0) mbar_arrive_cluster_relaxed(leader_empty + 8 * acc);
-            if (acc) tpar ^= 1u;
-            acc ^= 1;
+            if (acc || !two) tpar ^= 1u;
+            if (two) acc ^= 1;
         }
         if (lane == 0) bulk_wait_group_all();
     }

@@ -218,11 +218,10 @@ gemm_f16_status launch_pair(const Product& q, const Device& dev, const Sizes& sa
     if (!q.groups) {
         const int rows = static_cast<int>(q.m);
         int64_t best = p.width ? 0 : INT64_MAX;
-        for (int w = fp8_dev::kOneWidth; w && best; w -= 32) {
+        for (int w = fp8_dev::kMaxWidth; w && best; w -= 32) {
             const int parts = fp8_dev::parts_of(rows, w);
-            if (w > fp8_dev::kMaxWidth && parts * tiles_w > clusters) continue;
             const int64_t cost = fp8_dev::cost_of(static_cast<int>(parts * tiles_w), fp8_dev::width_of(rows, parts),
-                                                  static_cast<int>(clusters));
+                                                  static_cast<int>(clusters), p.steps);
             if (cost < best) best = cost, p.width = w;
         }
         p.width = fp8_dev::width_of(rows, fp8_dev::parts_of(rows, p.width));
