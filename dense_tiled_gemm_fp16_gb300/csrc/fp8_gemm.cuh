@@ -156,6 +156,9 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
 // One 128 x bn tile a cluster, its K slots dealt to the cluster's CTAs in
 // contiguous parts; with more than one CTA the parts are summed by rank over
 // distributed shared memory (a fixed order, no workspace and no atomics).
+// Few rows stream the weights once: 16 x 16384 x 8192, 134 MB in 256 CTAs, takes 25.4 us
+// with cold caches (5.3 TB/s), of which some 5 are the start, the first bytes' way from
+// DRAM, the sum over two CTAs and the end; 16 x 8192 x 8192 15.1 us.
 __global__ void __launch_bounds__(kTileThreads) gemm_fp8_tile(const __grid_constant__ TileParams p)
 {
     extern __shared__ uint8_t smem_raw[];
@@ -357,6 +360,13 @@ __global__ void __launch_bounds__(kTileThreads) gemm_fp8_tile(const __grid_const
 // Up to 224 columns two accumulators and the scales fit tensor memory (512 columns), and a
 // tile's MMAs follow the last one's without a pause.  Tiles of 256 columns have one, which
 // the epilogue reads before the next tile's MMAs begin.
+//
+// Large products are bound by the SM's 64 bytes a cycle of operands, close before the MMAs
+// (tensor pipe 85 % active), and in long runs by the power limit (1390 MHz at 1.38 kW): 131072 x
+// 2048 x 7168 takes 1050 us in short runs (3.66 PFLOP/s), 1190 to 1220 in long ones; 131072 x
+// 7168 x 2048 in 8 groups 1165 and 1325; 8192^3 306 and 345; gate/up of 65536 rows, 8 groups of
+// 2048 x 7168, 1045.  Few rows a group stream the weights: 512 rows, 64 groups of twice 2048 x
+// 7168, 280 us (6.6 TB/s).  Small K is the epilogue's: 131072 x 7168 x 512 410 us.
 //
 // Gate/up (kGated): the 256 lanes hold 128 rows of either weight, 16 of one and 16 of
 // the other by turns, so that a thread of the epilogue holds both values of an output.
