@@ -30,7 +30,6 @@ using mxf4_dev::kDrainNs;
 using mxf4_dev::mbar_arrive_cluster_relaxed;
 using mxf4_dev::scale_desc;
 using mxf4_dev::tmem_copy_scales;
-using mxf4_dev::tmem_copy_scales_pair;
 
 // D[tmem] (+)= A * B with block scales, 32 values of K.
 __device__ __forceinline__ void umma_mxf8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -40,18 +39,6 @@ __device__ __forceinline__ void umma_mxf8(uint32_t d_tmem, uint64_t adesc, uint6
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
-            d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
-}
-
-__device__ __forceinline__ void umma_mxf8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                               uint32_t sfa, uint32_t sfb, uint32_t accumulate)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
             d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
@@ -548,7 +535,7 @@ __device__ __forceinline__ void tma_store_2d_if(uint32_t on, const void* tmap, u
 __device__ __forceinline__ uint32_t mbar_test(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
                  : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok;
 }
@@ -613,7 +600,6 @@ __device__ __forceinline__ uint4 ld_smem_v4(uint32_t addr)
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
     return v;
 }
-
 
 template <bool kGated>
 __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_constant__ PairParams p)
@@ -694,7 +680,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
             const uint32_t xbytes = 128u * half;
             const int32_t wn = (o.w * 2 + static_cast<int>(rank)) * kRows, xr = o.row + static_cast<int>(rank) * half;
             for (int s = 0; s < p.steps; ++s) {
-                ok = mbar_wait(empty(st), par ^ 1u, abort, p.timeout_ns);
+                ok = mbar_wait_cluster(empty(st), par ^ 1u, abort, p.timeout_ns);
                 if (!ok) break;
                 const uint32_t a = base + st * stage_bytes;
                 const uint32_t bar = mapa_shared(full(st), 0);
@@ -755,7 +741,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
 #pragma unroll
                 for (int h = 0; h < 3; ++h)   // (a tile further is the next one's same line)
                     x[h] = h == 0 || o.width > 128 * (h - 1) ? line(p.sx, (o.row >> 7) + h, p.x_tiles, first) : none;
-                ok = __all_sync(~0u, mbar_wait(sempty(st), par ^ 1u, abort, p.timeout_ns));
+                ok = __all_sync(~0u, mbar_wait_cluster(sempty(st), par ^ 1u, abort, p.timeout_ns));
                 if (!ok) break;
                 par ^= 1u;
                 const uint32_t at = sets + st * kSetBytes + lane * 16;
@@ -790,9 +776,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
             int width = width_at(t);
             // waits for the operands at hand, for their scales and for an accumulator that has been read
             auto ready = [&](bool scales, bool room) {
-                return __all_sync(~0u, (!room || mbar_wait(tempty + 8 * acc, tpar ^ 1u, abort, p.timeout_ns)) &&
+                return __all_sync(~0u, (!room || mbar_wait_cluster(tempty + 8 * acc, tpar ^ 1u, abort, p.timeout_ns)) &&
                                            (!scales || mbar_wait_cluster(sfull(set), spar, abort, p.timeout_ns)) &&
-                                           mbar_wait(full(st), par, abort, p.timeout_ns)) != 0;
+                                           mbar_wait_cluster(full(st), par, abort, p.timeout_ns)) != 0;
             };
             if (ok && t < tiles) ok = ready(true, true);
             while (ok && t < tiles) {
@@ -872,7 +858,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
                     if (n < p.n) bias[i] = ld_nc_u16(p.bias + n);
                 }
             }
-            const bool ok = __all_sync(~0u, mbar_wait(tfull + 8 * acc, tpar, abort, p.timeout_ns));
+            const bool ok = __all_sync(~0u, mbar_wait_cluster(tfull + 8 * acc, tpar, abort, p.timeout_ns));
             if (!ok) {
                 if (lane == 0) fail();
                 break;
@@ -887,7 +873,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
             auto finish = [&](int b, float* v) {
                 const int left = o.rows - b * 32;   // rows of C among the 32
                 if (left <= 0 || n0 >= p.n) return;
-                const uint32_t box = box0 + (turn ^= kBoxBytes);
+                const uint32_t box = box0 + turn;
                 if (kGated) {
                     act_all<16>(p.act, v);
 #pragma unroll
@@ -904,7 +890,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
                 }
                 // to the box as rows of C: row tok at tok * 2 kN, its 16-byte parts shifted as TMA's
                 // swizzles have it, so that eight rows fall on different banks
-                if (lane == 0) bulk_wait_group_read<1>();   // the box's last store, the one before last, has read it
+                // (the last copy out of a box took the other one: this one's is the copy before)
+                if (lane == 0) bulk_wait_group_read<1>();
                 __syncwarp();
                 auto part = [&](int tok, int c) {
                     return box + tok * (2 * kN) + ((c ^ (kGated ? (tok >> 2) & 1 : (tok >> 1) & 3)) << 4);
@@ -923,6 +910,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
                     fence_proxy_async_smem();
                     __syncwarp();
                     tma_store_2d_if(lane == 0, &p.tmC, box, static_cast<int32_t>(n0), o.row + b * 32, policy);
+                    turn ^= kBoxBytes;
                     return;
                 }
                 __syncwarp();

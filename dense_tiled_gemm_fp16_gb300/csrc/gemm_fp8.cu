@@ -192,7 +192,7 @@ gemm_f16_status launch_pair(const Product& q, const Device& dev, const Sizes& sa
     p.ldc = q.ldc, p.rows = q.m, p.n = q.n;
     p.groups = static_cast<int32_t>(std::max<int64_t>(q.groups, 1));
     const int64_t tiles_w = cdiv(q.n, gated ? 128 : 256), tiles = (cdiv(q.m, 32) + p.groups) * tiles_w;
-    if (tiles > INT32_MAX) return GEMM_F16_ERR_INVALID_VALUE;   // (an upper bound of their number)
+    if (tiles > INT32_MAX - 4096) return GEMM_F16_ERR_INVALID_VALUE;   // (an upper bound of their number; they are stepped through)
     p.tiles_w = static_cast<int32_t>(tiles_w);
     // Weight tiles of at most 32 MB walked together, so that A's rows come from DRAM once
     // (131072 x 7168 x 2048 in 8 groups: 1405 us with 8 tiles, 1349 with all 28).

@@ -20,7 +20,7 @@ __device__ __forceinline__ void take16(const uint32_t* in, uint32_t o, uint32_t*
     const uint32_t bits = (o & 2u) * 8u;
     auto from = [&](auto k) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) out[c] = __funnelshift_r(in[k.value + c], in[k.value + c + 1 < 8 ? k.value + c + 1 : 7], bits);
+        for (int c = 0; c < 4; ++c) out[c] = __funnelshift_r(in[k.value + c], in[k.value + c + 1], bits);
     };
     switch (o >> 2) {
     case 0: from(Int<0>()); break;
