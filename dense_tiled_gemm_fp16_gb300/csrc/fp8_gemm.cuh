@@ -367,7 +367,7 @@ constexpr uint32_t kSfCol = 496, kAcc1 = 256;   // scales of the weights (4), of
 struct PairParams {
     CUtensorMap tmW, tmU;        // weight codes {pitch, n, groups}, boxes of 128 bytes x 128 rows (kGated: 16)
     CUtensorMap tmX[8];          // A's codes {pitch, rows}, boxes of 128 bytes x 16, 32, .. 128 rows (one group: of its width's)
-    CUtensorMap tmC;             // boxes of a warp's columns x 32 rows (c_tma)
+    CUtensorMap tmC;             // boxes of a warp's columns x 32 rows (c_unit 16)
     const uint8_t* sw;           // scale tiles of the weights, of the second ones, and of A
     const uint8_t* su;
     const uint8_t* sx;
@@ -378,7 +378,7 @@ struct PairParams {
     int64_t ldc, rows, n;
     int32_t groups, tiles_w, panel;   // panel: weight tiles walked together
     int32_t width;               // W; 0: of the groups' choice
-    int32_t k32, steps, act, bf16, c_tma;   // c_tma: C's rows take 16-byte stores, and TMA's
+    int32_t k32, steps, act, bf16, c_unit;   // c_unit: bytes that C's rows, their pitch and C are multiples of, at most 16
     int32_t test_stall;
     uint64_t timeout_ns;
     int* status;
@@ -594,12 +594,16 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uin
                  : "memory");
 }
 
-__device__ __forceinline__ uint4 ld_smem_v4(uint32_t addr)
+__device__ __forceinline__ void ld_smem(uint32_t addr, uint4* v)
 {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-    return v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v->x), "=r"(v->y), "=r"(v->z), "=r"(v->w) : "r"(addr) : "memory");
 }
+__device__ __forceinline__ void ld_smem(uint32_t addr, uint2* v)
+{
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v->x), "=r"(v->y) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ld_smem(uint32_t addr, uint32_t* v) { asm volatile("ld.shared.u32 %0, [%1];" : "=r"(*v) : "r"(addr) : "memory"); }
+__device__ __forceinline__ void ld_smem(uint32_t addr, uint16_t* v) { asm volatile("ld.shared.u16 %0, [%1];" : "=h"(*v) : "r"(addr) : "memory"); }
 
 template <bool kGated>
 __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_constant__ PairParams p)
@@ -642,7 +646,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
         fence_mbarrier_init();
         tma_prefetch_desc(&p.tmW);
         if (kGated) tma_prefetch_desc(&p.tmU);
-        if (p.c_tma) tma_prefetch_desc(&p.tmC);
+        if (p.c_unit == 16) tma_prefetch_desc(&p.tmC);
     }
     if (warp == 9) {
         tmem_alloc_pair(smem_u32(&tmem_slot), 512);
@@ -906,7 +910,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
                         stmatrix_x4_trans(part(8 * c + (lane & 7), lane >> 3), two(4 * c), two(4 * c + 2), two(16 + 4 * c),
                                           two(16 + 4 * c + 2));
                 }
-                if (p.c_tma && left >= 32) {   // (TMA leaves out columns past C's, not rows past the group's)
+                if (p.c_unit == 16 && left >= 32) {   // (TMA leaves out columns past C's, not rows past the group's)
                     fence_proxy_async_smem();
                     __syncwarp();
                     tma_store_2d_if(lane == 0, &p.tmC, box, static_cast<int32_t>(n0), o.row + b * 32, policy);
@@ -915,19 +919,32 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_fp8_pair(const __grid_co
                 }
                 __syncwarp();
                 uint16_t* to = p.C + (static_cast<int64_t>(o.row) + b * 32) * p.ldc + n0;
-                if (p.c_tma && n0 + kN <= p.n) {
-                    constexpr int kParts = kN / 8, kPass = 32 / kParts;   // 16-byte parts of a row, rows a pass
-                    const int c = lane % kParts;
+                // by units of as many bytes as C's rows are multiples of, a row's after one another
+                auto store = [&](auto unit) {
+                    using U = decltype(unit);
+                    constexpr int kParts = 2 * kN / sizeof(U), kPass = 32 / kParts, kRowsAtOnce = 8;
+                    const int c = lane % kParts, byte = c * static_cast<int>(sizeof(U)), first = lane / kParts;
+                    uint8_t* row = reinterpret_cast<uint8_t*>(to + first * p.ldc) + byte;
+                    const int64_t step = 2 * kPass * p.ldc;
+                    if (byte >= 2 * (p.n - n0)) return;
 #pragma unroll
-                    for (int tok = lane / kParts; tok < 32; tok += kPass)
-                        if (tok < left) *reinterpret_cast<uint4*>(to + tok * p.ldc + 8 * c) = ld_smem_v4(part(tok, c));
-                } else if (lane < kN && n0 + lane < p.n) {
-#pragma unroll 8
-                    for (int tok = 0; tok < 32; ++tok) {
-                        uint16_t x;
-                        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(part(tok, lane >> 3) + 2 * (lane & 7)) : "memory");
-                        if (tok < left) to[tok * p.ldc + lane] = x;
+                    for (int r0 = 0; r0 < 32 / kPass; r0 += kRowsAtOnce) {
+                        U x[kRowsAtOnce];
+#pragma unroll
+                        for (int r = r0; r < r0 + kRowsAtOnce && r < 32 / kPass; ++r) {
+                            const int tok = r * kPass + first;
+                            ld_smem(part(tok, byte >> 4) + (byte & 15), &x[r - r0]);
+                        }
+#pragma unroll
+                        for (int r = r0; r < r0 + kRowsAtOnce && r < 32 / kPass; ++r, row += step)
+                            if (r * kPass + first < left) *reinterpret_cast<U*>(row) = x[r - r0];
                     }
+                };
+                switch (p.c_unit) {
+                case 16: store(uint4()); break;
+                case 8: store(uint2()); break;
+                case 4: store(uint32_t()); break;
+                default: store(uint16_t()); break;
                 }
                 __syncwarp();
             };

@@ -201,7 +201,9 @@ gemm_f16_status launch_pair(const Product& q, const Device& dev, const Sizes& sa
     p.steps = static_cast<int32_t>(cdiv(q.k, 128));
     p.act = q.act;
     p.bf16 = q.dtype == FP8_BF16;
-    p.c_tma = q.n % 8 == 0 && q.ldc % 8 == 0 && q.ldc < int64_t(1) << 39 && aligned(q.c, 16);
+    p.c_unit = 16;   // (and rows of 16-byte units are stored by TMA)
+    while (p.c_unit > 2 && ((q.n | q.ldc) * 2 % p.c_unit != 0 || !aligned(q.c, p.c_unit) || (p.c_unit == 16 && q.ldc >> 39)))
+        p.c_unit /= 2;
     p.test_stall = option(GEMM_F16_OPT_TEST_STALL) == 1;
     p.timeout_ns = timeout_ns();
     p.status = dev.status;
@@ -209,7 +211,7 @@ gemm_f16_status launch_pair(const Product& q, const Device& dev, const Sizes& sa
     if (!encode_codes(&p.tmW, q.b_codes, q.n, p.groups, sb.pitch, box) ||
         (gated && !encode_codes(&p.tmU, q.u_codes, q.n, p.groups, sb.pitch, box)))
         return GEMM_F16_ERR_LAUNCH;
-    if (p.c_tma && !encode_out(&p.tmC, q.c, q.m, q.n, q.ldc, gated)) return GEMM_F16_ERR_LAUNCH;
+    if (p.c_unit == 16 && !encode_out(&p.tmC, q.c, q.m, q.n, q.ldc, gated)) return GEMM_F16_ERR_LAUNCH;
     const auto kernel = gated ? fp8_dev::gemm_fp8_pair<true> : fp8_dev::gemm_fp8_pair<false>;
     if (!allow_smem(reinterpret_cast<const void*>(kernel), gated ? 1 : 2, fp8_dev::kPairSmem)) return GEMM_F16_ERR_LAUNCH;
     const int64_t clusters = std::min<int64_t>(dev.sms / 2, tiles);
