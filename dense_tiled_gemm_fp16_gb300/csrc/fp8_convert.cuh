@@ -20,7 +20,7 @@ struct QuantParams {
     uint8_t* scales;
     int64_t rows, k, pitch;   // pitch: code bytes a row
     int64_t kt, row_tiles;
-    int64_t tile_rows;        // rows of a tile that a block takes: 128, or fewer of few rows
+    int64_t tile_rows;        // rows of a tile that a block takes: 8, 16 or 32 (strided: 128)
 };
 
 // Unit stride along k: a warp takes the 512 values of a row of the tile, 8 a lane twice,

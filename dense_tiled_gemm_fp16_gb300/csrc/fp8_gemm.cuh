@@ -334,15 +334,15 @@ __global__ void __launch_bounds__(kTileThreads) gemm_fp8_tile(const __grid_const
 // ------------------------------------------------------------------ pairs
 // Persistent clusters of two CTAs, one tile at a time, its MMAs over both
 // (cta_group::2).  The weights' rows take the 256 lanes and A's rows the columns, in
-// every product: a tile's columns are then as many as its rows need (32 to 224, a
+// every product: a tile's columns are then as many as its rows need (32 to 256, a
 // number in the instruction descriptor), so that one kernel serves groups of any
 // number of rows, which the host does not know.
 //
 // Tiles: each group's rows are cut into equal parts of at most W, a multiple of 32;
 // every CTA finds the W of least cost for itself from the row counts (choose_tiles).
 // A tile ends with its group; it may read rows of the next one, whose columns it
-// then leaves out.  A's scales begin at any row, so a warp puts their words in the
-// order of the scale tiles as it loads them, one set for 512 values of k.
+// then leaves out.  A's scales begin at any row, so warps put their words in the
+// order of the scale tiles as they load them, one set for 512 values of k.
 //
 // Up to 224 columns two accumulators and the scales fit tensor memory (512 columns), and a
 // tile's MMAs follow the last one's without a pause.  Tiles of 256 columns have one, which

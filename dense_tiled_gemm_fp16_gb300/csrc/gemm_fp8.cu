@@ -100,8 +100,12 @@ gemm_f16_status launch_quantize(fp8_dev::QuantParams p, int64_t batch, cudaStrea
 gemm_f16_status run_quantize(const void* x, int dtype, int64_t sb, int64_t sr, int64_t sk, void* codes, void* scales,
                              int64_t rows, int64_t k, int64_t batch, const Sizes& s, int sms, cudaStream_t stream)
 {
-    // few tiles: 16 rows a block, the least that keeps its loads in flight
-    const int64_t tile_rows = s.row_tiles * s.kt * batch >= 4 * sms ? 128 : 16;
+    // Rows of a block: 32 of many tiles, fewer of few, so that there are blocks for every SM.
+    // A row a warp (8) against 16: 1.5 and 2.1 us at 16 x 8192 (16 tiles), 3.7 and 3.8 at
+    // 1024 x 4096 (64), but 6.0 and 5.7 at 2048 x 4096 (128), 8.2 and 7.5 at 3001 x 4096 (192).
+    // 16, 32, 64, 128: 14.9, 14.6, 17.1, 19.1 at 4096 x 7168 (448 tiles), 56, 54, 55, 61 at
+    // 16384 x 7168, 427, 408, 407, 410 at 131072 x 7168 (all bf16).
+    const int64_t tiles = s.row_tiles * s.kt * batch, tile_rows = tiles >= 2 * sms ? 32 : 2 * tiles >= sms ? 16 : 8;
     const fp8_dev::QuantParams p{x, sb, sr, sk, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales), rows, k,
                                  s.pitch, s.kt, s.row_tiles, tile_rows};
     return dtype == FP8_F16    ? launch_quantize<__half>(p, batch, stream)

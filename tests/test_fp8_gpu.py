@@ -62,6 +62,14 @@ def test_quantize_and_back(rows, k, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("batch,rows,k", [(1, 9, 513), (9, 9, 5000), (1, 1281, 4100), (31, 33, 5000), (1, 5153, 4104)])
+def test_quantize_rows_a_block(batch, rows, k, dtype):
+    """Blocks of 8, 16 and 32 rows, the last of them with one row."""
+    x = _values((batch, rows, k), batch + rows + k, dtype)
+    _same(g.fp8_quantize(x.to(DEV)), x)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("rows,k", [(1, 300), (77, 1), (129, 513), (1000, 640)])
 def test_quantize_strided(rows, k, dtype):
     x = _values((rows, k), rows + k, dtype).to(DEV)
