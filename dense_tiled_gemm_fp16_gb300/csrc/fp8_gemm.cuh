@@ -18,6 +18,7 @@
 
 #include "activation.cuh"
 #include "fp8_format.cuh"
+#include "fp8_tiles.h"
 #include "gemm_f16.h"
 #include "mxf4_ptx.cuh"
 #include "ptx.cuh"
@@ -392,19 +393,6 @@ struct Groups {
     uint16_t width[kMaxGroups];  // columns of each part, at most
     int widest;                  // of all groups
 };
-
-__host__ __device__ inline int parts_of(int rows, int w) { return (rows + w - 1) / w; }
-__host__ __device__ inline int width_of(int rows, int parts) { return parts ? ((rows + parts - 1) / parts + 31) & ~31 : 0; }
-
-// What the clusters' turns cost in cycles: a step of 128 values brings 16 KB of weights and
-// 64 bytes a column to either CTA, at 64 bytes a cycle 256 + W cycles, which is no less
-// than its 2 W cycles of MMA (measured: 321 cycles at W = 64, 376 at 128, 485 at 224), and a
-// tile costs some 600 more, with one accumulator 3000.
-__host__ __device__ inline int64_t cost_of(int tiles, int widest, int clusters, int steps)
-{
-    const int turns = (tiles + clusters - 1) / clusters;
-    return turns * (static_cast<int64_t>(steps) * (widest + 256) + (widest > 224 && turns > 1 ? 3000 : 600));
-}
 
 // By one warp.  Counts below zero are taken as zero, rows past the matrix as absent.
 __device__ __forceinline__ void choose_tiles(const PairParams& p, Groups& g, int clusters, int lane)
