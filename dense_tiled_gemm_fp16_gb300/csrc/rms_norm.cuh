@@ -20,6 +20,7 @@ namespace norm_dev {
 
 using namespace gemm_f16_dev;
 using fp8_dev::Bool;
+using mxf4_dev::Elem;
 
 using mxf4_dev::fma2;
 using mxf4_dev::mul2;
@@ -46,6 +47,73 @@ struct Params {
     int64_t rows, d, pitch, kt, row_tiles;
     float eps;
 };
+
+// bf16 reaches further than its squares do in fp32: they are infinite from 2^64 on, and
+// below 2^-63 lose bits.  A row whose squares' sum is infinite, or whose mean square with eps
+// is below 2^-90 (more than 2^45 as a factor), is done here once more, `f` times as large,
+// 2^80 or 2^-80: bound by latency, out of the way of the others' registers.  By whole warps,
+// each of which sums up all of the row, so that the sum has one order here, too (at most 69
+// roundings of it); then every warp takes blocks of 128 values and writes over what the
+// kernel gave them.  That and h have been written, and the writes are visible to the warp.
+template <typename T, int kMost>
+__device__ __forceinline__ void far_row(const Params& p, float f)
+{
+    constexpr bool kWarpRow = kMost == 256;
+    const int lane = threadIdx.x & 31, d = static_cast<int>(p.d);
+    const int warp = kWarpRow ? 0 : threadIdx.x >> 5, warps = kWarpRow ? 1 : blockDim.x >> 5;
+    const int64_t row = kWarpRow ? static_cast<int64_t>(blockIdx.x) * (kMost / 32) + (threadIdx.x >> 5) : blockIdx.x;
+    if (row >= p.rows) return;
+    const uint16_t* h = p.residual ? p.sum + row * p.ss : p.x + row * p.sx;
+    auto value = [](const uint16_t* at) { return Elem<T>::to_f32(*at); };
+    float s = 0.f;
+#pragma unroll 1
+    for (int i0 = 0; i0 < d; i0 += 1024) {
+        float some = 0.f;
+#pragma unroll 1
+        for (int i = i0 + lane; i < min(d, i0 + 1024); i += 32) some = fmaf(value(h + i) * f, value(h + i) * f, some);
+        s += some;
+    }
+#pragma unroll
+    for (int k = 16; k; k /= 2) s += __shfl_xor_sync(~0u, s, k);
+    const float r = 1.f / sqrtf(s / static_cast<float>(d) + p.eps * f * f);
+    // f h is exact where f is large, and r f may be past fp32 there; where f is small h
+    // keeps its small values, and r f has 21 bits at least
+    const float fh = f > 1.f ? f : 1.f, fr = f > 1.f ? r : r * f;
+    const int end = static_cast<int>(p.y ? p.d : p.pitch);
+#pragma unroll 1
+    for (int i = warp * 128 + lane * 4; i - lane * 4 < end; i += warps * 128) {
+        float y[4], top = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            y[c] = i + c < d ? value(h + i + c) * fh * fr * value(p.weight + i + c) : 0.f;
+            top = max_nan(top, fabsf(y[c]));
+        }
+        if (p.y) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (i + c < d) p.y[row * p.sy + i + c] = static_cast<uint16_t>(row_dev::narrow2<T>(y[c], 0.f));
+            continue;
+        }
+#pragma unroll
+        for (int k = 16; k; k /= 2) top = max_nan(top, __shfl_xor_sync(~0u, top, k));
+        const uint32_t code = fp8_dev::scale_code_f32(top);
+        const float g = code == 255u ? 0.f : fp8_dev::inverse_scale(code);
+        *reinterpret_cast<uint32_t*>(p.codes + row * p.pitch + i) =
+            code == 255u ? 0u : fp8_dev::e4m3_of(y[0] * g, y[1] * g, y[2] * g, y[3] * g);
+        if (lane == 0) p.scales[fp8_dev::scale_at(row, i >> 7, p.kt)] = static_cast<uint8_t>(code);
+    }
+}
+
+// As a call, for two forms that are slower with it inside: of rows past 9216 values (68
+// registers a thread instead of 64 are a block less of three an SM: 4882 x 12288 44 us, 54 so)
+// and of 257 to 512 (117187 x 512 to 8 bits 44.8 us, 48.4 so).  In the others a call costs more:
+// it takes 40 registers, and rows of up to 256 values, whose form has 32, a fifth longer.
+// Over the kernel without far rows it is 1 to 4 %: 3001 x 4097 as it was, 16 x 4096 1.59 us, now 1.64.
+template <typename T, int kMost>
+__device__ __noinline__ void far_row_apart(const Params& p, float f)
+{
+    far_row<T, kMost>(p, f);
+}
 
 // kMost 256: a warp a row, eight rows a block.  Otherwise a block of at most kMost threads
 // a row.  A thread takes kVecs times 8 values.
@@ -224,6 +292,16 @@ __global__ void __launch_bounds__(kMost, kVecs == 3 && !kVec ? 3 : 0) rms_norm(c
             const int kt = static_cast<int>(p.kt), words = static_cast<int>(p.row_tiles * 128 - p.rows) * kt;
             for (int q = t; q < words; q += threads)
                 *reinterpret_cast<uint32_t*>(p.scales + fp8_dev::scale_at(p.rows + q / kt, 4 * (q % kt), p.kt)) = 0u;
+        }
+    }
+    if constexpr (Elem<T>::kInf == 0x7F80u) {
+        // (here, so that nothing of the others' is held over it or waits behind it)
+        if (!(r > 0.f && r <= 0x1p45f)) {   // (the same in all of a row's threads)
+            if (kWarpRow) __syncwarp();
+            else __syncthreads();
+            const float f = r > 1.f ? 0x1p80f : 0x1p-80f;
+            if constexpr (kMost == 832 || (kMost == 256 && kVecs == 2)) far_row_apart<T, kMost>(p, f);
+            else far_row<T, kMost>(p, f);
         }
     }
 }

@@ -7,7 +7,8 @@
  *
  * x, residual, weight and sum (h) are fp16 or bf16; the rest is computed in fp32
  * and rounded once, to the same type (y) or to 8 bits (codes and scales of a
- * rows x d matrix as gemm_fp8.h lays it out, what its products take).
+ * rows x d matrix as gemm_fp8.h lays it out, what its products take).  A bf16 row
+ * whose squares are out of fp32's range is summed 2^80 or 2^-80 times as large.
  */
 #ifndef RMS_NORM_H
 #define RMS_NORM_H
