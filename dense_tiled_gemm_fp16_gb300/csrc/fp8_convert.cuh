@@ -32,8 +32,9 @@ struct QuantParams {
 // One row at a time and full occupancy keep more loads under way than several rows and
 // less of it: 131072 x 7168 in fp16 565 us with four rows a warp, 445 with two, 409 so
 // (6.9 TB/s); fp32 has the bytes under way with half the occupancy (32768 x 7168: 175 us,
-// 6.7 TB/s).  Rows that start anywhere, 32768 x 4097 in bf16: 89 us (4.5 TB/s), by the second
-// load and the shift of every 16 bytes.
+// 6.7 TB/s).  (At 32 registers the aligned 16-bit form keeps 12 to 16 bytes a thread in local
+// memory.)  Rows that start anywhere, 32768 x 4097 in bf16: 89 us (4.5 TB/s), by the second
+// load and the shift of every 16 bytes, most of which the lane beside has loaded, too.
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kConvThreads, sizeof(T) == 4 ? 4 : 8) quantize_rows(const QuantParams p)
 {
@@ -84,7 +85,11 @@ __global__ void __launch_bounds__(kConvThreads, sizeof(T) == 4 ? 4 : 8) quantize
 
 // Any strides (a transposed view has unit stride along the rows): a lane takes a
 // block of a row and a warp 32 neighbouring rows, so that a unit row stride gives
-// contiguous loads; the codes, 128 bytes a row, are turned in shared memory.
+// contiguous loads; the codes, 128 bytes a row, are turned in shared memory.  A lane's 128
+// values stay in its registers from the largest magnitude on, 254 registers in fp16 and 182 in
+// bf16: one block of threads an SM, with too few loads of 64 bytes a warp under way.  A weight
+// [7168, 2048] takes 51 us in fp16 and 73 in bf16, 64 of them 2560 and 3570 (1.1 and 0.8 TB/s;
+// one that is contiguous along k 8.5 us, its bytes need 6.5).
 template <typename T>
 __global__ void __launch_bounds__(kConvThreads) quantize_strided(const QuantParams p)
 {

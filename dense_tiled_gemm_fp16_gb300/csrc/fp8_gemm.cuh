@@ -351,10 +351,12 @@ __global__ void __launch_bounds__(kTileThreads) gemm_fp8_tile(const __grid_const
 //
 // Large products are bound by the SM's 64 bytes a cycle of operands, close before the MMAs
 // (tensor pipe 85 % active), and in long runs by the power limit (1390 MHz at 1.38 kW): 131072 x
-// 2048 x 7168 takes 1050 us in short runs (3.66 PFLOP/s), 1190 to 1220 in long ones; 131072 x
-// 7168 x 2048 in 8 groups 1165 and 1325; 8192^3 306 and 345; gate/up of 65536 rows, 8 groups of
-// 2048 x 7168, 1045.  Few rows a group stream the weights: 512 rows, 64 groups of twice 2048 x
-// 7168, 280 us (6.6 TB/s).  Small K is the epilogue's: 131072 x 7168 x 512 410 us.
+// 2048 x 7168 takes 1050 to 1060 us in short runs (3.6 PFLOP/s), 1190 to 1250 in long ones (3.1
+// to 3.2), by the device; 131072 x 7168 x 2048 in 8 groups 1170 and 1325 to 1375; 8192^3 308 and
+// 350; gate/up of 65536 rows, 8 groups of 2048 x 7168, 1050.  Few rows a group stream the
+// weights: 512 rows, 64 groups of twice 2048 x 7168, 280 us (6.6 TB/s).  Small K is the
+// epilogue's: 131072 x 7168 x 512 410 to 416 us.  A in 16 bits is quantised before the product
+// begins: 131072 x 2048 x 7168 1515 and 1580 us, 131072 x 7168 x 2048 in 8 groups 1305 and 1460.
 //
 // Gate/up (kGated): the 256 lanes hold 128 rows of either weight, 16 of one and 16 of
 // the other by turns, so that a thread of the epilogue holds both values of an output.

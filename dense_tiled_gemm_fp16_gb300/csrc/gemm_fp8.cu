@@ -267,10 +267,10 @@ gemm_f16_status launch_tile(const Product& q, const Device& dev, const Sizes& sa
     p.tmem_cols = p.bn == 128 ? 256 : p.bn == 64 ? 128 : p.bn == 32 ? 64 : 32;
     const int64_t tiles = cdiv(p.M, 128) * cdiv(p.N, p.bn);
     int cluster = 1;
-    // As many CTAs a tile as the device holds at once, while each has 8 steps: their sums
-    // cost 1 to 5 us, more than a short K of a wide tile saves (16 steps, 512 x 512 x 2048:
-    // 6.5 us by one CTA a tile, 10.0 by two; 56 steps, 64 x 2048 x 7168: 15.6 by two, 11.0
-    // by seven or eight).
+    // CTAs a tile: 1, 2, 4 or 8, as many as the device holds at once while each has 8 steps, 16
+    // where a wide tile has fewer than 32: their sums cost 1 to 5 us, more than a short K
+    // saves there (16 steps, 512 x 512 x 2048: 6.5 us by one CTA a tile, 9.9 by two, 9.0 by four; 56
+    // steps, 64 x 2048 x 7168: 15.5 by two, 11.0 by the four that this gives, 11.1 by eight).
     const int least = p.bn == 16 || p.steps >= 32 ? 8 : 16;
     while (cluster < 8 && tiles * cluster * 2 <= 2 * dev.sms && cluster * 2 * least <= p.steps) cluster *= 2;
     if (tiles * cluster > INT32_MAX) return GEMM_F16_ERR_INVALID_VALUE;
@@ -297,11 +297,11 @@ gemm_f16_status product(Product q, cudaStream_t stream)
     }
     const int64_t pair = option(GEMM_F16_OPT_PAIR);   // (1 never, 2 always)
     // Small tiles, K shared out where it is long, for up to 32 rows or 64 columns (us, small
-    // and pair: 16 x 2048 x 7168 8.6, 13.4; 16 x 16384 x 8192 25.1, 26.4; 65536 x 64 x 1024
-    // 11.7, 19.0), for up to 64 rows with a long K and not many columns (64 x 2048 x 7168
-    // 11.0, 13.4; 64 x 8192 x 8192 17.5, 18.2; but x 16384 30.0, 27.0 and 64 x 7168 x 2048
-    // 11.0, 8.5), and where one turn of them takes a short K, 16-byte rows of C given (1024^3
-    // 4.9, 7.1; 1536^3 7.2, 8.4; 3000 x 300 x 300 13.0, 6.8).  Pairs start 2 us later.
+    // and pair: 16 x 2048 x 7168 8.6, 15.4; 16 x 16384 x 8192 25.1, 26.9; 65536 x 64 x 1024
+    // 11.4, 19.7), for up to 64 rows with a long K and not many columns (64 x 2048 x 7168
+    // 11.0, 15.7; 64 x 8192 x 8192 17.5, 18.9; but x 16384 29.6, 27.5 and 64 x 7168 x 2048
+    // 11.0, 9.5), and where one turn of them takes a short K, 16-byte rows of C given (1024^3
+    // 5.0, 7.8; 1536^3 8.3, 9.3; but 3000 x 300 x 300 12.2, 5.9).  Pairs start 2 us later.
     const int64_t steps = cdiv(q.k, 128);
     const bool few = q.m <= 32 || q.n <= 64 || (q.m <= 64 && steps >= 40 && q.n <= 8192),
                small = q.m > 64 && steps <= 16 && cdiv(q.m, 128) * cdiv(q.n, 128) <= dev.sms && q.n % 8 == 0 &&

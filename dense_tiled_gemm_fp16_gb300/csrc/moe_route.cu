@@ -17,8 +17,9 @@ namespace {
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 // Parts of the choices that moe_sort counts by themselves: one block each, at most 152,
-// so that every block can add up all counts.  One block alone takes 1024 choices at
-// once; 4096 took it 18 us, two kernels 10.
+// so that every block can add up all counts.  (A block for each SM of a GB300; a constant,
+// because the workspace's size hangs on it and is asked for where no device is.)  One block
+// alone takes 1024 choices at once; 4096 took it 18 us, two kernels 10.
 constexpr int64_t kFewChoices = 1024, kMaxParts = 152;
 
 bool sort_parts(int64_t tokens, int64_t top, int64_t experts, int64_t* part, int64_t* parts)

@@ -148,7 +148,7 @@ struct RowParams {
 };
 
 // Blocks of 128 threads, so that an SM always has some with their loads under way (256:
-// combining 16384 tokens of 8 choices of 7168 values took 388 us, this 321).
+// combining 16384 tokens of 8 choices of 7168 values took 388 us, this 309).
 constexpr int kRowThreads = 128, kChunk = kRowThreads * 8;   // values of a row a block takes at a time
 
 // (a place outside the rows, which no order of this library holds, is taken as none)
@@ -161,7 +161,7 @@ __device__ __forceinline__ int64_t place_of(const RowParams& p, int64_t t, int j
 // A token's row is read once and written to each of its places: the other way round, by
 // place, the rows would be read top times from a matrix that L2 does not hold.  Where
 // rows start anywhere a thread takes the values of 16 aligned bytes of each place's row.
-// 16384 tokens of 8 choices, 7168 values: 312 us (6.8 TB/s), 2049 values 159 us (3.8).
+// 16384 tokens of 8 choices, 7168 values: 312 to 318 us (6.7 TB/s), 2049 values 159 us (3.8).
 template <bool kVec>
 __global__ void __launch_bounds__(kRowThreads) gather_rows(const RowParams p)
 {
@@ -282,7 +282,9 @@ __global__ void __launch_bounds__(kRowThreads, kAtOnce == 8 ? 5 : kAtOnce == 4 ?
     }
 }
 
-// Rows held in 8 bits: the codes 16 bytes a thread, the scales a word of four blocks.
+// Rows held in 8 bits: the codes 16 bytes a thread, the scales a word of four blocks.  Bound
+// by HBM: 16384 tokens of 8 choices, 7168 values 166 us (6.4 TB/s), 2048 values 51 (6.0), 4096
+// tokens of 7168 values 44 (6.0); 16 tokens 2 us.
 struct Fp8RowParams {
     const uint8_t *codes, *scales;
     uint8_t *out_codes, *out_scales;

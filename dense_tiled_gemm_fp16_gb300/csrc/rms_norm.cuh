@@ -118,7 +118,8 @@ __device__ __noinline__ void far_row_apart(const Params& p, float f)
 // kMost 256: a warp a row, eight rows a block.  Otherwise a block of at most kMost threads
 // a row.  A thread takes kVecs times 8 values.
 // (At least three blocks of the largest an SM for rows that start anywhere, three times
-// eight values a thread: 32768 x 4097 in bf16 with a residual 233 us, 276 without.)
+// eight values a thread: 32768 x 4097 in bf16 with a residual 233 us, 276 without.  The other
+// forms were not measured with such a bound.)
 template <typename T, int kMost, int kVecs, bool kVec>
 __global__ void __launch_bounds__(kMost, kVecs == 3 && !kVec ? 3 : 0) rms_norm(const Params p)
 {
