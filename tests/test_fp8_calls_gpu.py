@@ -26,7 +26,7 @@ def _normal(*shape, seed, dtype, scale=1.0):
 
 
 def _views(x):
-    """x at strides of its own: transposed, rows and values apart, rows that start anywhere, one row repeated."""
+    """x at strides of its own: transposed, rows and values apart, rows that start anywhere."""
     m, k = x.shape
     wide = torch.zeros((2 * m, 3 * k + 1), dtype=x.dtype, device=DEV)
     wide[::2, 1::3] = x
